@@ -10,6 +10,7 @@
 #include <string>
 #include <tuple>
 
+#include "api_checks.h"
 #include "api_internal.h"
 #include "kernels.h"
 #include "plan.h"
@@ -25,32 +26,14 @@ namespace {
 constexpr size_t kChunkTarget1D = (size_t)128 << 20;
 constexpr size_t kChunkTarget = (size_t)64 << 20;
 
-size_t dtype_size(lconv_dtype_t dt) { return dt == LCONV_F32 ? 4 : 2; }
-bool dtype_ok(int dt) { return dt == LCONV_F32 || dt == LCONV_F16 || dt == LCONV_BF16; }
 // complex element bytes of the compute type used on the multi-pass path
 size_t work_complex_size(lconv_dtype_t dt, bool filter) { return (filter || dt == LCONV_F32) ? 8 : 4; }
-
-bool mul_ok(int64_t a, int64_t b, int64_t* out) {
-    if (a < 0 || b < 0) return false;
-    if (a != 0 && b > INT64_MAX / a) return false;
-    *out = a * b;
-    return true;
-}
-
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-    if (!a || !b || na == 0 || nb == 0) return false;
-    uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;
-    return a0 < b0 + nb && b0 < a0 + na;
-}
 
 // lengths the forward call and the filter transform take (any N: ragged rows are staged)
 bool n_in_range(int64_t N) { return N >= 1 && N <= LCONV_MAX_N; }
 // lengths the kernels take directly: rows of whole 16-byte groups
 bool n_supported(int64_t N) { return n_in_range(N) && (N % 8) == 0; }
 int64_t round8(int64_t N) { return (N + 7) / 8 * 8; }
-size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 // staging for N not a multiple of 8: `tensors` zero-padded copies of [rows][round8(N)]
 size_t staging_bytes(int64_t rows, int64_t N, lconv_dtype_t dt, int tensors) {
     if (N % 8 == 0) return 0;
@@ -71,8 +54,6 @@ int64_t chunk_seqs(int64_t total, int64_t M, size_t csz, size_t target = kChunkT
     if (per < 1) per = 1;
     return per < total ? per : total;
 }
-
-lconv_status_t hip_status(hipError_t e) { return e == hipSuccess ? LCONV_SUCCESS : LCONV_ERR_HIP; }
 
 // LCONV_LOG: one stderr line per distinct (call, B, H, N, dtype) with the plan it runs
 void log_plan(const char* call, int64_t B, int64_t H, int64_t N, lconv_dtype_t dtype, const Plan1D& p,

@@ -1,0 +1,204 @@
+// linattn.hip -- linear attention with a decay for each head: prompts, gradients, single tokens.
+#include "mixer_kernels.h"
+#include "mixer_io.h"
+
+namespace lcv {
+namespace {
+
+// Token by token: a workgroup holds 64 columns of one state, thread (part, col) rows part * 64 ..
+// part * 64 + 63 of its column in registers.  Per token the state's decay and update, the partial
+// products with Q, and their sum over the four parts through LDS.
+template <int IO, bool TAN>
+__global__ void __launch_bounds__(256) linattn_seq_kernel(LinTanArgs ta) {
+    const LinArgs& a = ta.a;
+    const LinRole& r = a.r;
+    __shared__ float red[4][64];
+    const int col = threadIdx.x & 63, part = threadIdx.x >> 6;
+    const int ncol = (r.DV + 63) / 64;
+    const int64_t bh = blockIdx.x / ncol;
+    const int64_t b = bh / a.H;
+    const int h = (int)(bh - b * a.H), n = (int)(blockIdx.x - bh * ncol) * 64 + col;
+    const int64_t len = row_len(a.lengths, b, a.N);
+    const int64_t qb = row_base(r.Q, b, h), kb = row_base(r.K, b, h), vb = row_base(r.V, b, h);
+    const int64_t ob = b * r.o.b + (int64_t)h * r.o.h;
+    const int64_t sb = bh * r.DK * r.DV + (int64_t)n * r.s_col;
+    const float gamma = expf(log_gamma(a.log_decay, h));
+    const bool on = n < r.DV;
+    float S[64], T[TAN ? 64 : 1];
+    float tan = 0.f;
+#pragma unroll
+    for (int i = 0; i < 64; ++i) {
+        const int d = part * 64 + i;
+        S[i] = r.s_in && on && d < r.DK ? r.s_in[sb + (int64_t)d * r.s_row] : 0.f;
+        if constexpr (TAN) T[i] = 0.f;
+    }
+    for (int64_t i = 0; i < len; ++i) {
+        const int64_t t = r.reverse ? len - 1 - i : i;
+        const float v = on ? load1<IO>(r.V.p, vb + t * r.V.s.n + n) * r.s_kv : 0.f;
+        const float g = r.reverse && i == 0 ? 1.f : gamma;
+        float acc = 0.f, tacc = 0.f;
+#pragma unroll
+        for (int j = 0; j < 64; ++j) {
+            const int d = part * 64 + j;
+            if (d < r.DK) {
+                const float q = load1<IO>(r.Q.p, qb + t * r.Q.s.n + d);
+                if constexpr (TAN) {
+                    T[j] = gamma * (T[j] + S[j]);
+                    tacc += T[j] * q;
+                }
+                S[j] = g * S[j] + load1<IO>(r.K.p, kb + t * r.K.s.n + d) * v;
+                acc += S[j] * q;
+            }
+        }
+        if constexpr (TAN) {
+            if (on) tan += r.s_q * tacc * load1<IO>(ta.q.p, row_base(ta.q, b, h) + t * ta.q.s.n + n);
+        } else if (r.O) {
+            red[part][col] = acc;
+            __syncthreads();
+            if (part == 0 && on) {
+                const float y = r.s_q * (red[0][col] + red[1][col] + red[2][col] + red[3][col]);
+                if (r.o_f32) ((float*)r.O)[ob + t * r.o.n + n] = y;
+                else store1<IO>(r.O, ob + t * r.o.n + n, y);
+            }
+            __syncthreads();
+        }
+    }
+    if constexpr (TAN) {
+        // <T, dstate_out>: the transposed layout, element (d, n) at n * DK + d
+        if (ta.ds_out && on) {
+#pragma unroll
+            for (int j = 0; j < 64; ++j) {
+                const int d = part * 64 + j;
+                if (d < r.DK) tan += T[j] * ta.ds_out[bh * r.DK * r.DV + (int64_t)n * r.DK + d];
+            }
+        }
+        red[part][col] = tan;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            float s = 0.f;
+            for (int p = 0; p < 4; ++p)
+                for (int c = 0; c < 64; ++c) s += red[p][c];
+            ta.part[((int64_t)h * a.B + b) * ncol + (blockIdx.x - bh * ncol)] = s;
+        }
+        return;
+    }
+    if (r.s_out && on) {
+        // a reversed state leaves with the decay of the token it would precede
+        const float g = r.reverse && len > 0 ? gamma : 1.f;
+#pragma unroll
+        for (int j = 0; j < 64; ++j) {
+            const int d = part * 64 + j;
+            if (d < r.DK) r.s_out[sb + (int64_t)d * r.s_row] = g * S[j];
+        }
+    }
+    if (r.O && part == 0 && on)
+        for (int64_t t = len; t < a.N; ++t) {
+            if (r.o_f32) ((float*)r.O)[ob + t * r.o.n + n] = 0.f;
+            else store1<IO>(r.O, ob + t * r.o.n + n, 0.f);
+        }
+}
+
+template <int IO>
+__global__ void __launch_bounds__(256) linattn_step_kernel(LinStepArgs a) {
+    const int64_t bh = blockIdx.x;
+    const int64_t b = bh / a.H;
+    const int h = (int)(bh - b * a.H);
+    const int64_t slot = a.slots ? (int64_t)a.slots[b] : b;
+    const bool live = slot >= 0 && slot < a.nslots;
+    const float gamma = expf(log_gamma(a.log_decay, h));
+    for (int n = threadIdx.x; n < a.DV; n += 256) {
+        float acc = 0.f;
+        if (live) {
+            float* S = a.state + (slot * a.H + h) * (int64_t)a.DK * a.DV + n;
+            const float v = load1<IO>(a.v.p, row_base(a.v, b, h) + n);
+            for (int d = 0; d < a.DK; ++d) {
+                const float s = gamma * S[(int64_t)d * a.DV] + load1<IO>(a.k.p, row_base(a.k, b, h) + d) * v;
+                S[(int64_t)d * a.DV] = s;
+                acc += s * load1<IO>(a.q.p, row_base(a.q, b, h) + d);
+            }
+        }
+        store1<IO>(a.y, b * a.ys.b + (int64_t)h * a.ys.h + n, acc * a.scale);
+    }
+}
+
+__global__ void __launch_bounds__(64) tan_sum_kernel(const float* part, float* dlog, int64_t n) {
+    float s = 0.f;
+    for (int64_t i = threadIdx.x; i < n; i += 64) s += part[blockIdx.x * n + i];
+    for (int w = 32; w; w >>= 1) s += __shfl_xor(s, w);
+    if (threadIdx.x == 0) dlog[blockIdx.x] = s;
+}
+
+template <int IO>
+__global__ void __launch_bounds__(256) head_sum_kernel(const float* in, void* out, lconv_strides_t os, int G, int share,
+                                                       int64_t N, int D, int64_t total) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+        const int64_t row = i / (D / 8);
+        const int d = (int)(i - row * (D / 8)) * 8;
+        const int64_t bg = row / N, t = row - bg * N;
+        const int64_t b = bg / G, g = bg - b * G;
+        float x[8] = {0.f};
+        for (int s = 0; s < share; ++s) {
+            const float* p = in + ((bg * share + s) * N + t) * D + d;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] += p[j];
+        }
+        store8<IO>(out, b * os.b + g * os.h + t * os.n + d, x);
+    }
+}
+
+__global__ void __launch_bounds__(256) copy_state_kernel(const float* in, float* out, int64_t n) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256)
+        out[i] = in ? in[i] : 0.f;
+}
+
+unsigned grid_1d(int64_t threads) {
+    const int64_t g = (threads + 255) / 256;
+    return (unsigned)(g < 8192 ? (g > 0 ? g : 1) : 8192);
+}
+
+template <typename F> hipError_t by_dtype(int dtype, F&& f) {
+    if (dtype == LCONV_F32) f(std::integral_constant<int, CT_F32>{});
+    else if (dtype == LCONV_F16) f(std::integral_constant<int, CT_F16>{});
+    else f(std::integral_constant<int, CT_BF16>{});
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_linattn(int dtype, const LinArgs& a, hipStream_t stream) {
+    LinTanArgs t{};
+    t.a = a;
+    const unsigned grid = (unsigned)(a.B * a.H * ((a.r.DV + 63) / 64));
+    return by_dtype(dtype, [&](auto io) { linattn_seq_kernel<io.value, false><<<grid, 256, 0, stream>>>(t); });
+}
+
+int linattn_tan_blocks(int DV) { return (DV + 63) / 64; }
+
+hipError_t launch_linattn_tan(int dtype, const LinTanArgs& t, float* dlog, hipStream_t stream) {
+    const int nb = linattn_tan_blocks(t.a.r.DV);
+    const unsigned grid = (unsigned)(t.a.B * t.a.H * nb);
+    const hipError_t e = by_dtype(dtype, [&](auto io) { linattn_seq_kernel<io.value, true><<<grid, 256, 0, stream>>>(t); });
+    if (e != hipSuccess) return e;
+    tan_sum_kernel<<<(unsigned)t.a.H, 64, 0, stream>>>(t.part, dlog, t.a.B * nb);
+    return hipGetLastError();
+}
+
+hipError_t launch_linattn_step(int dtype, const LinStepArgs& a, hipStream_t stream) {
+    const unsigned grid = (unsigned)(a.B * a.H);
+    return by_dtype(dtype, [&](auto io) { linattn_step_kernel<io.value><<<grid, 256, 0, stream>>>(a); });
+}
+
+hipError_t launch_head_sum(int dtype, const float* in, void* out, lconv_strides_t os, int64_t B, int G, int share,
+                           int64_t N, int D, hipStream_t stream) {
+    const int64_t total = B * G * N * (D / 8);
+    return by_dtype(dtype, [&](auto io) {
+        head_sum_kernel<io.value><<<grid_1d(total), 256, 0, stream>>>(in, out, os, G, share, N, D, total);
+    });
+}
+
+hipError_t launch_copy_state(const float* in, float* out, int64_t n, hipStream_t stream) {
+    copy_state_kernel<<<grid_1d(n), 256, 0, stream>>>(in, out, n);
+    return hipGetLastError();
+}
+
+}  // namespace lcv

@@ -1,0 +1,37 @@
+// mixer_io.h -- element access of the mixer kernels: groups of 8 elements of any dtype as fp32.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "fused_io.h"
+
+namespace lcv {
+namespace {
+
+template <int IO> struct Elem { using T = uint16_t; };
+template <> struct Elem<CT_F32> { using T = float; };
+
+template <int IO> __device__ __forceinline__ void store1(void* base, int64_t i, float v) {
+    if constexpr (IO == CT_F32) ((float*)base)[i] = v;
+    else ((uint16_t*)base)[i] = (uint16_t)(pack2<IO>(v, 0.f) & 0xffffu);
+}
+
+// The base of an operand's row (b, h): element offset of its token 0.
+__device__ __forceinline__ int64_t row_base(const LinOperand& o, int64_t b, int h) {
+    return b * o.s.b + (int64_t)(h / o.share) * o.s.h;
+}
+
+__device__ __forceinline__ int64_t row_len(const int32_t* lengths, int64_t b, int64_t N) {
+    if (!lengths) return N;
+    const int64_t n = lengths[b];
+    return n < 0 ? 0 : n < N ? n : N;
+}
+
+// log(gamma), kept finite so that gamma^0 is 1 also where gamma is 0 (a NaN stays one).
+__device__ __forceinline__ float log_gamma(const float* log_decay, int h) {
+    const float l = log_decay[h];
+    return l < -1e30f ? -1e30f : l;
+}
+
+}  // namespace
+}  // namespace lcv

@@ -7,13 +7,19 @@ There is no CPU fallback: if the library is missing, importing the entry points 
 Raw entry points keep the C names (``lconv_filter_fft``, ``lconv_fftconv_fwd``, ...), taking
 integer device pointers.  ``filter_fft``, ``fftconv``, ``fftconv_partial``, ``fftconv_sparse``,
 ``fftconv_bwd``, ``fftconv_save``, ``filter_fft2d`` and ``fftconv2d`` are convenience wrappers over torch
-tensors.
+tensors, and so are the mixer operators ``linear_attention``, ``linear_attention_bwd``,
+``linear_attention_step``, ``rotary`` (with ``rotary_frequencies``), ``layer_norm`` and
+``layer_norm_bwd``, which also take strided views whose last dimension is contiguous.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
+import math
 import os
 import re
+from collections import namedtuple
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "liblconv.so")
@@ -25,6 +31,14 @@ STATUS = {0: "LCONV_SUCCESS", 1: "LCONV_ERR_NULL_POINTER", 2: "LCONV_ERR_INVALID
           6: "LCONV_ERR_WORKSPACE", 7: "LCONV_ERR_HIP", 8: "LCONV_ERR_NOT_PREPARED",
           9: "LCONV_ERR_SCRATCH_LIMIT"}
 NOALLOC_SCRATCH_BYTES = 64 << 20   # LCONV_NOALLOC_SCRATCH_BYTES
+
+
+ROTARY_HALF, ROTARY_INTERLEAVED, ROTARY_INVERSE = 0, 1, 2
+
+
+class Strides(ctypes.Structure):
+    """lconv_strides_t: element strides of an operand [B][H][N][D]."""
+    _fields_ = [("b", ctypes.c_int64), ("h", ctypes.c_int64), ("n", ctypes.c_int64)]
 
 
 class LconvError(RuntimeError):
@@ -46,6 +60,7 @@ def load(path: str = LIB_PATH):
                            "(python -m fft_long_convolution_amd.build)")
     lib = ctypes.CDLL(path)
     vp, i64, sz, i = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
+    f32, sp = ctypes.c_float, ctypes.POINTER(Strides)
     sig = {
         "lconv_filter_fft_bytes": (sz, [i64, i64, i]),
         "lconv_filter_fft_workspace_bytes": (sz, [i64, i64, i]),
@@ -83,6 +98,16 @@ def load(path: str = LIB_PATH):
         "lconv_fftconv2d_fwd": (i, [vp, vp, vp, vp, i64, i64, i64, i64, i, vp, sz, vp]),
         "lconv_prepare": (i, [i64, i]),
         "lconv_fftconv_fwd_noalloc": (i, [vp, vp, vp, vp, vp, vp, i64, i64, i64, i, vp]),
+        "lconv_linattn_workspace_bytes": (sz, [i64] * 6 + [i]),
+        "lconv_linattn_fwd": (i, [vp, sp, vp, sp, vp, sp, vp, f32, vp, vp, vp, sp, vp] + [i64] * 6 + [i, vp, sz, vp]),
+        "lconv_linattn_bwd_workspace_bytes": (sz, [i64] * 6 + [i]),
+        "lconv_linattn_bwd": (i, [vp, sp, vp, sp, vp, sp, vp, sp, vp, f32, vp, vp, vp, vp, sp, vp, sp, vp, sp, vp, vp]
+                              + [i64] * 6 + [i, vp, sz, vp]),
+        "lconv_linattn_step": (i, [vp, sp, vp, sp, vp, sp, vp, f32, vp, vp, vp, sp] + [i64] * 6 + [i, vp]),
+        "lconv_rotary": (i, [vp, sp, vp, sp, vp, i64, vp, f32, vp, sp, vp, sp] + [i64] * 6 + [i, i, vp]),
+        "lconv_layernorm_fwd": (i, [vp, i64, vp, vp, vp, i64, vp, vp, i64, i64, f32, i, vp]),
+        "lconv_layernorm_bwd_workspace_bytes": (sz, [i64, i64]),
+        "lconv_layernorm_bwd": (i, [vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, vp, i64, i64, i, vp, sz, vp]),
         "lconv_status_string": (ctypes.c_char_p, [i]),
         "lconv_abi_version": (i, []),
         "lconv_release": (i, []),
@@ -256,6 +281,53 @@ def lconv_filter_fft3d(k, k_f, C, S, dtype, workspace, workspace_bytes, stream):
 
 def lconv_fftconv3d_fwd(u, k_f, D, y, B, C, S, dtype, workspace, workspace_bytes, stream):
     return load().lconv_fftconv3d_fwd(u, k_f, D, y, B, C, S, dtype, workspace, workspace_bytes, stream)
+
+
+def lconv_linattn_workspace_bytes(B, H, G, N, Dk, Dv, dtype):
+    return load().lconv_linattn_workspace_bytes(B, H, G, N, Dk, Dv, dtype)
+
+
+def lconv_linattn_fwd(q, qs, k, ks, v, vs, log_decay, scale, state_in, lengths, y, ys, state_out, B, H, G, N, Dk, Dv,
+                      dtype, workspace, workspace_bytes, stream):
+    return load().lconv_linattn_fwd(q, qs, k, ks, v, vs, log_decay, scale, state_in, lengths, y, ys, state_out, B, H,
+                                    G, N, Dk, Dv, dtype, workspace, workspace_bytes, stream)
+
+
+def lconv_linattn_bwd_workspace_bytes(B, H, G, N, Dk, Dv, dtype):
+    return load().lconv_linattn_bwd_workspace_bytes(B, H, G, N, Dk, Dv, dtype)
+
+
+def lconv_linattn_bwd(dy, dys, q, qs, k, ks, v, vs, log_decay, scale, state_in, dstate_out, lengths, dq, dqs, dk, dks,
+                      dv, dvs, dstate_in, dlog_decay, B, H, G, N, Dk, Dv, dtype, workspace, workspace_bytes, stream):
+    return load().lconv_linattn_bwd(dy, dys, q, qs, k, ks, v, vs, log_decay, scale, state_in, dstate_out, lengths, dq,
+                                    dqs, dk, dks, dv, dvs, dstate_in, dlog_decay, B, H, G, N, Dk, Dv, dtype, workspace,
+                                    workspace_bytes, stream)
+
+
+def lconv_linattn_step(q, qs, k, ks, v, vs, log_decay, scale, state, slots, y, ys, B, H, G, Dk, Dv, nslots, dtype,
+                       stream):
+    return load().lconv_linattn_step(q, qs, k, ks, v, vs, log_decay, scale, state, slots, y, ys, B, H, G, Dk, Dv,
+                                     nslots, dtype, stream)
+
+
+def lconv_rotary(q, qs, k, ks, positions, pos_stride, inv_freq, magnitude, yq, yqs, yk, yks, B, H, G, N, D, rot, flags,
+                 dtype, stream):
+    return load().lconv_rotary(q, qs, k, ks, positions, pos_stride, inv_freq, magnitude, yq, yqs, yk, yks, B, H, G, N,
+                               D, rot, flags, dtype, stream)
+
+
+def lconv_layernorm_fwd(x, x_stride, weight, bias, y, y_stride, mean, rstd, rows, C, eps, dtype, stream):
+    return load().lconv_layernorm_fwd(x, x_stride, weight, bias, y, y_stride, mean, rstd, rows, C, eps, dtype, stream)
+
+
+def lconv_layernorm_bwd_workspace_bytes(rows, C):
+    return load().lconv_layernorm_bwd_workspace_bytes(rows, C)
+
+
+def lconv_layernorm_bwd(dy, dy_stride, x, x_stride, weight, mean, rstd, dx, dx_stride, dweight, dbias, rows, C, dtype,
+                        workspace, workspace_bytes, stream):
+    return load().lconv_layernorm_bwd(dy, dy_stride, x, x_stride, weight, mean, rstd, dx, dx_stride, dweight, dbias,
+                                      rows, C, dtype, workspace, workspace_bytes, stream)
 
 
 def lconv_abi_version():
@@ -675,3 +747,326 @@ def fftconv2d_bwd(dy, u, k_f, D, need_dk=True, stream=None):
     _check(lconv_fftconv2d_bwd(_ptr(dy), _ptr(u), _ptr(k_f), _ptr(D), _ptr(du), _ptr(dk), _ptr(dD), B, C, Hs, Ws,
                                dt, _ptr(ws), wsb, _stream(stream)), "lconv_fftconv2d_bwd")
     return du, dk, dD
+
+
+# ---- linear attention, rotary positions, layer norm ---------------------------------------------
+
+def _at(dev, stream):
+    """(context, raw stream) of a mixer call on `dev`: outputs and workspaces made inside the context
+    belong to the stream that the call runs on, so they are not handed out again before it is done."""
+    torch = _torch()
+    if stream is not None:
+        return torch.cuda.stream(stream), stream.cuda_stream     # also makes its device the current one
+    if dev.index == torch.cuda.current_device():
+        return contextlib.nullcontext(), torch.cuda.current_stream(dev).cuda_stream
+    return torch.cuda.device(dev), torch.cuda.current_stream(dev).cuda_stream
+
+
+@functools.lru_cache(maxsize=256)
+def _strides_of(b, h, n):
+    return Strides(b, h, n)
+
+
+def _view(name, t, shape, dtype):
+    """An operand of any strides whose last dimension is contiguous: its lconv_strides_t (None: dense)."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor, got {type(t).__name__}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.is_contiguous():
+        return None
+    if t.stride(-1) != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    s = t.stride()
+    return _strides_of(s[0], s[1], s[2] if len(s) == 4 else 0)
+
+
+def _in_order_of(x, shape):
+    """An empty [B, H, N, D] tensor with x's order of heads and tokens."""
+    torch = _torch()
+    if x.dim() == 4 and x.shape[1] > 1 and x.shape[2] > 1 and x.stride(1) < x.stride(2):
+        return torch.empty((shape[0], shape[2], shape[1], shape[3]), dtype=x.dtype, device=x.device).transpose(1, 2)
+    return torch.empty(shape, dtype=x.dtype, device=x.device)
+
+
+def _linattn_shape(q, k, v, dims):
+    """(dtype, B, H, G, N, Dk, Dv) of a call's operands, checked where they fix the shape (dims 4: with
+    tokens, 3: single tokens)."""
+    torch = _torch()
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if not isinstance(t, torch.Tensor) or t.dim() != dims:
+            raise ValueError(f"{name} must be a {dims}-D torch tensor")
+    if q.dtype not in (torch.float32, torch.float16, torch.bfloat16):
+        raise ValueError(f"q has dtype {q.dtype}; supported: float32, float16, bfloat16")
+    B, H, Dk = q.shape[0], q.shape[1], q.shape[-1]
+    N = q.shape[2] if dims == 4 else 1
+    G, Dv = k.shape[1], v.shape[-1]
+    if G == 0 and H > 0 or G and H % G:
+        raise ValueError(f"q has {H} heads, not a multiple of k's {G}")
+    return q.dtype, B, H, G, N, Dk, Dv
+
+
+def _lengths(lengths, B):
+    torch = _torch()
+    if lengths is not None:
+        _need("lengths", lengths, (B,), torch.int32)
+
+
+def _outputs(name, t, shape, like):
+    """An output given by the caller, or a new one in `like`'s order: (tensor, strides)."""
+    if t is None:
+        t = _in_order_of(like, shape)
+    return t, _view(name, t, shape, like.dtype)
+
+
+def linear_attention(q, k, v, log_decay, scale=None, state=None, lengths=None, need_state=True, out=None,
+                     state_out=None, stream=None):
+    """Linear attention with a decay for each head over q [B, H, N, Dk], k [B, G, N, Dk] and
+    v [B, G, N, Dv] (head h uses k/v head h // (H // G)), from a state [B, H, Dk, Dv] in float32:
+
+        S_t = exp(log_decay[h]) S_{t-1} + k_t v_t^T,    y_t = scale S_t^T q_t
+
+    scale: 1 / sqrt(Dk) unless given.  lengths: int32 [B], tokens past a row's length count for
+    nothing and give y = 0.  Returns (y [B, H, N, Dv] in q's dtype and order of dimensions, the state
+    after each row's last token; None without need_state).  state_out may be `state` itself."""
+    torch = _torch()
+    tdt, B, H, G, N, Dk, Dv = _linattn_shape(q, k, v, 4)
+    qs, ks, vs = _view("q", q, (B, H, N, Dk), tdt), _view("k", k, (B, G, N, Dk), tdt), _view("v", v, (B, G, N, Dv), tdt)
+    _need("log_decay", log_decay, (H,), torch.float32)
+    _need("state", state, (B, H, Dk, Dv), torch.float32, optional=True)
+    _need("state_out", state_out, (B, H, Dk, Dv), torch.float32, optional=True)
+    _lengths(lengths, B)
+    dev = _on_gpu(q=q, k=k, v=v, log_decay=log_decay, state=state, lengths=lengths, out=out, state_out=state_out)
+    dt = dtype_code(tdt)
+    scale = 1.0 / math.sqrt(max(Dk, 1)) if scale is None else float(scale)
+    ctx, st = _at(dev, stream)
+    with ctx:
+        y, ys = _outputs("out", out, (B, H, N, Dv), q)
+        if state_out is None and need_state:
+            state_out = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=dev)
+        wsb = lconv_linattn_workspace_bytes(B, H, G, N, Dk, Dv, dt)
+        ws = torch.empty(wsb, dtype=torch.uint8, device=dev) if wsb else None
+        _check(lconv_linattn_fwd(_ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(log_decay), scale, _ptr(state),
+                                 _ptr(lengths), _ptr(y), ys, _ptr(state_out), B, H, G, N, Dk, Dv, dt, _ptr(ws), wsb, st),
+               "lconv_linattn_fwd")
+    return y, state_out
+
+
+LinearAttentionGrads = namedtuple("LinearAttentionGrads", "dq dk dv dstate dlog_decay")
+
+
+def linear_attention_bwd(dy, q, k, v, log_decay, scale=None, state=None, dstate=None, lengths=None,
+                         need_dlog_decay=False, stream=None):
+    """Gradients of linear_attention given dy [B, H, N, Dv] and, where the state it returned was used,
+    dstate [B, H, Dk, Dv] in float32.  Returns (dq, dk, dv, dstate, dlog_decay): dq, dk, dv shaped and
+    typed like q, k, v (dk and dv summed over the heads that share them), dstate the gradient of the
+    state that entered (None without one), dlog_decay [H] in float32 (None unless asked for)."""
+    torch = _torch()
+    tdt, B, H, G, N, Dk, Dv = _linattn_shape(q, k, v, 4)
+    qs, ks, vs = _view("q", q, (B, H, N, Dk), tdt), _view("k", k, (B, G, N, Dk), tdt), _view("v", v, (B, G, N, Dv), tdt)
+    dys = _view("dy", dy, (B, H, N, Dv), tdt)
+    _need("log_decay", log_decay, (H,), torch.float32)
+    _need("state", state, (B, H, Dk, Dv), torch.float32, optional=True)
+    _need("dstate", dstate, (B, H, Dk, Dv), torch.float32, optional=True)
+    _lengths(lengths, B)
+    dev = _on_gpu(dy=dy, q=q, k=k, v=v, log_decay=log_decay, state=state, dstate=dstate, lengths=lengths)
+    dt = dtype_code(tdt)
+    scale = 1.0 / math.sqrt(max(Dk, 1)) if scale is None else float(scale)
+    ctx, st = _at(dev, stream)
+    with ctx:
+        dq, dqs = _outputs("dq", None, (B, H, N, Dk), q)
+        dk, dks = _outputs("dk", None, (B, G, N, Dk), k)
+        dv, dvs = _outputs("dv", None, (B, G, N, Dv), v)
+        ds = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=dev) if state is not None else None
+        dl = torch.empty((H,), dtype=torch.float32, device=dev) if need_dlog_decay else None
+        wsb = lconv_linattn_bwd_workspace_bytes(B, H, G, N, Dk, Dv, dt)
+        ws = torch.empty(wsb, dtype=torch.uint8, device=dev) if wsb else None
+        _check(lconv_linattn_bwd(_ptr(dy), dys, _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(log_decay), scale,
+                                 _ptr(state), _ptr(dstate), _ptr(lengths), _ptr(dq), dqs, _ptr(dk), dks, _ptr(dv), dvs,
+                                 _ptr(ds), _ptr(dl), B, H, G, N, Dk, Dv, dt, _ptr(ws), wsb, st), "lconv_linattn_bwd")
+    return LinearAttentionGrads(dq, dk, dv, ds, dl)
+
+
+def linear_attention_step(q, k, v, log_decay, state, scale=None, slots=None, out=None, stream=None):
+    """One token of every sequence: q [B, H, Dk], k [B, G, Dk], v [B, G, Dv]; the states
+    [slots, H, Dk, Dv] in float32 are moved on in place.  slots: int32 [B], the state that each row
+    continues (outside the states: an idle row, y = 0); without it row b has state b.  No two rows may
+    have the same slot.  Returns y [B, H, Dv]."""
+    torch = _torch()
+    tdt, B, H, G, _, Dk, Dv = _linattn_shape(q, k, v, 3)
+    qs, ks, vs = _view("q", q, (B, H, Dk), tdt), _view("k", k, (B, G, Dk), tdt), _view("v", v, (B, G, Dv), tdt)
+    _need("log_decay", log_decay, (H,), torch.float32)
+    if not isinstance(state, torch.Tensor) or state.dim() != 4:
+        raise ValueError("state must be a 4-D torch tensor")
+    nslots = state.shape[0]
+    _need("state", state, (nslots, H, Dk, Dv), torch.float32)
+    if slots is not None:
+        _need("slots", slots, (B,), torch.int32)
+    elif nslots < B:
+        raise ValueError(f"{B} rows and {nslots} states: slots are needed")
+    dev = _on_gpu(q=q, k=k, v=v, log_decay=log_decay, state=state, slots=slots, out=out)
+    scale = 1.0 / math.sqrt(max(Dk, 1)) if scale is None else float(scale)
+    ctx, st = _at(dev, stream)
+    with ctx:
+        y, ys = _outputs("out", out, (B, H, Dv), q)
+        _check(lconv_linattn_step(_ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(log_decay), scale, _ptr(state),
+                                  _ptr(slots), _ptr(y), ys, B, H, G, Dk, Dv, nslots, dtype_code(tdt), st),
+               "lconv_linattn_step")
+    return y
+
+
+def rotary_frequencies(rot, base=10000.0, scaling=None, factor=1.0, original=4096, fast=32.0, slow=1.0, device="cuda"):
+    """(inv_freq [rot / 2] in float32, magnitude) for ``rotary``.  Unscaled: base^(-2p / rot), 1.
+    scaling, for contexts `factor` times the original's length:
+      "linear"    every frequency divided by factor (positions interpolated);
+      "base"      the base raised to base * factor^(rot / (rot - 2)): the fastest pair keeps its
+                  frequency, the slowest is divided by factor;
+      "by_parts"  pairs that turn more than `fast` times within `original` positions keep their
+                  frequency, those that turn less than `slow` times are divided by factor, a ramp in
+                  the pair's index between; magnitude 1 + 0.1 ln(factor)."""
+    torch = _torch()
+    if rot < 2 or rot % 2:
+        raise ValueError(f"rot must be even and at least 2, got {rot}")
+    if scaling not in (None, "linear", "base", "by_parts"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    if factor < 1.0:
+        raise ValueError(f"factor must be at least 1, got {factor}")
+    magnitude = 1.0
+    if scaling == "base" and rot > 2:
+        base = base * factor ** (rot / (rot - 2))
+    p = torch.arange(rot // 2, dtype=torch.float64)
+    f = base ** (-2.0 * p / rot)
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "by_parts":
+        # the pair whose wavelength fits `turns` times into the original context
+        pair = lambda turns: rot * math.log(original / (turns * 2.0 * math.pi)) / (2.0 * math.log(base))  # noqa: E731
+        lo, hi = max(math.floor(pair(fast)), 0), min(math.ceil(pair(slow)), rot - 1)
+        ramp = ((p - lo) / max(hi - lo, 1e-3)).clamp(0.0, 1.0)
+        f = f * (1.0 - ramp) + f / factor * ramp
+        magnitude = 1.0 + 0.1 * math.log(factor)
+    return f.to(torch.float32).to(device), magnitude
+
+
+def rotary(q, k, positions, inv_freq, interleaved=False, inverse=False, magnitude=1.0, out=None, stream=None):
+    """Rotary positions of q [B, H, N, D] and k [B, G, N, D] (or None) in one launch: the first
+    2 * len(inv_freq) dimensions of every head are turned in pairs by position * inv_freq, the others
+    copied.  Pairs are (p, p + rot / 2), or (2p, 2p + 1) with interleaved.  inverse turns back (with the
+    same magnitude: the gradient).  positions: int32 [B, N] or [N], or None for 0 .. N-1.  out: a pair of
+    outputs (q and k themselves for in place).  Returns (q', k')."""
+    torch = _torch()
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError("q must be a 4-D torch tensor")
+    if q.dtype not in (torch.float32, torch.float16, torch.bfloat16):
+        raise ValueError(f"q has dtype {q.dtype}; supported: float32, float16, bfloat16")
+    B, H, N, D = q.shape
+    qs = _view("q", q, (B, H, N, D), q.dtype)
+    G, ks = 0, None
+    if k is not None:
+        if not isinstance(k, torch.Tensor) or k.dim() != 4:
+            raise ValueError("k must be a 4-D torch tensor")
+        G = k.shape[1]
+        ks = _view("k", k, (B, G, N, D), q.dtype)
+    if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be a 1-D torch tensor")
+    rot = 2 * inv_freq.shape[0]
+    _need("inv_freq", inv_freq, (rot // 2,), torch.float32)
+    pos_stride = 0
+    if positions is not None:
+        if not isinstance(positions, torch.Tensor) or positions.dtype != torch.int32:
+            raise ValueError("positions must be an int32 torch tensor")
+        if tuple(positions.shape) not in ((B, N), (N,)):
+            raise ValueError(f"positions has shape {tuple(positions.shape)}, expected {(B, N)} or {(N,)}")
+        if N > 1 and positions.stride(-1) != 1:
+            raise ValueError("positions must be contiguous in its last dimension")
+        pos_stride = positions.stride(0) if positions.dim() == 2 and B > 1 else 0
+    oq, ok = (None, None) if out is None else out
+    if k is None and ok is not None:
+        raise ValueError("an output for k without k")
+    dev = _on_gpu(q=q, k=k, positions=positions, inv_freq=inv_freq, out_q=oq, out_k=ok)
+    flags = (ROTARY_INTERLEAVED if interleaved else ROTARY_HALF) | (ROTARY_INVERSE if inverse else 0)
+    ctx, st = _at(dev, stream)
+    with ctx:
+        yq, yqs = _outputs("out of q", oq, (B, H, N, D), q)
+        yk, yks = (None, None) if k is None else _outputs("out of k", ok, (B, G, N, D), k)
+        _check(lconv_rotary(_ptr(q), qs, _ptr(k), ks, _ptr(positions), pos_stride, _ptr(inv_freq), float(magnitude),
+                            _ptr(yq), yqs, _ptr(yk), yks, B, H, G, N, D, rot, flags, dtype_code(q.dtype), st),
+               "lconv_rotary")
+    return yq, yk
+
+
+def _rows(name, t, shape, dtype):
+    """(rows, C, row stride) of a tensor normalised over its last dimension: dense, or 2-D with a row
+    stride."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor, got {type(t).__name__}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    C = shape[-1]
+    rows = 1
+    for n in shape[:-1]:
+        rows *= n
+    if t.is_contiguous():
+        return rows, C, C
+    if t.dim() != 2 or t.stride(1) != 1 or t.stride(0) < C:
+        raise ValueError(f"{name} must be contiguous, or 2-D with contiguous rows")
+    return rows, C, t.stride(0)
+
+
+def layer_norm(x, weight=None, bias=None, eps=1e-5, need_stats=True, out=None, stream=None):
+    """Layer norm over the last dimension of x [..., C]: (x - mean) rstd weight + bias; weight and bias
+    [C] in x's dtype, or None.  Returns (y, mean, rstd), the statistics in float32 and x's leading shape
+    (None without need_stats).  out may be x."""
+    torch = _torch()
+    if not isinstance(x, torch.Tensor) or x.dim() < 1:
+        raise ValueError("x must be a torch tensor of at least one dimension")
+    if x.dtype not in (torch.float32, torch.float16, torch.bfloat16):
+        raise ValueError(f"x has dtype {x.dtype}; supported: float32, float16, bfloat16")
+    rows, C, xs = _rows("x", x, x.shape, x.dtype)
+    _need("weight", weight, (C,), x.dtype, optional=True)
+    _need("bias", bias, (C,), x.dtype, optional=True)
+    dev = _on_gpu(x=x, weight=weight, bias=bias, out=out)
+    ctx, st = _at(dev, stream)
+    with ctx:
+        y = torch.empty(x.shape, dtype=x.dtype, device=dev) if out is None else out
+        ys = _rows("out", y, x.shape, x.dtype)[2]
+        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev) if need_stats else None
+        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev) if need_stats else None
+        _check(lconv_layernorm_fwd(_ptr(x), xs, _ptr(weight), _ptr(bias), _ptr(y), ys, _ptr(mean), _ptr(rstd), rows, C,
+                                   float(eps), dtype_code(x.dtype), st), "lconv_layernorm_fwd")
+    return y, mean, rstd
+
+
+def layer_norm_bwd(dy, x, weight, mean, rstd, need_dweight=True, need_dbias=True, out=None, stream=None):
+    """Gradients of layer_norm given dy like x, with the statistics that it returned.  Returns
+    (dx in x's dtype, dweight [C], dbias [C] in float32); dweight is None without weight or
+    need_dweight, dbias without need_dbias.  out (dx) may be dy or x."""
+    torch = _torch()
+    if not isinstance(x, torch.Tensor) or x.dim() < 1:
+        raise ValueError("x must be a torch tensor of at least one dimension")
+    if x.dtype not in (torch.float32, torch.float16, torch.bfloat16):
+        raise ValueError(f"x has dtype {x.dtype}; supported: float32, float16, bfloat16")
+    rows, C, xs = _rows("x", x, x.shape, x.dtype)
+    dys = _rows("dy", dy, x.shape, x.dtype)[2]
+    _need("weight", weight, (C,), x.dtype, optional=True)
+    _need("mean", mean, x.shape[:-1], torch.float32)
+    _need("rstd", rstd, x.shape[:-1], torch.float32)
+    dev = _on_gpu(dy=dy, x=x, weight=weight, mean=mean, rstd=rstd, out=out)
+    ctx, st = _at(dev, stream)
+    with ctx:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=dev) if out is None else out
+        dxs = _rows("out", dx, x.shape, x.dtype)[2]
+        dw = torch.empty((C,), dtype=torch.float32, device=dev) if need_dweight and weight is not None else None
+        db = torch.empty((C,), dtype=torch.float32, device=dev) if need_dbias else None
+        wsb = lconv_layernorm_bwd_workspace_bytes(rows, C) if dw is not None or db is not None else 0
+        ws = torch.empty(wsb, dtype=torch.uint8, device=dev) if wsb else None
+        _check(lconv_layernorm_bwd(_ptr(dy), dys, _ptr(x), xs, _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dx), dxs,
+                                   _ptr(dw), _ptr(db), rows, C, dtype_code(x.dtype), _ptr(ws), wsb, st),
+               "lconv_layernorm_bwd")
+    return dx, dw, db

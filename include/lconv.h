@@ -51,7 +51,9 @@ extern "C" {
  * lconv_fftconv_fwd_save / lconv_fftconv_bwd_saved; the state-space workspace holds the scan's
  * part states.  4: lconv_prepare and lconv_fftconv_fwd_noalloc, two status codes.  5: 2D calls
  * take Hs x Ws images and a workspace; lconv_fftconv2d_workspace_bytes.  6: gradients and the
- * training pair for every supported N, with workspace arguments). */
+ * training pair for every supported N, with workspace arguments.  The mixer operators further
+ * down -- linear attention, rotary positions, layer norm -- came beside version 8: they change
+ * nothing that was there, and a caller finds them by their names). */
 #define LCONV_ABI_VERSION 8
 
 /* The last enumerator only widens the type's range to every int, so that any value a C caller
@@ -461,6 +463,138 @@ lconv_status_t lconv_prepare(int64_t N, lconv_dtype_t dtype);
 lconv_status_t lconv_fftconv_fwd_noalloc(const void* u, const void* k_f, const void* D, void* y,
                                          const void* q, const void* v, int64_t B, int64_t H, int64_t N,
                                          lconv_dtype_t dtype, hipStream_t stream);
+
+/* ---- operators around the long convolution: linear attention, rotary positions, layer norm --- */
+
+/*
+ * Strides, in elements, of an operand [B][H][N][D] whose last dimension is contiguous; NULL in
+ * place of a pointer to one means dense.  Token-major activations [B][N][H][D] and slices of a
+ * packed projection are passed as they are.  Strides over dimensions longer than one are
+ * non-negative multiples of 16 bytes (0 repeats an input); an output's rows must not overlap.
+ * Where two operands' address ranges meet, they count as overlapping unless both are slices of
+ * one token-major buffer (equal n strides, b strides equal and a multiple of them) at disjoint
+ * places.
+ */
+typedef struct {
+    int64_t b, h, n;
+} lconv_strides_t;
+
+/* Largest head dimension of linear attention. */
+#define LCONV_LINATTN_MAX_D 256
+
+/*
+ * Linear attention with a decay for each head.  With gamma = exp(log_decay[h]) and g = h / (H / G)
+ * (k and v heads shared by H / G query heads), for t < len[b]:
+ *   S_t = gamma S_{t-1} + k[b,g,t] v[b,g,t]^T,   S_{-1} = state_in[b,h]
+ *   y[b,h,t] = scale * S_t^T q[b,h,t];           y = 0 for t >= len[b];   state_out = S_{len-1}
+ * (state_out = state_in for a row of length 0).  Nothing past len[b] is read into a result.
+ *   q, y       [B][H][N][Dk], [B][H][N][Dv] dtype;   k, v  [B][G][N][Dk], [B][G][N][Dv] dtype
+ *   log_decay  [H] fp32, device; at most 0 (minus infinity: no memory beyond the token itself)
+ *   state_in   [B][H][Dk][Dv] fp32 or NULL (zeros);  state_out the same shape or NULL (not wanted);
+ *              the two may be one buffer
+ *   lengths    [B] int32, device, or NULL (every row N long); taken as min(max(len, 0), N)
+ *   workspace  lconv_linattn_workspace_bytes(...) bytes (may be NULL if that is 0)
+ * States and all sums are fp32; with 16-bit data the scores and the state are rounded once to the
+ * dtype as matrix-core operands, while what the state adds up is kept to fp32's accuracy.
+ * Supported: Dk, Dv multiples of 8 in [8, 256]; H a multiple of G; N < 2^31; every dtype.
+ * B, H or N = 0 is a no-op apart from state_out, which is set as for rows of length 0 (N = 0).
+ */
+size_t lconv_linattn_workspace_bytes(int64_t B, int64_t H, int64_t G, int64_t N, int64_t Dk, int64_t Dv,
+                                     lconv_dtype_t dtype);
+lconv_status_t lconv_linattn_fwd(const void* q, const lconv_strides_t* q_strides, const void* k,
+                                 const lconv_strides_t* k_strides, const void* v, const lconv_strides_t* v_strides,
+                                 const float* log_decay, float scale, const float* state_in, const int32_t* lengths,
+                                 void* y, const lconv_strides_t* y_strides, float* state_out, int64_t B, int64_t H,
+                                 int64_t G, int64_t N, int64_t Dk, int64_t Dv, lconv_dtype_t dtype, void* workspace,
+                                 size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Gradients of lconv_linattn_fwd, given dy = dL/dy and dstate_out = dL/dstate_out (NULL: zeros).
+ * With G_t = dL/dS_t = scale q_t dy_t^T + gamma G_{t+1} (for the last token dstate_out in place of
+ * gamma G_{t+1}):
+ *   dq_t = scale S_t dy_t,  dk_t = G_t v_t,  dv_t = G_t^T k_t,  dstate_in = gamma G_0,
+ *   dlog_decay[h] = sum_{b,t} <G_t, gamma S_{t-1}>;  dk and dv summed over the heads that share them.
+ *   dq [B][H][N][Dk], dk [B][G][N][Dk], dv [B][G][N][Dv] dtype, written (zeros past a row's length)
+ *   dstate_in  [B][H][Dk][Dv] fp32, written, or NULL;  dlog_decay [H] fp32, written, or NULL
+ *   workspace  lconv_linattn_bwd_workspace_bytes(...) bytes (may be NULL if that is 0)
+ * Limits and the other arguments as for lconv_linattn_fwd.  No atomics: results repeat bit for bit.
+ */
+size_t lconv_linattn_bwd_workspace_bytes(int64_t B, int64_t H, int64_t G, int64_t N, int64_t Dk, int64_t Dv,
+                                         lconv_dtype_t dtype);
+lconv_status_t lconv_linattn_bwd(const void* dy, const lconv_strides_t* dy_strides, const void* q,
+                                 const lconv_strides_t* q_strides, const void* k, const lconv_strides_t* k_strides,
+                                 const void* v, const lconv_strides_t* v_strides, const float* log_decay, float scale,
+                                 const float* state_in, const float* dstate_out, const int32_t* lengths, void* dq,
+                                 const lconv_strides_t* dq_strides, void* dk, const lconv_strides_t* dk_strides,
+                                 void* dv, const lconv_strides_t* dv_strides, float* dstate_in, float* dlog_decay,
+                                 int64_t B, int64_t H, int64_t G, int64_t N, int64_t Dk, int64_t Dv,
+                                 lconv_dtype_t dtype, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * One token of every sequence of a serving batch: S = gamma S + k v^T in place, y = scale S^T q.
+ *   q, y   [B][H][Dk], [B][H][Dv] dtype;  k, v  [B][G][Dk], [B][G][Dv] dtype (the strides' n is not used)
+ *   state  [nslots][H][Dk][Dv] fp32, read and written
+ *   slots  [B] int32, device: the state that row b continues; NULL: row b takes state b (nslots >= B).
+ *          A slot outside [0, nslots) marks an idle row: y = 0, no state touched.  No two rows may
+ *          name the same slot.
+ * Same limits; no workspace.
+ */
+lconv_status_t lconv_linattn_step(const void* q, const lconv_strides_t* q_strides, const void* k,
+                                  const lconv_strides_t* k_strides, const void* v, const lconv_strides_t* v_strides,
+                                  const float* log_decay, float scale, float* state, const int32_t* slots, void* y,
+                                  const lconv_strides_t* y_strides, int64_t B, int64_t H, int64_t G, int64_t Dk,
+                                  int64_t Dv, int64_t nslots, lconv_dtype_t dtype, hipStream_t stream);
+
+/*
+ * Rotary positions for q and, in the same launch, k: each pair (x1, x2) of the first `rot` dimensions
+ * of a head is turned by the angle a = position * inv_freq[p], p < rot / 2:
+ *   (x1, x2) -> magnitude * (x1 cos a - x2 sin a, x2 cos a + x1 sin a);   the other dimensions are copied.
+ * LCONV_ROTARY_HALF pairs x[p] with x[p + rot/2], LCONV_ROTARY_INTERLEAVED x[2p] with x[2p+1].
+ * LCONV_ROTARY_INVERSE turns by -a: with the same magnitude that is the gradient.  Scaling for long
+ * contexts is in inv_freq and magnitude.  The angle is formed and reduced in fp64, so positions of any
+ * int32 value keep fp32-accurate sines.
+ *   q, yq      [B][H][N][D] dtype;  k, yk  [B][G][N][D] dtype, or both NULL
+ *   positions  int32, device, row b at positions + b * pos_stride (0: one row for all); NULL: 0 .. N-1
+ *   inv_freq   [rot/2] fp32, device
+ * yq may be q itself (same pointer and strides), likewise yk and k; otherwise no overlap.
+ * Supported: D a multiple of 8 in [8, 1024]; rot even in [2, D]; every dtype.
+ */
+#define LCONV_ROTARY_HALF        0
+#define LCONV_ROTARY_INTERLEAVED 1
+#define LCONV_ROTARY_INVERSE     2
+lconv_status_t lconv_rotary(const void* q, const lconv_strides_t* q_strides, const void* k,
+                            const lconv_strides_t* k_strides, const int32_t* positions, int64_t pos_stride,
+                            const float* inv_freq, float magnitude, void* yq, const lconv_strides_t* yq_strides,
+                            void* yk, const lconv_strides_t* yk_strides, int64_t B, int64_t H, int64_t G, int64_t N,
+                            int64_t D, int64_t rot, int flags, lconv_dtype_t dtype, hipStream_t stream);
+
+/*
+ * Layer norm over the last dimension of x [rows][C]:
+ *   y = (x - mean) rstd weight + bias,  rstd = 1 / sqrt(mean((x - mean)^2) + eps)
+ *   x, y          [rows][C] dtype, rows x_stride and y_stride elements apart (>= C)
+ *   weight, bias  [C] dtype or NULL (ones, zeros)
+ *   mean, rstd    [rows] fp32, written, or NULL; the gradient call takes them
+ * Statistics are fp32, the variance from the centred values.  Any C >= 1 and any row stride (rows of
+ * 16-byte groups are fastest); C <= 65536.  y may be x itself (same pointer and stride).
+ */
+lconv_status_t lconv_layernorm_fwd(const void* x, int64_t x_stride, const void* weight, const void* bias, void* y,
+                                   int64_t y_stride, float* mean, float* rstd, int64_t rows, int64_t C, float eps,
+                                   lconv_dtype_t dtype, hipStream_t stream);
+
+/*
+ * Gradients of lconv_layernorm_fwd.  With xhat = (x - mean) rstd and h = dy weight:
+ *   dx = rstd (h - mean_C(h) - xhat mean_C(h xhat));   dweight = sum_rows dy xhat;   dbias = sum_rows dy
+ *   dx [rows][C] dtype, rows dx_stride apart, written;  dweight, dbias [C] fp32, written, or NULL
+ *   workspace  lconv_layernorm_bwd_workspace_bytes(rows, C) bytes, device (partial sums of the weight's
+ *              gradients; added in a fixed order, so results repeat bit for bit); may be NULL when
+ *              neither dweight nor dbias is wanted
+ * rows = 0 writes zeros to dweight and dbias.  dx may be dy or x itself (same pointer and stride).
+ */
+size_t lconv_layernorm_bwd_workspace_bytes(int64_t rows, int64_t C);
+lconv_status_t lconv_layernorm_bwd(const void* dy, int64_t dy_stride, const void* x, int64_t x_stride,
+                                   const void* weight, const float* mean, const float* rstd, void* dx,
+                                   int64_t dx_stride, float* dweight, float* dbias, int64_t rows, int64_t C,
+                                   lconv_dtype_t dtype, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* ---- misc ------------------------------------------------------------------------------- */
 

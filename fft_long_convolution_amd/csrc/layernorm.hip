@@ -110,11 +110,6 @@ hipError_t launch_layernorm_fwd(int dtype, const NormArgs& a, hipStream_t stream
     return by_dtype(dtype, [&](auto io) { ln_fwd_kernel<io.value><<<(unsigned)a.rows, 256, 0, stream>>>(a); });
 }
 
-int64_t layernorm_parts(int64_t rows, int64_t C) {
-    (void)C;
-    return rows < 256 ? rows : 256;
-}
-
 hipError_t launch_layernorm_bwd(int dtype, const NormArgs& a, hipStream_t stream) {
     hipError_t e = hipSuccess;
     if (a.dweight || a.dbias) {

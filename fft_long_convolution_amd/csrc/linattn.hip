@@ -5,11 +5,11 @@
 namespace lcv {
 namespace {
 
-// Token by token: a workgroup holds 64 columns of one state, thread (part, col) rows part * 64 ..
-// part * 64 + 63 of its column in registers.  Per token the state's decay and update, the partial
-// products with Q, and their sum over the four parts through LDS.
-template <int IO, bool TAN>
-__global__ void __launch_bounds__(256) linattn_seq_kernel(LinTanArgs ta) {
+// The tangent of the state along log_decay, token by token: T_t = gamma (T_{t-1} + S_{t-1}).  A
+// workgroup holds 64 columns of S and T, thread (part, col) rows part * 64 .. part * 64 + 63 of its
+// column in registers; the partial sums of s_q (T^T dy_t) . q_t leave it as one number.
+template <int IO>
+__global__ void __launch_bounds__(256) linattn_tan_kernel(LinTanArgs ta) {
     const LinArgs& a = ta.a;
     const LinRole& r = a.r;
     __shared__ float red[4][64];
@@ -19,83 +19,72 @@ __global__ void __launch_bounds__(256) linattn_seq_kernel(LinTanArgs ta) {
     const int64_t b = bh / a.H;
     const int h = (int)(bh - b * a.H), n = (int)(blockIdx.x - bh * ncol) * 64 + col;
     const int64_t len = row_len(a.lengths, b, a.N);
-    const int64_t qb = row_base(r.Q, b, h), kb = row_base(r.K, b, h), vb = row_base(r.V, b, h);
-    const int64_t ob = b * r.o.b + (int64_t)h * r.o.h;
+    const int64_t qb = row_base(r.Q, b, h), kb = row_base(r.K, b, h), vb = row_base(r.V, b, h), tb = row_base(ta.q, b, h);
     const int64_t sb = bh * r.DK * r.DV + (int64_t)n * r.s_col;
     const float gamma = expf(log_gamma(a.log_decay, h));
     const bool on = n < r.DV;
-    float S[64], T[TAN ? 64 : 1];
-    float tan = 0.f;
+    float S[64], T[64], tan = 0.f;
 #pragma unroll
     for (int i = 0; i < 64; ++i) {
         const int d = part * 64 + i;
         S[i] = r.s_in && on && d < r.DK ? r.s_in[sb + (int64_t)d * r.s_row] : 0.f;
-        if constexpr (TAN) T[i] = 0.f;
+        T[i] = 0.f;
     }
-    for (int64_t i = 0; i < len; ++i) {
-        const int64_t t = r.reverse ? len - 1 - i : i;
-        const float v = on ? load1<IO>(r.V.p, vb + t * r.V.s.n + n) * r.s_kv : 0.f;
-        const float g = r.reverse && i == 0 ? 1.f : gamma;
-        float acc = 0.f, tacc = 0.f;
+    for (int64_t t = 0; t < len; ++t) {
+        const float v = on ? load1<IO>(r.V.p, vb + t * r.V.s.n + n) : 0.f;
+        float acc = 0.f;
 #pragma unroll
         for (int j = 0; j < 64; ++j) {
             const int d = part * 64 + j;
             if (d < r.DK) {
-                const float q = load1<IO>(r.Q.p, qb + t * r.Q.s.n + d);
-                if constexpr (TAN) {
-                    T[j] = gamma * (T[j] + S[j]);
-                    tacc += T[j] * q;
-                }
-                S[j] = g * S[j] + load1<IO>(r.K.p, kb + t * r.K.s.n + d) * v;
-                acc += S[j] * q;
+                T[j] = gamma * (T[j] + S[j]);
+                acc += T[j] * load1<IO>(r.Q.p, qb + t * r.Q.s.n + d);
+                S[j] = gamma * S[j] + load1<IO>(r.K.p, kb + t * r.K.s.n + d) * v;
             }
         }
-        if constexpr (TAN) {
-            if (on) tan += r.s_q * tacc * load1<IO>(ta.q.p, row_base(ta.q, b, h) + t * ta.q.s.n + n);
-        } else if (r.O) {
-            red[part][col] = acc;
-            __syncthreads();
-            if (part == 0 && on) {
-                const float y = r.s_q * (red[0][col] + red[1][col] + red[2][col] + red[3][col]);
-                if (r.o_f32) ((float*)r.O)[ob + t * r.o.n + n] = y;
-                else store1<IO>(r.O, ob + t * r.o.n + n, y);
-            }
-            __syncthreads();
-        }
+        if (on) tan += r.s_q * acc * load1<IO>(ta.q.p, tb + t * ta.q.s.n + n);
     }
-    if constexpr (TAN) {
-        // <T, dstate_out>: the transposed layout, element (d, n) at n * DK + d
-        if (ta.ds_out && on) {
-#pragma unroll
-            for (int j = 0; j < 64; ++j) {
-                const int d = part * 64 + j;
-                if (d < r.DK) tan += T[j] * ta.ds_out[bh * r.DK * r.DV + (int64_t)n * r.DK + d];
-            }
-        }
-        red[part][col] = tan;
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            float s = 0.f;
-            for (int p = 0; p < 4; ++p)
-                for (int c = 0; c < 64; ++c) s += red[p][c];
-            ta.part[((int64_t)h * a.B + b) * ncol + (blockIdx.x - bh * ncol)] = s;
-        }
-        return;
-    }
-    if (r.s_out && on) {
-        // a reversed state leaves with the decay of the token it would precede
-        const float g = r.reverse && len > 0 ? gamma : 1.f;
+    // <T, dstate_out>: the transposed layout, element (d, n) at n * DK + d
+    if (ta.ds_out && on) {
 #pragma unroll
         for (int j = 0; j < 64; ++j) {
             const int d = part * 64 + j;
-            if (d < r.DK) r.s_out[sb + (int64_t)d * r.s_row] = g * S[j];
+            if (d < r.DK) tan += T[j] * ta.ds_out[bh * r.DK * r.DV + (int64_t)n * r.DK + d];
         }
     }
-    if (r.O && part == 0 && on)
-        for (int64_t t = len; t < a.N; ++t) {
-            if (r.o_f32) ((float*)r.O)[ob + t * r.o.n + n] = 0.f;
-            else store1<IO>(r.O, ob + t * r.o.n + n, 0.f);
-        }
+    red[part][col] = tan;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        float s = 0.f;
+        for (int p = 0; p < 4; ++p)
+            for (int c = 0; c < 64; ++c) s += red[p][c];
+        ta.part[((int64_t)h * a.B + b) * ncol + (blockIdx.x - bh * ncol)] = s;
+    }
+}
+
+// Slot s of a row's states holds what segment s - 1 added up from zero; it becomes the state that
+// enters segment s, slot 0 the state that enters the row.  Four columns to a thread.
+__global__ void __launch_bounds__(256) linattn_join_kernel(LinJob a) {
+    const LinRole& r = a.r[blockIdx.y];
+    const int per = r.DK * r.DV / 4;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t bh = i / per;
+    if (bh >= a.B * a.H) return;
+    const int e = (int)(i - bh * per) * 4, d = e / r.DV, n = e - d * r.DV;
+    const int64_t size = (int64_t)r.DK * r.DV;
+    f32x4 S = {0.f, 0.f, 0.f, 0.f};
+    if (r.s_in) {
+        const float* s = r.s_in + bh * size + (int64_t)d * r.s_row + (int64_t)n * r.s_col;
+        for (int j = 0; j < 4; ++j) S[j] = s[(int64_t)j * r.s_col];
+    }
+    float* st = r.states + bh * a.nseg * size + e;
+    *(f32x4*)st = S;
+    const int64_t len = row_len(a.lengths, bh / a.H, a.N);
+    const float em1 = expm1f(log_gamma(a.log_decay, (int)(bh % a.H)) * (float)a.seg_len);
+    for (int s = 1; s < a.nseg && s * a.seg_len < len; ++s) {
+        S += S * em1 + *(f32x4*)(st + s * size);
+        *(f32x4*)(st + s * size) = S;
+    }
 }
 
 template <int IO>
@@ -165,19 +154,25 @@ template <typename F> hipError_t by_dtype(int dtype, F&& f) {
 
 }  // namespace
 
-hipError_t launch_linattn(int dtype, const LinArgs& a, hipStream_t stream) {
-    LinTanArgs t{};
-    t.a = a;
-    const unsigned grid = (unsigned)(a.B * a.H * ((a.r.DV + 63) / 64));
-    return by_dtype(dtype, [&](auto io) { linattn_seq_kernel<io.value, false><<<grid, 256, 0, stream>>>(t); });
+hipError_t launch_linattn(int dtype, const LinJob& a, hipStream_t stream) {
+    return dtype == LCONV_F32 ? launch_linattn_f32(a, stream) : dtype == LCONV_F16 ? launch_linattn_f16(a, stream)
+                                                                                   : launch_linattn_bf16(a, stream);
 }
 
-int linattn_tan_blocks(int DV) { return (DV + 63) / 64; }
+hipError_t launch_linattn_join(const LinJob& a, hipStream_t stream) {
+    int64_t most = 0;
+    for (int i = 0; i < a.nroles; ++i) {
+        const int64_t n = a.B * a.H * ((int64_t)a.r[i].DK * a.r[i].DV / 4);
+        if (n > most) most = n;
+    }
+    linattn_join_kernel<<<dim3((unsigned)((most + 255) / 256), a.nroles), 256, 0, stream>>>(a);
+    return hipGetLastError();
+}
 
 hipError_t launch_linattn_tan(int dtype, const LinTanArgs& t, float* dlog, hipStream_t stream) {
     const int nb = linattn_tan_blocks(t.a.r.DV);
     const unsigned grid = (unsigned)(t.a.B * t.a.H * nb);
-    const hipError_t e = by_dtype(dtype, [&](auto io) { linattn_seq_kernel<io.value, true><<<grid, 256, 0, stream>>>(t); });
+    const hipError_t e = by_dtype(dtype, [&](auto io) { linattn_tan_kernel<io.value><<<grid, 256, 0, stream>>>(t); });
     if (e != hipSuccess) return e;
     tan_sum_kernel<<<(unsigned)t.a.H, 64, 0, stream>>>(t.part, dlog, t.a.B * nb);
     return hipGetLastError();

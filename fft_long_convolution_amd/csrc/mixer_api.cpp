@@ -102,6 +102,28 @@ size_t head_grads_bytes(int64_t B, int64_t H, int64_t G, int64_t N, int64_t D) {
     return H == G ? 0 : round256((size_t)(B * H) * (size_t)N * (size_t)D * 4);
 }
 
+void set_plan(LinJob* a, const LinPlan& p) {
+    a->kt = p.kt; a->nw = p.nw; a->ncb = p.ncb; a->nseg = p.nseg; a->seg_len = p.seg_len;
+}
+
+// The gradients' three roles: dq and dk contract over Dv, dv over Dk.  Where both widths take the same
+// tiles they go in one launch.
+struct BwdPlan {
+    bool together;
+    LinPlan qk, v;
+    size_t sqk, sv;           // bytes of a role's segment states
+};
+BwdPlan bwd_plan(int64_t B, int64_t H, int64_t N, int64_t Dk, int64_t Dv, lconv_dtype_t dtype) {
+    BwdPlan p;
+    const int64_t rows = B * H, wide = Dk > Dv ? Dk : Dv;
+    p.together = linattn_kt(Dk) == linattn_kt(Dv);
+    p.qk = p.together ? linattn_plan(rows, 3, N, wide, wide, dtype) : linattn_plan(rows, 2, N, Dv, Dk, dtype);
+    p.v = p.together ? p.qk : linattn_plan(rows, 1, N, Dk, Dv, dtype);
+    p.sqk = linattn_states_bytes(p.qk, rows, Dk, Dv);
+    p.sv = linattn_states_bytes(p.v, rows, Dk, Dv);
+    return p;
+}
+
 size_t tan_bytes(int64_t B, int64_t H, int64_t Dk) {
     return round256((size_t)(B * H) * (size_t)linattn_tan_blocks((int)Dk) * 4);
 }
@@ -112,8 +134,8 @@ extern "C" {
 
 size_t lconv_linattn_workspace_bytes(int64_t B, int64_t H, int64_t G, int64_t N, int64_t Dk, int64_t Dv,
                                      lconv_dtype_t dtype) {
-    (void)B; (void)H; (void)G; (void)N; (void)Dk; (void)Dv; (void)dtype;
-    return 0;
+    if (!dtype_ok(dtype) || B <= 0 || H <= 0 || N <= 0 || !linattn_dims_ok(B, H, G, N, Dk, Dv)) return 0;
+    return linattn_states_bytes(linattn_plan(B * H, 1, N, Dk, Dv, dtype), B * H, Dk, Dv);
 }
 
 lconv_status_t lconv_linattn_fwd(const void* q, const lconv_strides_t* q_strides, const void* k,
@@ -131,13 +153,14 @@ lconv_status_t lconv_linattn_fwd(const void* q, const lconv_strides_t* q_strides
     const Range rsi = buffer(state_in, states, 4), rso = buffer(state_out, states, 4);
     if (state_in != state_out && overlap(rso, rsi)) return LCONV_ERR_ALIASING;
     if (N == 0) return state_out && state_in != state_out ? hip_status(launch_copy_state(state_in, state_out, states, stream)) : LCONV_SUCCESS;
-    LinArgs a{};
+    LinJob a{};
+    LinRole& r = a.r[0];
     Range rq, rk, rv, ry;
     lconv_status_t st;
-    if ((st = operand(q, q_strides, B, H, N, Dk, dtype, false, &a.r.Q.s, &rq)) != LCONV_SUCCESS) return st;
-    if ((st = operand(k, k_strides, B, G, N, Dk, dtype, false, &a.r.K.s, &rk)) != LCONV_SUCCESS) return st;
-    if ((st = operand(v, v_strides, B, G, N, Dv, dtype, false, &a.r.V.s, &rv)) != LCONV_SUCCESS) return st;
-    if ((st = operand(y, y_strides, B, H, N, Dv, dtype, true, &a.r.o, &ry)) != LCONV_SUCCESS) return st;
+    if ((st = operand(q, q_strides, B, H, N, Dk, dtype, false, &r.Q.s, &rq)) != LCONV_SUCCESS) return st;
+    if ((st = operand(k, k_strides, B, G, N, Dk, dtype, false, &r.K.s, &rk)) != LCONV_SUCCESS) return st;
+    if ((st = operand(v, v_strides, B, G, N, Dv, dtype, false, &r.V.s, &rv)) != LCONV_SUCCESS) return st;
+    if ((st = operand(y, y_strides, B, H, N, Dv, dtype, true, &r.o, &ry)) != LCONV_SUCCESS) return st;
     if (!log_decay) return LCONV_ERR_NULL_POINTER;
     const Range rld = buffer(log_decay, H, 4), rlen = buffer(lengths, B, 4);
     if (clash({ry, rso}, {rq, rk, rv, rld, rlen}) || overlap(ry, rsi)) return LCONV_ERR_ALIASING;
@@ -147,22 +170,26 @@ lconv_status_t lconv_linattn_fwd(const void* q, const lconv_strides_t* q_strides
         if (!aligned16(workspace)) return LCONV_ERR_MISALIGNED;
         if (clash({buffer(workspace, (int64_t)need, 1)}, {rq, rk, rv, ry, rsi, rso, rld, rlen})) return LCONV_ERR_ALIASING;
     }
-    a.r.Q.p = q; a.r.Q.share = 1;
-    a.r.K.p = k; a.r.K.share = (int)(H / G);
-    a.r.V.p = v; a.r.V.share = (int)(H / G);
-    a.r.O = y;
-    a.r.DK = (int)Dk; a.r.DV = (int)Dv;
-    a.r.s_in = state_in; a.r.s_out = state_out; a.r.s_row = (int)Dv; a.r.s_col = 1;
-    a.r.s_q = scale; a.r.s_kv = 1.f;
+    r.Q.p = q; r.Q.share = 1;
+    r.K.p = k; r.K.share = (int)(H / G);
+    r.V.p = v; r.V.share = (int)(H / G);
+    r.O = y;
+    r.DK = (int)Dk; r.DV = (int)Dv;
+    r.s_in = state_in; r.s_out = state_out; r.s_row = (int)Dv; r.s_col = 1;
+    r.states = (float*)workspace;
+    r.s_q = scale; r.s_kv = 1.f;
+    a.nroles = 1;
     a.log_decay = log_decay; a.lengths = lengths;
     a.B = B; a.H = (int)H; a.N = N;
+    set_plan(&a, linattn_plan(B * H, 1, N, Dk, Dv, dtype));
     return hip_status(launch_linattn(dtype, a, stream));
 }
 
 size_t lconv_linattn_bwd_workspace_bytes(int64_t B, int64_t H, int64_t G, int64_t N, int64_t Dk, int64_t Dv,
                                          lconv_dtype_t dtype) {
     if (!dtype_ok(dtype) || B <= 0 || H <= 0 || N <= 0 || !linattn_dims_ok(B, H, G, N, Dk, Dv)) return 0;
-    return head_grads_bytes(B, H, G, N, Dk) + head_grads_bytes(B, H, G, N, Dv) + tan_bytes(B, H, Dk);
+    const BwdPlan p = bwd_plan(B, H, N, Dk, Dv, dtype);
+    return head_grads_bytes(B, H, G, N, Dk) + head_grads_bytes(B, H, G, N, Dv) + tan_bytes(B, H, Dk) + 2 * p.sqk + p.sv;
 }
 
 lconv_status_t lconv_linattn_bwd(const void* dy, const lconv_strides_t* dy_strides, const void* q,
@@ -215,40 +242,62 @@ lconv_status_t lconv_linattn_bwd(const void* dy, const lconv_strides_t* dy_strid
     float* gv = share > 1 ? (float*)ws : nullptr;
     ws += head_grads_bytes(B, H, G, N, Dv);
 
-    LinArgs a{};
+    const BwdPlan plan = bwd_plan(B, H, N, Dk, Dv, dtype);
+    float* tan = (float*)ws;
+    ws += tan_bytes(B, H, Dk);
+
+    LinJob a{};
     a.log_decay = log_decay; a.lengths = lengths;
     a.B = B; a.H = (int)H; a.N = N;
 
     // dq: dy, v, k in the places of q, k, v, with the state transposed
-    LinRole& r = a.r;
-    r.Q = ody; r.K = ov; r.V = ok;
-    r.O = dq; r.o = sdq; r.o_f32 = 0;
-    r.DK = (int)Dv; r.DV = (int)Dk;
-    r.s_in = state_in; r.s_out = nullptr; r.s_row = 1; r.s_col = (int)Dv;
-    r.s_q = scale; r.s_kv = 1.f; r.reverse = 0;
-    if (launch_linattn(dtype, a, stream) != hipSuccess) return LCONV_ERR_HIP;
-    if (dlog_decay) {
-        LinTanArgs t{};
-        t.a = a; t.q = oq; t.ds_out = dstate_out; t.part = (float*)ws;
-        if (launch_linattn_tan(dtype, t, dlog_decay, stream) != hipSuccess) return LCONV_ERR_HIP;
-    }
+    LinRole& rq_ = a.r[0];
+    rq_.Q = ody; rq_.K = ov; rq_.V = ok;
+    rq_.O = dq; rq_.o = sdq;
+    rq_.DK = (int)Dv; rq_.DV = (int)Dk;
+    rq_.s_in = state_in; rq_.s_row = 1; rq_.s_col = (int)Dv;
+    rq_.s_q = scale; rq_.s_kv = 1.f;
+    rq_.states = (float*)ws;
 
     // dk: v, dy, q from the last token to the first
-    r.Q = ov; r.K = ody; r.V = oq;
-    r.O = share > 1 ? (void*)gk : dk;
-    r.o = share > 1 ? lconv_strides_t{H * N * Dk, N * Dk, Dk} : sdk;
-    r.o_f32 = share > 1;
-    r.s_in = dstate_out;
-    r.s_q = 1.f; r.s_kv = scale; r.reverse = 1;
-    if (launch_linattn(dtype, a, stream) != hipSuccess) return LCONV_ERR_HIP;
+    LinRole& rk_ = a.r[1];
+    rk_ = rq_;
+    rk_.Q = ov; rk_.K = ody; rk_.V = oq;
+    rk_.O = share > 1 ? (void*)gk : dk;
+    rk_.o = share > 1 ? lconv_strides_t{H * N * Dk, N * Dk, Dk} : sdk;
+    rk_.o_f32 = share > 1;
+    rk_.s_in = dstate_out;
+    rk_.s_q = 1.f; rk_.s_kv = scale; rk_.reverse = 1;
+    rk_.states = (float*)(ws + plan.sqk);
 
     // dv and the gradient of the state that entered: k, q, dy
-    r.Q = ok; r.K = oq; r.V = ody;
-    r.O = share > 1 ? (void*)gv : dv;
-    r.o = share > 1 ? lconv_strides_t{H * N * Dv, N * Dv, Dv} : sdv;
-    r.DK = (int)Dk; r.DV = (int)Dv;
-    r.s_out = dstate_in; r.s_row = (int)Dv; r.s_col = 1;
+    LinRole& rv_ = a.r[2];
+    rv_ = rk_;
+    rv_.Q = ok; rv_.K = oq; rv_.V = ody;
+    rv_.O = share > 1 ? (void*)gv : dv;
+    rv_.o = share > 1 ? lconv_strides_t{H * N * Dv, N * Dv, Dv} : sdv;
+    rv_.DK = (int)Dk; rv_.DV = (int)Dv;
+    rv_.s_out = dstate_in; rv_.s_row = (int)Dv; rv_.s_col = 1;
+    rv_.states = (float*)(ws + 2 * plan.sqk);
+
+    a.nroles = plan.together ? 3 : 2;
+    set_plan(&a, plan.qk);
     if (launch_linattn(dtype, a, stream) != hipSuccess) return LCONV_ERR_HIP;
+    if (!plan.together) {
+        LinJob one = a;
+        one.r[0] = rv_;
+        one.nroles = 1;
+        set_plan(&one, plan.v);
+        if (launch_linattn(dtype, one, stream) != hipSuccess) return LCONV_ERR_HIP;
+    }
+    if (dlog_decay) {
+        LinTanArgs t{};
+        t.a.r = rq_;
+        t.a.log_decay = log_decay; t.a.lengths = lengths;
+        t.a.B = B; t.a.H = (int)H; t.a.N = N;
+        t.q = oq; t.ds_out = dstate_out; t.part = tan;
+        if (launch_linattn_tan(dtype, t, dlog_decay, stream) != hipSuccess) return LCONV_ERR_HIP;
+    }
     if (share > 1) {
         if (launch_head_sum(dtype, gk, dk, sdk, B, (int)G, share, N, (int)Dk, stream) != hipSuccess) return LCONV_ERR_HIP;
         if (launch_head_sum(dtype, gv, dv, sdv, B, (int)G, share, N, (int)Dv, stream) != hipSuccess) return LCONV_ERR_HIP;

@@ -4,6 +4,7 @@
 #include <stdint.h>
 
 #include "fused_io.h"
+#include "mixer_kernels.h"
 
 namespace lcv {
 namespace {

@@ -1,10 +1,11 @@
 // mixer_kernels.h -- launchers of the linear-attention, rotary and layer-norm kernels
-// (host-callable, defined in linattn.hip, rotary.hip and layernorm.hip).
+// (host-callable, defined in linattn*.hip, rotary.hip and layernorm.hip).
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
 #include "lconv.h"
+#include "mixer_plan.h"
 
 namespace lcv {
 
@@ -31,8 +32,21 @@ struct LinRole {
     const float* s_in;        // [B][H] states, element (d, n) at d * s_row + n * s_col; NULL: zeros
     float* s_out;             // the same layout; NULL: not wanted
     int s_row, s_col;
+    float* states;            // [B][H][nseg][DK][DV]: the states that enter the segments (nseg > 1)
     float s_q, s_kv;
     int reverse;
+};
+
+// Up to three linear attentions over the same tokens in one launch, with one plan (linattn_plan).
+struct LinJob {
+    LinRole r[3];
+    int nroles;
+    const float* log_decay;   // [H]
+    const int32_t* lengths;   // [B] or NULL
+    int64_t B;
+    int H;
+    int64_t N, seg_len;
+    int kt, nw, ncb, nseg;
 };
 
 struct LinArgs {
@@ -65,9 +79,13 @@ struct LinTanArgs {
     float* part;              // [H][B][blocks]
 };
 
-hipError_t launch_linattn(int dtype, const LinArgs& a, hipStream_t stream);
+hipError_t launch_linattn(int dtype, const LinJob& a, hipStream_t stream);
+hipError_t launch_linattn_f32(const LinJob& a, hipStream_t stream);
+hipError_t launch_linattn_f16(const LinJob& a, hipStream_t stream);
+hipError_t launch_linattn_bf16(const LinJob& a, hipStream_t stream);
+// the segments' own states to the states that enter them
+hipError_t launch_linattn_join(const LinJob& a, hipStream_t stream);
 hipError_t launch_linattn_step(int dtype, const LinStepArgs& a, hipStream_t stream);
-int linattn_tan_blocks(int DV);
 hipError_t launch_linattn_tan(int dtype, const LinTanArgs& a, float* dlog, hipStream_t stream);
 // out[b][g][n][:] = sum over the `share` heads of g of the fp32 rows in[b][h][n][:] (dense)
 hipError_t launch_head_sum(int dtype, const float* in, void* out, lconv_strides_t os, int64_t B, int G, int share,
@@ -99,7 +117,5 @@ struct NormArgs {
 };
 hipError_t launch_layernorm_fwd(int dtype, const NormArgs& a, hipStream_t stream);
 hipError_t launch_layernorm_bwd(int dtype, const NormArgs& a, hipStream_t stream);
-// row blocks whose partial sums of dweight and dbias the gradient call keeps (host arithmetic only)
-int64_t layernorm_parts(int64_t rows, int64_t C);
 
 }  // namespace lcv

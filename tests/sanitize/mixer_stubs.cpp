@@ -3,7 +3,7 @@
 
 namespace lcv {
 #define LCV_STUB(sig) sig { return hipErrorInvalidValue; }
-LCV_STUB(hipError_t launch_linattn(int, const LinArgs&, hipStream_t))
+LCV_STUB(hipError_t launch_linattn(int, const LinJob&, hipStream_t))
 LCV_STUB(hipError_t launch_linattn_step(int, const LinStepArgs&, hipStream_t))
 LCV_STUB(hipError_t launch_linattn_tan(int, const LinTanArgs&, float*, hipStream_t))
 LCV_STUB(hipError_t launch_head_sum(int, const float*, void*, lconv_strides_t, int64_t, int, int, int64_t, int, hipStream_t))

@@ -36,7 +36,7 @@ namespace {
 
 template <int IO> struct Mx {  // bf16, fp16
     using E = uint16_t;
-    static constexpr int C = 64;        // tokens of a chunk
+    static constexpr int C = 32;        // tokens of a chunk
     static constexpr int TK = 2;        // 16-wide tiles of one contraction step
     static constexpr int PADR = 8;      // row padding in LDS, elements: rows 4 banks apart (row reads)
     static constexpr int PADT = 16;     // 8 banks apart (transposed reads)
@@ -128,8 +128,8 @@ __global__ void __launch_bounds__(256, KT > 8 ? 1 : 2) linattn_chunk_kernel(LinJ
     constexpr int C = M::C, TK = M::TK, CT = C / 16, CJ = CT / TK, KS = KT / TK, ES = TK * 4;
     constexpr int DKP = KT * 16, DVB = 64 * NW, RS = DKP + M::PADR, VS = DVB + M::PADT;
     constexpr int VEC = M::VEC, KV_ROW = DKP / VEC, V_ROW = DVB / VEC;   // 16-byte groups of a row
-    constexpr int NK = C * KV_ROW / 256, NV = C * V_ROW / 256;           // groups per thread
-    static_assert(NK >= 1 && NV >= 1, "a chunk feeds every thread");
+    constexpr int NK = (C * KV_ROW + 255) / 256, NV = C * V_ROW / 256;   // groups per thread
+    static_assert(NV >= 1 && C * V_ROW % 256 == 0 && (NK == 1 || C * KV_ROW % 256 == 0), "whole passes");
     __shared__ __attribute__((aligned(16))) E Qs[STATE ? 8 : C * RS];
     __shared__ __attribute__((aligned(16))) E Ks[C * RS];
     __shared__ __attribute__((aligned(16))) E Vs[C * VS];
@@ -210,31 +210,51 @@ __global__ void __launch_bounds__(256, KT > 8 ? 1 : 2) linattn_chunk_kernel(LinJ
             }
     }
 
-    // ---- global loads of a chunk, one ahead of the arithmetic
-    const int64_t qb = row_base(r.Q, b, h), kb = row_base(r.K, b, h), vb = row_base(r.V, b, h);
+    // ---- global loads of a chunk, one ahead of the arithmetic.  Each thread's groups keep their row in
+    // the chunk and their columns, so their pointers only move on.
+    const auto first = [&](const LinOperand& o, int row, int c) LCV_INLINE {
+        const int64_t p = beg + row;
+        return (const E*)o.p + row_base(o, b, h) + (r.reverse ? len - 1 - p : p) * o.s.n + c;
+    };
+    const int64_t dir = r.reverse ? -(int64_t)C : C;
+    const E *pq[STATE ? 1 : NK], *pk[NK], *pv[NV];
+#pragma unroll
+    for (int i = 0; i < NK; ++i) {
+        const int e = tid + 256 * i;
+        pk[i] = first(r.K, e / KV_ROW, (e % KV_ROW) * VEC);
+        if constexpr (!STATE) pq[i] = first(r.Q, e / KV_ROW, (e % KV_ROW) * VEC);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int e = tid + 256 * i;
+        pv[i] = first(r.V, e / V_ROW, cb * DVB + (e % V_ROW) * VEC);
+    }
+    const bool kin = C * KV_ROW >= 256 || tid < C * KV_ROW;      // a narrow chunk leaves threads without a group
+    const bool kon = kin && tid % KV_ROW * VEC < r.DK, von = cb * DVB + tid % V_ROW * VEC < r.DV;  // 256 is a multiple of both
     uint4 rq[STATE ? 1 : NK], rk[NK], rv[NV];
-    const auto fetch = [&](int64_t at) LCV_INLINE {
+    const auto fetch = [&](int64_t left) LCV_INLINE {
 #pragma unroll
         for (int i = 0; i < NK; ++i) {
-            const int e = tid + 256 * i, row = e / KV_ROW, c = (e % KV_ROW) * VEC;
-            const int64_t p = at + row;
-            const int64_t t = r.reverse ? len - 1 - p : p;
-            const bool on = p < end && c < r.DK;
-            rk[i] = on ? *(const uint4*)((const E*)r.K.p + kb + t * r.K.s.n + c) : make_uint4(0, 0, 0, 0);
-            if constexpr (!STATE) rq[i] = on ? *(const uint4*)((const E*)r.Q.p + qb + t * r.Q.s.n + c) : make_uint4(0, 0, 0, 0);
+            const bool on = kon && (tid + 256 * i) / KV_ROW < left;
+            rk[i] = on ? *(const uint4*)pk[i] : make_uint4(0, 0, 0, 0);
+            pk[i] += dir * r.K.s.n;
+            if constexpr (!STATE) {
+                rq[i] = on ? *(const uint4*)pq[i] : make_uint4(0, 0, 0, 0);
+                pq[i] += dir * r.Q.s.n;
+            }
         }
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int e = tid + 256 * i, row = e / V_ROW, c = cb * DVB + (e % V_ROW) * VEC;
-            const int64_t p = at + row;
-            const int64_t t = r.reverse ? len - 1 - p : p;
-            rv[i] = p < end && c < r.DV ? *(const uint4*)((const E*)r.V.p + vb + t * r.V.s.n + c) : make_uint4(0, 0, 0, 0);
+            const bool on = von && (tid + 256 * i) / V_ROW < left;
+            rv[i] = on ? *(const uint4*)pv[i] : make_uint4(0, 0, 0, 0);
+            pv[i] += dir * r.V.s.n;
         }
     };
     const auto stage = [&]() LCV_INLINE {
 #pragma unroll
         for (int i = 0; i < NK; ++i) {
             const int e = tid + 256 * i, row = e / KV_ROW, c = (e % KV_ROW) * VEC;
+            if (!kin) continue;
             *(uint4*)(Ks + row * RS + c) = rk[i];
             if constexpr (!STATE) *(uint4*)(Qs + row * RS + c) = rq[i];
         }
@@ -267,27 +287,24 @@ __global__ void __launch_bounds__(256, KT > 8 ? 1 : 2) linattn_chunk_kernel(LinJ
     const E* krow = Ks + x * RS + 4 * g;
     const E* ktr = Ks + M::tr_start(g, x, RS);
     const E* vtr = Vs + M::tr_start(g, x, VS) + wave * 16 * NW;
+    // the lane's place in the output: token 4 g of the chunk, its first column
+    const int64_t odir = r.reverse ? -r.o.n : r.o.n;
+    int64_t oat = STATE ? 0 : ob + (r.reverse ? len - 1 - beg : beg) * r.o.n + 4 * g * odir + col;
 
-    float em1 = expm1f(lg * (float)C);
-    if (beg < end) fetch(beg);
-    for (int64_t at = beg; at < end; at += C) {
-        const int c = end - at < C ? (int)(end - at) : C;
-        __syncthreads();
-        stage();
-        __syncthreads();
-        if (at + C < end) fetch(at + C);
-        if (at == beg || c < C) {
-            em1 = expm1f(lg * (float)c);
+    float em1 = 0.f;
+    const auto weigh = [&](int c) LCV_INLINE {
+        em1 = expm1f(lg * (float)c);
 #pragma unroll
-            for (int j = 0; j < CJ; ++j)
+        for (int j = 0; j < CJ; ++j)
 #pragma unroll
-                for (int s = 0; s < ES; ++s) {
-                    const int tok = 16 * TK * j + 16 * (s >> 2) + 4 * g + (s & 3);
-                    const int e = c - 1 - tok + off;     // past the row's end V is zero; the power is kept finite
-                    wU[j][s] = r.s_kv * expf(lg * (float)(e > 0 ? e : 0));
-                }
-        }
+            for (int s = 0; s < ES; ++s) {
+                const int tok = 16 * TK * j + 16 * (s >> 2) + 4 * g + (s & 3);
+                const int e = c - 1 - tok + off;     // past the row's end V is zero; the power is kept finite
+                wU[j][s] = r.s_kv * expf(lg * (float)(e > 0 ? e : 0));
+            }
+    };
 
+    const auto chunk = [&](int c) LCV_INLINE {
         Frag vf[CJ][NW];
 #pragma unroll
         for (int j = 0; j < CJ; ++j)
@@ -295,10 +312,18 @@ __global__ void __launch_bounds__(256, KT > 8 ? 1 : 2) linattn_chunk_kernel(LinJ
             for (int n = 0; n < NW; ++n) vf[j][n] = M::load_tr(vtr + 16 * n, VS, j);
 
         if constexpr (!STATE) {
-            Frag sf[KS][NW];
+            Frag qf[CT][KS], kf[CT][KS], sf[KS][NW];
+#pragma unroll
+            for (int it = 0; it < CT; ++it)
+#pragma unroll
+                for (int t = 0; t < KS; ++t) {
+                    qf[it][t] = M::load_row(qrow + 16 * it * RS, t);
+                    kf[it][t] = M::load_row(krow + 16 * it * RS, t);
+                }
             float sback[NW];
 #pragma unroll
             for (int n = 0; n < NW; ++n) {
+                float to = 1.f;
                 sback[n] = 1.f;
                 if constexpr (IO == CT_F16) {
                     float m = 0.f;
@@ -306,57 +331,55 @@ __global__ void __launch_bounds__(256, KT > 8 ? 1 : 2) linattn_chunk_kernel(LinJ
                     for (int t = 0; t < KT; ++t)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) m = fmaxf(m, fabsf(S[t][n][i]));
-                    const float to = to_f16_range(max_over_g(m), &sback[n]);
+                    to = to_f16_range(max_over_g(m), &sback[n]);
+                }
 #pragma unroll
-                    for (int t = 0; t < KS; ++t) {
-                        const f32x4 u[2] = {S[2 * t][n] * to, S[2 * t + 1][n] * to};
-                        sf[t][n] = M::pack(u);
-                    }
-                } else {
+                for (int t = 0; t < KS; ++t) {
+                    f32x4 u[TK];
 #pragma unroll
-                    for (int t = 0; t < KS; ++t) {
-                        f32x4 u[TK];
-#pragma unroll
-                        for (int k = 0; k < TK; ++k) u[k] = S[TK * t + k][n];
-                        sf[t][n] = M::pack(u);
-                    }
+                    for (int k = 0; k < TK; ++k) u[k] = IO == CT_F16 ? S[TK * t + k][n] * to : S[TK * t + k][n];
+                    sf[t][n] = M::pack(u);
                 }
             }
+            f32x4 acc[CT][NW], p[CT][CT];
 #pragma unroll
             for (int it = 0; it < CT; ++it) {
-                if (16 * it >= c) break;
-                Frag qf[KS];
 #pragma unroll
-                for (int t = 0; t < KS; ++t) qf[t] = M::load_row(qrow + 16 * it * RS, t);
-                f32x4 acc[NW];
+                for (int n = 0; n < NW; ++n) acc[it][n] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int n = 0; n < NW; ++n) {
-                    acc[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+                for (int jt = 0; jt < CT; ++jt) p[it][jt] = f32x4{0.f, 0.f, 0.f, 0.f};
+            }
 #pragma unroll
-                    for (int t = 0; t < KS; ++t) acc[n] = M::mma(qf[t], sf[t][n], acc[n]);
+            for (int t = 0; t < KS; ++t)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[n][i] *= wI[i] * wT[it] * sback[n];
+                for (int it = 0; it < CT; ++it) {
+#pragma unroll
+                    for (int jt = 0; jt <= it; ++jt) p[it][jt] = M::mma(kf[jt][t], qf[it][t], p[it][jt]);
+#pragma unroll
+                    for (int n = 0; n < NW; ++n) acc[it][n] = M::mma(qf[it][t], sf[t][n], acc[it][n]);
                 }
-                f32x4 p[CT];
 #pragma unroll
-                for (int jt = 0; jt < CT; ++jt) {
-                    p[jt] = f32x4{0.f, 0.f, 0.f, 0.f};
-                    if (jt > it) continue;
+            for (int it = 0; it < CT; ++it) {
 #pragma unroll
-                    for (int t = 0; t < KS; ++t) p[jt] = M::mma(M::load_row(krow + 16 * jt * RS, t), qf[t], p[jt]);
+                for (int i = 0; i < 4; ++i) {
+                    const float w = wI[i] * wT[it];
+#pragma unroll
+                    for (int n = 0; n < NW; ++n) acc[it][n][i] *= IO == CT_F16 ? w * sback[n] : w;
+                }
+#pragma unroll
+                for (int jt = 0; jt <= it; ++jt)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)   // later tokens are left out, not weighed with 0: they may not be finite
-                        p[jt][i] = jt < it || x >= 4 * g + i ? p[jt][i] * wP[it - jt][i] : 0.f;
-                }
+                        p[it][jt][i] = jt < it || x >= 4 * g + i ? p[it][jt][i] * wP[it - jt][i] : 0.f;
                 if constexpr (IO == CT_F16) {
                     float m = 0.f, back;
 #pragma unroll
                     for (int jt = 0; jt <= it; ++jt)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) m = fmaxf(m, fabsf(p[jt][i]));
+                        for (int i = 0; i < 4; ++i) m = fmaxf(m, fabsf(p[it][jt][i]));
                     const float to = to_f16_range(max_over_g(m), &back);
 #pragma unroll
-                    for (int jt = 0; jt <= it; ++jt) p[jt] *= to;
+                    for (int jt = 0; jt <= it; ++jt) p[it][jt] *= to;
                     float rb[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) rb[i] = __shfl(back, 4 * g + i);
@@ -364,138 +387,115 @@ __global__ void __launch_bounds__(256, KT > 8 ? 1 : 2) linattn_chunk_kernel(LinJ
                     for (int n = 0; n < NW; ++n) {
                         f32x4 o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                        for (int j = 0; j <= it / TK; ++j) o = M::mma(M::pack(p + TK * j), vf[j][n], o);
+                        for (int j = 0; j <= it / TK; ++j) o = M::mma(M::pack(p[it] + TK * j), vf[j][n], o);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) acc[n][i] += o[i] * rb[i];
+                        for (int i = 0; i < 4; ++i) acc[it][n][i] += o[i] * rb[i];
                     }
                 } else {
 #pragma unroll
                     for (int j = 0; j <= it / TK; ++j) {
-                        const Frag pf = M::pack(p + TK * j);
+                        const Frag pf = M::pack(p[it] + TK * j);
 #pragma unroll
-                        for (int n = 0; n < NW; ++n) acc[n] = M::mma(pf, vf[j][n], acc[n]);
+                        for (int n = 0; n < NW; ++n) acc[it][n] = M::mma(pf, vf[j][n], acc[it][n]);
                     }
                 }
-                if (r.O && col < r.DV) {
+            }
+            if (col < r.DV) {
+#pragma unroll
+                for (int it = 0; it < CT; ++it)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int tok = 16 * it + 4 * g + i;
-                        if (tok >= c) continue;
-                        const int64_t t = r.reverse ? len - 1 - at - tok : at + tok;
-                        const int64_t o = ob + t * r.o.n + col;
-                        if constexpr (NW == 1) {
-                            if (r.o_f32) ((float*)r.O)[o] = r.s_q * acc[0][i];
-                            else store1<IO>(r.O, o, r.s_q * acc[0][i]);
+                        if (16 * it + 4 * g + i >= c) continue;
+                        const int64_t o = oat + (16 * it + i) * odir;
+                        const float y0 = r.s_q * acc[it][0][i], y1 = r.s_q * acc[it][NW - 1][i];
+                        if (IO == CT_F32 || r.o_f32) {
+                            if constexpr (NW == 1) ((float*)r.O)[o] = y0;
+                            else *(float2*)((float*)r.O + o) = make_float2(y0, y1);
                         } else {
-                            const float y0 = r.s_q * acc[0][i], y1 = r.s_q * acc[1][i];
-                            if (IO == CT_F32 || r.o_f32) *(float2*)((float*)r.O + o) = make_float2(y0, y1);
+                            if constexpr (NW == 1) store1<IO>(r.O, o, y0);
                             else *(uint32_t*)((uint16_t*)r.O + o) = pack2<IO == CT_F32 ? CT_BF16 : IO>(y0, y1);
                         }
                     }
-                }
             }
+            oat += C * odir;
         }
 
         // ---- the state moves on
-        if constexpr (IO == CT_F32) {
-            Frag u[CJ][NW];
+        constexpr int PARTS = IO == CT_F32 ? 1 : IO == CT_F16 ? 2 : 3;
+        Frag u[PARTS][CJ][NW];
+        float back[NW];
 #pragma unroll
-            for (int j = 0; j < CJ; ++j)
+        for (int n = 0; n < NW; ++n) {
+            float v[CJ][ES], m = 0.f;
 #pragma unroll
-                for (int n = 0; n < NW; ++n)
+            for (int j = 0; j < CJ; ++j) {
+                M::unpack(vf[j][n], v[j]);
 #pragma unroll
-                    for (int s = 0; s < 4; ++s) u[j][n].v[s] = vf[j][n].v[s] * wU[j][s];
-#pragma unroll
-            for (int t = 0; t < KT; ++t) {
-#pragma unroll
-                for (int n = 0; n < NW; ++n) S[t][n] += S[t][n] * em1;
-#pragma unroll
-                for (int j = 0; j < CJ; ++j) {
-                    const Frag kf = M::load_tr(ktr + 16 * t, RS, j);
-#pragma unroll
-                    for (int n = 0; n < NW; ++n) S[t][n] = M::mma(kf, u[j][n], S[t][n]);
+                for (int s = 0; s < ES; ++s) {
+                    v[j][s] *= wU[j][s];
+                    if constexpr (IO == CT_F16) m = fmaxf(m, fabsf(v[j][s]));
                 }
             }
-        } else if constexpr (IO == CT_BF16) {
-            Frag u1[CJ][NW], u2[CJ][NW], u3[CJ][NW];
-#pragma unroll
-            for (int j = 0; j < CJ; ++j)
-#pragma unroll
-                for (int n = 0; n < NW; ++n) {
-                    float v[8], p[8];
-                    M::unpack(vf[j][n], v);
-#pragma unroll
-                    for (int s = 0; s < 8; ++s) v[s] *= wU[j][s];
-                    u1[j][n] = M::pack(v);
-                    M::unpack(u1[j][n], p);
-#pragma unroll
-                    for (int s = 0; s < 8; ++s) v[s] -= p[s];
-                    u2[j][n] = M::pack(v);
-                    M::unpack(u2[j][n], p);
-#pragma unroll
-                    for (int s = 0; s < 8; ++s) v[s] -= p[s];
-                    u3[j][n] = M::pack(v);
-                }
-#pragma unroll
-            for (int t = 0; t < KT; ++t) {
-#pragma unroll
-                for (int n = 0; n < NW; ++n) S[t][n] += S[t][n] * em1;
-#pragma unroll
-                for (int j = 0; j < CJ; ++j) {
-                    const Frag kf = M::load_tr(ktr + 16 * t, RS, j);
-#pragma unroll
-                    for (int n = 0; n < NW; ++n) {
-                        S[t][n] = M::mma(kf, u1[j][n], S[t][n]);
-                        S[t][n] = M::mma(kf, u2[j][n], S[t][n]);
-                        S[t][n] = M::mma(kf, u3[j][n], S[t][n]);
-                    }
-                }
-            }
-        } else {
-            Frag u1[CJ][NW], u2[CJ][NW];
-            float back[NW];
-#pragma unroll
-            for (int n = 0; n < NW; ++n) {
-                float v[CJ][8], p[8], m = 0.f;
-#pragma unroll
-                for (int j = 0; j < CJ; ++j) {
-                    M::unpack(vf[j][n], v[j]);
-#pragma unroll
-                    for (int s = 0; s < 8; ++s) {
-                        v[j][s] *= wU[j][s];
-                        m = fmaxf(m, fabsf(v[j][s]));
-                    }
-                }
+            if constexpr (IO == CT_F16) {
                 const float to = to_f16_range(max_over_g(m), &back[n]);
 #pragma unroll
-                for (int j = 0; j < CJ; ++j) {
+                for (int j = 0; j < CJ; ++j)
 #pragma unroll
-                    for (int s = 0; s < 8; ++s) v[j][s] *= to;
-                    u1[j][n] = M::pack(v[j]);
-                    M::unpack(u1[j][n], p);
-#pragma unroll
-                    for (int s = 0; s < 8; ++s) v[j][s] -= p[s];
-                    u2[j][n] = M::pack(v[j]);
-                }
+                    for (int s = 0; s < ES; ++s) v[j][s] *= to;
             }
 #pragma unroll
-            for (int t = 0; t < KT; ++t) {
-                f32x4 d[NW];
+            for (int j = 0; j < CJ; ++j)
 #pragma unroll
-                for (int n = 0; n < NW; ++n) d[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+                for (int k = 0; k < PARTS; ++k) {
+                    u[k][j][n] = M::pack(v[j]);
+                    if (k + 1 < PARTS) {
+                        float q[ES];
+                        M::unpack(u[k][j][n], q);
 #pragma unroll
-                for (int j = 0; j < CJ; ++j) {
-                    const Frag kf = M::load_tr(ktr + 16 * t, RS, j);
-#pragma unroll
-                    for (int n = 0; n < NW; ++n) {
-                        d[n] = M::mma(kf, u1[j][n], d[n]);
-                        d[n] = M::mma(kf, u2[j][n], d[n]);
+                        for (int s = 0; s < ES; ++s) v[j][s] -= q[s];
                     }
                 }
+        }
 #pragma unroll
-                for (int n = 0; n < NW; ++n) S[t][n] += S[t][n] * em1 + d[n] * back[n];
+        for (int t = 0; t < KT; ++t) {
+            f32x4 d[NW];
+#pragma unroll
+            for (int n = 0; n < NW; ++n) d[n] = IO == CT_F16 ? f32x4{0.f, 0.f, 0.f, 0.f} : S[t][n] + S[t][n] * em1;
+#pragma unroll
+            for (int j = 0; j < CJ; ++j) {
+                const Frag kt = M::load_tr(ktr + 16 * t, RS, j);
+#pragma unroll
+                for (int k = 0; k < PARTS; ++k)
+#pragma unroll
+                    for (int n = 0; n < NW; ++n) d[n] = M::mma(kt, u[k][j][n], d[n]);
+            }
+#pragma unroll
+            for (int n = 0; n < NW; ++n) {
+                if constexpr (IO == CT_F16) S[t][n] += S[t][n] * em1 + d[n] * back[n];
+                else S[t][n] = d[n];
             }
         }
+    };
+
+    if (beg < end) {
+        fetch(end - beg);
+        weigh(C);
+    }
+    int64_t at = beg;
+    for (; at + C <= end; at += C) {
+        __syncthreads();
+        stage();
+        __syncthreads();
+        if (at + C < end) fetch(end - at - C);
+        chunk(C);
+    }
+    if (at < end) {
+        const int c = (int)(end - at);
+        __syncthreads();
+        stage();
+        weigh(c);
+        __syncthreads();
+        chunk(c);
     }
 
     // ---- the state that leaves

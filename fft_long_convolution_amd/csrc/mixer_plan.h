@@ -20,7 +20,8 @@ inline LinPlan linattn_plan(int64_t rows, int nroles, int64_t N, int64_t DK, int
     p.kt = linattn_kt(DK);
     p.nw = DV > 64 ? 2 : 1;
     p.ncb = (int)((DV + 64 * p.nw - 1) / (64 * p.nw));
-    const int64_t C = dtype == LCONV_F32 ? 32 : 64;
+    const int64_t C = 64;                       // a multiple of the kernels' chunk
+    (void)dtype;
     const int64_t wgs = rows * nroles * p.ncb;
     int64_t nseg = 1;
     if (wgs < 256) {

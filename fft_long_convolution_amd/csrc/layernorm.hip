@@ -1,100 +1,355 @@
 // layernorm.hip -- layer norm: forward, and the gradients of its input, weight and bias.
+//
+//   y = (x - mean) rstd w + b;   with xhat = (x - mean) rstd and h = dy w:
+//   dx = rstd (h - mean_C(h) - xhat mean_C(h xhat)),  dw = sum_rows dy xhat,  db = sum_rows dy
+// Both are bound by HBM: x (and dy) are read once, y (dx) written once.  A row lives in the registers of
+// LANES lanes of one wave (C <= 4096) or of one workgroup (C <= 8192), 8-element groups dealt out in
+// turn, so the sums need no second read; longer rows are read again through the caches.  Waves walk the
+// rows with the weight (and, in the gradient, the column sums of their rows) held in registers.
+//
+// The mean takes two sums: the first is off by the rounding of adding up the values themselves, what is
+// left of it shows in the sum of the centred values and is taken out of mean and variance.
 #include "mixer_kernels.h"
 #include "mixer_io.h"
 
 namespace lcv {
 namespace {
 
-__device__ __forceinline__ float block_sum(float v, float* red) {
-    for (int w = 32; w; w >>= 1) v += __shfl_xor(v, w);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-    __syncthreads();
-    return red[0] + red[1] + red[2] + red[3];
+template <int LANES> __device__ __forceinline__ float row_sum(float v, float* red) {
+    constexpr int W = LANES < 64 ? LANES : 64;
+#pragma unroll
+    for (int w = W / 2; w; w >>= 1) v += __shfl_xor(v, w);
+    if constexpr (LANES > 64) {
+        __syncthreads();
+        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = red[0];
+#pragma unroll
+        for (int i = 1; i < LANES / 64; ++i) v += red[i];
+    }
+    return v;
 }
 
-// One workgroup per row.
-template <int IO>
+// raw 8-element groups of a row: group k of lane l is elements 8 (l + LANES k) ..
+template <int IO> struct Group { uint4 r[IO == CT_F32 ? 2 : 1]; };
+template <int IO> __device__ __forceinline__ Group<IO> load_group(const void* p, int64_t row, int c, int C) {
+    Group<IO> v;
+    const typename Elem<IO>::T* q = (const typename Elem<IO>::T*)p + row + c;
+    if (c + 8 <= C) {
+        __builtin_memcpy(v.r, q, sizeof(v.r));
+    } else {
+        typename Elem<IO>::T e[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e[i] = c + i < C ? q[i] : (typename Elem<IO>::T)0;
+        __builtin_memcpy(v.r, e, sizeof(v.r));
+    }
+    return v;
+}
+
+// elements of group c that the row has
+__device__ __forceinline__ int left(int c, int C) { return C - c < 8 ? C - c : 8; }
+
+template <int IO, int LANES, int K>
 __global__ void __launch_bounds__(256) ln_fwd_kernel(NormArgs a) {
     __shared__ float red[4];
-    const int64_t row = blockIdx.x, xo = row * a.xs, yo = row * a.ys;
-    const int C = (int)a.C;
-    float s = 0.f;
-    for (int c = threadIdx.x; c < C; c += 256) s += load1<IO>(a.x, xo + c);
-    // the first mean is off by the rounding of a sum of the values themselves; what is left of it
-    // shows in the centred sum and is taken out
-    const float first = block_sum(s, red) / (float)C;
-    float s2 = 0.f;
-    s = 0.f;
-    for (int c = threadIdx.x; c < C; c += 256) {
-        const float d = load1<IO>(a.x, xo + c) - first;
-        s += d;
-        s2 += d * d;
+    constexpr int ROWS = 256 / LANES;            // rows a workgroup has in hand
+    const int lane = threadIdx.x % LANES, C = (int)a.C;
+    const float inv = 1.f / (float)C;
+    Group<IO> w[K], b[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int c = 8 * (lane + LANES * k);
+        if (a.weight) w[k] = load_group<IO>(a.weight, 0, c, C);
+        if (a.bias) b[k] = load_group<IO>(a.bias, 0, c, C);
     }
-    const float rest = block_sum(s, red) / (float)C;
-    const float mean = first + rest;
-    const float rstd = 1.f / sqrtf(fmaxf(block_sum(s2, red) / (float)C - rest * rest, 0.f) + a.eps);
-    for (int c = threadIdx.x; c < C; c += 256) {
-        float y = (load1<IO>(a.x, xo + c) - first - rest) * rstd;
-        if (a.weight) y *= load1<IO>(a.weight, c);
-        if (a.bias) y += load1<IO>(a.bias, c);
-        store1<IO>(a.y, yo + c, y);
-    }
-    if (threadIdx.x == 0) {
-        if (a.mean) a.mean[row] = mean;
-        if (a.rstd) a.rstd[row] = rstd;
+    // every lane of a wave takes part in each turn's sums: rows past the last compute on row 0's data
+    for (int64_t r0 = (int64_t)blockIdx.x * ROWS; r0 < a.rows; r0 += (int64_t)gridDim.x * ROWS) {
+        const int64_t row = r0 + threadIdx.x / LANES;
+        const bool on = row < a.rows;
+        float x[K][8], s = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int c = 8 * (lane + LANES * k);
+            const Group<IO> g = load_group<IO>(a.x, (on ? row : 0) * a.xs, c, C);
+            unpack_raw<IO>(g.r, x[k]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s += x[k][i];
+        }
+        const float first = row_sum<LANES>(s, red) * inv;
+        float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int n = left(8 * (lane + LANES * k), C);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                x[k][i] = i < n ? x[k][i] - first : 0.f;
+                s1 += x[k][i];
+                s2 += x[k][i] * x[k][i];
+            }
+        }
+        const float rest = row_sum<LANES>(s1, red) * inv;
+        const float var = fmaxf(row_sum<LANES>(s2, red) * inv - rest * rest, 0.f);
+        const float rstd = 1.f / sqrtf(var + a.eps);
+        if (!on) continue;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int c = 8 * (lane + LANES * k);
+            if (c >= C) continue;
+            float y[8], p[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = (x[k][i] - rest) * rstd;
+            if (a.weight) {
+                unpack_raw<IO>(w[k].r, p);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[i] *= p[i];
+            }
+            if (a.bias) {
+                unpack_raw<IO>(b[k].r, p);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[i] += p[i];
+            }
+            store8_part<IO>(a.y, row * a.ys + c, left(c, C), y);
+        }
+        if (lane == 0) {
+            if (a.mean) a.mean[row] = first + rest;
+            if (a.rstd) a.rstd[row] = rstd;
+        }
     }
 }
 
+// Rows too long for registers: three passes through the caches, one workgroup to a row.
 template <int IO>
-__global__ void __launch_bounds__(256) ln_dx_kernel(NormArgs a) {
+__global__ void __launch_bounds__(256) ln_fwd_long_kernel(NormArgs a) {
     __shared__ float red[4];
-    const int64_t row = blockIdx.x, xo = row * a.xs, yo = row * a.ys, go = row * a.dys;
     const int C = (int)a.C;
-    const float mean = a.mean[row], rstd = a.rstd[row];
-    float s1 = 0.f, s2 = 0.f;
-    for (int c = threadIdx.x; c < C; c += 256) {
-        float g = load1<IO>(a.dy, go + c);
-        if (a.weight) g *= load1<IO>(a.weight, c);
-        s1 += g;
-        s2 += g * (load1<IO>(a.x, xo + c) - mean) * rstd;
-    }
-    s1 = block_sum(s1, red) / (float)C;
-    s2 = block_sum(s2, red) / (float)C;
-    for (int c = threadIdx.x; c < C; c += 256) {
-        float g = load1<IO>(a.dy, go + c);
-        if (a.weight) g *= load1<IO>(a.weight, c);
-        const float xh = (load1<IO>(a.x, xo + c) - mean) * rstd;
-        store1<IO>(a.y, yo + c, rstd * (g - s1 - xh * s2));
+    const float inv = 1.f / (float)C;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        const int64_t xo = row * a.xs;
+        float s = 0.f, x[8], p[8];
+        for (int c = 8 * threadIdx.x; c < C; c += 2048) {
+            load8_part<IO>(a.x, xo + c, left(c, C), x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s += x[i];
+        }
+        const float first = row_sum<256>(s, red) * inv;
+        float s1 = 0.f, s2 = 0.f;
+        for (int c = 8 * threadIdx.x; c < C; c += 2048) {
+            const int n = left(c, C);
+            load8_part<IO>(a.x, xo + c, n, x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float d = i < n ? x[i] - first : 0.f;
+                s1 += d;
+                s2 += d * d;
+            }
+        }
+        const float rest = row_sum<256>(s1, red) * inv;
+        const float var = fmaxf(row_sum<256>(s2, red) * inv - rest * rest, 0.f);
+        const float rstd = 1.f / sqrtf(var + a.eps);
+        for (int c = 8 * threadIdx.x; c < C; c += 2048) {
+            const int n = left(c, C);
+            load8_part<IO>(a.x, xo + c, n, x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = (x[i] - first - rest) * rstd;
+            if (a.weight) {
+                load8_part<IO>(a.weight, c, n, p);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] *= p[i];
+            }
+            if (a.bias) {
+                load8_part<IO>(a.bias, c, n, p);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] += p[i];
+            }
+            store8_part<IO>(a.y, row * a.ys + c, n, x);
+        }
+        if (threadIdx.x == 0) {
+            if (a.mean) a.mean[row] = first + rest;
+            if (a.rstd) a.rstd[row] = rstd;
+        }
     }
 }
 
-// Partial column sums of block blockIdx.y's rows: part[0 / 1][block][C] for dweight / dbias.  It reads
-// dy and x before the dx kernel may overwrite one of them in place.
+// The gradient: dx of every row, and the column sums of the workgroup's rows to part[0 / 1][block][C].
+// A row is read before it is written, so dx may stand in place of dy or x.
+template <int IO, int LANES, int K>
+__global__ void __launch_bounds__(256) ln_bwd_kernel(NormArgs a) {
+    __shared__ float red[4];
+    constexpr int ROWS = 256 / LANES;
+    const int lane = threadIdx.x % LANES, C = (int)a.C;
+    const float inv = 1.f / (float)C;
+    const bool sums = a.part != nullptr;
+    Group<IO> w[K];
+    float sw[K][8], sb[K][8];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        if (a.weight) w[k] = load_group<IO>(a.weight, 0, 8 * (lane + LANES * k), C);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sw[k][i] = sb[k][i] = 0.f;
+    }
+    for (int64_t r0 = (int64_t)blockIdx.x * ROWS; r0 < a.rows; r0 += (int64_t)gridDim.x * ROWS) {
+        const int64_t row = r0 + threadIdx.x / LANES, at = row < a.rows ? row : 0;
+        const bool on = row < a.rows;
+        const float mean = a.mean[at], rstd = a.rstd[at];
+        float xh[K][8], g[K][8], s1 = 0.f, s2 = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int c = 8 * (lane + LANES * k), n = on ? left(c, C) : 0;
+            const Group<IO> gx = load_group<IO>(a.x, at * a.xs, c, C), gg = load_group<IO>(a.dy, at * a.dys, c, C);
+            unpack_raw<IO>(gx.r, xh[k]);
+            unpack_raw<IO>(gg.r, g[k]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                xh[k][i] = i < n ? (xh[k][i] - mean) * rstd : 0.f;
+                if (i >= n) g[k][i] = 0.f;
+                sw[k][i] += g[k][i] * xh[k][i];
+                sb[k][i] += g[k][i];
+            }
+            if (a.weight) {
+                float p[8];
+                unpack_raw<IO>(w[k].r, p);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) g[k][i] *= p[i];
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                s1 += g[k][i];
+                s2 += g[k][i] * xh[k][i];
+            }
+        }
+        s1 = row_sum<LANES>(s1, red) * inv;
+        s2 = row_sum<LANES>(s2, red) * inv;
+        if (!on) continue;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int c = 8 * (lane + LANES * k);
+            if (c >= C) continue;
+            float d[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) d[i] = rstd * (g[k][i] - s1 - xh[k][i] * s2);
+            store8_part<IO>(a.y, row * a.ys + c, left(c, C), d);
+        }
+    }
+    if (!sums) return;
+    // the rows of one workgroup join through LDS, in the order of its row groups
+    __shared__ float join[LANES < 256 ? 2 * 8 * 256 : 1];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        if constexpr (LANES < 256) {
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                join[i * 256 + threadIdx.x] = sw[k][i];
+                join[(8 + i) * 256 + threadIdx.x] = sb[k][i];
+            }
+            __syncthreads();
+            if (threadIdx.x < LANES) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    float u = 0.f, v = 0.f;
+#pragma unroll
+                    for (int q = 0; q < ROWS; ++q) {
+                        u += join[i * 256 + q * LANES + lane];
+                        v += join[(8 + i) * 256 + q * LANES + lane];
+                    }
+                    sw[k][i] = u;
+                    sb[k][i] = v;
+                }
+            }
+        }
+        const int c = 8 * (lane + LANES * k);
+        if (threadIdx.x < LANES && c < C) {
+            const int64_t o = (int64_t)blockIdx.x * C + c, nb = (int64_t)gridDim.x * C;
+            store8_part<CT_F32>(a.part, o, left(c, C), sw[k]);
+            store8_part<CT_F32>(a.part, nb + o, left(c, C), sb[k]);
+        }
+    }
+}
+
 template <int IO>
-__global__ void __launch_bounds__(256) ln_part_kernel(NormArgs a, int64_t nparts) {
-    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (c >= a.C) return;
-    float sw = 0.f, sb = 0.f;
-    for (int64_t row = blockIdx.y; row < a.rows; row += nparts) {
-        const float g = load1<IO>(a.dy, row * a.dys + c);
-        sw += g * (load1<IO>(a.x, row * a.xs + c) - a.mean[row]) * a.rstd[row];
-        sb += g;
+__global__ void __launch_bounds__(256) ln_dx_long_kernel(NormArgs a) {
+    __shared__ float red[4];
+    const int C = (int)a.C;
+    const float inv = 1.f / (float)C;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        const float mean = a.mean[row], rstd = a.rstd[row];
+        float s1 = 0.f, s2 = 0.f, x[8], g[8], p[8];
+        const auto load = [&](int c, int n) LCV_INLINE {
+            load8_part<IO>(a.x, row * a.xs + c, n, x);
+            load8_part<IO>(a.dy, row * a.dys + c, n, g);
+            if (a.weight) {
+                load8_part<IO>(a.weight, c, n, p);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) g[i] *= p[i];
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = i < n ? (x[i] - mean) * rstd : 0.f;
+        };
+        for (int c = 8 * threadIdx.x; c < C; c += 2048) {
+            load(c, left(c, C));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                s1 += g[i];
+                s2 += g[i] * x[i];
+            }
+        }
+        s1 = row_sum<256>(s1, red) * inv;
+        s2 = row_sum<256>(s2, red) * inv;
+        for (int c = 8 * threadIdx.x; c < C; c += 2048) {
+            const int n = left(c, C);
+            load(c, n);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = rstd * (g[i] - s1 - x[i] * s2);
+            store8_part<IO>(a.y, row * a.ys + c, n, x);
+        }
     }
-    a.part[blockIdx.y * a.C + c] = sw;
-    a.part[(nparts + blockIdx.y) * a.C + c] = sb;
 }
 
-__global__ void __launch_bounds__(256) ln_sum_kernel(NormArgs a, int64_t nparts) {
-    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (c >= a.C) return;
-    float sw = 0.f, sb = 0.f;
-    for (int64_t p = 0; p < nparts; ++p) {
-        sw += a.part[p * a.C + c];
-        sb += a.part[(nparts + p) * a.C + c];
+// Column sums for rows too long for registers: block blockIdx.y takes every gridDim.y-th row.  It runs
+// before the kernel above may write dx over dy or x.
+template <int IO>
+__global__ void __launch_bounds__(256) ln_part_long_kernel(NormArgs a) {
+    const int c = 8 * (blockIdx.x * 256 + threadIdx.x), C = (int)a.C;
+    if (c >= C) return;
+    const int n = left(c, C);
+    float sw[8] = {}, sb[8] = {}, x[8], g[8];
+    for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
+        load8_part<IO>(a.x, row * a.xs + c, n, x);
+        load8_part<IO>(a.dy, row * a.dys + c, n, g);
+        const float mean = a.mean[row], rstd = a.rstd[row];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            sw[i] += g[i] * ((x[i] - mean) * rstd);
+            sb[i] += g[i];
+        }
     }
-    if (a.dweight) a.dweight[c] = sw;
-    if (a.dbias) a.dbias[c] = sb;
+    const int64_t o = (int64_t)blockIdx.y * C + c, nb = (int64_t)gridDim.y * C;
+    store8_part<CT_F32>(a.part, o, n, sw);
+    store8_part<CT_F32>(a.part, nb + o, n, sb);
+}
+
+// dweight and dbias from the blocks' partial sums: a workgroup takes 32 columns, its 8 groups of lanes
+// every eighth block, and joins the groups in order.
+__global__ void __launch_bounds__(256) ln_sum_kernel(const float* part, float* dweight, float* dbias, int np, int C) {
+    __shared__ float join[2][8][32];
+    const int l = threadIdx.x & 31, q = threadIdx.x >> 5, c = blockIdx.x * 32 + l;
+    float u = 0.f, v = 0.f;
+    if (c < C) {
+#pragma unroll 8
+        for (int p = q; p < np; p += 8) {
+            u += part[(int64_t)p * C + c];
+            v += part[(int64_t)(np + p) * C + c];
+        }
+    }
+    join[0][q][l] = u;
+    join[1][q][l] = v;
+    __syncthreads();
+    if (q > 1 || c >= C) return;
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += join[q][i][l];
+    float* out = q ? dbias : dweight;
+    if (out) out[c] = s;
 }
 
 template <typename F> hipError_t by_dtype(int dtype, F&& f) {
@@ -104,27 +359,56 @@ template <typename F> hipError_t by_dtype(int dtype, F&& f) {
     return hipGetLastError();
 }
 
+// f(lanes, groups per lane) for rows of C <= 8192
+template <typename F> void by_width(int64_t C, F&& f) {
+    const auto go = [&](auto lanes, auto k) { f(lanes, k); };
+    using std::integral_constant;
+    if (C <= 128) go(integral_constant<int, 16>{}, integral_constant<int, 1>{});
+    else if (C <= 512) go(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+    else if (C <= 1024) go(integral_constant<int, 64>{}, integral_constant<int, 2>{});
+    else if (C <= 2048) go(integral_constant<int, 64>{}, integral_constant<int, 4>{});
+    else if (C <= 4096) go(integral_constant<int, 256>{}, integral_constant<int, 2>{});
+    else go(integral_constant<int, 256>{}, integral_constant<int, 4>{});
+}
+
 }  // namespace
 
 hipError_t launch_layernorm_fwd(int dtype, const NormArgs& a, hipStream_t stream) {
-    return by_dtype(dtype, [&](auto io) { ln_fwd_kernel<io.value><<<(unsigned)a.rows, 256, 0, stream>>>(a); });
+    if (a.C > kNormRegisterC) {
+        const unsigned grid = (unsigned)(a.rows < 4096 ? a.rows : 4096);
+        return by_dtype(dtype, [&](auto io) { ln_fwd_long_kernel<io.value><<<grid, 256, 0, stream>>>(a); });
+    }
+    return by_dtype(dtype, [&](auto io) {
+        by_width(a.C, [&](auto lanes, auto k) {
+            const int64_t wgs = (a.rows + 256 / lanes.value - 1) / (256 / lanes.value);
+            const unsigned grid = (unsigned)(wgs < 2048 ? wgs : 2048);
+            ln_fwd_kernel<io.value, lanes.value, k.value><<<grid, 256, 0, stream>>>(a);
+        });
+    });
 }
 
 hipError_t launch_layernorm_bwd(int dtype, const NormArgs& a, hipStream_t stream) {
+    const bool sums = a.dweight || a.dbias;
+    const int64_t np = layernorm_parts(a.rows, a.C);
     hipError_t e = hipSuccess;
-    if (a.dweight || a.dbias) {
-        const int64_t np = layernorm_parts(a.rows, a.C);
-        const unsigned gx = (unsigned)((a.C + 255) / 256);
-        if (np > 0) {
-            e = by_dtype(dtype, [&](auto io) { ln_part_kernel<io.value><<<dim3(gx, (unsigned)np), 256, 0, stream>>>(a, np); });
+    if (a.rows > 0 && a.C <= kNormRegisterC) {
+        e = by_dtype(dtype, [&](auto io) {
+            by_width(a.C, [&](auto lanes, auto k) {
+                ln_bwd_kernel<io.value, lanes.value, k.value><<<(unsigned)np, 256, 0, stream>>>(a);
+            });
+        });
+    } else if (a.rows > 0) {
+        if (sums) {
+            const unsigned gx = (unsigned)((a.C + 2047) / 2048);
+            e = by_dtype(dtype, [&](auto io) { ln_part_long_kernel<io.value><<<dim3(gx, (unsigned)np), 256, 0, stream>>>(a); });
             if (e != hipSuccess) return e;
         }
-        ln_sum_kernel<<<gx, 256, 0, stream>>>(a, np);
-        e = hipGetLastError();
-        if (e != hipSuccess) return e;
+        const unsigned grid = (unsigned)(a.rows < 4096 ? a.rows : 4096);
+        e = by_dtype(dtype, [&](auto io) { ln_dx_long_kernel<io.value><<<grid, 256, 0, stream>>>(a); });
     }
-    if (a.rows > 0) e = by_dtype(dtype, [&](auto io) { ln_dx_kernel<io.value><<<(unsigned)a.rows, 256, 0, stream>>>(a); });
-    return e;
+    if (e != hipSuccess || !sums) return e;
+    ln_sum_kernel<<<(unsigned)((a.C + 31) / 32), 256, 0, stream>>>(a.part, a.dweight, a.dbias, (int)np, (int)a.C);
+    return hipGetLastError();
 }
 
 }  // namespace lcv

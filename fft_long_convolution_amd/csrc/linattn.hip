@@ -81,32 +81,78 @@ __global__ void __launch_bounds__(256) linattn_join_kernel(LinJob a) {
     *(f32x4*)st = S;
     const int64_t len = row_len(a.lengths, bh / a.H, a.N);
     const float em1 = expm1f(log_gamma(a.log_decay, (int)(bh % a.H)) * (float)a.seg_len);
-    for (int s = 1; s < a.nseg && s * a.seg_len < len; ++s) {
-        S += S * em1 + *(f32x4*)(st + s * size);
-        *(f32x4*)(st + s * size) = S;
+    // a row's segments are in a chain of their own, but their sums are not: eight loads in flight
+    int last = a.nseg;
+    while (last > 1 && (last - 1) * a.seg_len >= len) --last;
+    for (int s = 1; s < last; s += 8) {
+        f32x4 v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (s + j < last) v[j] = *(const f32x4*)(st + (s + j) * size);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (s + j < last) {
+                S += S * em1 + v[j];
+                *(f32x4*)(st + (s + j) * size) = S;
+            }
     }
 }
 
-template <int IO>
+// One token: S = gamma S + k v^T in place, y = scale S^T q.  The state's 8 Dk Dv bytes are read and
+// written once, all else is small: bound by HBM, or by latency for few rows.  A workgroup takes CB columns
+// of one (b, h): 16-byte loads along a row, up to 16 of them in flight per thread, q and k as floats
+// through LDS while the state is on its way, y's sum over the rows through LDS.
+template <int IO, int CB>
 __global__ void __launch_bounds__(256) linattn_step_kernel(LinStepArgs a) {
-    const int64_t bh = blockIdx.x;
+    constexpr int LPR = CB / 4, RPP = 256 / LPR, BATCH = 16;   // lanes to a row, rows to a pass
+    __shared__ float qk[2][256];
+    __shared__ __attribute__((aligned(16))) f32x4 red[256];
+    const int ncb = (a.DV + CB - 1) / CB;
+    const int64_t bh = blockIdx.x / ncb;
+    const int cb = (int)(blockIdx.x - bh * ncb);
     const int64_t b = bh / a.H;
-    const int h = (int)(bh - b * a.H);
+    const int h = (int)(bh - b * a.H), tid = threadIdx.x;
+    const int n = cb * CB + tid % LPR * 4, d0 = tid / LPR;
+    const bool on = n < a.DV;
     const int64_t slot = a.slots ? (int64_t)a.slots[b] : b;
-    const bool live = slot >= 0 && slot < a.nslots;
+    const int64_t yo = b * a.ys.b + (int64_t)h * a.ys.h;
+    if (slot < 0 || slot >= a.nslots) {
+        if (d0 == 0 && on)
+            for (int i = 0; i < 4; ++i) store1<IO>(a.y, yo + n + i, 0.f);
+        return;
+    }
+    float* S = a.state + (slot * a.H + h) * (int64_t)a.DK * a.DV + n;
+    f32x4 s[BATCH];
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i)
+        if (on && d0 + i * RPP < a.DK) s[i] = *(const f32x4*)(S + (int64_t)(d0 + i * RPP) * a.DV);
+    if (tid < a.DK) {
+        qk[0][tid] = load1<IO>(a.q.p, row_base(a.q, b, h) + tid) * a.scale;
+        qk[1][tid] = load1<IO>(a.k.p, row_base(a.k, b, h) + tid);
+    }
+    f32x4 v = {0.f, 0.f, 0.f, 0.f}, y = {0.f, 0.f, 0.f, 0.f};
+    if (on)
+        for (int i = 0; i < 4; ++i) v[i] = load1<IO>(a.v.p, row_base(a.v, b, h) + n + i);
     const float gamma = expf(log_gamma(a.log_decay, h));
-    for (int n = threadIdx.x; n < a.DV; n += 256) {
-        float acc = 0.f;
-        if (live) {
-            float* S = a.state + (slot * a.H + h) * (int64_t)a.DK * a.DV + n;
-            const float v = load1<IO>(a.v.p, row_base(a.v, b, h) + n);
-            for (int d = 0; d < a.DK; ++d) {
-                const float s = gamma * S[(int64_t)d * a.DV] + load1<IO>(a.k.p, row_base(a.k, b, h) + d) * v;
-                S[(int64_t)d * a.DV] = s;
-                acc += s * load1<IO>(a.q.p, row_base(a.q, b, h) + d);
-            }
+    __syncthreads();
+    for (int base = 0; base < a.DK; base += BATCH * RPP) {
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            const int d = base + d0 + i * RPP;
+            if (!on || d >= a.DK) continue;
+            if (base) s[i] = *(const f32x4*)(S + (int64_t)d * a.DV);
+            s[i] = s[i] * gamma + v * qk[1][d];
+            y += s[i] * qk[0][d];
+            *(f32x4*)(S + (int64_t)d * a.DV) = s[i];
         }
-        store1<IO>(a.y, b * a.ys.b + (int64_t)h * a.ys.h + n, acc * a.scale);
+    }
+    red[tid] = y;
+    __syncthreads();
+    if (tid < CB && cb * CB + tid < a.DV) {
+        float t = 0.f;
+#pragma unroll
+        for (int i = 0; i < RPP; ++i) t += ((const float*)red)[i * CB + tid];
+        store1<IO>(a.y, yo + cb * CB + tid, t);
     }
 }
 
@@ -179,8 +225,15 @@ hipError_t launch_linattn_tan(int dtype, const LinTanArgs& t, float* dlog, hipSt
 }
 
 hipError_t launch_linattn_step(int dtype, const LinStepArgs& a, hipStream_t stream) {
-    const unsigned grid = (unsigned)(a.B * a.H);
-    return by_dtype(dtype, [&](auto io) { linattn_step_kernel<io.value><<<grid, 256, 0, stream>>>(a); });
+    // few rows: 32 columns to a workgroup, four times the workgroups to share the latency
+    const int64_t rows = a.B * a.H;
+    const bool narrow = rows * ((a.DV + 127) / 128) < 512;
+    const int cb = narrow ? 32 : 128;
+    const unsigned grid = (unsigned)(rows * ((a.DV + cb - 1) / cb));
+    return by_dtype(dtype, [&](auto io) {
+        if (narrow) linattn_step_kernel<io.value, 32><<<grid, 256, 0, stream>>>(a);
+        else linattn_step_kernel<io.value, 128><<<grid, 256, 0, stream>>>(a);
+    });
 }
 
 hipError_t launch_head_sum(int dtype, const float* in, void* out, lconv_strides_t os, int64_t B, int G, int share,

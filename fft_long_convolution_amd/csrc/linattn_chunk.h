@@ -10,10 +10,10 @@
 //
 // How the four products follow each other in registers (lane = 16 g + x, tiles of 16 x 16, the
 // accumulator holds rows 4 g + r, r < 4, of column x):
-//   P^T = K Q^T   accumulator: tokens j = 4g + r of query i = x, which is what the next product takes
-//   O  += P V     as its left operand (row i, contraction over j): no lane moves
-//   O  += Q S     S's accumulators (rows d = 4g + r, column n = x) are the right operand as they are
-//   S  += K^T V   both operands stand transposed to their rows in LDS: ds_read_b64_tr_b16 for 16-bit
+//   P^T  = K Q^T      accumulator: tokens j = 4g + r of query i = x, which is what the next product
+//   O^T += V^T P^T    takes as its right operand (column i, contraction over j): no lane moves
+//   O^T += S^T Q^T    S's accumulators (rows d = 4g + r, column n = x) are the left operand as they are
+//   S   += K^T V      both operands stand transposed to their rows in LDS: ds_read_b64_tr_b16 for 16-bit
 //                 types, four strided reads for fp32
 // The contraction order inside an operand is {16 t + 4 g + s, 16 (t + 1) + 4 g + s} for a step of 32
 // (16-bit) and {16 t + 4 g + s} for fp32, alike on both sides.  Every wave forms all of P (4 of about
@@ -22,8 +22,8 @@
 // Precision.  S, P and every sum are fp32.  For 16-bit types P and S are rounded to the type once as
 // operands, like the result itself.  What S adds up is not: gamma^.. V is split into three bf16 parts
 // (two where no state leaves the call, whose error is 2^-17) or two fp16 parts, so that the state keeps fp32's accuracy over any length.
-// fp16 operands that may pass its range (P, S, gamma^.. V) are scaled to it by a power of two, per query
-// or per column.  gamma^c S is S + (gamma^c - 1) S, so that a decay near one does not lose by rounding
+// fp16 operands that may pass its range (P, S, gamma^.. V) are scaled to it by a power of two, per query,
+// per 16 columns and per column.  gamma^c S is S + (gamma^c - 1) S, so that a decay near one does not lose by rounding
 // its power.
 #pragma once
 #include "mixer_io.h"
@@ -117,6 +117,12 @@ __device__ __forceinline__ float max_over_g(float m) {
     return fmaxf(m, __shfl_xor(m, 32));
 }
 
+__device__ __forceinline__ float max_over_wave(float m) {
+#pragma unroll
+    for (int w = 1; w < 16; w *= 2) m = fmaxf(m, __shfl_xor(m, w));
+    return max_over_g(m);
+}
+
 // ---- one segment of one (b, h), 64 NW columns -------------------------------------------------
 
 // STATE: only the state that the segment adds up from zero, for the segments after it.
@@ -151,7 +157,7 @@ __global__ void __launch_bounds__(256, KT > 8 ? 1 : 2) linattn_chunk_kernel(LinJ
     if (STATE && beg + a.seg_len >= len) return;   // no segment follows
 
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, g = lane >> 4, x = lane & 15;
-    const int col = cb * DVB + wave * 16 * NW + x * NW;    // the lane's NW columns
+    const int wcol = cb * DVB + wave * 16 * NW;             // the wave's first column
     const int64_t ob = b * r.o.b + (int64_t)h * r.o.h;
     const int osize = r.o_f32 ? 4 : (int)sizeof(E);
 
@@ -172,18 +178,16 @@ __global__ void __launch_bounds__(256, KT > 8 ? 1 : 2) linattn_chunk_kernel(LinJ
     // ---- weights of the chunk's tokens
     const float lg = log_gamma(a.log_decay, h);
     const int off = r.reverse;
-    float wP[CT][4], wI[4], wT[CT], wU[CJ][ES];
+    float wP[CT][4], wI[CT], wU[CJ][ES];
 #pragma unroll
     for (int t = 0; t < CT; ++t) {
-        wT[t] = expf(lg * (float)(16 * t));
+        wI[t] = r.s_q * expf(lg * (float)(16 * t + x + 1 - off));
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int e = 16 * t + x - 4 * g - i;
-            wP[t][i] = r.s_kv * expf(lg * (float)(e > 0 ? e : 0));
+            wP[t][i] = r.s_q * r.s_kv * expf(lg * (float)(e > 0 ? e : 0));
         }
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) wI[i] = expf(lg * (float)(4 * g + i + 1 - off));
 
     // ---- the state that enters
     f32x4 S[KT][NW];
@@ -196,7 +200,7 @@ __global__ void __launch_bounds__(256, KT > 8 ? 1 : 2) linattn_chunk_kernel(LinJ
         for (int t = 0; t < KT; ++t)
 #pragma unroll
             for (int n = 0; n < NW; ++n) {
-                const int d = 16 * t + 4 * g, c = col + n;
+                const int d = 16 * t + 4 * g, c = wcol + 16 * n + x;
                 f32x4 v = {0.f, 0.f, 0.f, 0.f};
                 if (s && d < r.DK && c < r.DV) {
                     if (srow == 1) {
@@ -261,25 +265,7 @@ __global__ void __launch_bounds__(256, KT > 8 ? 1 : 2) linattn_chunk_kernel(LinJ
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int e = tid + 256 * i, row = e / V_ROW, c = (e % V_ROW) * VEC;
-            if constexpr (NW == 1) {
-                *(uint4*)(Vs + row * VS + c) = rv[i];
-            } else {
-                // column 32 w + 2 x + n stands at 32 w + 16 n + x: a lane's two columns are neighbours
-                // in memory, so that it writes both at once
-                uint2 even, odd;
-                if constexpr (IO == CT_F32) {
-                    even = make_uint2(rv[i].x, rv[i].z);
-                    odd = make_uint2(rv[i].y, rv[i].w);
-                } else {
-                    even.x = __builtin_amdgcn_perm(rv[i].y, rv[i].x, 0x05040100u);
-                    even.y = __builtin_amdgcn_perm(rv[i].w, rv[i].z, 0x05040100u);
-                    odd.x = __builtin_amdgcn_perm(rv[i].y, rv[i].x, 0x07060302u);
-                    odd.y = __builtin_amdgcn_perm(rv[i].w, rv[i].z, 0x07060302u);
-                }
-                E* p = Vs + row * VS + (c & ~31) + (c & 31) / 2;
-                *(uint2*)p = even;
-                *(uint2*)(p + 16) = odd;
-            }
+            *(uint4*)(Vs + row * VS + c) = rv[i];
         }
     };
 
@@ -287,9 +273,9 @@ __global__ void __launch_bounds__(256, KT > 8 ? 1 : 2) linattn_chunk_kernel(LinJ
     const E* krow = Ks + x * RS + 4 * g;
     const E* ktr = Ks + M::tr_start(g, x, RS);
     const E* vtr = Vs + M::tr_start(g, x, VS) + wave * 16 * NW;
-    // the lane's place in the output: token 4 g of the chunk, its first column
+    // the lane's place in the output: token x of the chunk, the first of its four columns
     const int64_t odir = r.reverse ? -r.o.n : r.o.n;
-    int64_t oat = STATE ? 0 : ob + (r.reverse ? len - 1 - beg : beg) * r.o.n + 4 * g * odir + col;
+    int64_t oat = STATE ? 0 : ob + (r.reverse ? len - 1 - beg : beg) * r.o.n + x * odir + wcol + 4 * g;
 
     float em1 = 0.f;
     const auto weigh = [&](int c) LCV_INLINE {
@@ -331,7 +317,7 @@ __global__ void __launch_bounds__(256, KT > 8 ? 1 : 2) linattn_chunk_kernel(LinJ
                     for (int t = 0; t < KT; ++t)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) m = fmaxf(m, fabsf(S[t][n][i]));
-                    to = to_f16_range(max_over_g(m), &sback[n]);
+                    to = to_f16_range(max_over_wave(m), &sback[n]);
                 }
 #pragma unroll
                 for (int t = 0; t < KS; ++t) {
@@ -356,16 +342,12 @@ __global__ void __launch_bounds__(256, KT > 8 ? 1 : 2) linattn_chunk_kernel(LinJ
 #pragma unroll
                     for (int jt = 0; jt <= it; ++jt) p[it][jt] = M::mma(kf[jt][t], qf[it][t], p[it][jt]);
 #pragma unroll
-                    for (int n = 0; n < NW; ++n) acc[it][n] = M::mma(qf[it][t], sf[t][n], acc[it][n]);
+                    for (int n = 0; n < NW; ++n) acc[it][n] = M::mma(sf[t][n], qf[it][t], acc[it][n]);
                 }
 #pragma unroll
             for (int it = 0; it < CT; ++it) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float w = wI[i] * wT[it];
-#pragma unroll
-                    for (int n = 0; n < NW; ++n) acc[it][n][i] *= IO == CT_F16 ? w * sback[n] : w;
-                }
+                for (int n = 0; n < NW; ++n) acc[it][n] *= IO == CT_F16 ? wI[it] * sback[n] : wI[it];
 #pragma unroll
                 for (int jt = 0; jt <= it; ++jt)
 #pragma unroll
@@ -380,42 +362,34 @@ __global__ void __launch_bounds__(256, KT > 8 ? 1 : 2) linattn_chunk_kernel(LinJ
                     const float to = to_f16_range(max_over_g(m), &back);
 #pragma unroll
                     for (int jt = 0; jt <= it; ++jt) p[it][jt] *= to;
-                    float rb[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) rb[i] = __shfl(back, 4 * g + i);
 #pragma unroll
                     for (int n = 0; n < NW; ++n) {
                         f32x4 o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                        for (int j = 0; j <= it / TK; ++j) o = M::mma(M::pack(p[it] + TK * j), vf[j][n], o);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) acc[it][n][i] += o[i] * rb[i];
+                        for (int j = 0; j <= it / TK; ++j) o = M::mma(vf[j][n], M::pack(p[it] + TK * j), o);
+                        acc[it][n] += o * back;
                     }
                 } else {
 #pragma unroll
                     for (int j = 0; j <= it / TK; ++j) {
                         const Frag pf = M::pack(p[it] + TK * j);
 #pragma unroll
-                        for (int n = 0; n < NW; ++n) acc[it][n] = M::mma(pf, vf[j][n], acc[it][n]);
+                        for (int n = 0; n < NW; ++n) acc[it][n] = M::mma(vf[j][n], pf, acc[it][n]);
                     }
                 }
             }
-            if (col < r.DV) {
 #pragma unroll
-                for (int it = 0; it < CT; ++it)
+            for (int it = 0; it < CT; ++it) {
+                if (16 * it + x >= c) continue;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (16 * it + 4 * g + i >= c) continue;
-                        const int64_t o = oat + (16 * it + i) * odir;
-                        const float y0 = r.s_q * acc[it][0][i], y1 = r.s_q * acc[it][NW - 1][i];
-                        if (IO == CT_F32 || r.o_f32) {
-                            if constexpr (NW == 1) ((float*)r.O)[o] = y0;
-                            else *(float2*)((float*)r.O + o) = make_float2(y0, y1);
-                        } else {
-                            if constexpr (NW == 1) store1<IO>(r.O, o, y0);
-                            else *(uint32_t*)((uint16_t*)r.O + o) = pack2<IO == CT_F32 ? CT_BF16 : IO>(y0, y1);
-                        }
-                    }
+                for (int n = 0; n < NW; ++n) {
+                    if (wcol + 16 * n + 4 * g >= r.DV) continue;
+                    const int64_t o = oat + 16 * it * odir + 16 * n;
+                    const f32x4 y = acc[it][n];
+                    if (IO == CT_F32 || r.o_f32) *(f32x4*)((float*)r.O + o) = y;
+                    else *(uint2*)((uint16_t*)r.O + o) = make_uint2(pack2<IO == CT_F32 ? CT_BF16 : IO>(y[0], y[1]),
+                                                                    pack2<IO == CT_F32 ? CT_BF16 : IO>(y[2], y[3]));
+                }
             }
             oat += C * odir;
         }
@@ -513,7 +487,7 @@ __global__ void __launch_bounds__(256, KT > 8 ? 1 : 2) linattn_chunk_kernel(LinJ
         for (int t = 0; t < KT; ++t)
 #pragma unroll
             for (int n = 0; n < NW; ++n) {
-                const int d = 16 * t + 4 * g, c = col + n;
+                const int d = 16 * t + 4 * g, c = wcol + 16 * n + x;
                 if (d >= r.DK || c >= r.DV) continue;
                 if (srow == 1) {
                     *(f32x4*)(s + (int64_t)c * scol + d) = S[t][n];

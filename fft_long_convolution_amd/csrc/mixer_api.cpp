@@ -478,7 +478,8 @@ lconv_status_t lconv_layernorm_bwd(const void* dy, int64_t dy_stride, const void
     }
     a.dy = dy; a.x = x; a.weight = weight; a.y = dx; a.dys = dy_stride; a.xs = x_stride; a.ys = dx_stride;
     a.mean = const_cast<float*>(mean); a.rstd = const_cast<float*>(rstd);
-    a.part = (float*)workspace; a.rows = rows;
+    a.part = dweight || dbias ? (float*)workspace : nullptr;
+    a.rows = rows;
     return hip_status(launch_layernorm_bwd(dtype, a, stream));
 }
 

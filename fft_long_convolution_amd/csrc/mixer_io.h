@@ -17,6 +17,40 @@ template <int IO> __device__ __forceinline__ void store1(void* base, int64_t i, 
     else ((uint16_t*)base)[i] = (uint16_t)(pack2<IO>(v, 0.f) & 0xffffu);
 }
 
+// 8 elements in a row from any element on (16-byte accesses need no alignment here).
+template <int IO> __device__ __forceinline__ void load8_any(const void* base, int64_t i, float* x) {
+    uint4 r[IO == CT_F32 ? 2 : 1];
+    __builtin_memcpy(r, (const typename Elem<IO>::T*)base + i, sizeof(r));
+    unpack_raw<IO>(r, x);
+}
+template <int IO> __device__ __forceinline__ void store8_any(void* base, int64_t i, const float* x) {
+    typename Elem<IO>::T* p = (typename Elem<IO>::T*)base + i;
+    if constexpr (IO == CT_F32) {
+        __builtin_memcpy(p, x, 32);
+    } else {
+        const uint4 w = make_uint4(pack2<IO>(x[0], x[1]), pack2<IO>(x[2], x[3]), pack2<IO>(x[4], x[5]), pack2<IO>(x[6], x[7]));
+        __builtin_memcpy(p, &w, 16);
+    }
+}
+// the first n of 8 elements, the others zero
+template <int IO> __device__ __forceinline__ void load8_part(const void* base, int64_t i, int n, float* x) {
+    if (n >= 8) {
+        load8_any<IO>(base, i, x);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = j < n ? load1<IO>(base, i + j) : 0.f;
+    }
+}
+template <int IO> __device__ __forceinline__ void store8_part(void* base, int64_t i, int n, const float* x) {
+    if (n >= 8) {
+        store8_any<IO>(base, i, x);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < n) store1<IO>(base, i + j, x[j]);
+    }
+}
+
 // The base of an operand's row (b, h): element offset of its token 0.
 __device__ __forceinline__ int64_t row_base(const LinOperand& o, int64_t b, int h) {
     return b * o.s.b + (int64_t)(h / o.share) * o.s.h;

@@ -45,10 +45,16 @@ inline size_t linattn_states_bytes(const LinPlan& p, int64_t rows, int64_t DK, i
 // column blocks of the decay's gradient
 inline int linattn_tan_blocks(int64_t DV) { return (int)((DV + 63) / 64); }
 
-// row blocks whose partial sums of dweight and dbias the layer norm's gradient call keeps
+// Layer norm: rows up to this width are held in registers.
+constexpr int64_t kNormRegisterC = 8192;
+
+// Workgroups of the gradient call, each with a partial sum of dweight and dbias over its rows: enough to
+// fill the chip (two to four on each of 256 compute units, by their registers), no more than turns of
+// rows, since every one costs 8 C bytes written and read.
 inline int64_t layernorm_parts(int64_t rows, int64_t C) {
-    (void)C;
-    return rows < 256 ? rows : 256;
+    const int64_t per = C <= 128 ? 16 : C <= 2048 ? 4 : 1;   // rows a workgroup has in hand
+    const int64_t turns = (rows + per - 1) / per, most = C <= 2048 ? 512 : 768;
+    return turns < most ? turns : most;
 }
 
 }  // namespace lcv

@@ -11,6 +11,7 @@
 // left of it shows in the sum of the centred values and is taken out of mean and variance.
 #include "mixer_kernels.h"
 #include "mixer_io.h"
+#include "mixer_plan.h"
 
 namespace lcv {
 namespace {

@@ -1,6 +1,7 @@
 // linattn.hip -- linear attention with a decay for each head: prompts, gradients, single tokens.
 #include "mixer_kernels.h"
 #include "mixer_io.h"
+#include "mixer_plan.h"
 
 namespace lcv {
 namespace {

@@ -15,13 +15,12 @@
 //   O^T += S^T Q^T    S's accumulators (rows d = 4g + r, column n = x) are the left operand as they are
 //   S   += K^T V      both operands stand transposed to their rows in LDS: ds_read_b64_tr_b16 for 16-bit
 //                 types, four strided reads for fp32
-// The contraction order inside an operand is {16 t + 4 g + s, 16 (t + 1) + 4 g + s} for a step of 32
-// (16-bit) and {16 t + 4 g + s} for fp32, alike on both sides.  Every wave forms all of P (4 of about
-// 18 matrix steps per tile) rather than share it through LDS and a barrier.
+// Every wave forms all of P (12 of its 80 matrix products for a bf16 chunk at D = 128) rather than share it
+// through LDS and a barrier.
 //
 // Precision.  S, P and every sum are fp32.  For 16-bit types P and S are rounded to the type once as
 // operands, like the result itself.  What S adds up is not: gamma^.. V is split into three bf16 parts
-// (two where no state leaves the call, whose error is 2^-17) or two fp16 parts, so that the state keeps fp32's accuracy over any length.
+// (two where no state leaves the call: 2^-17) or two fp16 parts, so that the state keeps fp32's accuracy over any length.
 // fp16 operands that may pass its range (P, S, gamma^.. V) are scaled to it by a power of two, per query,
 // per 16 columns and per column.  gamma^c S is S + (gamma^c - 1) S, so that a decay near one does not lose by rounding
 // its power.
@@ -34,12 +33,19 @@ namespace {
 
 // ---- matrix-core operands -------------------------------------------------------------------
 
+// A tile in LDS is [rows][R groups of 16 bytes], no padding; logical group c of a row stands at c ^ f(row),
+// so that the 16 rows of a row read, and the rows of a transposed read, fall on all banks.  (Rows of less
+// than 256 bytes share a line of banks: f takes the row's place beyond it.)
+__device__ __forceinline__ constexpr int swizzle(int row, int R) {
+    const int s = R >= 16 ? row : R == 8 ? row >> 1 : row >> 2, h = R >= 16 ? 8 : R / 2;
+    const int top = R >= 16 ? s >> 3 : R == 8 ? s >> 2 : s >> 1;
+    return 2 * (s & (h - 1)) | (top & 1);
+}
+
 template <int IO> struct Mx {  // bf16, fp16
     using E = uint16_t;
     static constexpr int C = 32;        // tokens of a chunk
     static constexpr int TK = 2;        // 16-wide tiles of one contraction step
-    static constexpr int PADR = 8;      // row padding in LDS, elements: rows 4 banks apart (row reads)
-    static constexpr int PADT = 16;     // 8 banks apart (transposed reads)
     static constexpr int VEC = 8;       // elements of 16 bytes
     struct Frag { uint32_t w[4]; };
     static __device__ __forceinline__ f32x4 mma(const Frag& a, const Frag& b, f32x4 c) {
@@ -49,20 +55,36 @@ template <int IO> struct Mx {  // bf16, fp16
         else
             return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, av), __builtin_bit_cast(f16x8, bv), c, 0, 0, 0);
     }
-    // p: the lane's row + 4 g
-    static __device__ __forceinline__ Frag load_row(const E* p, int t) {
-        const uint2 lo = *(const uint2*)(p + 32 * t), hi = *(const uint2*)(p + 32 * t + 16);
-        return Frag{{lo.x, lo.y, hi.x, hi.y}};
+    // A state tile's row m is the contraction index of step t / 2, place 8 (m / 4) + 4 (t & 1) + m % 4: two
+    // tiles' accumulators are then 8 neighbours, the 16 bytes that a row read takes at once.
+    static __device__ __forceinline__ int state_row(int t, int g) { return 32 * (t >> 1) + 8 * g + 4 * (t & 1); }
+    // The lane's places in a tile: row x for row reads; for transposed reads (16 lanes read 4 rows of four
+    // 8-byte pieces, and each gets a column of 4) K's pieces stand 16 bytes apart, V's side by side.
+    // Step t is an exclusive or away.
+    struct At { int row, tr, col; };
+    static __device__ __forceinline__ At at(int g, int x, int R) {
+        const int r = 4 * g + (x >> 2), f = swizzle(r, R);
+        return At{x * R * 16 + (g ^ swizzle(x, R)) * 16, r * R * 16 + ((x & 3) ^ f) * 16,
+                  r * R * 16 + (((x & 3) >> 1) ^ f) * 16 + (x & 1) * 8};
     }
-    static __device__ __forceinline__ uint2 tr(const E* p) {
+    static __device__ __forceinline__ Frag load_row(const char* p, const At& l, int t) {
+        const uint4 w = *(const uint4*)(p + (l.row ^ (64 * t)));
+        return Frag{{w.x, w.y, w.z, w.w}};
+    }
+    static __device__ __forceinline__ uint2 tr(const char* p) {
         typedef short s16x4 __attribute__((__vector_size__(8)));
         typedef __attribute__((address_space(3))) s16x4* P;
         return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)p));
     }
-    // the lane's start in a tile [rows][stride] for transposed reads (16 lanes read 4 rows of 16)
-    static __device__ __forceinline__ int tr_start(int g, int x, int stride) { return (4 * g + (x >> 2)) * stride + (x & 3) * 4; }
-    static __device__ __forceinline__ Frag load_tr(const E* p, int stride, int j) {
-        const uint2 lo = tr(p + 32 * j * stride), hi = tr(p + (32 * j + 16) * stride);
+    // the state's tile t of K^T, and the 16 columns from 16 t of V, over the tokens of a step
+    static __device__ __forceinline__ Frag load_kt(const char* p, const At& l, int t, int R) {
+        const char* q = p + (l.tr ^ (64 * (t >> 1))) + 8 * (t & 1);
+        const uint2 lo = tr(q), hi = tr(q + 16 * R * 16);
+        return Frag{{lo.x, lo.y, hi.x, hi.y}};
+    }
+    static __device__ __forceinline__ Frag load_v(const char* p, const At& l, int t, int R) {
+        const char* q = p + (l.col ^ (32 * t));
+        const uint2 lo = tr(q), hi = tr(q + 16 * R * 16);
         return Frag{{lo.x, lo.y, hi.x, hi.y}};
     }
     static __device__ __forceinline__ Frag pack(const f32x4* t) {
@@ -83,18 +105,33 @@ template <int IO> struct Mx {  // bf16, fp16
 
 template <> struct Mx<CT_F32> {
     using E = float;
-    static constexpr int C = 32, TK = 1, PADR = 4, PADT = 4, VEC = 4;
+    static constexpr int C = 32, TK = 1, VEC = 4;
     struct Frag { f32x4 v; };
     static __device__ __forceinline__ f32x4 mma(const Frag& a, const Frag& b, f32x4 c) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[i], b.v[i], c, 0, 0, 0);
         return c;
     }
-    static __device__ __forceinline__ Frag load_row(const E* p, int t) { return Frag{*(const f32x4*)(p + 16 * t)}; }
-    static __device__ __forceinline__ int tr_start(int g, int x, int stride) { return 4 * g * stride + x; }
-    static __device__ __forceinline__ Frag load_tr(const E* p, int stride, int j) {
-        const E* q = p + 16 * j * stride;
-        return Frag{{q[0], q[stride], q[2 * stride], q[3 * stride]}};
+    static __device__ __forceinline__ int state_row(int t, int g) { return 16 * t + 4 * g; }
+    struct At { int row, tr[4]; };
+    static __device__ __forceinline__ At at(int g, int x, int R) {
+        At l;
+        l.row = x * R * 16 + (g ^ swizzle(x, R)) * 16;
+        for (int s = 0; s < 4; ++s) {
+            const int r = 4 * g + s;
+            l.tr[s] = r * R * 16 + ((x >> 2) ^ swizzle(r, R)) * 16 + (x & 3) * 4;
+        }
+        return l;
+    }
+    static __device__ __forceinline__ Frag load_row(const char* p, const At& l, int t) {
+        return Frag{*(const f32x4*)(p + (l.row ^ (64 * t)))};
+    }
+    static __device__ __forceinline__ Frag load_v(const char* p, const At& l, int t, int R) { return load_kt(p, l, t, R); }
+    static __device__ __forceinline__ Frag load_kt(const char* p, const At& l, int t, int R) {
+        Frag f;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) f.v[s] = *(const float*)(p + (l.tr[s] ^ (64 * t)));
+        return f;
     }
     static __device__ __forceinline__ Frag pack(const f32x4* t) { return Frag{t[0]}; }
     static __device__ __forceinline__ void unpack(const Frag& f, float* v) {
@@ -103,6 +140,31 @@ template <> struct Mx<CT_F32> {
     }
     static __device__ __forceinline__ Frag pack(const float* v) { return Frag{{v[0], v[1], v[2], v[3]}}; }
 };
+
+// Global memory from a scalar address on, by 32-bit offsets of the lanes: raw buffer accesses, whose address
+// takes no vector arithmetic.  Every offset lies within the buffer's 2^32 - 1 bytes by the host's limit on
+// token strides.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const char* base) {
+    return __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, 0xffffffff, 0x00020000);
+}
+// 64 lanes' 16 bytes each to 1 KB of LDS in lane order, without registers for the data
+__device__ __forceinline__ void to_lds(const char* base, uint32_t off, char* dst) {
+    typedef __attribute__((address_space(3))) void* L;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer_at(base), (L)dst, 16, off, 0, 0, 0);
+}
+// Barrier of a workgroup whose waves have waited for what they wrote: a fence would also wait for the
+// loads to LDS of the chunks ahead.
+__device__ __forceinline__ void barrier_only() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+// at most `vm` vector memory operations outstanding, no LDS operation
+template <int vm> __device__ __forceinline__ void wait_for_all_but() {
+    static_assert(vm < 64, "six bits");
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((vm & 15) | ((vm >> 4) << 14) | (7 << 4));
+}
 
 // 2^(14 - e) and its inverse for a magnitude of binade e: brings the magnitude below 2^15
 __device__ __forceinline__ float to_f16_range(float m, float* back) {
@@ -125,30 +187,41 @@ __device__ __forceinline__ float max_over_wave(float m) {
 
 // ---- one segment of one (b, h), 64 NW columns -------------------------------------------------
 
-// STATE: only the state that the segment adds up from zero, for the segments after it.
-template <int IO, int KT, int NW, bool STATE>
-__global__ void __launch_bounds__(256, KT > 8 ? 1 : 2) linattn_chunk_kernel(LinJob a) {
+// STATE: only the state that the segment adds up from zero, for the segments after it.  WIDE: O in fp32.
+// EXACT: the state's sums to fp32's accuracy.
+template <int IO, int KT, int NW, bool STATE, bool WIDE, bool EXACT>
+__global__ void __launch_bounds__(256, KT > 8 ? 1 : NW == 1 && IO != CT_F32 ? 3 : 2) linattn_chunk_kernel(LinJob a) {
     using M = Mx<IO>;
     using E = typename M::E;
     using Frag = typename M::Frag;
     constexpr int C = M::C, TK = M::TK, CT = C / 16, CJ = CT / TK, KS = KT / TK, ES = TK * 4;
-    constexpr int DKP = KT * 16, DVB = 64 * NW, RS = DKP + M::PADR, VS = DVB + M::PADT;
-    constexpr int VEC = M::VEC, KV_ROW = DKP / VEC, V_ROW = DVB / VEC;   // 16-byte groups of a row
-    constexpr int NK = (C * KV_ROW + 255) / 256, NV = C * V_ROW / 256;   // groups per thread
-    static_assert(NV >= 1 && C * V_ROW % 256 == 0 && (NK == 1 || C * KV_ROW % 256 == 0), "whole passes");
-    __shared__ __attribute__((aligned(16))) E Qs[STATE ? 8 : C * RS];
-    __shared__ __attribute__((aligned(16))) E Ks[C * RS];
-    __shared__ __attribute__((aligned(16))) E Vs[C * VS];
+    constexpr int DKP = KT * 16, DVB = 64 * NW, VEC = M::VEC;
+    constexpr int RK = DKP / VEC, RV = DVB / VEC;               // 16-byte groups of a row
+    constexpr int QB = STATE ? 0 : C * RK * 16, KB = C * RK * 16, STAGE = QB + KB + C * RV * 16;
+    constexpr int NK = C * RK / 256, NV = C * RV / 256;         // loads of a chunk: rounds of 4 waves x 64 lanes
+    constexpr bool KHALF = NK == 0;                             // a narrow tile takes two waves
+    constexpr int NKR = KHALF ? 1 : NK, LOADS = (STATE ? 1 : 2) * NKR + NV, STORES = STATE ? 0 : CT * NW;   // of a wave
+    static_assert(NV >= 1 && (NK >= 1 || C * RK == 128), "rounds of whole waves");
+    // chunks in LDS: one in hand, and two on their way where a compute unit then still holds the workgroups
+    // that its registers allow (NW = 1: three, which hide each other's loads)
+    constexpr int STAGES = 3 * STAGE <= (KT > 8 ? 160 : NW == 1 ? 53 : 80) * 1024 ? 3 : 2;
+    __shared__ __attribute__((aligned(16))) char lds0[STAGE], lds1[STAGE];
+    char* lds2 = nullptr;
+    if constexpr (STAGES == 3) {
+        __shared__ __attribute__((aligned(16))) char third[STAGE];
+        lds2 = third;
+    }
 
-    const LinRole& r = a.r[blockIdx.y];
-    const int ncb = (r.DV + DVB - 1) / DVB;
-    int64_t id = blockIdx.x;
-    const int cb = (int)(id % a.ncb);
-    id /= a.ncb;
-    if (cb >= ncb) return;
-    const int nseg = STATE ? a.nseg - 1 : a.nseg;
-    const int64_t bh = id / nseg;
-    const int seg = (int)(id - bh * nseg);
+    // Workgroups that read the same tokens (a segment's roles and column blocks) go to one XCD, whose L2
+    // they share: consecutive ids go round the eight XCDs.
+    const int per = a.nroles * a.ncb, nseg = STATE ? a.nseg - 1 : a.nseg;
+    const int64_t slot = blockIdx.x / 8, group = slot / per * 8 + blockIdx.x % 8;
+    if (group >= a.B * a.H * nseg) return;
+    const int member = (int)(slot % per), cb = member % a.ncb;
+    const LinRole r = a.r[member / a.ncb];       // a copy: its fields stay in scalar registers
+    if (cb * DVB >= r.DV) return;
+    const int64_t bh = group / nseg;
+    const int seg = (int)(group - bh * nseg);
     const int64_t b = bh / a.H;
     const int h = (int)(bh - b * a.H);
     const int64_t len = row_len(a.lengths, b, a.N);
@@ -156,14 +229,14 @@ __global__ void __launch_bounds__(256, KT > 8 ? 1 : 2) linattn_chunk_kernel(LinJ
     const int64_t end = beg + a.seg_len < len ? beg + a.seg_len : len;
     if (STATE && beg + a.seg_len >= len) return;   // no segment follows
 
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, g = lane >> 4, x = lane & 15;
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, g = lane >> 4, x = lane & 15;
     const int wcol = cb * DVB + wave * 16 * NW;             // the wave's first column
     const int64_t ob = b * r.o.b + (int64_t)h * r.o.h;
-    const int osize = r.o_f32 ? 4 : (int)sizeof(E);
+    constexpr int osize = WIDE ? 4 : (int)sizeof(E);
 
     if constexpr (!STATE) {
         // tokens past the row's length: zeros (16-byte groups of this workgroup's columns)
-        const int per = 16 / osize;
+        constexpr int per = 16 / osize;
         const int groups = ((r.DV - cb * DVB < DVB ? r.DV - cb * DVB : DVB)) / per;
         int64_t t0 = beg > len ? beg : len, t1 = beg + a.seg_len < a.N ? beg + a.seg_len : a.N;
         if (r.O && t1 > t0)
@@ -200,7 +273,7 @@ __global__ void __launch_bounds__(256, KT > 8 ? 1 : 2) linattn_chunk_kernel(LinJ
         for (int t = 0; t < KT; ++t)
 #pragma unroll
             for (int n = 0; n < NW; ++n) {
-                const int d = 16 * t + 4 * g, c = wcol + 16 * n + x;
+                const int d = M::state_row(t, g), c = wcol + 16 * n + x;
                 f32x4 v = {0.f, 0.f, 0.f, 0.f};
                 if (s && d < r.DK && c < r.DV) {
                     if (srow == 1) {
@@ -214,68 +287,90 @@ __global__ void __launch_bounds__(256, KT > 8 ? 1 : 2) linattn_chunk_kernel(LinJ
             }
     }
 
-    // ---- global loads of a chunk, one ahead of the arithmetic.  Each thread's groups keep their row in
-    // the chunk and their columns, so their pointers only move on.
-    const auto first = [&](const LinOperand& o, int row, int c) LCV_INLINE {
-        const int64_t p = beg + row;
-        return (const E*)o.p + row_base(o, b, h) + (r.reverse ? len - 1 - p : p) * o.s.n + c;
+    // ---- loads of a chunk straight to LDS, two chunks ahead of the arithmetic.  Round i of a tile fills
+    // 16-byte slots 256 i + 64 wave + lane; a slot's row and columns stay, so its pointer only moves on.
+    // Its address is a scalar that moves on, at the chunk's lowest token, plus the lane's own offset.
+    const int64_t low = r.reverse ? len - beg - C : beg, dir = r.reverse ? -(int64_t)C : C;
+    const auto start = [&](const LinOperand& o) LCV_INLINE { return (const char*)o.p + (row_base(o, b, h) + low * o.s.n) * (int)sizeof(E); };
+    const auto offset = [&](const LinOperand& o, int row, int c) LCV_INLINE {
+        return (uint32_t)(r.reverse ? C - 1 - row : row) * (uint32_t)(o.s.n * (int)sizeof(E)) + (uint32_t)(c * (int)sizeof(E));
     };
-    const int64_t dir = r.reverse ? -(int64_t)C : C;
-    const E *pq[STATE ? 1 : NK], *pk[NK], *pv[NV];
+    const char *pq = STATE ? nullptr : start(r.Q), *pk = start(r.K), *pv = start(r.V);
+    const int64_t dq = dir * r.Q.s.n * (int)sizeof(E), dk = dir * r.K.s.n * (int)sizeof(E), dv = dir * r.V.s.n * (int)sizeof(E);
+    uint32_t oq[NKR], ok[NKR], ov[NV];
+    bool kon[NKR], von[NV];
+    const bool kin = !KHALF || wave < 2;
 #pragma unroll
-    for (int i = 0; i < NK; ++i) {
-        const int e = tid + 256 * i;
-        pk[i] = first(r.K, e / KV_ROW, (e % KV_ROW) * VEC);
-        if constexpr (!STATE) pq[i] = first(r.Q, e / KV_ROW, (e % KV_ROW) * VEC);
+    for (int i = 0; i < NKR; ++i) {
+        const int s = 256 * i + tid, row = s / RK % C, c = ((s % RK) ^ swizzle(row, RK)) * VEC;
+        kon[i] = kin && c < r.DK;
+        ok[i] = offset(r.K, row, c);
+        oq[i] = STATE ? 0 : offset(r.Q, row, c);
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int e = tid + 256 * i;
-        pv[i] = first(r.V, e / V_ROW, cb * DVB + (e % V_ROW) * VEC);
+        const int s = 256 * i + tid, row = s / RV, c = cb * DVB + ((s % RV) ^ swizzle(row, RV)) * VEC;
+        von[i] = c < r.DV;
+        ov[i] = offset(r.V, row, c);
     }
-    const bool kin = C * KV_ROW >= 256 || tid < C * KV_ROW;      // a narrow chunk leaves threads without a group
-    const bool kon = kin && tid % KV_ROW * VEC < r.DK, von = cb * DVB + tid % V_ROW * VEC < r.DV;  // 256 is a multiple of both
-    uint4 rq[STATE ? 1 : NK], rk[NK], rv[NV];
-    const auto fetch = [&](int64_t left) LCV_INLINE {
+    // whole chunks of whole tiles take every load of every wave: only then is their number known
+    const bool whole = !KHALF && r.DK == DKP && cb * DVB + DVB <= r.DV;
+    if (!whole) {       // columns that the operands do not have stay zero
+        for (int i = tid; i < STAGE / 16; i += 256) {
+            *(uint4*)(lds0 + 16 * i) = make_uint4(0, 0, 0, 0);
+            *(uint4*)(lds1 + 16 * i) = make_uint4(0, 0, 0, 0);
+            if constexpr (STAGES == 3) *(uint4*)(lds2 + 16 * i) = make_uint4(0, 0, 0, 0);
+        }
+        __syncthreads();
+    }
+    // load i of a whole chunk's LOADS
+    const auto piece = [&](auto i, char* to) LCV_INLINE {
+        constexpr int I = i.value, Q = STATE ? 0 : NKR;
+        char* const t = to + 1024 * wave;
+        if constexpr (I < Q) to_lds(pq, oq[I], t + 4096 * I);
+        else if constexpr (I < Q + NKR) to_lds(pk, ok[I - Q], t + QB + 4096 * (I - Q));
+        else if constexpr (I < LOADS) to_lds(pv, ov[I - Q - NKR], t + QB + KB + 4096 * (I - Q - NKR));
+    };
+    const auto move_on = [&]() LCV_INLINE {
+        if constexpr (!STATE) pq += dq;
+        pk += dk;
+        pv += dv;
+    };
+    const auto fetch = [&](char* to, int64_t left) LCV_INLINE {
+        if (whole && left >= C) {
+            static_for<0, LOADS>([&](auto i) LCV_INLINE { piece(i, to); });
+        } else {
+            // columns that there are not, and zeros for the tokens that a last chunk lacks
+            char* const t = to + 1024 * wave;
 #pragma unroll
-        for (int i = 0; i < NK; ++i) {
-            const bool on = kon && (tid + 256 * i) / KV_ROW < left;
-            rk[i] = on ? *(const uint4*)pk[i] : make_uint4(0, 0, 0, 0);
-            pk[i] += dir * r.K.s.n;
-            if constexpr (!STATE) {
-                rq[i] = on ? *(const uint4*)pq[i] : make_uint4(0, 0, 0, 0);
-                pq[i] += dir * r.Q.s.n;
+            for (int i = 0; i < NKR; ++i) {
+                const bool in = (256 * i + tid) / RK % C < left;
+                if (kon[i] && in) {
+                    if constexpr (!STATE) to_lds(pq, oq[i], t + 4096 * i);
+                    to_lds(pk, ok[i], t + QB + 4096 * i);
+                }
+                if (kin && !in) {
+                    if constexpr (!STATE) *(uint4*)(t + 4096 * i + 16 * lane) = make_uint4(0, 0, 0, 0);
+                    *(uint4*)(t + QB + 4096 * i + 16 * lane) = make_uint4(0, 0, 0, 0);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const bool in = (256 * i + tid) / RV < left;
+                if (von[i] && in) to_lds(pv, ov[i], t + QB + KB + 4096 * i);
+                if (!in) *(uint4*)(t + QB + KB + 4096 * i + 16 * lane) = make_uint4(0, 0, 0, 0);
             }
         }
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const bool on = von && (tid + 256 * i) / V_ROW < left;
-            rv[i] = on ? *(const uint4*)pv[i] : make_uint4(0, 0, 0, 0);
-            pv[i] += dir * r.V.s.n;
-        }
-    };
-    const auto stage = [&]() LCV_INLINE {
-#pragma unroll
-        for (int i = 0; i < NK; ++i) {
-            const int e = tid + 256 * i, row = e / KV_ROW, c = (e % KV_ROW) * VEC;
-            if (!kin) continue;
-            *(uint4*)(Ks + row * RS + c) = rk[i];
-            if constexpr (!STATE) *(uint4*)(Qs + row * RS + c) = rq[i];
-        }
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int e = tid + 256 * i, row = e / V_ROW, c = (e % V_ROW) * VEC;
-            *(uint4*)(Vs + row * VS + c) = rv[i];
-        }
+        move_on();
     };
 
-    const E* qrow = Qs + (STATE ? 0 : x * RS + 4 * g);
-    const E* krow = Ks + x * RS + 4 * g;
-    const E* ktr = Ks + M::tr_start(g, x, RS);
-    const E* vtr = Vs + M::tr_start(g, x, VS) + wave * 16 * NW;
-    // the lane's place in the output: token x of the chunk, the first of its four columns
-    const int64_t odir = r.reverse ? -r.o.n : r.o.n;
-    int64_t oat = STATE ? 0 : ob + (r.reverse ? len - 1 - beg : beg) * r.o.n + x * odir + wcol + 4 * g;
+    const typename M::At lk = M::at(g, x, RK), lv = M::at(g, x, RV);
+    // the output likewise: lane x's token, the first of its four columns; token tiles of 16 and column tiles
+    // are steps of the scalar
+    constexpr int osz = WIDE || IO == CT_F32 ? 4 : 2;
+    char* po = STATE ? nullptr : (char*)r.O + (ob + low * r.o.n) * osz;
+    const int64_t d_o = dir * r.o.n * osz, o16 = 16 * r.o.n * osz;
+    const uint32_t oo = (uint32_t)(r.reverse ? 15 - x : x) * (uint32_t)(r.o.n * osz) + (uint32_t)((wcol + 4 * g) * osz);
 
     float em1 = 0.f;
     const auto weigh = [&](int c) LCV_INLINE {
@@ -290,116 +385,45 @@ __global__ void __launch_bounds__(256, KT > 8 ? 1 : 2) linattn_chunk_kernel(LinJ
             }
     };
 
-    const auto chunk = [&](int c) LCV_INLINE {
+    f32x4 acc[CT][NW];
+    const auto put = [&](int it, int n) LCV_INLINE {
+        const __amdgpu_buffer_rsrc_t o = buffer_at(po + (r.reverse ? CT - 1 - it : it) * o16 + 16 * n * osz);
+        const f32x4 y = acc[it][n];
+        if constexpr (osz == 4) {
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, y), o, oo, 0, 0);
+        } else {
+            typedef uint32_t u32x2 __attribute__((__vector_size__(8)));
+            const u32x2 w = {pack2<IO>(y[0], y[1]), pack2<IO>(y[2], y[3])};
+            __builtin_amdgcn_raw_buffer_store_b64(w, o, oo, 0, 0);
+        }
+    };
+    const auto emit = [&](int c) LCV_INLINE {
+        if constexpr (!STATE) {
+#pragma unroll
+            for (int it = 0; it < CT; ++it)
+#pragma unroll
+                for (int n = 0; n < NW; ++n)
+                    if (16 * it + x < c && wcol + 16 * n + 4 * g < r.DV) put(it, n);
+            po += d_o;
+        }
+    };
+
+    // One chunk.  FULL: a whole chunk with a whole one to fetch; its loads and its stores stand between the
+    // products (issued in a row they hold the wave up, some 180 cycles a load).
+    const auto chunk = [&](auto full, const char* L, char* then) LCV_INLINE {
+        constexpr bool FULL = full.value;
+        const char *const Lk = L + QB, *const Lv = L + QB + KB;
         Frag vf[CJ][NW];
 #pragma unroll
         for (int j = 0; j < CJ; ++j)
 #pragma unroll
-            for (int n = 0; n < NW; ++n) vf[j][n] = M::load_tr(vtr + 16 * n, VS, j);
+            for (int n = 0; n < NW; ++n) vf[j][n] = M::load_v(Lv + j * TK * 16 * RV * 16, lv, wave * NW + n, RV);
 
-        if constexpr (!STATE) {
-            Frag qf[CT][KS], kf[CT][KS], sf[KS][NW];
-#pragma unroll
-            for (int it = 0; it < CT; ++it)
-#pragma unroll
-                for (int t = 0; t < KS; ++t) {
-                    qf[it][t] = M::load_row(qrow + 16 * it * RS, t);
-                    kf[it][t] = M::load_row(krow + 16 * it * RS, t);
-                }
-            float sback[NW];
-#pragma unroll
-            for (int n = 0; n < NW; ++n) {
-                float to = 1.f;
-                sback[n] = 1.f;
-                if constexpr (IO == CT_F16) {
-                    float m = 0.f;
-#pragma unroll
-                    for (int t = 0; t < KT; ++t)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) m = fmaxf(m, fabsf(S[t][n][i]));
-                    to = to_f16_range(max_over_wave(m), &sback[n]);
-                }
-#pragma unroll
-                for (int t = 0; t < KS; ++t) {
-                    f32x4 u[TK];
-#pragma unroll
-                    for (int k = 0; k < TK; ++k) u[k] = IO == CT_F16 ? S[TK * t + k][n] * to : S[TK * t + k][n];
-                    sf[t][n] = M::pack(u);
-                }
-            }
-            f32x4 acc[CT][NW], p[CT][CT];
-#pragma unroll
-            for (int it = 0; it < CT; ++it) {
-#pragma unroll
-                for (int n = 0; n < NW; ++n) acc[it][n] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int jt = 0; jt < CT; ++jt) p[it][jt] = f32x4{0.f, 0.f, 0.f, 0.f};
-            }
-#pragma unroll
-            for (int t = 0; t < KS; ++t)
-#pragma unroll
-                for (int it = 0; it < CT; ++it) {
-#pragma unroll
-                    for (int jt = 0; jt <= it; ++jt) p[it][jt] = M::mma(kf[jt][t], qf[it][t], p[it][jt]);
-#pragma unroll
-                    for (int n = 0; n < NW; ++n) acc[it][n] = M::mma(sf[t][n], qf[it][t], acc[it][n]);
-                }
-#pragma unroll
-            for (int it = 0; it < CT; ++it) {
-#pragma unroll
-                for (int n = 0; n < NW; ++n) acc[it][n] *= IO == CT_F16 ? wI[it] * sback[n] : wI[it];
-#pragma unroll
-                for (int jt = 0; jt <= it; ++jt)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)   // later tokens are left out, not weighed with 0: they may not be finite
-                        p[it][jt][i] = jt < it || x >= 4 * g + i ? p[it][jt][i] * wP[it - jt][i] : 0.f;
-                if constexpr (IO == CT_F16) {
-                    float m = 0.f, back;
-#pragma unroll
-                    for (int jt = 0; jt <= it; ++jt)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) m = fmaxf(m, fabsf(p[it][jt][i]));
-                    const float to = to_f16_range(max_over_g(m), &back);
-#pragma unroll
-                    for (int jt = 0; jt <= it; ++jt) p[it][jt] *= to;
-#pragma unroll
-                    for (int n = 0; n < NW; ++n) {
-                        f32x4 o = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                        for (int j = 0; j <= it / TK; ++j) o = M::mma(vf[j][n], M::pack(p[it] + TK * j), o);
-                        acc[it][n] += o * back;
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j <= it / TK; ++j) {
-                        const Frag pf = M::pack(p[it] + TK * j);
-#pragma unroll
-                        for (int n = 0; n < NW; ++n) acc[it][n] = M::mma(vf[j][n], pf, acc[it][n]);
-                    }
-                }
-            }
-#pragma unroll
-            for (int it = 0; it < CT; ++it) {
-                if (16 * it + x >= c) continue;
-#pragma unroll
-                for (int n = 0; n < NW; ++n) {
-                    if (wcol + 16 * n + 4 * g >= r.DV) continue;
-                    const int64_t o = oat + 16 * it * odir + 16 * n;
-                    const f32x4 y = acc[it][n];
-                    if (IO == CT_F32 || r.o_f32) *(f32x4*)((float*)r.O + o) = y;
-                    else *(uint2*)((uint16_t*)r.O + o) = make_uint2(pack2<IO == CT_F32 ? CT_BF16 : IO>(y[0], y[1]),
-                                                                    pack2<IO == CT_F32 ? CT_BF16 : IO>(y[2], y[3]));
-                }
-            }
-            oat += C * odir;
-        }
-
-        // ---- the state moves on
-        constexpr int PARTS = IO == CT_F32 ? 1 : IO == CT_F16 ? 2 : 3;
+        // gamma^.. V in parts that add up to its fp32 value
+        constexpr int PARTS = IO == CT_F32 ? 1 : IO == CT_F16 || !EXACT ? 2 : 3;
         Frag u[PARTS][CJ][NW];
         float back[NW];
-#pragma unroll
-        for (int n = 0; n < NW; ++n) {
+        const auto split = [&](int n) LCV_INLINE {
             float v[CJ][ES], m = 0.f;
 #pragma unroll
             for (int j = 0; j < CJ; ++j) {
@@ -411,11 +435,11 @@ __global__ void __launch_bounds__(256, KT > 8 ? 1 : 2) linattn_chunk_kernel(LinJ
                 }
             }
             if constexpr (IO == CT_F16) {
-                const float to = to_f16_range(max_over_g(m), &back[n]);
+                const float up = to_f16_range(max_over_g(m), &back[n]);
 #pragma unroll
                 for (int j = 0; j < CJ; ++j)
 #pragma unroll
-                    for (int s = 0; s < ES; ++s) v[j][s] *= to;
+                    for (int s = 0; s < ES; ++s) v[j][s] *= up;
             }
 #pragma unroll
             for (int j = 0; j < CJ; ++j)
@@ -429,15 +453,101 @@ __global__ void __launch_bounds__(256, KT > 8 ? 1 : 2) linattn_chunk_kernel(LinJ
                         for (int s = 0; s < ES; ++s) v[j][s] -= q[s];
                     }
                 }
+        };
+
+        if constexpr (!STATE) {
+            float to[NW], sback[NW];
+#pragma unroll
+            for (int n = 0; n < NW; ++n) {
+                to[n] = sback[n] = 1.f;
+                if constexpr (IO == CT_F16) {
+                    float m = 0.f;
+#pragma unroll
+                    for (int t = 0; t < KT; ++t)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) m = fmaxf(m, fabsf(S[t][n][i]));
+                    to[n] = to_f16_range(max_over_wave(m), &sback[n]);
+                }
+            }
+            f32x4 p[CT][CT];
+#pragma unroll
+            for (int it = 0; it < CT; ++it) {
+#pragma unroll
+                for (int n = 0; n < NW; ++n) acc[it][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int jt = 0; jt < CT; ++jt) p[it][jt] = f32x4{0.f, 0.f, 0.f, 0.f};
+            }
+            static_for<0, KS>([&](auto ti) LCV_INLINE {
+                constexpr int t = ti.value;
+                Frag qf[CT], kf[CT], sf[NW];
+#pragma unroll
+                for (int it = 0; it < CT; ++it) {
+                    qf[it] = M::load_row(L + 16 * it * RK * 16, lk, t);
+                    kf[it] = M::load_row(Lk + 16 * it * RK * 16, lk, t);
+                }
+#pragma unroll
+                for (int n = 0; n < NW; ++n) {
+                    f32x4 w[TK];
+#pragma unroll
+                    for (int k = 0; k < TK; ++k) w[k] = IO == CT_F16 ? S[TK * t + k][n] * to[n] : S[TK * t + k][n];
+                    sf[n] = M::pack(w);
+                }
+                if constexpr (FULL) static_for<t * LOADS / KS, (t + 1) * LOADS / KS>([&](auto i) LCV_INLINE { piece(i, then); });
+#pragma unroll
+                for (int it = 0; it < CT; ++it) {
+#pragma unroll
+                    for (int jt = 0; jt <= it; ++jt) p[it][jt] = M::mma(kf[jt], qf[it], p[it][jt]);
+#pragma unroll
+                    for (int n = 0; n < NW; ++n) acc[it][n] = M::mma(sf[n], qf[it], acc[it][n]);
+                }
+            });
+#pragma unroll
+            for (int it = 0; it < CT; ++it) {
+#pragma unroll
+                for (int n = 0; n < NW; ++n) acc[it][n] *= IO == CT_F16 ? wI[it] * sback[n] : wI[it];
+#pragma unroll
+                for (int jt = 0; jt <= it; ++jt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)   // later tokens are left out, not weighed with 0: they may not be finite
+                        p[it][jt][i] = jt < it || x >= 4 * g + i ? p[it][jt][i] * wP[it - jt][i] : 0.f;
+                if constexpr (IO == CT_F16) {
+                    float m = 0.f, pback;
+#pragma unroll
+                    for (int jt = 0; jt <= it; ++jt)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) m = fmaxf(m, fabsf(p[it][jt][i]));
+                    const float up = to_f16_range(max_over_g(m), &pback);
+#pragma unroll
+                    for (int jt = 0; jt <= it; ++jt) p[it][jt] *= up;
+#pragma unroll
+                    for (int n = 0; n < NW; ++n) {
+                        f32x4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int j = 0; j <= it / TK; ++j) o = M::mma(vf[j][n], M::pack(p[it] + TK * j), o);
+                        acc[it][n] += o * pback;
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j <= it / TK; ++j) {
+                        const Frag pf = M::pack(p[it] + TK * j);
+#pragma unroll
+                        for (int n = 0; n < NW; ++n) acc[it][n] = M::mma(vf[j][n], pf, acc[it][n]);
+                    }
+                }
+            }
         }
 #pragma unroll
-        for (int t = 0; t < KT; ++t) {
+        for (int n = 0; n < NW; ++n) split(n);
+
+        // ---- the state moves on
+        static_for<0, KT>([&](auto ti) LCV_INLINE {
+            constexpr int t = ti.value;
             f32x4 d[NW];
 #pragma unroll
             for (int n = 0; n < NW; ++n) d[n] = IO == CT_F16 ? f32x4{0.f, 0.f, 0.f, 0.f} : S[t][n] + S[t][n] * em1;
 #pragma unroll
             for (int j = 0; j < CJ; ++j) {
-                const Frag kt = M::load_tr(ktr + 16 * t, RS, j);
+                const Frag kt = M::load_kt(Lk + j * TK * 16 * RK * 16, lk, t, RK);
 #pragma unroll
                 for (int k = 0; k < PARTS; ++k)
 #pragma unroll
@@ -448,28 +558,68 @@ __global__ void __launch_bounds__(256, KT > 8 ? 1 : 2) linattn_chunk_kernel(LinJ
                 if constexpr (IO == CT_F16) S[t][n] += S[t][n] * em1 + d[n] * back[n];
                 else S[t][n] = d[n];
             }
+            if constexpr (FULL && STATE) {
+                static_for<t * LOADS / KT, (t + 1) * LOADS / KT>([&](auto i) LCV_INLINE { piece(i, then); });
+            } else if constexpr (FULL) {
+                static_for<t * STORES / KT, (t + 1) * STORES / KT>([&](auto i) LCV_INLINE { put(i.value / NW, i.value % NW); });
+            }
+        });
+        if constexpr (FULL) {
+            move_on();
+            if constexpr (!STATE) po += d_o;
         }
     };
 
-    if (beg < end) {
-        fetch(end - beg);
-        weigh(C);
+    // ---- the chunks.  A chunk's loads have to be in when it begins: of what a wave has issued since, the
+    // next chunk's loads and the last chunk's stores may be outstanding.
+    int64_t left = end - beg;                  // tokens from the chunk in hand on
+    if (left > 0) {
+        weigh(left < C ? (int)left : C);
+        fetch(lds0, left);
+        if (STAGES == 3 && left > C) fetch(lds1, left - C);
     }
-    int64_t at = beg;
-    for (; at + C <= end; at += C) {
-        __syncthreads();
-        stage();
-        __syncthreads();
-        if (at + C < end) fetch(end - at - C);
-        chunk(C);
+    // STAGES chunks a turn, each stage by its own name: then the compiler knows which loads a read waits for.
+    // What may be outstanding is, with three stages, the next chunk's loads and the last one's stores, with two
+    // the last one's stores.
+    constexpr int LAST = STAGES == 3 ? 5 : 3;
+    if (whole && left >= LAST * C) {
+        std::integral_constant<bool, true> full;
+        wait_for_all_but<STAGES == 3 ? LOADS : 0>();
+        const auto turn = [&](char* now, char* then) LCV_INLINE {
+            wait_for_all_but<STAGES == 3 ? LOADS + STORES : STORES>();
+            barrier_only();
+            chunk(full, now, then);
+        };
+        do {
+            if constexpr (STAGES == 3) {
+                turn(lds0, lds2);
+                turn(lds1, lds0);
+                turn(lds2, lds1);
+            } else {
+                turn(lds0, lds1);
+                turn(lds1, lds0);
+            }
+            left -= STAGES * C;
+        } while (left >= LAST * C);
     }
-    if (at < end) {
-        const int c = (int)(end - at);
-        __syncthreads();
-        stage();
-        weigh(c);
-        __syncthreads();
-        chunk(c);
+    // the last chunks, and calls whose operands leave columns free
+    for (int t = 0; left > 0; left -= C) {
+        char *now = lds0, *then = lds1;
+        if constexpr (STAGES == 3) {
+            if (t == 0) then = lds2;
+            if (t == 1) { now = lds1; then = lds0; }
+            if (t == 2) now = lds2;
+        } else if (t == 1) {
+            now = lds1;
+            then = lds0;
+        }
+        wait_for_all_but<0>();
+        barrier_only();
+        if (left > (STAGES - 1) * C) fetch(then, left - (STAGES - 1) * C);
+        if (left < C && end - beg > C) weigh((int)left);
+        chunk(std::integral_constant<bool, false>{}, now, nullptr);
+        emit(left < C ? (int)left : C);
+        t = t + 1 == STAGES ? 0 : t + 1;
     }
 
     // ---- the state that leaves
@@ -487,7 +637,7 @@ __global__ void __launch_bounds__(256, KT > 8 ? 1 : 2) linattn_chunk_kernel(LinJ
         for (int t = 0; t < KT; ++t)
 #pragma unroll
             for (int n = 0; n < NW; ++n) {
-                const int d = 16 * t + 4 * g, c = wcol + 16 * n + x;
+                const int d = M::state_row(t, g), c = wcol + 16 * n + x;
                 if (d >= r.DK || c >= r.DV) continue;
                 if (srow == 1) {
                     *(f32x4*)(s + (int64_t)c * scol + d) = S[t][n];
@@ -499,18 +649,27 @@ __global__ void __launch_bounds__(256, KT > 8 ? 1 : 2) linattn_chunk_kernel(LinJ
     }
 }
 
-template <int IO, int KT, int NW>
-hipError_t launch_chunk(const LinJob& a, hipStream_t stream) {
+template <int IO, int KT, int NW, bool WIDE, bool EXACT>
+hipError_t launch_chunk_as(const LinJob& a, hipStream_t stream) {
     const int64_t rows = a.B * a.H;
+    const auto grid = [&](int64_t groups) { return (unsigned)((groups + 7) / 8 * 8 * a.nroles * a.ncb); };
     if (a.nseg > 1) {
-        linattn_chunk_kernel<IO, KT, NW, true><<<dim3((unsigned)(rows * (a.nseg - 1) * a.ncb), a.nroles), 256, 0, stream>>>(a);
+        linattn_chunk_kernel<IO, KT, NW, true, false, EXACT><<<grid(rows * (a.nseg - 1)), 256, 0, stream>>>(a);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
         e = launch_linattn_join(a, stream);
         if (e != hipSuccess) return e;
     }
-    linattn_chunk_kernel<IO, KT, NW, false><<<dim3((unsigned)(rows * a.nseg * a.ncb), a.nroles), 256, 0, stream>>>(a);
+    linattn_chunk_kernel<IO, KT, NW, false, WIDE, EXACT><<<grid(rows * a.nseg), 256, 0, stream>>>(a);
     return hipGetLastError();
+}
+
+template <int IO, int KT, int NW>
+hipError_t launch_chunk(const LinJob& a, hipStream_t stream) {
+    // fp32 is wide as it is, and only bf16 has a third part to leave out
+    constexpr bool W = IO != CT_F32, X = IO == CT_BF16;
+    if (a.exact || !X) return W && a.wide ? launch_chunk_as<IO, KT, NW, W, true>(a, stream) : launch_chunk_as<IO, KT, NW, false, true>(a, stream);
+    return W && a.wide ? launch_chunk_as<IO, KT, NW, W, !X>(a, stream) : launch_chunk_as<IO, KT, NW, false, !X>(a, stream);
 }
 
 template <int IO>

@@ -6,6 +6,7 @@
 
 #include "api_checks.h"
 #include "mixer_kernels.h"
+#include "mixer_plan.h"
 
 using namespace lcv;
 
@@ -97,6 +98,14 @@ bool linattn_dims_ok(int64_t B, int64_t H, int64_t G, int64_t N, int64_t Dk, int
     return mul_ok(B, H, &rows) && rows < ((int64_t)1 << 26);  // workgroups of a launch: a few per (b, h)
 }
 
+// The chunk kernel reaches a chunk's 32 tokens by 32-bit byte offsets from its first: 31 strides have to fit.
+constexpr int64_t kTokenStrideBytes = (int64_t)1 << 27;
+bool far_apart(int64_t N, lconv_dtype_t dt, std::initializer_list<lconv_strides_t> all) {
+    for (const lconv_strides_t& s : all)
+        if (N > 1 && s.n > kTokenStrideBytes / (int64_t)dtype_size(dt)) return true;
+    return false;
+}
+
 // fp32 gradients of each query head, before the sum over the heads that share a k/v head
 size_t head_grads_bytes(int64_t B, int64_t H, int64_t G, int64_t N, int64_t D) {
     return H == G ? 0 : round256((size_t)(B * H) * (size_t)N * (size_t)D * 4);
@@ -106,21 +115,32 @@ void set_plan(LinJob* a, const LinPlan& p) {
     a->kt = p.kt; a->nw = p.nw; a->ncb = p.ncb; a->nseg = p.nseg; a->seg_len = p.seg_len;
 }
 
-// The gradients' three roles: dq and dk contract over Dv, dv over Dk.  Where both widths take the same
-// tiles they go in one launch.
+// The gradients' roles by launch: dq and dk contract over Dv and have Dk columns, dv the other way round.
+// Roles of the same tiles go together, apart from dq where dk and dv leave in fp32 (shared heads).
 struct BwdPlan {
-    bool together;
-    LinPlan qk, v;
-    size_t sqk, sv;           // bytes of a role's segment states
+    int launches, first[3], roles[3];   // roles first .. first + roles - 1 of (dq, dk, dv)
+    LinPlan plan[3];
+    size_t states[3];                   // bytes of one role's segment states
+    size_t total;
 };
-BwdPlan bwd_plan(int64_t B, int64_t H, int64_t N, int64_t Dk, int64_t Dv, lconv_dtype_t dtype) {
-    BwdPlan p;
-    const int64_t rows = B * H, wide = Dk > Dv ? Dk : Dv;
-    p.together = linattn_kt(Dk) == linattn_kt(Dv);
-    p.qk = p.together ? linattn_plan(rows, 3, N, wide, wide, dtype) : linattn_plan(rows, 2, N, Dv, Dk, dtype);
-    p.v = p.together ? p.qk : linattn_plan(rows, 1, N, Dk, Dv, dtype);
-    p.sqk = linattn_states_bytes(p.qk, rows, Dk, Dv);
-    p.sv = linattn_states_bytes(p.v, rows, Dk, Dv);
+BwdPlan bwd_plan(int64_t B, int64_t H, int64_t G, int64_t N, int64_t Dk, int64_t Dv, lconv_dtype_t dtype) {
+    BwdPlan p{};
+    const int64_t rows = B * H;
+    const bool alike = linattn_kt(Dk) == linattn_kt(Dv), apart = H != G;
+    int cut[4] = {0, 0, 0, 3}, n = 1;
+    if (apart) cut[n++] = 1;
+    if (!alike) cut[n++] = 2;
+    cut[n] = 3;
+    p.launches = n;
+    for (int i = 0; i < n; ++i) {
+        p.first[i] = cut[i];
+        p.roles[i] = cut[i + 1] - cut[i];
+        const bool v = cut[i] == 2, both = cut[i] < 2 && cut[i + 1] == 3;   // dv alone; dv with the others
+        const int64_t wide = Dk > Dv ? Dk : Dv;
+        p.plan[i] = linattn_plan(rows, p.roles[i], N, both ? wide : v ? Dk : Dv, both ? wide : v ? Dv : Dk, dtype);
+        p.states[i] = linattn_states_bytes(p.plan[i], rows, Dk, Dv);
+        p.total += (size_t)p.roles[i] * p.states[i];
+    }
     return p;
 }
 
@@ -161,6 +181,7 @@ lconv_status_t lconv_linattn_fwd(const void* q, const lconv_strides_t* q_strides
     if ((st = operand(k, k_strides, B, G, N, Dk, dtype, false, &r.K.s, &rk)) != LCONV_SUCCESS) return st;
     if ((st = operand(v, v_strides, B, G, N, Dv, dtype, false, &r.V.s, &rv)) != LCONV_SUCCESS) return st;
     if ((st = operand(y, y_strides, B, H, N, Dv, dtype, true, &r.o, &ry)) != LCONV_SUCCESS) return st;
+    if (far_apart(N, dtype, {r.Q.s, r.K.s, r.V.s, r.o})) return LCONV_ERR_UNSUPPORTED;
     if (!log_decay) return LCONV_ERR_NULL_POINTER;
     const Range rld = buffer(log_decay, H, 4), rlen = buffer(lengths, B, 4);
     if (clash({ry, rso}, {rq, rk, rv, rld, rlen}) || overlap(ry, rsi)) return LCONV_ERR_ALIASING;
@@ -179,6 +200,7 @@ lconv_status_t lconv_linattn_fwd(const void* q, const lconv_strides_t* q_strides
     r.states = (float*)workspace;
     r.s_q = scale; r.s_kv = 1.f;
     a.nroles = 1;
+    a.exact = state_out != nullptr;
     a.log_decay = log_decay; a.lengths = lengths;
     a.B = B; a.H = (int)H; a.N = N;
     set_plan(&a, linattn_plan(B * H, 1, N, Dk, Dv, dtype));
@@ -188,8 +210,8 @@ lconv_status_t lconv_linattn_fwd(const void* q, const lconv_strides_t* q_strides
 size_t lconv_linattn_bwd_workspace_bytes(int64_t B, int64_t H, int64_t G, int64_t N, int64_t Dk, int64_t Dv,
                                          lconv_dtype_t dtype) {
     if (!dtype_ok(dtype) || B <= 0 || H <= 0 || N <= 0 || !linattn_dims_ok(B, H, G, N, Dk, Dv)) return 0;
-    const BwdPlan p = bwd_plan(B, H, N, Dk, Dv, dtype);
-    return head_grads_bytes(B, H, G, N, Dk) + head_grads_bytes(B, H, G, N, Dv) + tan_bytes(B, H, Dk) + 2 * p.sqk + p.sv;
+    return head_grads_bytes(B, H, G, N, Dk) + head_grads_bytes(B, H, G, N, Dv) + tan_bytes(B, H, Dk) +
+           bwd_plan(B, H, G, N, Dk, Dv, dtype).total;
 }
 
 lconv_status_t lconv_linattn_bwd(const void* dy, const lconv_strides_t* dy_strides, const void* q,
@@ -225,6 +247,7 @@ lconv_status_t lconv_linattn_bwd(const void* dy, const lconv_strides_t* dy_strid
     if ((st = operand(dq, dq_strides, B, H, N, Dk, dtype, true, &sdq, &rdq)) != LCONV_SUCCESS) return st;
     if ((st = operand(dk, dk_strides, B, G, N, Dk, dtype, true, &sdk, &rdk)) != LCONV_SUCCESS) return st;
     if ((st = operand(dv, dv_strides, B, G, N, Dv, dtype, true, &sdv, &rdv)) != LCONV_SUCCESS) return st;
+    if (far_apart(N, dtype, {ody.s, oq.s, ok.s, ov.s, sdq, sdk, sdv})) return LCONV_ERR_UNSUPPORTED;
     if (!log_decay) return LCONV_ERR_NULL_POINTER;
     const Range rld = buffer(log_decay, H, 4), rlen = buffer(lengths, B, 4);
     if (clash({rdq, rdk, rdv, rdsi, rdl}, {rdy, rq, rk, rv, rld, rlen, rsi, rdso})) return LCONV_ERR_ALIASING;
@@ -242,7 +265,7 @@ lconv_status_t lconv_linattn_bwd(const void* dy, const lconv_strides_t* dy_strid
     float* gv = share > 1 ? (float*)ws : nullptr;
     ws += head_grads_bytes(B, H, G, N, Dv);
 
-    const BwdPlan plan = bwd_plan(B, H, N, Dk, Dv, dtype);
+    const BwdPlan plan = bwd_plan(B, H, G, N, Dk, Dv, dtype);
     float* tan = (float*)ws;
     ws += tan_bytes(B, H, Dk);
 
@@ -251,48 +274,45 @@ lconv_status_t lconv_linattn_bwd(const void* dy, const lconv_strides_t* dy_strid
     a.B = B; a.H = (int)H; a.N = N;
 
     // dq: dy, v, k in the places of q, k, v, with the state transposed
-    LinRole& rq_ = a.r[0];
-    rq_.Q = ody; rq_.K = ov; rq_.V = ok;
-    rq_.O = dq; rq_.o = sdq;
-    rq_.DK = (int)Dv; rq_.DV = (int)Dk;
-    rq_.s_in = state_in; rq_.s_row = 1; rq_.s_col = (int)Dv;
-    rq_.s_q = scale; rq_.s_kv = 1.f;
-    rq_.states = (float*)ws;
+    LinRole role[3] = {};
+    LinRole &rdq_ = role[0], &rdk_ = role[1], &rdv_ = role[2];
+    rdq_.Q = ody; rdq_.K = ov; rdq_.V = ok;
+    rdq_.O = dq; rdq_.o = sdq;
+    rdq_.DK = (int)Dv; rdq_.DV = (int)Dk;
+    rdq_.s_in = state_in; rdq_.s_row = 1; rdq_.s_col = (int)Dv;
+    rdq_.s_q = scale; rdq_.s_kv = 1.f;
 
     // dk: v, dy, q from the last token to the first
-    LinRole& rk_ = a.r[1];
-    rk_ = rq_;
-    rk_.Q = ov; rk_.K = ody; rk_.V = oq;
-    rk_.O = share > 1 ? (void*)gk : dk;
-    rk_.o = share > 1 ? lconv_strides_t{H * N * Dk, N * Dk, Dk} : sdk;
-    rk_.o_f32 = share > 1;
-    rk_.s_in = dstate_out;
-    rk_.s_q = 1.f; rk_.s_kv = scale; rk_.reverse = 1;
-    rk_.states = (float*)(ws + plan.sqk);
+    rdk_ = rdq_;
+    rdk_.Q = ov; rdk_.K = ody; rdk_.V = oq;
+    rdk_.O = share > 1 ? (void*)gk : dk;
+    rdk_.o = share > 1 ? lconv_strides_t{H * N * Dk, N * Dk, Dk} : sdk;
+    rdk_.s_in = dstate_out;
+    rdk_.s_q = 1.f; rdk_.s_kv = scale; rdk_.reverse = 1;
 
     // dv and the gradient of the state that entered: k, q, dy
-    LinRole& rv_ = a.r[2];
-    rv_ = rk_;
-    rv_.Q = ok; rv_.K = oq; rv_.V = ody;
-    rv_.O = share > 1 ? (void*)gv : dv;
-    rv_.o = share > 1 ? lconv_strides_t{H * N * Dv, N * Dv, Dv} : sdv;
-    rv_.DK = (int)Dk; rv_.DV = (int)Dv;
-    rv_.s_out = dstate_in; rv_.s_row = (int)Dv; rv_.s_col = 1;
-    rv_.states = (float*)(ws + 2 * plan.sqk);
+    rdv_ = rdk_;
+    rdv_.Q = ok; rdv_.K = oq; rdv_.V = ody;
+    rdv_.O = share > 1 ? (void*)gv : dv;
+    rdv_.o = share > 1 ? lconv_strides_t{H * N * Dv, N * Dv, Dv} : sdv;
+    rdv_.DK = (int)Dk; rdv_.DV = (int)Dv;
+    rdv_.s_out = dstate_in; rdv_.s_row = (int)Dv; rdv_.s_col = 1;
 
-    a.nroles = plan.together ? 3 : 2;
-    set_plan(&a, plan.qk);
-    if (launch_linattn(dtype, a, stream) != hipSuccess) return LCONV_ERR_HIP;
-    if (!plan.together) {
-        LinJob one = a;
-        one.r[0] = rv_;
-        one.nroles = 1;
-        set_plan(&one, plan.v);
-        if (launch_linattn(dtype, one, stream) != hipSuccess) return LCONV_ERR_HIP;
+    for (int i = 0; i < plan.launches; ++i) {
+        a.nroles = plan.roles[i];
+        for (int j = 0; j < a.nroles; ++j) {
+            a.r[j] = role[plan.first[i] + j];
+            a.r[j].states = (float*)ws;
+            ws += plan.states[i];
+        }
+        a.wide = share > 1 && plan.first[i] > 0;
+        a.exact = dstate_in && plan.first[i] + plan.roles[i] == 3;
+        set_plan(&a, plan.plan[i]);
+        if (launch_linattn(dtype, a, stream) != hipSuccess) return LCONV_ERR_HIP;
     }
     if (dlog_decay) {
         LinTanArgs t{};
-        t.a.r = rq_;
+        t.a.r = rdq_;
         t.a.log_decay = log_decay; t.a.lengths = lengths;
         t.a.B = B; t.a.H = (int)H; t.a.N = N;
         t.q = oq; t.ds_out = dstate_out; t.part = tan;

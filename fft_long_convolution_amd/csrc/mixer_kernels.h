@@ -5,7 +5,6 @@
 #include <stdint.h>
 
 #include "lconv.h"
-#include "mixer_plan.h"
 
 namespace lcv {
 
@@ -27,7 +26,6 @@ struct LinRole {
     LinOperand Q, K, V;
     void* O;                  // NULL: only the state is wanted
     lconv_strides_t o;
-    int o_f32;                // O in fp32 (sums over shared heads follow), else the dtype
     int DK, DV;
     const float* s_in;        // [B][H] states, element (d, n) at d * s_row + n * s_col; NULL: zeros
     float* s_out;             // the same layout; NULL: not wanted
@@ -47,6 +45,8 @@ struct LinJob {
     int H;
     int64_t N, seg_len;
     int kt, nw, ncb, nseg;
+    int exact;                // a state leaves the call
+    int wide;                 // every O in fp32 (sums over shared heads follow), else in the dtype
 };
 
 struct LinArgs {

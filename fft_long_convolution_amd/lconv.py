@@ -751,15 +751,30 @@ def fftconv2d_bwd(dy, u, k_f, D, need_dk=True, stream=None):
 
 # ---- linear attention, rotary positions, layer norm ---------------------------------------------
 
+_HERE = contextlib.nullcontext()
+
+
 def _at(dev, stream):
     """(context, raw stream) of a mixer call on `dev`: outputs and workspaces made inside the context
     belong to the stream that the call runs on, so they are not handed out again before it is done."""
     torch = _torch()
     if stream is not None:
         return torch.cuda.stream(stream), stream.cuda_stream     # also makes its device the current one
-    if dev.index == torch.cuda.current_device():
-        return contextlib.nullcontext(), torch.cuda.current_stream(dev).cuda_stream
+    if dev == torch.cuda.current_device():
+        return _HERE, torch.cuda.current_stream().cuda_stream
     return torch.cuda.device(dev), torch.cuda.current_stream(dev).cuda_stream
+
+
+def _same_gpu(names, operands):
+    """The device's index, once every given operand is a GPU tensor on one device (the cheap form of
+    _on_gpu for calls of a few microseconds)."""
+    dev = None
+    for t in operands:
+        if t is not None:
+            if not t.is_cuda or (dev is not None and t.get_device() != dev):
+                _on_gpu(**dict(zip(names.split(), operands)))    # says which
+            dev = t.get_device()
+    return dev
 
 
 @functools.lru_cache(maxsize=256)
@@ -772,7 +787,7 @@ def _view(name, t, shape, dtype):
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor, got {type(t).__name__}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
@@ -792,21 +807,37 @@ def _in_order_of(x, shape):
     return torch.empty(shape, dtype=x.dtype, device=x.device)
 
 
+def _float_dtype(name, t):
+    """The library's code of a tensor's dtype."""
+    code = _FLOATS.get(t.dtype) if _FLOATS else None
+    if code is None:
+        torch = _torch()
+        _FLOATS.update({torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16})
+        code = _FLOATS.get(t.dtype)
+        if code is None:
+            raise ValueError(f"{name} has dtype {t.dtype}; supported: float32, float16, bfloat16")
+    return code
+
+
+_FLOATS = {}
+
+
 def _linattn_shape(q, k, v, dims):
-    """(dtype, B, H, G, N, Dk, Dv) of a call's operands, checked where they fix the shape (dims 4: with
+    """(dtype, its code, B, H, G, N, Dk, Dv) of a call's operands, checked where they fix the shape (dims 4: with
     tokens, 3: single tokens)."""
     torch = _torch()
     for name, t in (("q", q), ("k", k), ("v", v)):
         if not isinstance(t, torch.Tensor) or t.dim() != dims:
             raise ValueError(f"{name} must be a {dims}-D torch tensor")
-    if q.dtype not in (torch.float32, torch.float16, torch.bfloat16):
-        raise ValueError(f"q has dtype {q.dtype}; supported: float32, float16, bfloat16")
-    B, H, Dk = q.shape[0], q.shape[1], q.shape[-1]
-    N = q.shape[2] if dims == 4 else 1
+    dt = _float_dtype("q", q)
+    if dims == 4:
+        B, H, N, Dk = q.shape
+    else:
+        (B, H, Dk), N = q.shape, 1
     G, Dv = k.shape[1], v.shape[-1]
     if G == 0 and H > 0 or G and H % G:
         raise ValueError(f"q has {H} heads, not a multiple of k's {G}")
-    return q.dtype, B, H, G, N, Dk, Dv
+    return q.dtype, dt, B, H, G, N, Dk, Dv
 
 
 def _lengths(lengths, B):
@@ -818,6 +849,9 @@ def _lengths(lengths, B):
 def _outputs(name, t, shape, like):
     """An output given by the caller, or a new one in `like`'s order: (tensor, strides)."""
     if t is None:
+        torch = _torch()
+        if len(shape) == 3 or like.is_contiguous():
+            return torch.empty(shape, dtype=like.dtype, device=like.device), None
         t = _in_order_of(like, shape)
     return t, _view(name, t, shape, like.dtype)
 
@@ -833,14 +867,13 @@ def linear_attention(q, k, v, log_decay, scale=None, state=None, lengths=None, n
     nothing and give y = 0.  Returns (y [B, H, N, Dv] in q's dtype and order of dimensions, the state
     after each row's last token; None without need_state).  state_out may be `state` itself."""
     torch = _torch()
-    tdt, B, H, G, N, Dk, Dv = _linattn_shape(q, k, v, 4)
+    tdt, dt, B, H, G, N, Dk, Dv = _linattn_shape(q, k, v, 4)
     qs, ks, vs = _view("q", q, (B, H, N, Dk), tdt), _view("k", k, (B, G, N, Dk), tdt), _view("v", v, (B, G, N, Dv), tdt)
     _need("log_decay", log_decay, (H,), torch.float32)
     _need("state", state, (B, H, Dk, Dv), torch.float32, optional=True)
     _need("state_out", state_out, (B, H, Dk, Dv), torch.float32, optional=True)
     _lengths(lengths, B)
-    dev = _on_gpu(q=q, k=k, v=v, log_decay=log_decay, state=state, lengths=lengths, out=out, state_out=state_out)
-    dt = dtype_code(tdt)
+    dev = _same_gpu("q k v log_decay state lengths out state_out", (q, k, v, log_decay, state, lengths, out, state_out))
     scale = 1.0 / math.sqrt(max(Dk, 1)) if scale is None else float(scale)
     ctx, st = _at(dev, stream)
     with ctx:
@@ -865,15 +898,14 @@ def linear_attention_bwd(dy, q, k, v, log_decay, scale=None, state=None, dstate=
     typed like q, k, v (dk and dv summed over the heads that share them), dstate the gradient of the
     state that entered (None without one), dlog_decay [H] in float32 (None unless asked for)."""
     torch = _torch()
-    tdt, B, H, G, N, Dk, Dv = _linattn_shape(q, k, v, 4)
+    tdt, dt, B, H, G, N, Dk, Dv = _linattn_shape(q, k, v, 4)
     qs, ks, vs = _view("q", q, (B, H, N, Dk), tdt), _view("k", k, (B, G, N, Dk), tdt), _view("v", v, (B, G, N, Dv), tdt)
     dys = _view("dy", dy, (B, H, N, Dv), tdt)
     _need("log_decay", log_decay, (H,), torch.float32)
     _need("state", state, (B, H, Dk, Dv), torch.float32, optional=True)
     _need("dstate", dstate, (B, H, Dk, Dv), torch.float32, optional=True)
     _lengths(lengths, B)
-    dev = _on_gpu(dy=dy, q=q, k=k, v=v, log_decay=log_decay, state=state, dstate=dstate, lengths=lengths)
-    dt = dtype_code(tdt)
+    dev = _same_gpu("dy q k v log_decay state dstate lengths", (dy, q, k, v, log_decay, state, dstate, lengths))
     scale = 1.0 / math.sqrt(max(Dk, 1)) if scale is None else float(scale)
     ctx, st = _at(dev, stream)
     with ctx:
@@ -896,7 +928,7 @@ def linear_attention_step(q, k, v, log_decay, state, scale=None, slots=None, out
     continues (outside the states: an idle row, y = 0); without it row b has state b.  No two rows may
     have the same slot.  Returns y [B, H, Dv]."""
     torch = _torch()
-    tdt, B, H, G, _, Dk, Dv = _linattn_shape(q, k, v, 3)
+    tdt, dt, B, H, G, _, Dk, Dv = _linattn_shape(q, k, v, 3)
     qs, ks, vs = _view("q", q, (B, H, Dk), tdt), _view("k", k, (B, G, Dk), tdt), _view("v", v, (B, G, Dv), tdt)
     _need("log_decay", log_decay, (H,), torch.float32)
     if not isinstance(state, torch.Tensor) or state.dim() != 4:
@@ -907,13 +939,13 @@ def linear_attention_step(q, k, v, log_decay, state, scale=None, slots=None, out
         _need("slots", slots, (B,), torch.int32)
     elif nslots < B:
         raise ValueError(f"{B} rows and {nslots} states: slots are needed")
-    dev = _on_gpu(q=q, k=k, v=v, log_decay=log_decay, state=state, slots=slots, out=out)
+    dev = _same_gpu("q k v log_decay state slots out", (q, k, v, log_decay, state, slots, out))
     scale = 1.0 / math.sqrt(max(Dk, 1)) if scale is None else float(scale)
     ctx, st = _at(dev, stream)
     with ctx:
         y, ys = _outputs("out", out, (B, H, Dv), q)
         _check(lconv_linattn_step(_ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(log_decay), scale, _ptr(state),
-                                  _ptr(slots), _ptr(y), ys, B, H, G, Dk, Dv, nslots, dtype_code(tdt), st),
+                                  _ptr(slots), _ptr(y), ys, B, H, G, Dk, Dv, nslots, dt, st),
                "lconv_linattn_step")
     return y
 
@@ -960,8 +992,7 @@ def rotary(q, k, positions, inv_freq, interleaved=False, inverse=False, magnitud
     torch = _torch()
     if not isinstance(q, torch.Tensor) or q.dim() != 4:
         raise ValueError("q must be a 4-D torch tensor")
-    if q.dtype not in (torch.float32, torch.float16, torch.bfloat16):
-        raise ValueError(f"q has dtype {q.dtype}; supported: float32, float16, bfloat16")
+    dt = _float_dtype("q", q)
     B, H, N, D = q.shape
     qs = _view("q", q, (B, H, N, D), q.dtype)
     G, ks = 0, None
@@ -986,14 +1017,14 @@ def rotary(q, k, positions, inv_freq, interleaved=False, inverse=False, magnitud
     oq, ok = (None, None) if out is None else out
     if k is None and ok is not None:
         raise ValueError("an output for k without k")
-    dev = _on_gpu(q=q, k=k, positions=positions, inv_freq=inv_freq, out_q=oq, out_k=ok)
+    dev = _same_gpu("q k positions inv_freq out_q out_k", (q, k, positions, inv_freq, oq, ok))
     flags = (ROTARY_INTERLEAVED if interleaved else ROTARY_HALF) | (ROTARY_INVERSE if inverse else 0)
     ctx, st = _at(dev, stream)
     with ctx:
         yq, yqs = _outputs("out of q", oq, (B, H, N, D), q)
         yk, yks = (None, None) if k is None else _outputs("out of k", ok, (B, G, N, D), k)
         _check(lconv_rotary(_ptr(q), qs, _ptr(k), ks, _ptr(positions), pos_stride, _ptr(inv_freq), float(magnitude),
-                            _ptr(yq), yqs, _ptr(yk), yks, B, H, G, N, D, rot, flags, dtype_code(q.dtype), st),
+                            _ptr(yq), yqs, _ptr(yk), yks, B, H, G, N, D, rot, flags, dt, st),
                "lconv_rotary")
     return yq, yk
 
@@ -1026,12 +1057,11 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, need_stats=True, out=None, s
     torch = _torch()
     if not isinstance(x, torch.Tensor) or x.dim() < 1:
         raise ValueError("x must be a torch tensor of at least one dimension")
-    if x.dtype not in (torch.float32, torch.float16, torch.bfloat16):
-        raise ValueError(f"x has dtype {x.dtype}; supported: float32, float16, bfloat16")
+    dt = _float_dtype("x", x)
     rows, C, xs = _rows("x", x, x.shape, x.dtype)
     _need("weight", weight, (C,), x.dtype, optional=True)
     _need("bias", bias, (C,), x.dtype, optional=True)
-    dev = _on_gpu(x=x, weight=weight, bias=bias, out=out)
+    dev = _same_gpu("x weight bias out", (x, weight, bias, out))
     ctx, st = _at(dev, stream)
     with ctx:
         y = torch.empty(x.shape, dtype=x.dtype, device=dev) if out is None else out
@@ -1039,7 +1069,7 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, need_stats=True, out=None, s
         mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev) if need_stats else None
         rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev) if need_stats else None
         _check(lconv_layernorm_fwd(_ptr(x), xs, _ptr(weight), _ptr(bias), _ptr(y), ys, _ptr(mean), _ptr(rstd), rows, C,
-                                   float(eps), dtype_code(x.dtype), st), "lconv_layernorm_fwd")
+                                   float(eps), dt, st), "lconv_layernorm_fwd")
     return y, mean, rstd
 
 
@@ -1050,14 +1080,13 @@ def layer_norm_bwd(dy, x, weight, mean, rstd, need_dweight=True, need_dbias=True
     torch = _torch()
     if not isinstance(x, torch.Tensor) or x.dim() < 1:
         raise ValueError("x must be a torch tensor of at least one dimension")
-    if x.dtype not in (torch.float32, torch.float16, torch.bfloat16):
-        raise ValueError(f"x has dtype {x.dtype}; supported: float32, float16, bfloat16")
+    dt = _float_dtype("x", x)
     rows, C, xs = _rows("x", x, x.shape, x.dtype)
     dys = _rows("dy", dy, x.shape, x.dtype)[2]
     _need("weight", weight, (C,), x.dtype, optional=True)
     _need("mean", mean, x.shape[:-1], torch.float32)
     _need("rstd", rstd, x.shape[:-1], torch.float32)
-    dev = _on_gpu(dy=dy, x=x, weight=weight, mean=mean, rstd=rstd, out=out)
+    dev = _same_gpu("dy x weight mean rstd out", (dy, x, weight, mean, rstd, out))
     ctx, st = _at(dev, stream)
     with ctx:
         dx = torch.empty(x.shape, dtype=x.dtype, device=dev) if out is None else out
@@ -1067,6 +1096,6 @@ def layer_norm_bwd(dy, x, weight, mean, rstd, need_dweight=True, need_dbias=True
         wsb = lconv_layernorm_bwd_workspace_bytes(rows, C) if dw is not None or db is not None else 0
         ws = torch.empty(wsb, dtype=torch.uint8, device=dev) if wsb else None
         _check(lconv_layernorm_bwd(_ptr(dy), dys, _ptr(x), xs, _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dx), dxs,
-                                   _ptr(dw), _ptr(db), rows, C, dtype_code(x.dtype), _ptr(ws), wsb, st),
+                                   _ptr(dw), _ptr(db), rows, C, dt, _ptr(ws), wsb, st),
                "lconv_layernorm_bwd")
     return dx, dw, db

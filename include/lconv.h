@@ -496,7 +496,10 @@ typedef struct {
  *   workspace  lconv_linattn_workspace_bytes(...) bytes (may be NULL if that is 0)
  * States and all sums are fp32; with 16-bit data the scores and the state are rounded once to the
  * dtype as matrix-core operands, while what the state adds up is kept to fp32's accuracy.
- * Supported: Dk, Dv multiples of 8 in [8, 256]; H a multiple of G; N < 2^31; every dtype.
+ * Tokens are taken 32 at a time: a value that is not finite in k or v reaches the outputs from its token on,
+ * one in v those of the up to 31 tokens before it as well; one in q its own row's.
+ * Supported: Dk, Dv multiples of 8 in [8, 256]; H a multiple of G; N < 2^31; tokens at most 2^27 bytes apart
+ * (strides' n, N > 1); every dtype.
  * B, H or N = 0 is a no-op apart from state_out, which is set as for rows of length 0 (N = 0).
  */
 size_t lconv_linattn_workspace_bytes(int64_t B, int64_t H, int64_t G, int64_t N, int64_t Dk, int64_t Dv,

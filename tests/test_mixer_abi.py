@@ -44,6 +44,21 @@ def test_linattn_fwd_refusals():
     assert fwd(ln=A[4] + 16) == ALIAS
 
 
+@pytest.mark.parametrize("dt,size", [(F32, 4), (F16, 2), (BF16, 2)])
+def test_linattn_refuses_tokens_too_far_apart(dt, size):
+    """Offsets within 32 tokens are 32-bit: token strides past 2^27 bytes are refused, and only for N > 1."""
+    far = 2 ** 27 // size + 16 // size
+    big = [1 << 44, 1 << 45, 1 << 46, 1 << 47]
+    for name in ("qs", "ks", "vs", "ys"):
+        s = st(8 * 8 * far, 8 * far, far)
+        assert fwd(q=big[0], k=big[1], v=big[2], y=big[3], dt=dt, **{name: s}) == UNSUP
+    assert bwd(dq=big[3], dt=dt, dqs=st(8 * 8 * far, 8 * far, far)) == UNSUP
+    # the limit itself passes on to the next check
+    s = st(8 * 8 * (far - 16 // size), 8 * (far - 16 // size), far - 16 // size)
+    assert fwd(q=big[0], dt=dt, qs=s, ld=None) == NULLP
+    assert fwd(q=big[0], dt=dt, N=1, qs=st(4 * far, far, far), ld=None) == NULLP
+
+
 def test_linattn_slices_of_one_buffer_do_not_alias():
     """y between q and k in a token-major buffer is apart; one that meets q's columns is not."""
     B, H, N, D = 2, 4, 8, 16

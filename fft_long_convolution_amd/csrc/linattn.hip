@@ -165,8 +165,11 @@ __global__ void __launch_bounds__(64) tan_sum_kernel(const float* part, float* d
 }
 
 template <int IO>
-__global__ void __launch_bounds__(256) head_sum_kernel(const float* in, void* out, lconv_strides_t os, int G, int share,
-                                                       int64_t N, int D, int64_t total) {
+__global__ void __launch_bounds__(256) head_sum_kernel(HeadSumArgs a) {
+    const int which = blockIdx.y, D = a.D[which], share = a.share, G = a.G;
+    const float* const in = a.in[which];
+    const lconv_strides_t os = a.os[which];
+    const int64_t N = a.N, total = a.B * G * N * (D / 8);
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
         const int64_t row = i / (D / 8);
         const int d = (int)(i - row * (D / 8)) * 8;
@@ -178,7 +181,7 @@ __global__ void __launch_bounds__(256) head_sum_kernel(const float* in, void* ou
 #pragma unroll
             for (int j = 0; j < 8; ++j) x[j] += p[j];
         }
-        store8<IO>(out, b * os.b + g * os.h + t * os.n + d, x);
+        store8<IO>(a.out[which], b * os.b + g * os.h + t * os.n + d, x);
     }
 }
 
@@ -237,12 +240,9 @@ hipError_t launch_linattn_step(int dtype, const LinStepArgs& a, hipStream_t stre
     });
 }
 
-hipError_t launch_head_sum(int dtype, const float* in, void* out, lconv_strides_t os, int64_t B, int G, int share,
-                           int64_t N, int D, hipStream_t stream) {
-    const int64_t total = B * G * N * (D / 8);
-    return by_dtype(dtype, [&](auto io) {
-        head_sum_kernel<io.value><<<grid_1d(total), 256, 0, stream>>>(in, out, os, G, share, N, D, total);
-    });
+hipError_t launch_head_sum(int dtype, const HeadSumArgs& a, hipStream_t stream) {
+    const int64_t total = a.B * a.G * a.N * ((a.D[0] > a.D[1] ? a.D[0] : a.D[1]) / 8);
+    return by_dtype(dtype, [&](auto io) { head_sum_kernel<io.value><<<dim3(grid_1d(total), 2), 256, 0, stream>>>(a); });
 }
 
 hipError_t launch_copy_state(const float* in, float* out, int64_t n, hipStream_t stream) {

@@ -187,10 +187,10 @@ __device__ __forceinline__ float max_over_wave(float m) {
 
 // ---- one segment of one (b, h), 64 NW columns -------------------------------------------------
 
-// STATE: only the state that the segment adds up from zero, for the segments after it.  WIDE: O in fp32.
+// STATE: only the state that the segment adds up from zero, for the segments after it.  WIDE: some roles' O leaves in fp32.
 // EXACT: the state's sums to fp32's accuracy.
 template <int IO, int KT, int NW, bool STATE, bool WIDE, bool EXACT>
-__global__ void __launch_bounds__(256, KT > 8 ? 1 : NW == 1 && IO != CT_F32 ? 3 : 2) linattn_chunk_kernel(LinJob a) {
+__global__ void __launch_bounds__(256, KT > 8 || (IO == CT_F32 && NW == 2) ? 1 : NW == 1 && IO != CT_F32 ? 3 : 2) linattn_chunk_kernel(LinJob a) {
     using M = Mx<IO>;
     using E = typename M::E;
     using Frag = typename M::Frag;
@@ -232,18 +232,19 @@ __global__ void __launch_bounds__(256, KT > 8 ? 1 : NW == 1 && IO != CT_F32 ? 3 
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, g = lane >> 4, x = lane & 15;
     const int wcol = cb * DVB + wave * 16 * NW;             // the wave's first column
     const int64_t ob = b * r.o.b + (int64_t)h * r.o.h;
-    constexpr int osize = WIDE ? 4 : (int)sizeof(E);
 
+    const bool wide = IO == CT_F32 || (WIDE && r.wide);
+    const int osz = wide ? 4 : 2;
     if constexpr (!STATE) {
         // tokens past the row's length: zeros (16-byte groups of this workgroup's columns)
-        constexpr int per = 16 / osize;
+        const int per = 16 / osz;
         const int groups = ((r.DV - cb * DVB < DVB ? r.DV - cb * DVB : DVB)) / per;
         int64_t t0 = beg > len ? beg : len, t1 = beg + a.seg_len < a.N ? beg + a.seg_len : a.N;
         if (r.O && t1 > t0)
             for (int64_t i = tid; i < (t1 - t0) * groups; i += 256) {
                 const int64_t t = t0 + i / groups;
                 const int c = cb * DVB + (int)(i % groups) * per;
-                *(uint4*)((char*)r.O + (ob + t * r.o.n + c) * osize) = make_uint4(0, 0, 0, 0);
+                *(uint4*)((char*)r.O + (ob + t * r.o.n + c) * osz) = make_uint4(0, 0, 0, 0);
             }
         if (end <= beg && !(seg == 0 && r.s_out)) return;
     }
@@ -367,7 +368,6 @@ __global__ void __launch_bounds__(256, KT > 8 ? 1 : NW == 1 && IO != CT_F32 ? 3 
     const typename M::At lk = M::at(g, x, RK), lv = M::at(g, x, RV);
     // the output likewise: lane x's token, the first of its four columns; token tiles of 16 and column tiles
     // are steps of the scalar
-    constexpr int osz = WIDE || IO == CT_F32 ? 4 : 2;
     char* po = STATE ? nullptr : (char*)r.O + (ob + low * r.o.n) * osz;
     const int64_t d_o = dir * r.o.n * osz, o16 = 16 * r.o.n * osz;
     const uint32_t oo = (uint32_t)(r.reverse ? 15 - x : x) * (uint32_t)(r.o.n * osz) + (uint32_t)((wcol + 4 * g) * osz);
@@ -389,9 +389,9 @@ __global__ void __launch_bounds__(256, KT > 8 ? 1 : NW == 1 && IO != CT_F32 ? 3 
     const auto put = [&](int it, int n) LCV_INLINE {
         const __amdgpu_buffer_rsrc_t o = buffer_at(po + (r.reverse ? CT - 1 - it : it) * o16 + 16 * n * osz);
         const f32x4 y = acc[it][n];
-        if constexpr (osz == 4) {
+        if (wide) {
             __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, y), o, oo, 0, 0);
-        } else {
+        } else if constexpr (IO != CT_F32) {
             typedef uint32_t u32x2 __attribute__((__vector_size__(8)));
             const u32x2 w = {pack2<IO>(y[0], y[1]), pack2<IO>(y[2], y[3])};
             __builtin_amdgcn_raw_buffer_store_b64(w, o, oo, 0, 0);
@@ -668,17 +668,22 @@ template <int IO, int KT, int NW>
 hipError_t launch_chunk(const LinJob& a, hipStream_t stream) {
     // fp32 is wide as it is, and only bf16 has a third part to leave out
     constexpr bool W = IO != CT_F32, X = IO == CT_BF16;
-    if (a.exact || !X) return W && a.wide ? launch_chunk_as<IO, KT, NW, W, true>(a, stream) : launch_chunk_as<IO, KT, NW, false, true>(a, stream);
-    return W && a.wide ? launch_chunk_as<IO, KT, NW, W, !X>(a, stream) : launch_chunk_as<IO, KT, NW, false, !X>(a, stream);
+    bool wide = false;
+    for (int i = 0; i < a.nroles; ++i) wide |= W && a.r[i].wide;
+    if (a.exact || !X) return wide ? launch_chunk_as<IO, KT, NW, W, true>(a, stream) : launch_chunk_as<IO, KT, NW, false, true>(a, stream);
+    return wide ? launch_chunk_as<IO, KT, NW, W, !X>(a, stream) : launch_chunk_as<IO, KT, NW, false, !X>(a, stream);
 }
 
-template <int IO>
-hipError_t launch_chunk_io(const LinJob& a, hipStream_t stream) {
-    const int k = a.kt, n = a.nw;
-    if (k == 2) return n == 1 ? launch_chunk<IO, 2, 1>(a, stream) : launch_chunk<IO, 2, 2>(a, stream);
-    if (k == 4) return n == 1 ? launch_chunk<IO, 4, 1>(a, stream) : launch_chunk<IO, 4, 2>(a, stream);
-    if (k == 8) return n == 1 ? launch_chunk<IO, 8, 1>(a, stream) : launch_chunk<IO, 8, 2>(a, stream);
-    return n == 1 ? launch_chunk<IO, 16, 1>(a, stream) : launch_chunk<IO, 16, 2>(a, stream);
+template <int IO, int NW>
+hipError_t launch_chunk_nw(const LinJob& a, hipStream_t stream) {
+    if (a.kt == 2) return launch_chunk<IO, 2, NW>(a, stream);
+    if (a.kt == 4) return launch_chunk<IO, 4, NW>(a, stream);
+    if (a.kt == 8) return launch_chunk<IO, 8, NW>(a, stream);
+    return launch_chunk<IO, 16, NW>(a, stream);
+}
+
+template <int IO> hipError_t launch_chunk_io(const LinJob& a, hipStream_t stream) {
+    return a.nw == 1 ? launch_chunk_nw<IO, 1>(a, stream) : launch_chunk_nw<IO, 2>(a, stream);
 }
 
 }  // namespace

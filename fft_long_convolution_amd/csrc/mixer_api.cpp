@@ -116,28 +116,23 @@ void set_plan(LinJob* a, const LinPlan& p) {
 }
 
 // The gradients' roles by launch: dq and dk contract over Dv and have Dk columns, dv the other way round.
-// Roles of the same tiles go together, apart from dq where dk and dv leave in fp32 (shared heads).
+// Roles of the same tiles go together: all three, or dq and dk.
 struct BwdPlan {
-    int launches, first[3], roles[3];   // roles first .. first + roles - 1 of (dq, dk, dv)
-    LinPlan plan[3];
-    size_t states[3];                   // bytes of one role's segment states
+    int launches, first[2], roles[2];   // roles first .. first + roles - 1 of (dq, dk, dv)
+    LinPlan plan[2];
+    size_t states[2];                   // bytes of one role's segment states
     size_t total;
 };
-BwdPlan bwd_plan(int64_t B, int64_t H, int64_t G, int64_t N, int64_t Dk, int64_t Dv, lconv_dtype_t dtype) {
+BwdPlan bwd_plan(int64_t B, int64_t H, int64_t N, int64_t Dk, int64_t Dv, lconv_dtype_t dtype) {
     BwdPlan p{};
     const int64_t rows = B * H;
-    const bool alike = linattn_kt(Dk) == linattn_kt(Dv), apart = H != G;
-    int cut[4] = {0, 0, 0, 3}, n = 1;
-    if (apart) cut[n++] = 1;
-    if (!alike) cut[n++] = 2;
-    cut[n] = 3;
-    p.launches = n;
-    for (int i = 0; i < n; ++i) {
-        p.first[i] = cut[i];
-        p.roles[i] = cut[i + 1] - cut[i];
-        const bool v = cut[i] == 2, both = cut[i] < 2 && cut[i + 1] == 3;   // dv alone; dv with the others
-        const int64_t wide = Dk > Dv ? Dk : Dv;
-        p.plan[i] = linattn_plan(rows, p.roles[i], N, both ? wide : v ? Dk : Dv, both ? wide : v ? Dv : Dk, dtype);
+    const bool alike = linattn_kt(Dk) == linattn_kt(Dv);
+    const int64_t wide = Dk > Dv ? Dk : Dv;
+    p.launches = alike ? 1 : 2;
+    for (int i = 0; i < p.launches; ++i) {
+        p.first[i] = 2 * i;
+        p.roles[i] = alike ? 3 : 2 - i;
+        p.plan[i] = linattn_plan(rows, p.roles[i], N, alike ? wide : i ? Dk : Dv, alike ? wide : i ? Dv : Dk, dtype);
         p.states[i] = linattn_states_bytes(p.plan[i], rows, Dk, Dv);
         p.total += (size_t)p.roles[i] * p.states[i];
     }
@@ -211,7 +206,7 @@ size_t lconv_linattn_bwd_workspace_bytes(int64_t B, int64_t H, int64_t G, int64_
                                          lconv_dtype_t dtype) {
     if (!dtype_ok(dtype) || B <= 0 || H <= 0 || N <= 0 || !linattn_dims_ok(B, H, G, N, Dk, Dv)) return 0;
     return head_grads_bytes(B, H, G, N, Dk) + head_grads_bytes(B, H, G, N, Dv) + tan_bytes(B, H, Dk) +
-           bwd_plan(B, H, G, N, Dk, Dv, dtype).total;
+           bwd_plan(B, H, N, Dk, Dv, dtype).total;
 }
 
 lconv_status_t lconv_linattn_bwd(const void* dy, const lconv_strides_t* dy_strides, const void* q,
@@ -265,7 +260,7 @@ lconv_status_t lconv_linattn_bwd(const void* dy, const lconv_strides_t* dy_strid
     float* gv = share > 1 ? (float*)ws : nullptr;
     ws += head_grads_bytes(B, H, G, N, Dv);
 
-    const BwdPlan plan = bwd_plan(B, H, G, N, Dk, Dv, dtype);
+    const BwdPlan plan = bwd_plan(B, H, N, Dk, Dv, dtype);
     float* tan = (float*)ws;
     ws += tan_bytes(B, H, Dk);
 
@@ -286,6 +281,7 @@ lconv_status_t lconv_linattn_bwd(const void* dy, const lconv_strides_t* dy_strid
     rdk_ = rdq_;
     rdk_.Q = ov; rdk_.K = ody; rdk_.V = oq;
     rdk_.O = share > 1 ? (void*)gk : dk;
+    rdk_.wide = share > 1;
     rdk_.o = share > 1 ? lconv_strides_t{H * N * Dk, N * Dk, Dk} : sdk;
     rdk_.s_in = dstate_out;
     rdk_.s_q = 1.f; rdk_.s_kv = scale; rdk_.reverse = 1;
@@ -305,7 +301,6 @@ lconv_status_t lconv_linattn_bwd(const void* dy, const lconv_strides_t* dy_strid
             a.r[j].states = (float*)ws;
             ws += plan.states[i];
         }
-        a.wide = share > 1 && plan.first[i] > 0;
         a.exact = dstate_in && plan.first[i] + plan.roles[i] == 3;
         set_plan(&a, plan.plan[i]);
         if (launch_linattn(dtype, a, stream) != hipSuccess) return LCONV_ERR_HIP;
@@ -319,8 +314,8 @@ lconv_status_t lconv_linattn_bwd(const void* dy, const lconv_strides_t* dy_strid
         if (launch_linattn_tan(dtype, t, dlog_decay, stream) != hipSuccess) return LCONV_ERR_HIP;
     }
     if (share > 1) {
-        if (launch_head_sum(dtype, gk, dk, sdk, B, (int)G, share, N, (int)Dk, stream) != hipSuccess) return LCONV_ERR_HIP;
-        if (launch_head_sum(dtype, gv, dv, sdv, B, (int)G, share, N, (int)Dv, stream) != hipSuccess) return LCONV_ERR_HIP;
+        const HeadSumArgs s{{gk, gv}, {dk, dv}, {sdk, sdv}, {(int)Dk, (int)Dv}, B, N, (int)G, share};
+        if (launch_head_sum(dtype, s, stream) != hipSuccess) return LCONV_ERR_HIP;
     }
     return LCONV_SUCCESS;
 }

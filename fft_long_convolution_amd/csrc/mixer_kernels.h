@@ -33,6 +33,7 @@ struct LinRole {
     float* states;            // [B][H][nseg][DK][DV]: the states that enter the segments (nseg > 1)
     float s_q, s_kv;
     int reverse;
+    int wide;                 // O in fp32 (a sum over shared heads follows), else in the dtype
 };
 
 // Up to three linear attentions over the same tokens in one launch, with one plan (linattn_plan).
@@ -46,7 +47,6 @@ struct LinJob {
     int64_t N, seg_len;
     int kt, nw, ncb, nseg;
     int exact;                // a state leaves the call
-    int wide;                 // every O in fp32 (sums over shared heads follow), else in the dtype
 };
 
 struct LinArgs {
@@ -83,13 +83,21 @@ hipError_t launch_linattn(int dtype, const LinJob& a, hipStream_t stream);
 hipError_t launch_linattn_f32(const LinJob& a, hipStream_t stream);
 hipError_t launch_linattn_f16(const LinJob& a, hipStream_t stream);
 hipError_t launch_linattn_bf16(const LinJob& a, hipStream_t stream);
+hipError_t launch_linattn_bf16_wide(const LinJob& a, hipStream_t stream);   // nw = 2
 // the segments' own states to the states that enter them
 hipError_t launch_linattn_join(const LinJob& a, hipStream_t stream);
 hipError_t launch_linattn_step(int dtype, const LinStepArgs& a, hipStream_t stream);
 hipError_t launch_linattn_tan(int dtype, const LinTanArgs& a, float* dlog, hipStream_t stream);
-// out[b][g][n][:] = sum over the `share` heads of g of the fp32 rows in[b][h][n][:] (dense)
-hipError_t launch_head_sum(int dtype, const float* in, void* out, lconv_strides_t os, int64_t B, int G, int share,
-                           int64_t N, int D, hipStream_t stream);
+// For both of two tensors: out[b][g][n][:] = sum over the `share` heads of g of the fp32 rows in[b][h][n][:] (dense)
+struct HeadSumArgs {
+    const float* in[2];
+    void* out[2];
+    lconv_strides_t os[2];
+    int D[2];
+    int64_t B, N;
+    int G, share;
+};
+hipError_t launch_head_sum(int dtype, const HeadSumArgs& a, hipStream_t stream);
 // state_out = state_in (or zeros) for calls without tokens
 hipError_t launch_copy_state(const float* in, float* out, int64_t n, hipStream_t stream);
 

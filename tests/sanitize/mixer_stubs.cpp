@@ -6,7 +6,7 @@ namespace lcv {
 LCV_STUB(hipError_t launch_linattn(int, const LinJob&, hipStream_t))
 LCV_STUB(hipError_t launch_linattn_step(int, const LinStepArgs&, hipStream_t))
 LCV_STUB(hipError_t launch_linattn_tan(int, const LinTanArgs&, float*, hipStream_t))
-LCV_STUB(hipError_t launch_head_sum(int, const float*, void*, lconv_strides_t, int64_t, int, int, int64_t, int, hipStream_t))
+LCV_STUB(hipError_t launch_head_sum(int, const HeadSumArgs&, hipStream_t))
 LCV_STUB(hipError_t launch_copy_state(const float*, float*, int64_t, hipStream_t))
 LCV_STUB(hipError_t launch_rotary(int, const RotaryArgs&, hipStream_t))
 LCV_STUB(hipError_t launch_layernorm_fwd(int, const NormArgs&, hipStream_t))

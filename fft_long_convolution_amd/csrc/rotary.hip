@@ -1,21 +1,52 @@
 // rotary.hip -- rotary positions of q and k in one launch.
 //
 // (x1, x2) -> m (x1 cos a - x2 sin a, x2 cos a + x1 sin a), a = position * inv_freq[p]: one read and one
-// write of q and k, bound by HBM.  A thread owns 8 pairs of one token (or 16 copied elements) in HEADS heads, whose
-// loads are all on their way while it forms the sines they share; every access is 16 bytes, at any element's alignment (half layouts whose halves do not start
-// on a 16-byte group).  The angle is formed and reduced in fp64: position * inv_freq is exact there for
-// any int32 position, while fp32 would be off by a fifth of a radian at a position of a million.
+// write of q and k, bound by HBM.  A thread owns 8 pairs of one token (or 16 copied elements) in up to four heads,
+// which share the pairs' sines, one head at a time with the next one's loads on their way; every access is 16
+// bytes, at any element's alignment (half layouts whose halves do not start on a 16-byte group).  Measured, 16384
+// tokens of 32 heads of 128, bf16 (268 MB): one head to a thread 70 us, two 54, four 52 (5.1 TB/s, what a copy
+// reaches), eight 52; with two or four heads' loads at a time 49 to 59 by layout.
+// The angle is formed and reduced to a quarter turn in fp64: position * inv_freq is exact there for any int32
+// position, while fp32 would be off by a fifth of a radian at a position of a million.  The sines of what is left,
+// at most pi / 4, are Taylor polynomials in fp32 (next terms: x^11 / 11! < 2e-9, x^12 / 12! < 2e-10).
 #include "mixer_kernels.h"
 #include "mixer_io.h"
 
 namespace lcv {
 namespace {
 
-template <int IO, int HEADS>
-__global__ void __launch_bounds__(256) rotary_kernel(RotaryArgs a, int units, int turns, int hgroups, int64_t total) {
+// 8 elements as they are stored; the first n of them, the others zero
+template <int IO> struct Raw8 { uint4 w[IO == CT_F32 ? 2 : 1]; };
+template <int IO> __device__ __forceinline__ Raw8<IO> raw8_part(const void* base, int64_t i, int n) {
+    Raw8<IO> r;
+    const typename Elem<IO>::T* p = (const typename Elem<IO>::T*)base + i;
+    if (n >= 8) {
+        __builtin_memcpy(&r, p, sizeof(r));
+    } else {
+        typename Elem<IO>::T e[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) e[j] = j < n ? p[j] : 0;
+        __builtin_memcpy(&r, e, sizeof(r));
+    }
+    return r;
+}
+
+__device__ __forceinline__ void sines(double angle, float* s, float* c) {
+    const double q = rint(angle * 0.6366197723675814);           // quarter turns
+    const float x = (float)fma(q, -1.5707963267948966, angle), x2 = x * x;
+    const int n = (int)(q - 4.0 * floor(q * 0.25));
+    const float p = x + x * x2 * (-1.f / 6 + x2 * (1.f / 120 + x2 * (-1.f / 5040 + x2 * (1.f / 362880))));
+    const float r = 1.f + x2 * (-0.5f + x2 * (1.f / 24 + x2 * (-1.f / 720 + x2 * (1.f / 40320 - x2 * (1.f / 3628800)))));
+    const float a = n & 1 ? r : p, b = n & 1 ? p : r;
+    *s = n & 2 ? -a : a;
+    *c = (n + 1) & 2 ? -b : b;
+}
+
+template <int IO>
+__global__ void __launch_bounds__(256) rotary_kernel(RotaryArgs a, int units, int turns, int per, int hgroups, int64_t total) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= total) return;
-    // thread order: units of a head fastest, then heads, then tokens
+    // thread order: units of a token fastest, then groups of heads, then tokens
     const int u = (int)(i % units);
     const int64_t j = i / units;
     const int hg = (int)(j % hgroups);
@@ -32,19 +63,15 @@ __global__ void __launch_bounds__(256) rotary_kernel(RotaryArgs a, int units, in
     const int nlo = !turn ? a.D - lo : inter ? 2 * n : n;
     const int nhi = !turn ? a.D - hi : inter ? 2 * n - 8 : n;
 
-    // the heads' data first, the sines while it is on its way
-    float x[HEADS][16];
-    const int h0 = hg * HEADS, heads = a.H + a.G;
-#pragma unroll
-    for (int k = 0; k < HEADS; ++k) {
-        const int h = h0 + k;
-        if (h >= heads) break;
+    struct Head { Raw8<IO> lo, hi; };
+    const int h0 = hg * per, end = h0 + per < a.H + a.G ? h0 + per : a.H + a.G;
+    const auto load = [&](int h) LCV_INLINE {
         const bool isk = h >= a.H;
         const LinOperand& o = isk ? a.k : a.q;
         const int64_t xi = b * o.s.b + (int64_t)(isk ? h - a.H : h) * o.s.h + t * o.s.n;
-        load8_part<IO>(o.p, xi + lo, nlo, x[k]);
-        load8_part<IO>(o.p, xi + hi, nhi, x[k] + 8);
-    }
+        return Head{raw8_part<IO>(o.p, xi + lo, nlo), raw8_part<IO>(o.p, xi + hi, nhi)};
+    };
+    Head x = load(h0);
     float c[8], s[8];
     if (turn) {
         const int64_t pos = a.positions ? (int64_t)a.positions[b * a.pos_stride + t] : t;
@@ -52,36 +79,35 @@ __global__ void __launch_bounds__(256) rotary_kernel(RotaryArgs a, int units, in
         load8_part<CT_F32>(a.inv_freq, p, n, f);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            double ang = (double)pos * (double)f[k];
-            ang -= 6.283185307179586 * rint(ang * 0.15915494309189535);
-            sincosf((float)ang, &s[k], &c[k]);
+            sines((double)pos * (double)f[k], &s[k], &c[k]);
             c[k] *= a.magnitude;
             s[k] *= a.flags & LCONV_ROTARY_INVERSE ? -a.magnitude : a.magnitude;
         }
     }
-#pragma unroll
-    for (int k = 0; k < HEADS; ++k) {
-        const int h = h0 + k;
-        if (h >= heads) break;
+    for (int h = h0; h < end; ++h) {
+        const Head now = x;
+        if (h + 1 < end) x = load(h + 1);
         const bool isk = h >= a.H;
         const lconv_strides_t ys = isk ? a.yks : a.yqs;
         void* y = isk ? a.yk : a.yq;
         if (!turn && y == (isk ? a.k.p : a.q.p)) continue;     // in place: nothing to copy
-        float z[16];
+        float v[16], z[16];
+        unpack_raw<IO>(now.lo.w, v);
+        unpack_raw<IO>(now.hi.w, v + 8);
         if (!turn) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) z[e] = x[k][e];
+            for (int e = 0; e < 16; ++e) z[e] = v[e];
         } else if (inter) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                z[2 * e] = x[k][2 * e] * c[e] - x[k][2 * e + 1] * s[e];
-                z[2 * e + 1] = x[k][2 * e + 1] * c[e] + x[k][2 * e] * s[e];
+                z[2 * e] = v[2 * e] * c[e] - v[2 * e + 1] * s[e];
+                z[2 * e + 1] = v[2 * e + 1] * c[e] + v[2 * e] * s[e];
             }
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                z[e] = x[k][e] * c[e] - x[k][e + 8] * s[e];
-                z[e + 8] = x[k][e + 8] * c[e] + x[k][e] * s[e];
+                z[e] = v[e] * c[e] - v[e + 8] * s[e];
+                z[e + 8] = v[e + 8] * c[e] + v[e] * s[e];
             }
         }
         const int64_t yi = b * ys.b + (int64_t)(isk ? h - a.H : h) * ys.h + t * ys.n;
@@ -94,13 +120,12 @@ template <int IO>
 void go(const RotaryArgs& a, hipStream_t stream) {
     const int turns = (a.rot / 2 + 7) / 8, units = turns + (a.D - a.rot + 15) / 16, heads = a.H + a.G;
     const int64_t each = a.B * a.N * units;
-    // four heads to a thread where that still gives every compute unit a few waves of them
-    const int per = each * ((heads + 3) / 4) >= 256 * 256 ? 4 : 1;
+    // four heads to a thread where that leaves eight waves to a compute unit
+    int per = 4;
+    while (per > 1 && each * ((heads + per - 1) / per) < 256 * 512) per /= 2;
     const int hgroups = (heads + per - 1) / per;
     const int64_t total = each * hgroups;
-    const unsigned grid = (unsigned)((total + 255) / 256);
-    if (per == 4) rotary_kernel<IO, 4><<<grid, 256, 0, stream>>>(a, units, turns, hgroups, total);
-    else rotary_kernel<IO, 1><<<grid, 256, 0, stream>>>(a, units, turns, hgroups, total);
+    rotary_kernel<IO><<<(unsigned)((total + 255) / 256), 256, 0, stream>>>(a, units, turns, per, hgroups, total);
 }
 
 }  // namespace

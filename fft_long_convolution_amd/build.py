@@ -23,7 +23,7 @@ ARCH = "gfx950"
 HIP_SOURCES = ["fused1d_conv.hip", "fused1d_adj.hip", "fused1d_part.hip", "fused1d_sparse.hip", "fused1d_save.hip",
                "fused1d.hip", "bwd1d.hip", "multipass.hip", "fftconv2d.hip", "fftconv3d.hip",
                "stage.hip", "ssm.hip", "noalloc.hip", "colmx.hip", "butterfly.hip", "fused1d_lbf.hip",
-               "linattn.hip", "linattn_f32.hip", "linattn_f16.hip", "linattn_bf16.hip", "linattn_bf16_wide.hip",
+               "linattn.hip", "linattn_f32.hip", "linattn_f16.hip", "linattn_bf16.hip", "linattn_bf16_wide.hip", "linattn_tan.hip",
                "rotary.hip", "layernorm.hip"]
 CPP_SOURCES = ["plan.cpp", "lconv_api.cpp", "mixer_api.cpp"]
 COMMON = ["-O3", "-fPIC", "-std=c++17", "-I", INCLUDE, "-I", CSRC, "-Wall", "-Wno-unused-function"]

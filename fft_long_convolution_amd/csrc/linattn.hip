@@ -6,63 +6,6 @@
 namespace lcv {
 namespace {
 
-// The tangent of the state along log_decay, token by token: T_t = gamma (T_{t-1} + S_{t-1}).  A
-// workgroup holds 64 columns of S and T, thread (part, col) rows part * 64 .. part * 64 + 63 of its
-// column in registers; the partial sums of s_q (T^T dy_t) . q_t leave it as one number.
-template <int IO>
-__global__ void __launch_bounds__(256) linattn_tan_kernel(LinTanArgs ta) {
-    const LinArgs& a = ta.a;
-    const LinRole& r = a.r;
-    __shared__ float red[4][64];
-    const int col = threadIdx.x & 63, part = threadIdx.x >> 6;
-    const int ncol = (r.DV + 63) / 64;
-    const int64_t bh = blockIdx.x / ncol;
-    const int64_t b = bh / a.H;
-    const int h = (int)(bh - b * a.H), n = (int)(blockIdx.x - bh * ncol) * 64 + col;
-    const int64_t len = row_len(a.lengths, b, a.N);
-    const int64_t qb = row_base(r.Q, b, h), kb = row_base(r.K, b, h), vb = row_base(r.V, b, h), tb = row_base(ta.q, b, h);
-    const int64_t sb = bh * r.DK * r.DV + (int64_t)n * r.s_col;
-    const float gamma = expf(log_gamma(a.log_decay, h));
-    const bool on = n < r.DV;
-    float S[64], T[64], tan = 0.f;
-#pragma unroll
-    for (int i = 0; i < 64; ++i) {
-        const int d = part * 64 + i;
-        S[i] = r.s_in && on && d < r.DK ? r.s_in[sb + (int64_t)d * r.s_row] : 0.f;
-        T[i] = 0.f;
-    }
-    for (int64_t t = 0; t < len; ++t) {
-        const float v = on ? load1<IO>(r.V.p, vb + t * r.V.s.n + n) : 0.f;
-        float acc = 0.f;
-#pragma unroll
-        for (int j = 0; j < 64; ++j) {
-            const int d = part * 64 + j;
-            if (d < r.DK) {
-                T[j] = gamma * (T[j] + S[j]);
-                acc += T[j] * load1<IO>(r.Q.p, qb + t * r.Q.s.n + d);
-                S[j] = gamma * S[j] + load1<IO>(r.K.p, kb + t * r.K.s.n + d) * v;
-            }
-        }
-        if (on) tan += r.s_q * acc * load1<IO>(ta.q.p, tb + t * ta.q.s.n + n);
-    }
-    // <T, dstate_out>: the transposed layout, element (d, n) at n * DK + d
-    if (ta.ds_out && on) {
-#pragma unroll
-        for (int j = 0; j < 64; ++j) {
-            const int d = part * 64 + j;
-            if (d < r.DK) tan += T[j] * ta.ds_out[bh * r.DK * r.DV + (int64_t)n * r.DK + d];
-        }
-    }
-    red[part][col] = tan;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        float s = 0.f;
-        for (int p = 0; p < 4; ++p)
-            for (int c = 0; c < 64; ++c) s += red[p][c];
-        ta.part[((int64_t)h * a.B + b) * ncol + (blockIdx.x - bh * ncol)] = s;
-    }
-}
-
 // Slot s of a row's states holds what segment s - 1 added up from zero; it becomes the state that
 // enters segment s, slot 0 the state that enters the row.  Four columns to a thread.
 __global__ void __launch_bounds__(256) linattn_join_kernel(LinJob a) {
@@ -157,13 +100,6 @@ __global__ void __launch_bounds__(256) linattn_step_kernel(LinStepArgs a) {
     }
 }
 
-__global__ void __launch_bounds__(64) tan_sum_kernel(const float* part, float* dlog, int64_t n) {
-    float s = 0.f;
-    for (int64_t i = threadIdx.x; i < n; i += 64) s += part[blockIdx.x * n + i];
-    for (int w = 32; w; w >>= 1) s += __shfl_xor(s, w);
-    if (threadIdx.x == 0) dlog[blockIdx.x] = s;
-}
-
 template <int IO>
 __global__ void __launch_bounds__(256) head_sum_kernel(HeadSumArgs a) {
     const int which = blockIdx.y, D = a.D[which], share = a.share, G = a.G;
@@ -216,15 +152,6 @@ hipError_t launch_linattn_join(const LinJob& a, hipStream_t stream) {
         if (n > most) most = n;
     }
     linattn_join_kernel<<<dim3((unsigned)((most + 255) / 256), a.nroles), 256, 0, stream>>>(a);
-    return hipGetLastError();
-}
-
-hipError_t launch_linattn_tan(int dtype, const LinTanArgs& t, float* dlog, hipStream_t stream) {
-    const int nb = linattn_tan_blocks(t.a.r.DV);
-    const unsigned grid = (unsigned)(t.a.B * t.a.H * nb);
-    const hipError_t e = by_dtype(dtype, [&](auto io) { linattn_tan_kernel<io.value><<<grid, 256, 0, stream>>>(t); });
-    if (e != hipSuccess) return e;
-    tan_sum_kernel<<<(unsigned)t.a.H, 64, 0, stream>>>(t.part, dlog, t.a.B * nb);
     return hipGetLastError();
 }
 

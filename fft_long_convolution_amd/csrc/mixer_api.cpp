@@ -139,8 +139,13 @@ BwdPlan bwd_plan(int64_t B, int64_t H, int64_t N, int64_t Dk, int64_t Dv, lconv_
     return p;
 }
 
-size_t tan_bytes(int64_t B, int64_t H, int64_t Dk) {
-    return round256((size_t)(B * H) * (size_t)linattn_tan_blocks((int)Dk) * 4);
+// the decay's gradient: partial sums, and the segments' states
+size_t tan_part_bytes(int64_t rows, int64_t N, int64_t Dv) {
+    return round256((size_t)(rows * linattn_tan_plan(rows, N, Dv).nseg) * (size_t)linattn_tan_blocks(Dv) * 4);
+}
+size_t tan_bytes(int64_t rows, int64_t N, int64_t Dk, int64_t Dv) {
+    const int nseg = linattn_tan_plan(rows, N, Dv).nseg;
+    return tan_part_bytes(rows, N, Dv) + (nseg > 1 ? round256((size_t)(rows * nseg) * 2 * (size_t)(Dk * Dv) * 4) : 0);
 }
 
 }  // namespace
@@ -205,7 +210,7 @@ lconv_status_t lconv_linattn_fwd(const void* q, const lconv_strides_t* q_strides
 size_t lconv_linattn_bwd_workspace_bytes(int64_t B, int64_t H, int64_t G, int64_t N, int64_t Dk, int64_t Dv,
                                          lconv_dtype_t dtype) {
     if (!dtype_ok(dtype) || B <= 0 || H <= 0 || N <= 0 || !linattn_dims_ok(B, H, G, N, Dk, Dv)) return 0;
-    return head_grads_bytes(B, H, G, N, Dk) + head_grads_bytes(B, H, G, N, Dv) + tan_bytes(B, H, Dk) +
+    return head_grads_bytes(B, H, G, N, Dk) + head_grads_bytes(B, H, G, N, Dv) + tan_bytes(B * H, N, Dk, Dv) +
            bwd_plan(B, H, N, Dk, Dv, dtype).total;
 }
 
@@ -261,8 +266,9 @@ lconv_status_t lconv_linattn_bwd(const void* dy, const lconv_strides_t* dy_strid
     ws += head_grads_bytes(B, H, G, N, Dv);
 
     const BwdPlan plan = bwd_plan(B, H, N, Dk, Dv, dtype);
-    float* tan = (float*)ws;
-    ws += tan_bytes(B, H, Dk);
+    float* const tan = (float*)ws;
+    float* const tan_states = (float*)(ws + tan_part_bytes(B * H, N, Dv));
+    ws += tan_bytes(B * H, N, Dk, Dv);
 
     LinJob a{};
     a.log_decay = log_decay; a.lengths = lengths;
@@ -306,11 +312,14 @@ lconv_status_t lconv_linattn_bwd(const void* dy, const lconv_strides_t* dy_strid
         if (launch_linattn(dtype, a, stream) != hipSuccess) return LCONV_ERR_HIP;
     }
     if (dlog_decay) {
+        const LinTanPlan p = linattn_tan_plan(B * H, N, Dv);
         LinTanArgs t{};
-        t.a.r = rdq_;
-        t.a.log_decay = log_decay; t.a.lengths = lengths;
-        t.a.B = B; t.a.H = (int)H; t.a.N = N;
-        t.q = oq; t.ds_out = dstate_out; t.part = tan;
+        t.q = oq; t.k = ok; t.v = ov; t.dy = ody;
+        t.s_in = state_in; t.ds_out = dstate_out;
+        t.log_decay = log_decay; t.lengths = lengths;
+        t.states = tan_states; t.part = tan; t.scale = scale;
+        t.B = B; t.N = N; t.seg_len = p.seg_len; t.nseg = p.nseg;
+        t.H = (int)H; t.DK = (int)Dk; t.DV = (int)Dv;
         if (launch_linattn_tan(dtype, t, dlog_decay, stream) != hipSuccess) return LCONV_ERR_HIP;
     }
     if (share > 1) {

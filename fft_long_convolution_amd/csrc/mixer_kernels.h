@@ -49,15 +49,6 @@ struct LinJob {
     int exact;                // a state leaves the call
 };
 
-struct LinArgs {
-    LinRole r;
-    const float* log_decay;   // [H]
-    const int32_t* lengths;   // [B] or NULL
-    int64_t B;
-    int H;
-    int64_t N;
-};
-
 struct LinStepArgs {
     LinOperand q, k, v;       // strides' n unused
     void* y;
@@ -70,13 +61,17 @@ struct LinStepArgs {
     int H, DK, DV;
 };
 
-// d/dlog_decay: the tangent T_t = gamma (T_{t-1} + S_{t-1}) of the state, in the transposed roles
-// of dq (Q = dy, K = v, V = k): partial sums of s_q (T^T dy_t) . q_t + <T, dstate_out>.
+// The decay's gradient: see linattn_tan.hip.  nseg and seg_len from linattn_tan_plan.
 struct LinTanArgs {
-    LinArgs a;                // the role of dq
-    LinOperand q;
-    const float* ds_out;      // [B][H][Dk][Dv] or NULL
-    float* part;              // [H][B][blocks]
+    LinOperand q, k, v, dy;
+    const float *s_in, *ds_out;   // [B][H][DK][DV] or NULL
+    const float* log_decay;       // [H]
+    const int32_t* lengths;       // [B] or NULL
+    float* states;                // [B][H][nseg][2][DK][DV] (nseg > 1)
+    float* part;                  // [H][B][nseg][column blocks]
+    float scale;
+    int64_t B, N, seg_len;
+    int H, DK, DV, nseg;
 };
 
 hipError_t launch_linattn(int dtype, const LinJob& a, hipStream_t stream);

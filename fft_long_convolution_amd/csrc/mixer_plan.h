@@ -69,8 +69,19 @@ inline size_t linattn_states_bytes(const LinPlan& p, int64_t rows, int64_t DK, i
     return p.nseg > 1 ? ((size_t)rows * (size_t)p.nseg * (size_t)(DK * DV) * 4 + 255) / 256 * 256 : 0;
 }
 
-// column blocks of the decay's gradient
+// The decay's gradient: column blocks, and segments of at least eight chunks until two workgroups to a compute unit.
+#ifdef __HIPCC__
+__host__ __device__
+#endif
 inline int linattn_tan_blocks(int64_t DV) { return (int)((DV + 63) / 64); }
+struct LinTanPlan { int nseg; int64_t seg_len; };
+inline LinTanPlan linattn_tan_plan(int64_t rows, int64_t N, int64_t DV) {
+    const int64_t chunks = (N + 31) / 32, wgs = rows * linattn_tan_blocks(DV);
+    int64_t nseg = 1;
+    while (nseg * 16 <= chunks && wgs * nseg * 2 <= 512) nseg *= 2;
+    const int64_t len = (chunks + nseg - 1) / nseg * 32;
+    return LinTanPlan{(int)((N + len - 1) / len), len};
+}
 
 // Layer norm: rows up to this width are held in registers.
 constexpr int64_t kNormRegisterC = 8192;

@@ -45,7 +45,12 @@ __global__ void __launch_bounds__(256, KT > 8 || (IO == CT_F32 && NW == 2) ? 1 :
     constexpr int QB = STATE ? 0 : C * RK * 16, KB = C * RK * 16, STAGE = QB + KB + C * RV * 16;
     constexpr int NK = C * RK / 256, NV = C * RV / 256;         // loads of a chunk: rounds of 4 waves x 64 lanes
     constexpr bool KHALF = NK == 0;                             // a narrow tile takes two waves
-    constexpr int NKR = KHALF ? 1 : NK, LOADS = (STATE ? 1 : 2) * NKR + NV, STORES = STATE ? 0 : CT * NW;   // of a wave
+    constexpr int NKR = KHALF ? 1 : NK, LOADS = (STATE ? 1 : 2) * NKR + NV;   // of a wave
+    // 16-bit data at NW = 2 deals a wave's columns to its two tiles in fours: a lane's accumulators are then 8
+    // neighbours of a token, one 16-byte store, of which four lanes make 64 bytes (gradients of 128 rows of 2048
+    // tokens 166 us; with stores of 8 bytes, 32 to a token, 182).
+    constexpr bool FOURS = IO != CT_F32 && NW == 2;
+    constexpr int PUTS = FOURS ? CT : CT * NW, STORES = STATE ? 0 : PUTS;     // of a wave; a wide FOURS put takes two
     static_assert(NV >= 1 && (NK >= 1 || C * RK == 128), "rounds of whole waves");
     // chunks in LDS: one in hand, and two on their way where a compute unit then still holds the workgroups
     // that its registers allow (NW = 1: three, which hide each other's loads)
@@ -76,6 +81,7 @@ __global__ void __launch_bounds__(256, KT > 8 || (IO == CT_F32 && NW == 2) ? 1 :
 
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, g = lane >> 4, x = lane & 15;
     const int wcol = cb * DVB + wave * 16 * NW;             // the wave's first column
+    const auto column = [&](int n) LCV_INLINE { return wcol + (FOURS ? 8 * (x >> 2) + 4 * n + (x & 3) : 16 * n + x); };   // tile n's column x
     const int64_t ob = b * r.o.b + (int64_t)h * r.o.h;
 
     const bool wide = IO == CT_F32 || (WIDE && r.wide);
@@ -119,7 +125,7 @@ __global__ void __launch_bounds__(256, KT > 8 || (IO == CT_F32 && NW == 2) ? 1 :
         for (int t = 0; t < KT; ++t)
 #pragma unroll
             for (int n = 0; n < NW; ++n) {
-                const int d = M::state_row(t, g), c = wcol + 16 * n + x;
+                const int d = M::state_row(t, g), c = column(n);
                 f32x4 v = {0.f, 0.f, 0.f, 0.f};
                 if (s && d < r.DK && c < r.DV) {
                     if (srow == 1) {
@@ -211,11 +217,12 @@ __global__ void __launch_bounds__(256, KT > 8 || (IO == CT_F32 && NW == 2) ? 1 :
     };
 
     const typename M::At lk = M::at(g, x, RK), lv = M::at(g, x, RV);
-    // the output likewise: lane x's token, the first of its four columns; token tiles of 16 and column tiles
+    // the output likewise: lane x's token, the first of its columns; token tiles of 16 and column tiles
     // are steps of the scalar
     char* po = STATE ? nullptr : (char*)r.O + (ob + low * r.o.n) * osz;
     const int64_t d_o = dir * r.o.n * osz, o16 = 16 * r.o.n * osz;
-    const uint32_t oo = (uint32_t)(r.reverse ? 15 - x : x) * (uint32_t)(r.o.n * osz) + (uint32_t)((wcol + 4 * g) * osz);
+    const int mine = wcol + (FOURS ? 8 : 4) * g;
+    const uint32_t oo = (uint32_t)(r.reverse ? 15 - x : x) * (uint32_t)(r.o.n * osz) + (uint32_t)(mine * osz);
 
     float em1 = 0.f;
     const auto weigh = [&](int c) LCV_INLINE {
@@ -231,11 +238,16 @@ __global__ void __launch_bounds__(256, KT > 8 || (IO == CT_F32 && NW == 2) ? 1 :
     };
 
     f32x4 acc[CT][NW];
-    const auto put = [&](int it, int n) LCV_INLINE {
+    const auto put = [&](int i) LCV_INLINE {
+        const int it = FOURS ? i : i / NW, n = FOURS ? 0 : i % NW;
         const __amdgpu_buffer_rsrc_t o = buffer_at(po + (r.reverse ? CT - 1 - it : it) * o16 + 16 * n * osz);
-        const f32x4 y = acc[it][n];
+        const f32x4 y = acc[it][n], y2 = acc[it][NW - 1];
         if (wide) {
             __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, y), o, oo, 0, 0);
+            if constexpr (FOURS) __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, y2), o, oo + 16, 0, 0);
+        } else if constexpr (FOURS) {
+            const u32x4 w = {pack2<IO>(y[0], y[1]), pack2<IO>(y[2], y[3]), pack2<IO>(y2[0], y2[1]), pack2<IO>(y2[2], y2[3])};
+            __builtin_amdgcn_raw_buffer_store_b128(w, o, oo, 0, 0);
         } else if constexpr (IO != CT_F32) {
             typedef uint32_t u32x2 __attribute__((__vector_size__(8)));
             const u32x2 w = {pack2<IO>(y[0], y[1]), pack2<IO>(y[2], y[3])};
@@ -245,10 +257,8 @@ __global__ void __launch_bounds__(256, KT > 8 || (IO == CT_F32 && NW == 2) ? 1 :
     const auto emit = [&](int c) LCV_INLINE {
         if constexpr (!STATE) {
 #pragma unroll
-            for (int it = 0; it < CT; ++it)
-#pragma unroll
-                for (int n = 0; n < NW; ++n)
-                    if (16 * it + x < c && wcol + 16 * n + 4 * g < r.DV) put(it, n);
+            for (int i = 0; i < PUTS; ++i)
+                if (16 * (FOURS ? i : i / NW) + x < c && mine + (FOURS ? 0 : 16 * (i % NW)) < r.DV) put(i);
             po += d_o;
         }
     };
@@ -262,7 +272,10 @@ __global__ void __launch_bounds__(256, KT > 8 || (IO == CT_F32 && NW == 2) ? 1 :
 #pragma unroll
         for (int j = 0; j < CJ; ++j)
 #pragma unroll
-            for (int n = 0; n < NW; ++n) vf[j][n] = M::load_v(Lv + j * TK * 16 * RV * 16, lv, wave * NW + n, RV);
+            for (int n = 0; n < NW; ++n) {
+                const char* const v = Lv + j * TK * 16 * RV * 16;
+                vf[j][n] = FOURS ? M::load_kt(v, lv, wave * NW + n, RV) : M::load_v(v, lv, wave * NW + n, RV);
+            }
 
         // gamma^.. V in parts that add up to its fp32 value
         constexpr int PARTS = IO == CT_F32 ? 1 : IO == CT_F16 || !EXACT ? 2 : 3;
@@ -406,7 +419,7 @@ __global__ void __launch_bounds__(256, KT > 8 || (IO == CT_F32 && NW == 2) ? 1 :
             if constexpr (FULL && STATE) {
                 static_for<t * LOADS / KT, (t + 1) * LOADS / KT>([&](auto i) LCV_INLINE { piece(i, then); });
             } else if constexpr (FULL) {
-                static_for<t * STORES / KT, (t + 1) * STORES / KT>([&](auto i) LCV_INLINE { put(i.value / NW, i.value % NW); });
+                static_for<t * PUTS / KT, (t + 1) * PUTS / KT>([&](auto i) LCV_INLINE { put(i.value); });
             }
         });
         if constexpr (FULL) {
@@ -424,14 +437,15 @@ __global__ void __launch_bounds__(256, KT > 8 || (IO == CT_F32 && NW == 2) ? 1 :
         if (STAGES == 3 && left > C) fetch(lds1, left - C);
     }
     // STAGES chunks a turn, each stage by its own name: then the compiler knows which loads a read waits for.
-    // What may be outstanding is, with three stages, the next chunk's loads and the last one's stores, with two
-    // the last one's stores.
+    // Operations are counted in their order.  With three stages a chunk's loads are older than the stores of the two
+    // chunks before it and the next chunk's loads, which may all be outstanding; with two stages older than the last
+    // chunk's stores.  The first two chunks' loads have no such stores behind them and are waited for ahead of the loop.
     constexpr int LAST = STAGES == 3 ? 5 : 3;
     if (whole && left >= LAST * C) {
         std::integral_constant<bool, true> full;
-        wait_for_all_but<STAGES == 3 ? LOADS : 0>();
+        wait_for_all_but<0>();
         const auto turn = [&](char* now, char* then) LCV_INLINE {
-            wait_for_all_but<STAGES == 3 ? LOADS + STORES : STORES>();
+            wait_for_all_but<STAGES == 3 ? LOADS + 2 * STORES : STORES>();
             barrier_only();
             chunk(full, now, then);
         };
@@ -482,7 +496,7 @@ __global__ void __launch_bounds__(256, KT > 8 || (IO == CT_F32 && NW == 2) ? 1 :
         for (int t = 0; t < KT; ++t)
 #pragma unroll
             for (int n = 0; n < NW; ++n) {
-                const int d = M::state_row(t, g), c = wcol + 16 * n + x;
+                const int d = M::state_row(t, g), c = column(n);
                 if (d >= r.DK || c >= r.DV) continue;
                 if (srow == 1) {
                     *(f32x4*)(s + (int64_t)c * scol + d) = S[t][n];

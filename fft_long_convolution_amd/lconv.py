@@ -760,9 +760,17 @@ def _at(dev, stream):
     torch = _torch()
     if stream is not None:
         return torch.cuda.stream(stream), stream.cuda_stream     # also makes its device the current one
-    if dev == torch.cuda.current_device():
-        return _HERE, torch.cuda.current_stream().cuda_stream
-    return torch.cuda.device(dev), torch.cuda.current_stream(dev).cuda_stream
+    raw = _raw_stream()(dev)
+    return (_HERE if dev == torch.cuda.current_device() else torch.cuda.device(dev)), raw
+
+
+@functools.lru_cache(maxsize=None)
+def _raw_stream():
+    """The call that gives a device's current stream as a raw handle: torch's direct one (0.2 us) where this torch has
+    it, else through a Stream object (2.8 us, a fifth of a single-token call)."""
+    torch = _torch()
+    direct = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return direct or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _same_gpu(names, operands):
@@ -850,6 +858,8 @@ def _outputs(name, t, shape, like):
     """An output given by the caller, or a new one in `like`'s order: (tensor, strides)."""
     if t is None:
         torch = _torch()
+        if like.is_contiguous() and like.shape == shape:
+            return torch.empty_like(like), None
         if len(shape) == 3 or like.is_contiguous():
             return torch.empty(shape, dtype=like.dtype, device=like.device), None
         t = _in_order_of(like, shape)
@@ -1065,7 +1075,7 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, need_stats=True, out=None, s
     ctx, st = _at(dev, stream)
     with ctx:
         y = torch.empty(x.shape, dtype=x.dtype, device=dev) if out is None else out
-        ys = _rows("out", y, x.shape, x.dtype)[2]
+        ys = C if out is None else _rows("out", y, x.shape, x.dtype)[2]
         mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev) if need_stats else None
         rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev) if need_stats else None
         _check(lconv_layernorm_fwd(_ptr(x), xs, _ptr(weight), _ptr(bias), _ptr(y), ys, _ptr(mean), _ptr(rstd), rows, C,
@@ -1090,7 +1100,7 @@ def layer_norm_bwd(dy, x, weight, mean, rstd, need_dweight=True, need_dbias=True
     ctx, st = _at(dev, stream)
     with ctx:
         dx = torch.empty(x.shape, dtype=x.dtype, device=dev) if out is None else out
-        dxs = _rows("out", dx, x.shape, x.dtype)[2]
+        dxs = C if out is None else _rows("out", dx, x.shape, x.dtype)[2]
         dw = torch.empty((C,), dtype=torch.float32, device=dev) if need_dweight and weight is not None else None
         db = torch.empty((C,), dtype=torch.float32, device=dev) if need_dbias else None
         wsb = lconv_layernorm_bwd_workspace_bytes(rows, C) if dw is not None or db is not None else 0

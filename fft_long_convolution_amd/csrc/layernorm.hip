@@ -3,9 +3,11 @@
 //   y = (x - mean) rstd w + b;   with xhat = (x - mean) rstd and h = dy w:
 //   dx = rstd (h - mean_C(h) - xhat mean_C(h xhat)),  dw = sum_rows dy xhat,  db = sum_rows dy
 // Both are bound by HBM: x (and dy) are read once, y (dx) written once.  A row lives in the registers of
-// LANES lanes of one wave (C <= 4096) or of one workgroup (C <= 8192), 8-element groups dealt out in
+// LANES lanes of one wave (C <= 2048) or of one workgroup (C <= 8192), 8-element groups dealt out in
 // turn, so the sums need no second read; longer rows are read again through the caches.  Waves walk the
 // rows with the weight (and, in the gradient, the column sums of their rows) held in registers.
+// Measured, 16384 rows of 4096 in bf16: forward 52 us (5.2 TB/s, what a copy reaches), gradient 83 us (4.8 TB/s with the
+// workgroups' column sums) and 7 us for their sum; 333 rows of 1001 in fp32: 5.2, 7.5 and 3.2 us (latency).
 //
 // The mean takes two sums: the first is off by the rounding of adding up the values themselves, what is
 // left of it shows in the sum of the centred values and is taken out of mean and variance.

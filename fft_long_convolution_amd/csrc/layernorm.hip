@@ -3,7 +3,7 @@
 //   y = (x - mean) rstd w + b;   with xhat = (x - mean) rstd and h = dy w:
 //   dx = rstd (h - mean_C(h) - xhat mean_C(h xhat)),  dw = sum_rows dy xhat,  db = sum_rows dy
 // Both are bound by HBM: x (and dy) are read once, y (dx) written once.  A row lives in the registers of
-// LANES lanes of one wave (C <= 2048) or of one workgroup (C <= 8192), 8-element groups dealt out in
+// LANES lanes of one wave (C <= 1024) or of several (C <= 8192), 8-element groups dealt out in
 // turn, so the sums need no second read; longer rows are read again through the caches.  Waves walk the
 // rows with the weight (and, in the gradient, the column sums of their rows) held in registers.
 // Measured, 16384 rows of 4096 in bf16: forward 52 us (5.2 TB/s, what a copy reaches), gradient 83 us (4.8 TB/s with the
@@ -18,19 +18,33 @@
 namespace lcv {
 namespace {
 
-template <int LANES> __device__ __forceinline__ float row_sum(float v, float* red) {
+// Two sums over a row's lanes.  Rows of several waves join through red, which two sums in a row must not share: then one
+// barrier is enough, since the next one is passed only once every wave has read.
+template <int LANES> struct RowRed { float v[2][2][LANES > 64 ? (LANES < 256 ? 256 : LANES) / 64 : 1]; };   // by wave of the workgroup
+template <int LANES> __device__ __forceinline__ void row_sums(float& a, float& b, RowRed<LANES>& red, int which) {
     constexpr int W = LANES < 64 ? LANES : 64;
 #pragma unroll
-    for (int w = W / 2; w; w >>= 1) v += __shfl_xor(v, w);
-    if constexpr (LANES > 64) {
-        __syncthreads();
-        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-        __syncthreads();
-        v = red[0];
-#pragma unroll
-        for (int i = 1; i < LANES / 64; ++i) v += red[i];
+    for (int w = W / 2; w; w >>= 1) {
+        a += __shfl_xor(a, w);
+        b += __shfl_xor(b, w);
     }
-    return v;
+    if constexpr (LANES > 64) {
+        constexpr int N = LANES / 64;
+        const int wave = threadIdx.x >> 6, first = wave / N * N;     // of the row
+        float *const f = red.v[which][0], *const e = red.v[which][1];
+        if ((threadIdx.x & 63) == 0) {
+            f[wave] = a;
+            e[wave] = b;
+        }
+        __syncthreads();
+        a = f[first];
+        b = e[first];
+#pragma unroll
+        for (int i = 1; i < N; ++i) {
+            a += f[first + i];
+            b += e[first + i];
+        }
+    }
 }
 
 // raw 8-element groups of a row: group k of lane l is elements 8 (l + LANES k) ..
@@ -53,9 +67,9 @@ template <int IO> __device__ __forceinline__ Group<IO> load_group(const void* p,
 __device__ __forceinline__ int left(int c, int C) { return C - c < 8 ? C - c : 8; }
 
 template <int IO, int LANES, int K>
-__global__ void __launch_bounds__(256) ln_fwd_kernel(NormArgs a) {
-    __shared__ float red[4];
-    constexpr int ROWS = 256 / LANES;            // rows a workgroup has in hand
+__global__ void __launch_bounds__(LANES < 256 ? 256 : LANES) ln_fwd_kernel(NormArgs a) {
+    __shared__ RowRed<LANES> red;
+    constexpr int ROWS = LANES < 256 ? 256 / LANES : 1;      // rows a workgroup has in hand
     const int lane = threadIdx.x % LANES, C = (int)a.C;
     const float inv = 1.f / (float)C;
     Group<IO> w[K], b[K];
@@ -78,8 +92,9 @@ __global__ void __launch_bounds__(256) ln_fwd_kernel(NormArgs a) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) s += x[k][i];
         }
-        const float first = row_sum<LANES>(s, red) * inv;
-        float s1 = 0.f, s2 = 0.f;
+        float none = 0.f, s1 = 0.f, s2 = 0.f;
+        row_sums<LANES>(s, none, red, 0);
+        const float first = s * inv;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int n = left(8 * (lane + LANES * k), C);
@@ -90,8 +105,8 @@ __global__ void __launch_bounds__(256) ln_fwd_kernel(NormArgs a) {
                 s2 += x[k][i] * x[k][i];
             }
         }
-        const float rest = row_sum<LANES>(s1, red) * inv;
-        const float var = fmaxf(row_sum<LANES>(s2, red) * inv - rest * rest, 0.f);
+        row_sums<LANES>(s1, s2, red, 1);
+        const float rest = s1 * inv, var = fmaxf(s2 * inv - rest * rest, 0.f);
         const float rstd = 1.f / sqrtf(var + a.eps);
         if (!on) continue;
 #pragma unroll
@@ -123,7 +138,7 @@ __global__ void __launch_bounds__(256) ln_fwd_kernel(NormArgs a) {
 // Rows too long for registers: three passes through the caches, one workgroup to a row.
 template <int IO>
 __global__ void __launch_bounds__(256) ln_fwd_long_kernel(NormArgs a) {
-    __shared__ float red[4];
+    __shared__ RowRed<256> red;
     const int C = (int)a.C;
     const float inv = 1.f / (float)C;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
@@ -134,8 +149,9 @@ __global__ void __launch_bounds__(256) ln_fwd_long_kernel(NormArgs a) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) s += x[i];
         }
-        const float first = row_sum<256>(s, red) * inv;
-        float s1 = 0.f, s2 = 0.f;
+        float none = 0.f, s1 = 0.f, s2 = 0.f;
+        row_sums<256>(s, none, red, 0);
+        const float first = s * inv;
         for (int c = 8 * threadIdx.x; c < C; c += 2048) {
             const int n = left(c, C);
             load8_part<IO>(a.x, xo + c, n, x);
@@ -146,8 +162,8 @@ __global__ void __launch_bounds__(256) ln_fwd_long_kernel(NormArgs a) {
                 s2 += d * d;
             }
         }
-        const float rest = row_sum<256>(s1, red) * inv;
-        const float var = fmaxf(row_sum<256>(s2, red) * inv - rest * rest, 0.f);
+        row_sums<256>(s1, s2, red, 1);
+        const float rest = s1 * inv, var = fmaxf(s2 * inv - rest * rest, 0.f);
         const float rstd = 1.f / sqrtf(var + a.eps);
         for (int c = 8 * threadIdx.x; c < C; c += 2048) {
             const int n = left(c, C);
@@ -176,9 +192,9 @@ __global__ void __launch_bounds__(256) ln_fwd_long_kernel(NormArgs a) {
 // The gradient: dx of every row, and the column sums of the workgroup's rows to part[0 / 1][block][C].
 // A row is read before it is written, so dx may stand in place of dy or x.
 template <int IO, int LANES, int K>
-__global__ void __launch_bounds__(256) ln_bwd_kernel(NormArgs a) {
-    __shared__ float red[4];
-    constexpr int ROWS = 256 / LANES;
+__global__ void __launch_bounds__(LANES < 256 ? 256 : LANES) ln_bwd_kernel(NormArgs a) {
+    __shared__ RowRed<LANES> red;
+    constexpr int ROWS = LANES < 256 ? 256 / LANES : 1;
     const int lane = threadIdx.x % LANES, C = (int)a.C;
     const float inv = 1.f / (float)C;
     const bool sums = a.part != nullptr;
@@ -190,7 +206,8 @@ __global__ void __launch_bounds__(256) ln_bwd_kernel(NormArgs a) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) sw[k][i] = sb[k][i] = 0.f;
     }
-    for (int64_t r0 = (int64_t)blockIdx.x * ROWS; r0 < a.rows; r0 += (int64_t)gridDim.x * ROWS) {
+    int which = 0;
+    for (int64_t r0 = (int64_t)blockIdx.x * ROWS; r0 < a.rows; r0 += (int64_t)gridDim.x * ROWS, which ^= 1) {
         const int64_t row = r0 + threadIdx.x / LANES, at = row < a.rows ? row : 0;
         const bool on = row < a.rows;
         const float mean = a.mean[at], rstd = a.rstd[at];
@@ -220,8 +237,9 @@ __global__ void __launch_bounds__(256) ln_bwd_kernel(NormArgs a) {
                 s2 += g[k][i] * xh[k][i];
             }
         }
-        s1 = row_sum<LANES>(s1, red) * inv;
-        s2 = row_sum<LANES>(s2, red) * inv;
+        row_sums<LANES>(s1, s2, red, which);
+        s1 *= inv;
+        s2 *= inv;
         if (!on) continue;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
@@ -271,10 +289,11 @@ __global__ void __launch_bounds__(256) ln_bwd_kernel(NormArgs a) {
 
 template <int IO>
 __global__ void __launch_bounds__(256) ln_dx_long_kernel(NormArgs a) {
-    __shared__ float red[4];
+    __shared__ RowRed<256> red;
+    int which = 0;
     const int C = (int)a.C;
     const float inv = 1.f / (float)C;
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, which ^= 1) {
         const float mean = a.mean[row], rstd = a.rstd[row];
         float s1 = 0.f, s2 = 0.f, x[8], g[8], p[8];
         const auto load = [&](int c, int n) LCV_INLINE {
@@ -296,8 +315,9 @@ __global__ void __launch_bounds__(256) ln_dx_long_kernel(NormArgs a) {
                 s2 += g[i] * x[i];
             }
         }
-        s1 = row_sum<256>(s1, red) * inv;
-        s2 = row_sum<256>(s2, red) * inv;
+        row_sums<256>(s1, s2, red, which);
+        s1 *= inv;
+        s2 *= inv;
         for (int c = 8 * threadIdx.x; c < C; c += 2048) {
             const int n = left(c, C);
             load(c, n);
@@ -362,16 +382,20 @@ template <typename F> hipError_t by_dtype(int dtype, F&& f) {
     return hipGetLastError();
 }
 
-// f(lanes, groups per lane) for rows of C <= 8192
-template <typename F> void by_width(int64_t C, F&& f) {
+// f(lanes, groups per lane) for rows of C <= 8192: as few lanes as hold two groups each of the widest row, since every
+// further wave adds a step to the sums.  Measured (bf16, us, forward / gradient): 65536 rows of 128, 16 lanes 10 / 21,
+// 64 lanes 25 / 56; 32768 of 1024, 64 lanes 24 / 44, 128 lanes 26 / 44, 256 lanes 49 / 57; 16384 of 2048, 64 lanes with
+// four groups 25 / 46 (of 1500: 27 / 56), 128 lanes 25 / 46 (28 / 51); 16384 of 4096, 256 lanes 47 / 89, 512 lanes 52 / 82;
+// 8192 of 8192, 256 lanes with four groups 45 / 103, 512 lanes 47 / 90, read again through the caches 67 / 178.
+template <bool GRAD, typename F> void by_width(int64_t C, F&& f) {
     const auto go = [&](auto lanes, auto k) { f(lanes, k); };
     using std::integral_constant;
     if (C <= 128) go(integral_constant<int, 16>{}, integral_constant<int, 1>{});
     else if (C <= 512) go(integral_constant<int, 64>{}, integral_constant<int, 1>{});
     else if (C <= 1024) go(integral_constant<int, 64>{}, integral_constant<int, 2>{});
-    else if (C <= 2048) go(integral_constant<int, 64>{}, integral_constant<int, 4>{});
-    else if (C <= 4096) go(integral_constant<int, 256>{}, integral_constant<int, 2>{});
-    else go(integral_constant<int, 256>{}, integral_constant<int, 4>{});
+    else if (C <= 2048) go(integral_constant<int, 128>{}, integral_constant<int, 2>{});
+    else if (C <= 4096) go(integral_constant<int, GRAD ? 512 : 256>{}, integral_constant<int, GRAD ? 1 : 2>{});
+    else go(integral_constant<int, 512>{}, integral_constant<int, 2>{});
 }
 
 }  // namespace
@@ -382,10 +406,11 @@ hipError_t launch_layernorm_fwd(int dtype, const NormArgs& a, hipStream_t stream
         return by_dtype(dtype, [&](auto io) { ln_fwd_long_kernel<io.value><<<grid, 256, 0, stream>>>(a); });
     }
     return by_dtype(dtype, [&](auto io) {
-        by_width(a.C, [&](auto lanes, auto k) {
-            const int64_t wgs = (a.rows + 256 / lanes.value - 1) / (256 / lanes.value);
+        by_width<false>(a.C, [&](auto lanes, auto k) {
+            constexpr int threads = lanes.value < 256 ? 256 : lanes.value;
+            const int64_t wgs = (a.rows + threads / lanes.value - 1) / (threads / lanes.value);
             const unsigned grid = (unsigned)(wgs < 2048 ? wgs : 2048);
-            ln_fwd_kernel<io.value, lanes.value, k.value><<<grid, 256, 0, stream>>>(a);
+            ln_fwd_kernel<io.value, lanes.value, k.value><<<grid, threads, 0, stream>>>(a);
         });
     });
 }
@@ -396,8 +421,8 @@ hipError_t launch_layernorm_bwd(int dtype, const NormArgs& a, hipStream_t stream
     hipError_t e = hipSuccess;
     if (a.rows > 0 && a.C <= kNormRegisterC) {
         e = by_dtype(dtype, [&](auto io) {
-            by_width(a.C, [&](auto lanes, auto k) {
-                ln_bwd_kernel<io.value, lanes.value, k.value><<<(unsigned)np, 256, 0, stream>>>(a);
+            by_width<true>(a.C, [&](auto lanes, auto k) {
+                ln_bwd_kernel<io.value, lanes.value, k.value><<<(unsigned)np, lanes.value < 256 ? 256 : lanes.value, 0, stream>>>(a);
             });
         });
     } else if (a.rows > 0) {

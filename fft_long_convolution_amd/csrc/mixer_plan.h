@@ -69,7 +69,9 @@ inline size_t linattn_states_bytes(const LinPlan& p, int64_t rows, int64_t DK, i
     return p.nseg > 1 ? ((size_t)rows * (size_t)p.nseg * (size_t)(DK * DV) * 4 + 255) / 256 * 256 : 0;
 }
 
-// The decay's gradient: column blocks, and segments of at least eight chunks until two workgroups to a compute unit.
+// The decay's gradient: column blocks, and segments of at least four chunks until two workgroups to a compute unit.
+// Measured (bf16, us beside the other gradients): 32 rows of 4096 tokens, D = 128, one segment 286, 4: 110, 8: 86, 16: 104;
+// 16 rows of 65536: 8: 892, 16: 663, 32: 677; 8 rows of 1000, D = 64, 1: 55, 4: 30, 8: 25, 16: 26; 128 rows of 2048: 1: 156, 4: 175.
 #ifdef __HIPCC__
 __host__ __device__
 #endif
@@ -78,7 +80,7 @@ struct LinTanPlan { int nseg; int64_t seg_len; };
 inline LinTanPlan linattn_tan_plan(int64_t rows, int64_t N, int64_t DV) {
     const int64_t chunks = (N + 31) / 32, wgs = rows * linattn_tan_blocks(DV);
     int64_t nseg = 1;
-    while (nseg * 16 <= chunks && wgs * nseg * 2 <= 512) nseg *= 2;
+    while (nseg * 8 <= chunks && wgs * nseg * 2 <= 512) nseg *= 2;
     const int64_t len = (chunks + nseg - 1) / nseg * 32;
     return LinTanPlan{(int)((N + len - 1) / len), len};
 }
@@ -87,11 +89,12 @@ inline LinTanPlan linattn_tan_plan(int64_t rows, int64_t N, int64_t DV) {
 constexpr int64_t kNormRegisterC = 8192;
 
 // Workgroups of the gradient call, each with a partial sum of dweight and dbias over its rows: enough to
-// fill the chip (two to four on each of 256 compute units, by their registers), no more than turns of
-// rows, since every one costs 8 C bytes written and read.
+// fill the chip (three of 256 threads or two of 512 to each of 256 compute units), no more than turns of
+// rows, since every one costs 8 C bytes written and read.  Measured (bf16, us, at 256, 512, 768 and 1024): 32768 rows of
+// 768: 75, 48, 42, 41; 16384 of 2048: 64, 47, 46, 47; 16384 of 4096: 111, 82, 97, 88; 8192 of 8192: 102, 90, 103, 105.
 inline int64_t layernorm_parts(int64_t rows, int64_t C) {
-    const int64_t per = C <= 128 ? 16 : C <= 2048 ? 4 : 1;   // rows a workgroup has in hand
-    const int64_t turns = (rows + per - 1) / per, most = C <= 2048 ? 512 : 768;
+    const int64_t per = C <= 128 ? 16 : C <= 1024 ? 4 : C <= 2048 ? 2 : 1;   // rows a workgroup has in hand
+    const int64_t turns = (rows + per - 1) / per, most = C <= 2048 ? 768 : 512;
     return turns < most ? turns : most;
 }
 

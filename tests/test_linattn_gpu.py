@@ -92,6 +92,37 @@ CASES = [
 ]
 
 
+# Enough rows for the wide column blocks, and lengths past the pipelined loop's start: checked on the first and the last
+# batch row (every row is on its own)
+MANY = [
+    (9, 16, 4, 199, 128, 128, "bnhd", True, [199, 160, 1, 33, 64, 0, 199, 198, 193]),
+    (25, 16, 16, 170, 128, 128, "bhnd", False, None),
+    (25, 16, 8, 170, 128, 128, "bnhd", True, None),
+    (13, 10, 5, 170, 256, 256, "bhnd", False, None),
+    (33, 8, 2, 161, 64, 64, "bnhd", True, None),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("case", MANY, ids=lambda c: "-".join(map(str, c[:7])))
+def test_many_rows(lc, dtype, case):
+    B, H, G, N, Dk, Dv, order, state, lengths = case
+    say(f"[linattn many] {dtype} {case}")
+    d = inputs(700 + B, B, H, G, N, Dk, Dv, dtype, order, state, lengths)
+    y, S = lc.linear_attention(d["q"], d["k"], d["v"], d["ld"], state=d["state"], lengths=d["lengths"])
+    g = lc.linear_attention_bwd(d["dy"], d["q"], d["k"], d["v"], d["ld"], state=d["state"], dstate=d["dstate"],
+                                lengths=d["lengths"])
+    for b in (0, B - 1):
+        e = {n: (t if n in ("ld", "scale") or t is None else t[b:b + 1]) for n, t in d.items()}
+        ry, rS = ref_fwd(e)
+        r = mixer.linattn_bwd(wide(e["dy"]), wide(e["q"]), wide(e["k"]), wide(e["v"]), wide(e["ld"]), e["scale"],
+                              wide(e["state"]), wide(e["dstate"]), wide(e["lengths"]))
+        errs = [rel_rows(t[b:b + 1], x) for t, x in zip((y, g.dq, g.dk, g.dv), (ry, r[0], r[1], r[2]))]
+        eS = [rel_rows(S[b:b + 1], rS)] + ([rel_rows(g.dstate[b:b + 1], r[3])] if state else [])
+        say(f"   row {b}: y dq dk dv " + " ".join(f"{v:.2e}" for v in errs) + " states " + " ".join(f"{v:.2e}" for v in eS))
+        assert max(errs) <= TOL[dtype] and max(eS) <= TOL_F32
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(map(str, c[:7])))
 def test_forward(lc, dtype, case):

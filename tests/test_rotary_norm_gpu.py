@@ -112,7 +112,9 @@ def test_rotary_offsets_past_32_bits(lc):
 
 
 NORM = [(1, 1), (3, 2), (5, 7), (2, 63), (4, 64), (7, 100), (33, 256), (300, 257), (2, 1001), (9, 1024), (5, 2048),
-        (3, 4096), (2, 4100), (2, 8192), (2, 12289), (1, 65536), (2000, 48), (1030, 768)]
+        (3, 4096), (2, 4100), (2, 8192), (2, 12289), (1, 65536), (2000, 48), (1030, 768),
+        # more rows than the gradient's workgroups have in hand
+        (3100, 520), (1600, 1100), (520, 4096), (600, 2056), (530, 4104)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])

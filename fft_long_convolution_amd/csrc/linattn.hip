@@ -7,25 +7,31 @@ namespace lcv {
 namespace {
 
 // Slot s of a row's states holds what segment s - 1 added up from zero; it becomes the state that
-// enters segment s, slot 0 the state that enters the row.  Four columns to a thread, eight segments' loads in flight
-// (8 segments of 32 rows, D = 128, 34 MB: 7.4 us; one load at a time 13).
-__global__ void __launch_bounds__(256) linattn_join_kernel(LinJob a) {
+// enters segment s, slot 0 the state that enters the row.  Slots are the chunk kernel's registers: tiles of 16 x 16, 4 rows
+// to a lane.  Eight segments' loads in flight (one load at a time took nearly twice as long).
+__global__ void __launch_bounds__(256) linattn_join_kernel(LinJob a, int f32) {
     const LinRole& r = a.r[blockIdx.y];
-    const int per = r.DK * r.DV / 4;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t bh = i / per;
+    const uint32_t per = a.kt * a.ncb * 4 * a.nw * 64, i = blockIdx.x * 256 + threadIdx.x;   // lanes of a slot
+    const uint32_t bh = i / per, e = i - bh * per;
     if (bh >= a.B * a.H) return;
-    const int e = (int)(i - bh * per) * 4, d = e / r.DV, n = e - d * r.DV;
-    const int64_t size = (int64_t)r.DK * r.DV;
+    const int64_t size = 4 * (int64_t)per;
     f32x4 S = {0.f, 0.f, 0.f, 0.f};
+    const bool fours = !f32 && a.nw == 2;
+    const int lane = e & 63, g = lane >> 4, x = lane & 15, t = (e >> 6) & (a.kt - 1), m = (int)((e >> 6) / (uint32_t)a.kt);
+    const int d0 = f32 ? 16 * t : 32 * (t >> 1) + 4 * (t & 1), n0 = fours ? 32 * (m >> 1) + 4 * (m & 1) : 16 * m;
+    if (d0 >= r.DK || n0 >= r.DV) return;      // a tile that there is not
     if (r.s_in) {
-        const float* s = r.s_in + bh * size + (int64_t)d * r.s_row + (int64_t)n * r.s_col;
-        for (int j = 0; j < 4; ++j) S[j] = s[(int64_t)j * r.s_col];
+        const int d = d0 + (f32 ? 4 : 8) * g, n = n0 + (fours ? 8 * (x >> 2) + (x & 3) : x);
+        if (d < r.DK && n < r.DV) {
+            const float* s = r.s_in + (int64_t)bh * (r.DK * r.DV) + d * r.s_row + n * r.s_col;
+            for (int j = 0; j < 4; ++j) S[j] = s[j * r.s_row];
+        }
     }
-    float* st = r.states + bh * a.nseg * size + e;
+    float* st = r.states + (int64_t)bh * a.nseg * size + 4 * e;
     *(f32x4*)st = S;
-    const int64_t len = row_len(a.lengths, bh / a.H, a.N);
-    const float em1 = expm1f(log_gamma(a.log_decay, (int)(bh % a.H)) * (float)a.seg_len);
+    const uint32_t b = bh / (uint32_t)a.H;
+    const int64_t len = row_len(a.lengths, b, a.N);
+    const float em1 = expm1f(log_gamma(a.log_decay, (int)(bh - b * (uint32_t)a.H)) * (float)a.seg_len);
     // a row's segments are in a chain of their own, but their sums are not: eight loads in flight
     int last = a.nseg;
     while (last > 1 && (last - 1) * a.seg_len >= len) --last;
@@ -147,13 +153,9 @@ hipError_t launch_linattn(int dtype, const LinJob& a, hipStream_t stream) {
                                                                                    : launch_linattn_bf16(a, stream);
 }
 
-hipError_t launch_linattn_join(const LinJob& a, hipStream_t stream) {
-    int64_t most = 0;
-    for (int i = 0; i < a.nroles; ++i) {
-        const int64_t n = a.B * a.H * ((int64_t)a.r[i].DK * a.r[i].DV / 4);
-        if (n > most) most = n;
-    }
-    linattn_join_kernel<<<dim3((unsigned)((most + 255) / 256), a.nroles), 256, 0, stream>>>(a);
+hipError_t launch_linattn_join(const LinJob& a, bool f32, hipStream_t stream) {
+    const int64_t lanes = a.B * a.H * ((int64_t)a.kt * a.ncb * 4 * a.nw * 64);
+    linattn_join_kernel<<<dim3((unsigned)((lanes + 255) / 256), a.nroles), 256, 0, stream>>>(a, f32);
     return hipGetLastError();
 }
 

@@ -8,7 +8,8 @@
 // One pass over the data: a workgroup walks its (b, h), or a segment of it, chunk by chunk with S in
 // fp32 in the registers of its four waves; a wave owns 16 NW columns of S and of O, and every row.  Chunks come
 // straight to LDS two ahead of the arithmetic.  Few long rows are split into segments: a pass that only adds up each
-// segment's own state (K and V are read twice), a scan over them, and the main pass.
+// segment's own state (K and V are read twice), a scan over them, and the main pass.  The segments' states stand in memory
+// as they do in registers, 16 bytes to a lane (in rows, 4 bytes at a time, they cost the prompt below 3 us).
 //
 // How the four products follow each other in registers (lane = 16 g + x, tiles of 16 x 16, the
 // accumulator holds rows 4 g + r, r < 4, of column x):
@@ -23,7 +24,8 @@
 // What bounds it (bf16, D = 128).  Enough rows (gradients, 256 rows of 2048 tokens, 282 us): HBM, 4.8 TB/s of what is
 // read after the XCD's L2 has served the roles that walk together (7 tensors of the 9 asked for, by counters) and
 // written.  65536 tokens of 16 rows (361 us): HBM, the state pass 520 MB in 126 us and the main pass 1.1 GB in 208 us
-// (5.3 TB/s).  One workgroup to a compute unit: a chunk's chain, 1.22 us at NW = 2 and 0.91 at NW = 1; a wave's
+// (5.3 TB/s).  A prompt of 32 rows of 4096 (64 us): 24 us of state pass, 7 of scan, 33 of main pass, which moves 152 MB in
+// it; what is left to HBM's rate is the start and the end of workgroups that all begin at once.  One workgroup to a compute unit: a chunk's chain, 1.22 us at NW = 2 and 0.91 at NW = 1; a wave's
 // 254 vector instructions and 64 matrix products of a chunk take 2040 cycles back to back, 2270 are measured with
 // loads, stores and barriers left out.  Eight waves that share one 128-column tile take the same 1.22 us a chunk,
 // since the SIMD's instructions add up, and 64 tokens to a chunk spilled registers.
@@ -74,16 +76,15 @@ __global__ void __launch_bounds__(256, KT > 8 || (IO == CT_F32 && NW == 2) ? 1 :
 
     // Workgroups that read the same tokens (a segment's roles and column blocks) go to one XCD, whose L2
     // they share: consecutive ids go round the eight XCDs.
-    const int per = a.nroles * a.ncb, nseg = STATE ? a.nseg - 1 : a.nseg;
-    const int64_t slot = blockIdx.x / 8, group = slot / per * 8 + blockIdx.x % 8;
+    const uint32_t per = a.nroles * a.ncb, nseg = STATE ? a.nseg - 1 : a.nseg;    // 64-bit divisions take a microsecond
+    const uint32_t slot = blockIdx.x / 8, group = slot / per * 8 + blockIdx.x % 8;
     if (group >= a.B * a.H * nseg) return;
     const int member = (int)(slot % per), cb = member % a.ncb;
     const LinRole r = a.r[member / a.ncb];       // a copy: its fields stay in scalar registers
     if (cb * DVB >= r.DV) return;
-    const int64_t bh = group / nseg;
-    const int seg = (int)(group - bh * nseg);
-    const int64_t b = bh / a.H;
-    const int h = (int)(bh - b * a.H);
+    const uint32_t row = group / nseg, brow = row / (uint32_t)a.H;
+    const int seg = (int)(group - row * nseg), h = (int)(row - brow * (uint32_t)a.H);
+    const int64_t bh = row, b = brow;
     const int64_t len = row_len(a.lengths, b, a.N);
     const int64_t beg = seg * a.seg_len;
     const int64_t end = beg + a.seg_len < len ? beg + a.seg_len : len;
@@ -108,45 +109,6 @@ __global__ void __launch_bounds__(256, KT > 8 || (IO == CT_F32 && NW == 2) ? 1 :
                 *(uint4*)((char*)r.O + (ob + t * r.o.n + c) * osz) = make_uint4(0, 0, 0, 0);
             }
         if (end <= beg && !(seg == 0 && r.s_out)) return;
-    }
-
-    // ---- weights of the chunk's tokens
-    const float lg = log_gamma(a.log_decay, h);
-    const int off = r.reverse;
-    float wP[CT][4], wI[CT], wU[CJ][ES];
-#pragma unroll
-    for (int t = 0; t < CT; ++t) {
-        wI[t] = r.s_q * expf(lg * (float)(16 * t + x + 1 - off));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int e = 16 * t + x - 4 * g - i;
-            wP[t][i] = r.s_q * r.s_kv * expf(lg * (float)(e > 0 ? e : 0));
-        }
-    }
-
-    // ---- the state that enters
-    f32x4 S[KT][NW];
-    {
-        const bool from_ws = !STATE && a.nseg > 1;
-        const int64_t size = (int64_t)r.DK * r.DV;
-        const float* s = STATE ? nullptr : from_ws ? r.states + (bh * a.nseg + seg) * size : r.s_in ? r.s_in + bh * size : nullptr;
-        const int srow = from_ws ? r.DV : r.s_row, scol = from_ws ? 1 : r.s_col;
-#pragma unroll
-        for (int t = 0; t < KT; ++t)
-#pragma unroll
-            for (int n = 0; n < NW; ++n) {
-                const int d = M::state_row(t, g), c = column(n);
-                f32x4 v = {0.f, 0.f, 0.f, 0.f};
-                if (s && d < r.DK && c < r.DV) {
-                    if (srow == 1) {
-                        v = *(const f32x4*)(s + (int64_t)c * scol + d);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) v[i] = s[(int64_t)(d + i) * srow + c];
-                    }
-                }
-                S[t][n] = v;
-            }
     }
 
     // ---- loads of a chunk straight to LDS, two chunks ahead of the arithmetic.  Round i of a tile fills
@@ -225,6 +187,58 @@ __global__ void __launch_bounds__(256, KT > 8 || (IO == CT_F32 && NW == 2) ? 1 :
         }
         move_on();
     };
+
+    // the first chunks are on their way while the weights are formed and the state comes in
+    int64_t left = end - beg;                  // tokens from the chunk in hand on
+    if (left > 0) {
+        fetch(lds0, left);
+        if (STAGES == 3 && left > C) fetch(lds1, left - C);
+    }
+
+    // ---- weights of the chunk's tokens
+    const float lg = log_gamma(a.log_decay, h);
+    const int off = r.reverse;
+    float wP[CT][4], wI[CT], wU[CJ][ES];
+#pragma unroll
+    for (int t = 0; t < CT; ++t) {
+        wI[t] = r.s_q * expf(lg * (float)(16 * t + x + 1 - off));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int e = 16 * t + x - 4 * g - i;
+            wP[t][i] = r.s_q * r.s_kv * expf(lg * (float)(e > 0 ? e : 0));
+        }
+    }
+
+    // ---- the state that enters.  The segments' states stand as they are in registers: tiles, 16 bytes to a lane.
+    const auto state_tile = [&](int seg, int t, int n) LCV_INLINE {
+        const int tiles = KT * 4 * NW * a.ncb, tile = ((cb * 4 + wave) * NW + n) * KT + t;
+        return (f32x4*)(r.states + (((int64_t)bh * a.nseg + seg) * tiles + tile) * 256) + lane;
+    };
+    const auto has_tile = [&](int t, int n) LCV_INLINE { return M::state_row(t, 0) < r.DK && wcol + (FOURS ? 4 : 16) * n < r.DV; };
+    f32x4 S[KT][NW];
+    {
+        const bool from_ws = !STATE && a.nseg > 1;
+        const float* s = STATE || from_ws || !r.s_in ? nullptr : r.s_in + bh * ((int64_t)r.DK * r.DV);
+        const int srow = r.s_row, scol = r.s_col;
+#pragma unroll
+        for (int t = 0; t < KT; ++t)
+#pragma unroll
+            for (int n = 0; n < NW; ++n) {
+                const int d = M::state_row(t, g), c = column(n);
+                f32x4 v = {0.f, 0.f, 0.f, 0.f};
+                if (from_ws) {
+                    if (has_tile(t, n)) v = *state_tile(seg, t, n);
+                } else if (s && d < r.DK && c < r.DV) {
+                    if (srow == 1) {
+                        v = *(const f32x4*)(s + (int64_t)c * scol + d);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) v[i] = s[(int64_t)(d + i) * srow + c];
+                    }
+                }
+                S[t][n] = v;
+            }
+    }
 
     const typename M::At lk = M::at(g, x, RK), lv = M::at(g, x, RV);
     // the output likewise: lane x's token, the first of its columns; token tiles of 16 and column tiles
@@ -438,19 +452,14 @@ __global__ void __launch_bounds__(256, KT > 8 || (IO == CT_F32 && NW == 2) ? 1 :
         }
     };
 
-    // ---- the chunks.  A chunk's loads have to be in when it begins: of what a wave has issued since, the
-    // next chunk's loads and the last chunk's stores may be outstanding.
-    int64_t left = end - beg;                  // tokens from the chunk in hand on
-    if (left > 0) {
-        weigh(left < C ? (int)left : C);
-        fetch(lds0, left);
-        if (STAGES == 3 && left > C) fetch(lds1, left - C);
-    }
+    // ---- the chunks.  A chunk's loads have to be in when it begins.
+    if (left > 0) weigh(left < C ? (int)left : C);
     // STAGES chunks a turn, each stage by its own name: then the compiler knows which loads a read waits for.
     // Operations are counted in their order.  With three stages a chunk's loads are older than the stores of the two
     // chunks before it and the next chunk's loads, which may all be outstanding; with two stages older than the last
     // chunk's stores.  The first two chunks' loads have no such stores behind them and are waited for ahead of the loop.
     constexpr int LAST = STAGES == 3 ? 5 : 3;
+    bool stored = false, ahead = false;        // a whole chunk's stores, and after them nothing; a whole fetch before them
     if (whole && left >= LAST * C) {
         std::integral_constant<bool, true> full;
         wait_for_all_but<0>();
@@ -470,8 +479,12 @@ __global__ void __launch_bounds__(256, KT > 8 || (IO == CT_F32 && NW == 2) ? 1 :
             }
             left -= STAGES * C;
         } while (left >= LAST * C);
+        stored = true;
+        ahead = STAGES == 3;
     }
     // the last chunks, and calls whose operands leave columns free
+    // (what a whole chunk issued after the next one's loads, its own stores and perhaps a whole fetch, is known and may
+    // be outstanding)
     for (int t = 0; left > 0; left -= C) {
         char *now = lds0, *then = lds1;
         if constexpr (STAGES == 3) {
@@ -482,8 +495,12 @@ __global__ void __launch_bounds__(256, KT > 8 || (IO == CT_F32 && NW == 2) ? 1 :
             now = lds1;
             then = lds0;
         }
-        wait_for_all_but<0>();
+        if (whole && ahead) wait_for_all_but<STAGES == 3 ? LOADS + STORES : STORES>();
+        else if (whole && stored) wait_for_all_but<STORES>();
+        else wait_for_all_but<0>();
         barrier_only();
+        stored = true;
+        ahead = STAGES == 3 && left >= STAGES * C;
         if (left > (STAGES - 1) * C) fetch(then, left - (STAGES - 1) * C);
         if (left < C && end - beg > C) weigh((int)left);
         chunk(std::integral_constant<bool, false>{}, now, nullptr);
@@ -492,16 +509,15 @@ __global__ void __launch_bounds__(256, KT > 8 || (IO == CT_F32 && NW == 2) ? 1 :
     }
 
     // ---- the state that leaves
-    float* s = nullptr;
-    int srow = r.DV, scol = 1;
     if constexpr (STATE) {
-        s = r.states + (bh * a.nseg + seg + 1) * (int64_t)r.DK * r.DV;
+#pragma unroll
+        for (int t = 0; t < KT; ++t)
+#pragma unroll
+            for (int n = 0; n < NW; ++n)
+                if (has_tile(t, n)) *state_tile(seg + 1, t, n) = S[t][n];
     } else if (r.s_out && (end == len || len == 0) && (beg < len || seg == 0)) {
-        s = r.s_out + bh * (int64_t)r.DK * r.DV;
-        srow = r.s_row;
-        scol = r.s_col;
-    }
-    if (s) {
+        float* const s = r.s_out + bh * (int64_t)r.DK * r.DV;
+        const int srow = r.s_row, scol = r.s_col;
 #pragma unroll
         for (int t = 0; t < KT; ++t)
 #pragma unroll
@@ -526,7 +542,7 @@ hipError_t launch_chunk_as(const LinJob& a, hipStream_t stream) {
         linattn_chunk_kernel<IO, KT, NW, true, false, EXACT><<<grid(rows * (a.nseg - 1)), 256, 0, stream>>>(a);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
-        e = launch_linattn_join(a, stream);
+        e = launch_linattn_join(a, IO == CT_F32, stream);
         if (e != hipSuccess) return e;
     }
     linattn_chunk_kernel<IO, KT, NW, false, WIDE, EXACT><<<grid(rows * a.nseg), 256, 0, stream>>>(a);

@@ -133,7 +133,7 @@ BwdPlan bwd_plan(int64_t B, int64_t H, int64_t N, int64_t Dk, int64_t Dv, lconv_
         p.first[i] = 2 * i;
         p.roles[i] = alike ? 3 : 2 - i;
         p.plan[i] = linattn_plan(rows, p.roles[i], N, alike ? wide : i ? Dk : Dv, alike ? wide : i ? Dv : Dk, dtype);
-        p.states[i] = linattn_states_bytes(p.plan[i], rows, Dk, Dv);
+        p.states[i] = linattn_states_bytes(p.plan[i], rows);
         p.total += (size_t)p.roles[i] * p.states[i];
     }
     return p;
@@ -155,7 +155,7 @@ extern "C" {
 size_t lconv_linattn_workspace_bytes(int64_t B, int64_t H, int64_t G, int64_t N, int64_t Dk, int64_t Dv,
                                      lconv_dtype_t dtype) {
     if (!dtype_ok(dtype) || B <= 0 || H <= 0 || N <= 0 || !linattn_dims_ok(B, H, G, N, Dk, Dv)) return 0;
-    return linattn_states_bytes(linattn_plan(B * H, 1, N, Dk, Dv, dtype), B * H, Dk, Dv);
+    return linattn_states_bytes(linattn_plan(B * H, 1, N, Dk, Dv, dtype), B * H);
 }
 
 lconv_status_t lconv_linattn_fwd(const void* q, const lconv_strides_t* q_strides, const void* k,

@@ -30,7 +30,7 @@ struct LinRole {
     const float* s_in;        // [B][H] states, element (d, n) at d * s_row + n * s_col; NULL: zeros
     float* s_out;             // the same layout; NULL: not wanted
     int s_row, s_col;
-    float* states;            // [B][H][nseg][DK][DV]: the states that enter the segments (nseg > 1)
+    float* states;            // [B][H][nseg][column tiles][kt][256]: the states that enter the segments (nseg > 1)
     float s_q, s_kv;
     int reverse;
     int wide;                 // O in fp32 (a sum over shared heads follows), else in the dtype
@@ -80,7 +80,7 @@ hipError_t launch_linattn_f16(const LinJob& a, hipStream_t stream);
 hipError_t launch_linattn_bf16(const LinJob& a, hipStream_t stream);
 hipError_t launch_linattn_bf16_wide(const LinJob& a, hipStream_t stream);   // nw = 2
 // the segments' own states to the states that enter them
-hipError_t launch_linattn_join(const LinJob& a, hipStream_t stream);
+hipError_t launch_linattn_join(const LinJob& a, bool f32, hipStream_t stream);
 hipError_t launch_linattn_step(int dtype, const LinStepArgs& a, hipStream_t stream);
 hipError_t launch_linattn_tan(int dtype, const LinTanArgs& a, float* dlog, hipStream_t stream);
 // For both of two tensors: out[b][g][n][:] = sum over the `share` heads of g of the fp32 rows in[b][h][n][:] (dense)

@@ -64,9 +64,9 @@ inline LinPlan linattn_plan(int64_t rows, int nroles, int64_t N, int64_t DK, int
     return best;
 }
 
-// workspace of one role's segment states
-inline size_t linattn_states_bytes(const LinPlan& p, int64_t rows, int64_t DK, int64_t DV) {
-    return p.nseg > 1 ? ((size_t)rows * (size_t)p.nseg * (size_t)(DK * DV) * 4 + 255) / 256 * 256 : 0;
+// workspace of one role's segment states (whole tiles)
+inline size_t linattn_states_bytes(const LinPlan& p, int64_t rows) {
+    return p.nseg > 1 ? (size_t)rows * (size_t)p.nseg * (size_t)(p.kt * 16 * p.ncb * 64 * p.nw) * 4 : 0;
 }
 
 // The decay's gradient: column blocks, and segments of at least four chunks until two workgroups to a compute unit.

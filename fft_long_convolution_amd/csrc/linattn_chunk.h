@@ -24,11 +24,12 @@
 // What bounds it (bf16, D = 128).  Enough rows (gradients, 256 rows of 2048 tokens, 282 us): HBM, 4.8 TB/s of what is
 // read after the XCD's L2 has served the roles that walk together (7 tensors of the 9 asked for, by counters) and
 // written.  65536 tokens of 16 rows (361 us): HBM, the state pass 520 MB in 126 us and the main pass 1.1 GB in 208 us
-// (5.3 TB/s).  A prompt of 32 rows of 4096 (64 us): 24 us of state pass, 7 of scan, 33 of main pass, which moves 152 MB in
-// it; what is left to HBM's rate is the start and the end of workgroups that all begin at once.  One workgroup to a compute unit: a chunk's chain, 1.22 us at NW = 2 and 0.91 at NW = 1; a wave's
-// 254 vector instructions and 64 matrix products of a chunk take 2040 cycles back to back, 2270 are measured with
-// loads, stores and barriers left out.  Eight waves that share one 128-column tile take the same 1.22 us a chunk,
-// since the SIMD's instructions add up, and 64 tokens to a chunk spilled registers.
+// (5.3 TB/s).  A prompt of 32 rows of 4096 (64 us): 24 us of state pass, 7 of scan, 33 of main pass, which moves
+// 152 MB in it; what is left to HBM's rate is the start and the end of workgroups that all begin at once.  One
+// workgroup to a compute unit: a chunk's chain, 1.22 us at NW = 2 and 0.91 at NW = 1; a wave's 254 vector
+// instructions and 64 matrix products of a chunk take 2040 cycles back to back, 2270 are measured with loads, stores
+// and barriers left out.  Eight waves that share one 128-column tile take the same 1.22 us a chunk, since the SIMD's
+// instructions add up, and 64 tokens to a chunk spilled registers.
 //
 // Precision.  S, P and every sum are fp32.  For 16-bit types P and S are rounded to the type once as
 // operands, like the result itself.  What S adds up is not: gamma^.. V is split into three bf16 parts

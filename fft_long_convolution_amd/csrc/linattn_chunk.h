@@ -76,16 +76,22 @@ __global__ void __launch_bounds__(256, KT > 8 || (IO == CT_F32 && NW == 2) ? 1 :
     }
 
     // Workgroups that read the same tokens (a segment's roles and column blocks) go to one XCD, whose L2
-    // they share: consecutive ids go round the eight XCDs.
+    // they share, and next to them the other heads of these tokens, which lie beside them in token-major memory:
+    // consecutive ids go round the eight XCDs, each of which takes a row of groups (batch row, segment, head).
+    // Measured against groups dealt to the XCDs in turn, heads outermost (us): prompt of 32 rows of 4096 64, 68; gradients
+    // of 128 rows of 2048 157, 163 (head-major 149, 153); 16 rows of 65536 head-major 358, 359, token-major 374, 395.
+    // Rows of different lengths are dealt out in turn all the same, or the XCDs of short rows would stand idle (30 rows
+    // of 0 to 777 tokens 33, else 40).
     const uint32_t per = a.nroles * a.ncb, nseg = STATE ? a.nseg - 1 : a.nseg;    // 64-bit divisions take a microsecond
-    const uint32_t slot = blockIdx.x / 8, group = slot / per * 8 + blockIdx.x % 8;
-    if (group >= a.B * a.H * nseg) return;
+    const uint32_t slot = blockIdx.x / 8, groups = a.B * a.H * nseg, xcd = blockIdx.x % 8;
+    const uint32_t group = a.lengths ? slot / per * 8 + xcd : xcd * ((groups + 7) / 8) + slot / per;
+    if (group >= groups) return;
     const int member = (int)(slot % per), cb = member % a.ncb;
     const LinRole r = a.r[member / a.ncb];       // a copy: its fields stay in scalar registers
     if (cb * DVB >= r.DV) return;
-    const uint32_t row = group / nseg, brow = row / (uint32_t)a.H;
-    const int seg = (int)(group - row * nseg), h = (int)(row - brow * (uint32_t)a.H);
-    const int64_t bh = row, b = brow;
+    const uint32_t place = group / (uint32_t)a.H, brow = place / nseg;
+    const int seg = (int)(place - brow * nseg), h = (int)(group - place * (uint32_t)a.H);
+    const int64_t b = brow, bh = b * a.H + h;
     const int64_t len = row_len(a.lengths, b, a.N);
     const int64_t beg = seg * a.seg_len;
     const int64_t end = beg + a.seg_len < len ? beg + a.seg_len : len;

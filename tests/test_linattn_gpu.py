@@ -89,6 +89,9 @@ CASES = [
     (1, 2, 2, 700, 64, 64, "bhnd", True, None),
     (3, 2, 2, 1030, 32, 16, "bnhd", True, (1030, 513, 3)),
     (1, 1, 1, 4100, 128, 128, "bhnd", True, None),     # a long row: split over its length
+    (2, 4, 2, 1500, 72, 136, "bnhd", True, (1500, 700)),
+    (3, 2, 1, 2600, 256, 128, "bnhd", True, (2600, 0, 1)),
+    (1, 2, 2, 3001, 128, 24, "bhnd", False, None),
 ]
 
 

@@ -17,7 +17,7 @@ __global__ void __launch_bounds__(256) linattn_join_kernel(LinJob a, int f32) {
     const int64_t size = 4 * (int64_t)per;
     f32x4 S = {0.f, 0.f, 0.f, 0.f};
     const bool fours = !f32 && a.nw == 2;
-    const int lane = e & 63, g = lane >> 4, x = lane & 15, t = (e >> 6) & (a.kt - 1), m = (int)((e >> 6) / (uint32_t)a.kt);
+    const int lane = e & 63, g = lane >> 4, x = lane & 15, m = (int)((e >> 6) / (uint32_t)a.kt), t = (int)(e >> 6) - m * a.kt;
     const int d0 = f32 ? 16 * t : 32 * (t >> 1) + 4 * (t & 1), n0 = fours ? 32 * (m >> 1) + 4 * (m & 1) : 16 * m;
     if (d0 >= r.DK || n0 >= r.DV) return;      // a tile that there is not
     if (r.s_in) {

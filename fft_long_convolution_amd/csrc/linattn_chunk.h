@@ -48,13 +48,14 @@ namespace {
 // STATE: only the state that the segment adds up from zero, for the segments after it.  WIDE: some roles' O leaves in fp32.
 // EXACT: the state's sums to fp32's accuracy.
 template <int IO, int KT, int NW, bool STATE, bool WIDE, bool EXACT>
-__global__ void __launch_bounds__(256, KT > 8 || (IO == CT_F32 && NW == 2) ? 1 : NW == 1 && IO != CT_F32 ? 3 : 2) linattn_chunk_kernel(LinJob a) {
+__global__ void __launch_bounds__(256, KT > 8 || (IO == CT_F32 && NW == 2) ? 1 : NW == 1 && (IO == CT_BF16 || (IO == CT_F16 && KT <= 6)) ? 3 : 2) linattn_chunk_kernel(LinJob a) {
     using M = Mx<IO>;
     using E = typename M::E;
     using Frag = typename M::Frag;
     constexpr int C = M::C, TK = M::TK, CT = C / 16, CJ = CT / TK, KS = KT / TK, ES = TK * 4;
     constexpr int DKP = KT * 16, DVB = 64 * NW, VEC = M::VEC;
-    constexpr int RK = DKP / VEC, RV = DVB / VEC;               // 16-byte groups of a row
+    // 16-byte groups of a row in LDS: a power of two for the swizzle, also where the tiles are 6 or 12
+    constexpr int RK = lin_row_groups(DKP / VEC), RV = DVB / VEC;
     constexpr int QB = STATE ? 0 : C * RK * 16, KB = C * RK * 16, STAGE = QB + KB + C * RV * 16;
     constexpr int NK = C * RK / 256, NV = C * RV / 256;         // loads of a chunk: rounds of 4 waves x 64 lanes
     constexpr bool KHALF = NK == 0;                             // a narrow tile takes two waves
@@ -65,6 +66,7 @@ __global__ void __launch_bounds__(256, KT > 8 || (IO == CT_F32 && NW == 2) ? 1 :
     constexpr bool FOURS = IO != CT_F32 && NW == 2;
     constexpr int PUTS = FOURS ? CT : CT * NW, STORES = STATE ? 0 : PUTS;     // of a wave; a wide FOURS put takes two
     static_assert(NV >= 1 && (NK >= 1 || C * RK == 128), "rounds of whole waves");
+    constexpr int SURE = KHALF ? NV : LOADS;         // loads of a chunk that every wave issues
     // chunks in LDS: one in hand, and two on their way where a compute unit then still holds the workgroups
     // that its registers allow (NW = 1: three, which hide each other's loads)
     constexpr int STAGES = 3 * STAGE <= (KT > 8 ? 160 : NW == 1 ? 53 : 80) * 1024 ? 3 : 2;
@@ -128,25 +130,22 @@ __global__ void __launch_bounds__(256, KT > 8 || (IO == CT_F32 && NW == 2) ? 1 :
     };
     const char *pq = STATE ? nullptr : start(r.Q), *pk = start(r.K), *pv = start(r.V);
     const int64_t dq = dir * r.Q.s.n * (int)sizeof(E), dk = dir * r.K.s.n * (int)sizeof(E), dv = dir * r.V.s.n * (int)sizeof(E);
+    // A lane without a column has an offset past the buffer's end, where loads give zeros and stores do nothing: every
+    // wave issues every load and every store, so that their numbers are known.
     uint32_t oq[NKR], ok[NKR], ov[NV];
-    bool kon[NKR], von[NV];
     const bool kin = !KHALF || wave < 2;
 #pragma unroll
     for (int i = 0; i < NKR; ++i) {
         const int s = 256 * i + tid, row = s / RK % C, c = ((s % RK) ^ swizzle(row, RK)) * VEC;
-        kon[i] = kin && c < r.DK;
-        ok[i] = offset(r.K, row, c);
-        oq[i] = STATE ? 0 : offset(r.Q, row, c);
+        ok[i] = c < r.DK ? offset(r.K, row, c) : kNowhere;
+        oq[i] = STATE || c >= r.DK ? kNowhere : offset(r.Q, row, c);
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int s = 256 * i + tid, row = s / RV, c = cb * DVB + ((s % RV) ^ swizzle(row, RV)) * VEC;
-        von[i] = c < r.DV;
-        ov[i] = offset(r.V, row, c);
+        ov[i] = c < r.DV ? offset(r.V, row, c) : kNowhere;
     }
-    // whole chunks of whole tiles take every load of every wave: only then is their number known
-    const bool whole = !KHALF && r.DK == DKP && cb * DVB + DVB <= r.DV;
-    if (!whole) {       // columns that the operands do not have stay zero
+    if (r.DK < DKP || cb * DVB + DVB > r.DV) {       // columns that the operands do not have are zero
         for (int i = tid; i < STAGE / 16; i += 256) {
             *(uint4*)(lds0 + 16 * i) = make_uint4(0, 0, 0, 0);
             *(uint4*)(lds1 + 16 * i) = make_uint4(0, 0, 0, 0);
@@ -158,9 +157,14 @@ __global__ void __launch_bounds__(256, KT > 8 || (IO == CT_F32 && NW == 2) ? 1 :
     const auto piece = [&](auto i, char* to) LCV_INLINE {
         constexpr int I = i.value, Q = STATE ? 0 : NKR;
         char* const t = to + 1024 * wave;
-        if constexpr (I < Q) to_lds(pq, oq[I], t + 4096 * I);
-        else if constexpr (I < Q + NKR) to_lds(pk, ok[I - Q], t + QB + 4096 * (I - Q));
-        else if constexpr (I < LOADS) to_lds(pv, ov[I - Q - NKR], t + QB + KB + 4096 * (I - Q - NKR));
+        if constexpr (I < Q + NKR) {
+            if (kin) {
+                if constexpr (I < Q) to_lds(pq, oq[I], t + 4096 * I);
+                else to_lds(pk, ok[I - Q], t + QB + 4096 * (I - Q));
+            }
+        } else if constexpr (I < LOADS) {
+            to_lds(pv, ov[I - Q - NKR], t + QB + KB + 4096 * (I - Q - NKR));
+        }
     };
     const auto move_on = [&]() LCV_INLINE {
         if constexpr (!STATE) pq += dq;
@@ -168,15 +172,15 @@ __global__ void __launch_bounds__(256, KT > 8 || (IO == CT_F32 && NW == 2) ? 1 :
         pv += dv;
     };
     const auto fetch = [&](char* to, int64_t left) LCV_INLINE {
-        if (whole && left >= C) {
+        if (left >= C) {
             static_for<0, LOADS>([&](auto i) LCV_INLINE { piece(i, to); });
         } else {
-            // columns that there are not, and zeros for the tokens that a last chunk lacks
+            // zeros for the tokens that a last chunk lacks
             char* const t = to + 1024 * wave;
 #pragma unroll
             for (int i = 0; i < NKR; ++i) {
                 const bool in = (256 * i + tid) / RK % C < left;
-                if (kon[i] && in) {
+                if (kin && in) {
                     if constexpr (!STATE) to_lds(pq, oq[i], t + 4096 * i);
                     to_lds(pk, ok[i], t + QB + 4096 * i);
                 }
@@ -188,8 +192,8 @@ __global__ void __launch_bounds__(256, KT > 8 || (IO == CT_F32 && NW == 2) ? 1 :
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const bool in = (256 * i + tid) / RV < left;
-                if (von[i] && in) to_lds(pv, ov[i], t + QB + KB + 4096 * i);
-                if (!in) *(uint4*)(t + QB + KB + 4096 * i + 16 * lane) = make_uint4(0, 0, 0, 0);
+                if (in) to_lds(pv, ov[i], t + QB + KB + 4096 * i);
+                else *(uint4*)(t + QB + KB + 4096 * i + 16 * lane) = make_uint4(0, 0, 0, 0);
             }
         }
         move_on();
@@ -253,7 +257,10 @@ __global__ void __launch_bounds__(256, KT > 8 || (IO == CT_F32 && NW == 2) ? 1 :
     char* po = STATE ? nullptr : (char*)r.O + (ob + low * r.o.n) * osz;
     const int64_t d_o = dir * r.o.n * osz, o16 = 16 * r.o.n * osz;
     const int mine = wcol + (FOURS ? 8 : 4) * g;
-    const uint32_t oo = (uint32_t)(r.reverse ? 15 - x : x) * (uint32_t)(r.o.n * osz) + (uint32_t)(mine * osz);
+    uint32_t oo[FOURS ? 1 : NW];
+#pragma unroll
+    for (int n = 0; n < (FOURS ? 1 : NW); ++n)
+        oo[n] = mine + 16 * n < r.DV ? (uint32_t)(r.reverse ? 15 - x : x) * (uint32_t)(r.o.n * osz) + (uint32_t)(mine * osz) : kNowhere;
 
     float em1 = 0.f;
     const auto weigh = [&](int c) LCV_INLINE {
@@ -271,25 +278,25 @@ __global__ void __launch_bounds__(256, KT > 8 || (IO == CT_F32 && NW == 2) ? 1 :
     f32x4 acc[CT][NW];
     const auto put = [&](int i) LCV_INLINE {
         const int it = FOURS ? i : i / NW, n = FOURS ? 0 : i % NW;
-        const __amdgpu_buffer_rsrc_t o = buffer_at(po + (r.reverse ? CT - 1 - it : it) * o16 + 16 * n * osz);
+        char* const at = po + (r.reverse ? CT - 1 - it : it) * o16 + 16 * n * osz;
         const f32x4 y = acc[it][n], y2 = acc[it][NW - 1];
         if (wide) {
-            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, y), o, oo, 0, 0);
-            if constexpr (FOURS) __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, y2), o, oo + 16, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, y), buffer_at(at), oo[n], 0, 0);
+            if constexpr (FOURS) __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, y2), buffer_at(at + 16), oo[n], 0, 0);
         } else if constexpr (FOURS) {
             const u32x4 w = {pack2<IO>(y[0], y[1]), pack2<IO>(y[2], y[3]), pack2<IO>(y2[0], y2[1]), pack2<IO>(y2[2], y2[3])};
-            __builtin_amdgcn_raw_buffer_store_b128(w, o, oo, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b128(w, buffer_at(at), oo[n], 0, 0);
         } else if constexpr (IO != CT_F32) {
             typedef uint32_t u32x2 __attribute__((__vector_size__(8)));
             const u32x2 w = {pack2<IO>(y[0], y[1]), pack2<IO>(y[2], y[3])};
-            __builtin_amdgcn_raw_buffer_store_b64(w, o, oo, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b64(w, buffer_at(at), oo[n], 0, 0);
         }
     };
     const auto emit = [&](int c) LCV_INLINE {
         if constexpr (!STATE) {
 #pragma unroll
             for (int i = 0; i < PUTS; ++i)
-                if (16 * (FOURS ? i : i / NW) + x < c && mine + (FOURS ? 0 : 16 * (i % NW)) < r.DV) put(i);
+                if (16 * (FOURS ? i : i / NW) + x < c) put(i);
             po += d_o;
         }
     };
@@ -467,11 +474,11 @@ __global__ void __launch_bounds__(256, KT > 8 || (IO == CT_F32 && NW == 2) ? 1 :
     // chunk's stores.  The first two chunks' loads have no such stores behind them and are waited for ahead of the loop.
     constexpr int LAST = STAGES == 3 ? 5 : 3;
     bool stored = false, ahead = false;        // a whole chunk's stores, and after them nothing; a whole fetch before them
-    if (whole && left >= LAST * C) {
+    if (left >= LAST * C) {
         std::integral_constant<bool, true> full;
         wait_for_all_but<0>();
         const auto turn = [&](char* now, char* then) LCV_INLINE {
-            wait_for_all_but<STAGES == 3 ? LOADS + 2 * STORES : STORES>();
+            wait_for_all_but<STAGES == 3 ? SURE + 2 * STORES : STORES>();
             barrier_only();
             chunk(full, now, then);
         };
@@ -489,7 +496,7 @@ __global__ void __launch_bounds__(256, KT > 8 || (IO == CT_F32 && NW == 2) ? 1 :
         stored = true;
         ahead = STAGES == 3;
     }
-    // the last chunks, and calls whose operands leave columns free
+    // the last chunks
     // (what a whole chunk issued after the next one's loads, its own stores and perhaps a whole fetch, is known and may
     // be outstanding)
     for (int t = 0; left > 0; left -= C) {
@@ -502,8 +509,8 @@ __global__ void __launch_bounds__(256, KT > 8 || (IO == CT_F32 && NW == 2) ? 1 :
             now = lds1;
             then = lds0;
         }
-        if (whole && ahead) wait_for_all_but<STAGES == 3 ? LOADS + STORES : STORES>();
-        else if (whole && stored) wait_for_all_but<STORES>();
+        if (ahead) wait_for_all_but<STAGES == 3 ? SURE + STORES : STORES>();
+        else if (stored) wait_for_all_but<STORES>();
         else wait_for_all_but<0>();
         barrier_only();
         stored = true;
@@ -570,7 +577,9 @@ template <int IO, int NW>
 hipError_t launch_chunk_nw(const LinJob& a, hipStream_t stream) {
     if (a.kt == 2) return launch_chunk<IO, 2, NW>(a, stream);
     if (a.kt == 4) return launch_chunk<IO, 4, NW>(a, stream);
+    if (a.kt == 6) return launch_chunk<IO, 6, NW>(a, stream);
     if (a.kt == 8) return launch_chunk<IO, 8, NW>(a, stream);
+    if (a.kt == 12) return launch_chunk<IO, 12, NW>(a, stream);
     return launch_chunk<IO, 16, NW>(a, stream);
 }
 

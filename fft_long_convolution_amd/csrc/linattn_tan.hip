@@ -338,7 +338,7 @@ template <int IO, int KT> hipError_t go(const LinTanArgs& a, hipStream_t stream)
 
 template <int IO> hipError_t go(const LinTanArgs& a, hipStream_t stream) {
     const int kt = linattn_kt(a.DK);
-    return kt == 2 ? go<IO, 2>(a, stream) : kt == 4 ? go<IO, 4>(a, stream) : kt == 8 ? go<IO, 8>(a, stream) : go<IO, 16>(a, stream);
+    return kt == 2 ? go<IO, 2>(a, stream) : kt == 4 ? go<IO, 4>(a, stream) : kt <= 8 ? go<IO, 8>(a, stream) : go<IO, 16>(a, stream);
 }
 
 }  // namespace

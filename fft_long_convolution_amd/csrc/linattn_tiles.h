@@ -18,6 +18,12 @@ __device__ __forceinline__ constexpr int swizzle(int row, int R) {
     return 2 * (s & (h - 1)) | (top & 1);
 }
 
+constexpr int lin_row_groups(int groups) {
+    int r = 4;
+    while (r < groups) r *= 2;
+    return r;
+}
+
 template <int IO> struct Mx {  // bf16, fp16
     using E = uint16_t;
     static constexpr int C = 32;        // tokens of a chunk
@@ -118,10 +124,11 @@ template <> struct Mx<CT_F32> {
 };
 
 // Global memory from a scalar address on, by 32-bit offsets of the lanes: raw buffer accesses, whose address
-// takes no vector arithmetic.  Every offset lies within the buffer's 2^32 - 1 bytes by the host's limit on
-// token strides.
+// takes no vector arithmetic.  Every offset lies within the buffer's size by the host's limit on token strides
+// (31 of at most 2^27 bytes); kNowhere does not.
+constexpr uint32_t kBufferBytes = 0xfc000000u, kNowhere = 0xfffffff0u;
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const char* base) {
-    return __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, 0xffffffff, 0x00020000);
+    return __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, (int)kBufferBytes, 0x00020000);
 }
 // 64 lanes' 16 bytes each to 1 KB of LDS in lane order, without registers for the data
 __device__ __forceinline__ void to_lds(const char* base, uint32_t off, char* dst) {

@@ -6,14 +6,14 @@
 
 namespace lcv {
 
-// Linear attention: tiles of the contraction (16 wide, padded to 2, 4, 8 or 16), 16-column tiles per
+// Linear attention: tiles of the contraction (16 wide, padded to 2, 4, 6, 8, 12 or 16), 16-column tiles per
 // wave, column blocks of 64 nw, and segments of seg_len tokens that a (b, h) is split into.
 struct LinPlan {
     int kt, nw, ncb, nseg;
     int64_t seg_len;
 };
 
-inline int linattn_kt(int64_t DK) { return DK <= 32 ? 2 : DK <= 64 ? 4 : DK <= 128 ? 8 : 16; }
+inline int linattn_kt(int64_t DK) { return DK <= 32 ? 2 : DK <= 64 ? 4 : DK <= 96 ? 6 : DK <= 128 ? 8 : DK <= 192 ? 12 : 16; }
 
 // Microseconds that a workgroup alone on its compute unit takes for a chunk of 32 tokens, measured at DK = DV = 64, 128, 256:
 // a chunk's chain of waits is much the same for narrow heads; fp16 scales its operands; fp32's matrix products take sixteen
@@ -22,7 +22,7 @@ inline double linattn_chunk_us(int kt, int nw, lconv_dtype_t dtype) {
     static const double us[3][3][2] = {{{3.0, 4.5}, {3.9, 6.4}, {7.8, 12.8}},      // fp32; 64 and 128 columns
                                        {{1.25, 1.75}, {1.5, 2.4}, {2.5, 4.0}},     // fp16
                                        {{0.9, 1.2}, {0.95, 1.25}, {1.55, 2.45}}};  // bf16
-    return us[dtype == LCONV_F32 ? 0 : dtype == LCONV_F16 ? 1 : 2][kt <= 4 ? 0 : kt == 8 ? 1 : 2][nw - 1];
+    return us[dtype == LCONV_F32 ? 0 : dtype == LCONV_F16 ? 1 : 2][kt <= 4 ? 0 : kt <= 8 ? 1 : 2][nw - 1] * (kt == 12 ? 0.8 : 1.0);
 }
 
 // Chosen by estimated time over the two tile widths and powers of two of segments.  With n chunks in a segment and L
@@ -46,7 +46,7 @@ inline LinPlan linattn_plan(int64_t rows, int nroles, int64_t N, int64_t DK, int
         const int64_t ncb = (DV + 64 * nw - 1) / (64 * nw), wgs = rows * nroles * ncb;
         for (int64_t nseg = 1; nseg == 1 || (nseg <= 1024 && nseg * 2 <= chunks && wgs * nseg <= 4096); nseg *= 2) {
             const int64_t per = (chunks + nseg - 1) / nseg, load = (wgs * nseg + 255) / 256;
-            const double shared = kt == 16 || (nw == 2 && dtype == LCONV_F32) ? (double)load : 1.0 + 0.35 * (double)(load - 1);
+            const double shared = kt > 8 || (nw == 2 && dtype == LCONV_F32) ? (double)load : 1.0 + 0.35 * (double)(load - 1);
             const double pass = (double)per * linattn_chunk_us(kt, nw, dtype) * shared;
             const double floor = bytes / (nw == 1 && ncb > 1 ? 4.2e6 : 4.8e6) * (load == 1 ? 1.08 : 1.0);  // two of the four operands
             double t = pass > 2 * floor ? pass : 2 * floor;

@@ -26,7 +26,7 @@ static void plans() {
     for (int64_t rows : {(int64_t)1, (int64_t)3, (int64_t)30, (int64_t)256, (int64_t)4096, ((int64_t)1 << 26) - 1})
         for (int roles : {1, 2, 3})
             for (int64_t N : {(int64_t)1, (int64_t)31, (int64_t)33, (int64_t)1001, (int64_t)65536, (int64_t)1 << 20, ((int64_t)1 << 31) - 1})
-                for (int64_t DK : {8, 64, 88, 128, 256})
+                for (int64_t DK : {8, 64, 88, 128, 136, 192, 256})
                     for (int64_t DV : {8, 64, 72, 128, 200, 256})
                         for (lconv_dtype_t dt : {LCONV_F32, LCONV_F16, LCONV_BF16}) {
                             const lcv::LinPlan p = lcv::linattn_plan(rows, roles, N, DK, DV, dt);

@@ -92,6 +92,13 @@ CASES = [
     (2, 4, 2, 1500, 72, 136, "bnhd", True, (1500, 700)),
     (3, 2, 1, 2600, 256, 128, "bnhd", True, (2600, 0, 1)),
     (1, 2, 2, 3001, 128, 24, "bhnd", False, None),
+    # widths between the tiles', past the pipelined loop's start
+    (1, 3, 3, 200, 24, 40, "bnhd", True, None),
+    (1, 2, 2, 400, 16, 136, "bhnd", True, None),
+    (2, 2, 2, 300, 96, 80, "bnhd", False, (300, 222)),
+    (2, 2, 1, 333, 192, 192, "bnhd", True, None),
+    (2, 2, 2, 257, 168, 184, "bhnd", True, (250, 257)),
+    (1, 2, 2, 290, 248, 8, "bhnd", True, None),
 ]
 
 

@@ -39,6 +39,7 @@
 // its power.
 #pragma once
 #include "linattn_tiles.h"
+#include "mixer_plan.h"
 
 namespace lcv {
 namespace {
@@ -48,7 +49,7 @@ namespace {
 // STATE: only the state that the segment adds up from zero, for the segments after it.  WIDE: some roles' O leaves in fp32.
 // EXACT: the state's sums to fp32's accuracy.
 template <int IO, int KT, int NW, bool STATE, bool WIDE, bool EXACT>
-__global__ void __launch_bounds__(256, KT > 8 || (IO == CT_F32 && NW == 2) ? 1 : NW == 1 && (IO == CT_BF16 || (IO == CT_F16 && KT <= 6)) ? 3 : 2) linattn_chunk_kernel(LinJob a) {
+__global__ void __launch_bounds__(256, linattn_alone(KT, NW, IO == CT_F32) ? 1 : NW == 1 && KT <= (IO == CT_BF16 ? 8 : IO == CT_F16 ? 6 : 0) ? 3 : 2) linattn_chunk_kernel(LinJob a) {
     using M = Mx<IO>;
     using E = typename M::E;
     using Frag = typename M::Frag;
@@ -69,7 +70,7 @@ __global__ void __launch_bounds__(256, KT > 8 || (IO == CT_F32 && NW == 2) ? 1 :
     constexpr int SURE = KHALF ? NV : LOADS;         // loads of a chunk that every wave issues
     // chunks in LDS: one in hand, and two on their way where a compute unit then still holds the workgroups
     // that its registers allow (NW = 1: three, which hide each other's loads)
-    constexpr int STAGES = 3 * STAGE <= (KT > 8 ? 160 : NW == 1 ? 53 : 80) * 1024 ? 3 : 2;
+    constexpr int STAGES = 3 * STAGE <= (linattn_alone(KT, NW, IO == CT_F32) ? 160 : NW == 1 && KT <= 8 ? 53 : 80) * 1024 ? 3 : 2;
     __shared__ __attribute__((aligned(16))) char lds0[STAGE], lds1[STAGE];
     char* lds2 = nullptr;
     if constexpr (STAGES == 3) {

@@ -15,27 +15,30 @@ struct LinPlan {
 
 inline int linattn_kt(int64_t DK) { return DK <= 32 ? 2 : DK <= 64 ? 4 : DK <= 96 ? 6 : DK <= 128 ? 8 : DK <= 192 ? 12 : 16; }
 
-// Microseconds that a workgroup alone on its compute unit takes for a chunk of 32 tokens, measured at DK = DV = 64, 128, 256:
-// a chunk's chain of waits is much the same for narrow heads; fp16 scales its operands; fp32's matrix products take sixteen
-// times as long.
+// Microseconds that a workgroup alone on its compute unit takes for a chunk of 32 tokens, measured: a chunk's chain of waits
+// is much the same for narrow heads; fp16 scales its operands; fp32's matrix products take sixteen times as long.
 inline double linattn_chunk_us(int kt, int nw, lconv_dtype_t dtype) {
-    static const double us[3][3][2] = {{{3.0, 4.5}, {3.9, 6.4}, {7.8, 12.8}},      // fp32; 64 and 128 columns
-                                       {{1.25, 1.75}, {1.5, 2.4}, {2.5, 4.0}},     // fp16
-                                       {{0.9, 1.2}, {0.95, 1.25}, {1.55, 2.45}}};  // bf16
-    return us[dtype == LCONV_F32 ? 0 : dtype == LCONV_F16 ? 1 : 2][kt <= 4 ? 0 : kt <= 8 ? 1 : 2][nw - 1] * (kt == 12 ? 0.8 : 1.0);
+    static const double us[3][5][2] = {     // contraction of 32, 64, 96 and 128, 192, 256; 64 and 128 columns
+        {{2.0, 3.0}, {3.0, 4.5}, {3.9, 6.4}, {6.0, 10.0}, {7.8, 12.8}},       // fp32
+        {{0.7, 0.9}, {1.25, 1.75}, {1.5, 2.4}, {2.1, 3.1}, {2.5, 4.0}},       // fp16
+        {{0.45, 0.6}, {0.9, 1.2}, {0.95, 1.25}, {1.2, 2.0}, {1.55, 2.45}}};   // bf16
+    return us[dtype == LCONV_F32 ? 0 : dtype == LCONV_F16 ? 1 : 2][kt == 2 ? 0 : kt == 4 ? 1 : kt <= 8 ? 2 : kt == 12 ? 3 : 4][nw - 1];
 }
+
+// Whether a compute unit holds one workgroup at most: the widest heads and fp32 at 128 columns fill its registers and LDS.
+constexpr bool linattn_alone(int kt, int nw, bool f32) { return kt == 16 || (kt == 12 && (nw == 2 || f32)) || (nw == 2 && f32); }
 
 // Chosen by estimated time over the two tile widths and powers of two of segments.  With n chunks in a segment and L
 // workgroups on a compute unit (256 of them),
-//   main pass   n chunks of linattn_chunk_us, 1 + 0.35 (L - 1) as long where they share the unit (L for the widest heads
-//               and for fp32 at 128 columns, which fill it), but no less than the tokens' bytes at 4.8 TB/s (4.2 where
-//               several column blocks read Q and K, less 8 % for a single workgroup to a unit); three roles share some
-//               of what they read in the L2
+//   main pass   2 us and n chunks of linattn_chunk_us, 1 + 0.35 (L - 1) as long where they share the unit (L where they
+//               cannot), but no less than the tokens' bytes at 4.8 TB/s (4.2 where several column blocks read Q and K,
+//               less 8 % for a single workgroup to a unit); three roles share some of what they read in the L2
 //   more than one segment adds the state pass, 0.65 of that, 12 us for its two launches, and the segments'
 //   states, written and read twice, at 8 TB/s.
 // Both sides measured (us): bf16 D = 128, 32 rows N 4096: one segment 128, 4: 76, 8: 70, 16: 76; 128 rows N 2048: 1: 82, 2: 111;
 // gradients of 256 rows N 2048: 64 columns 340, 128 columns 302; of 16 rows N 1024: 33 in one segment, 39 in two; 16 rows
-// N 65536: 64 columns 384, 128 columns 365; fp16 gradients D = 64 of 32 rows N 1001: one segment 52, 8: 38.
+// N 65536: 64 columns 384, 128 columns 365; fp16 gradients D = 64 of 32 rows N 1001: one segment 52, 8: 38;
+// D = 192 bf16, 32 rows N 4096: 64 columns 122 in 8 segments, 128 columns 146 in 4; D = 24: 8 segments 31, 16: 28, 128: 41.
 inline LinPlan linattn_plan(int64_t rows, int nroles, int64_t N, int64_t DK, int64_t DV, lconv_dtype_t dtype) {
     const int64_t chunks = (N + 31) / 32;
     const int kt = linattn_kt(DK);
@@ -46,8 +49,8 @@ inline LinPlan linattn_plan(int64_t rows, int nroles, int64_t N, int64_t DK, int
         const int64_t ncb = (DV + 64 * nw - 1) / (64 * nw), wgs = rows * nroles * ncb;
         for (int64_t nseg = 1; nseg == 1 || (nseg <= 1024 && nseg * 2 <= chunks && wgs * nseg <= 4096); nseg *= 2) {
             const int64_t per = (chunks + nseg - 1) / nseg, load = (wgs * nseg + 255) / 256;
-            const double shared = kt > 8 || (nw == 2 && dtype == LCONV_F32) ? (double)load : 1.0 + 0.35 * (double)(load - 1);
-            const double pass = (double)per * linattn_chunk_us(kt, nw, dtype) * shared;
+            const double shared = linattn_alone(kt, nw, dtype == LCONV_F32) ? (double)load : 1.0 + 0.35 * (double)(load - 1);
+            const double pass = (2.0 + (double)per * linattn_chunk_us(kt, nw, dtype)) * shared;
             const double floor = bytes / (nw == 1 && ncb > 1 ? 4.2e6 : 4.8e6) * (load == 1 ? 1.08 : 1.0);  // two of the four operands
             double t = pass > 2 * floor ? pass : 2 * floor;
             if (nseg > 1)

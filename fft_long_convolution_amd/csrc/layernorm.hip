@@ -189,7 +189,8 @@ __global__ void __launch_bounds__(256) ln_fwd_long_kernel(NormArgs a) {
     }
 }
 
-// The gradient: dx of every row, and the column sums of the workgroup's rows to part[0 / 1][block][C].
+// The gradient: dx of every row, and the column sums of the workgroup's rows to part[0 / 1][block][C], or, of a workgroup
+// alone, to dweight and dbias.
 // A row is read before it is written, so dx may stand in place of dy or x.
 template <int IO, int LANES, int K>
 __global__ void __launch_bounds__(LANES < 256 ? 256 : LANES) ln_bwd_kernel(NormArgs a) {
@@ -197,7 +198,7 @@ __global__ void __launch_bounds__(LANES < 256 ? 256 : LANES) ln_bwd_kernel(NormA
     constexpr int ROWS = LANES < 256 ? 256 / LANES : 1;
     const int lane = threadIdx.x % LANES, C = (int)a.C;
     const float inv = 1.f / (float)C;
-    const bool sums = a.part != nullptr;
+    const bool sums = a.dweight || a.dbias, alone = gridDim.x == 1;
     Group<IO> w[K];
     float sw[K][8], sb[K][8];
 #pragma unroll
@@ -281,8 +282,10 @@ __global__ void __launch_bounds__(LANES < 256 ? 256 : LANES) ln_bwd_kernel(NormA
         const int c = 8 * (lane + LANES * k);
         if (threadIdx.x < LANES && c < C) {
             const int64_t o = (int64_t)blockIdx.x * C + c, nb = (int64_t)gridDim.x * C;
-            store8_part<CT_F32>(a.part, o, left(c, C), sw[k]);
-            store8_part<CT_F32>(a.part, nb + o, left(c, C), sb[k]);
+            float* const pw = alone ? a.dweight : a.part;
+            float* const pb = alone ? a.dbias : a.part + nb;
+            if (pw) store8_part<CT_F32>(pw, o, left(c, C), sw[k]);
+            if (pb) store8_part<CT_F32>(pb, o, left(c, C), sb[k]);
         }
     }
 }
@@ -417,7 +420,7 @@ hipError_t launch_layernorm_fwd(int dtype, const NormArgs& a, hipStream_t stream
 
 hipError_t launch_layernorm_bwd(int dtype, const NormArgs& a, hipStream_t stream) {
     const bool sums = a.dweight || a.dbias;
-    const int64_t np = layernorm_parts(a.rows, a.C);
+    const int64_t np = a.rows > 0 ? layernorm_parts(a.rows, a.C) : 0;   // no rows: no partial sums to read
     hipError_t e = hipSuccess;
     if (a.rows > 0 && a.C <= kNormRegisterC) {
         e = by_dtype(dtype, [&](auto io) {
@@ -434,7 +437,7 @@ hipError_t launch_layernorm_bwd(int dtype, const NormArgs& a, hipStream_t stream
         const unsigned grid = (unsigned)(a.rows < 4096 ? a.rows : 4096);
         e = by_dtype(dtype, [&](auto io) { ln_dx_long_kernel<io.value><<<grid, 256, 0, stream>>>(a); });
     }
-    if (e != hipSuccess || !sums) return e;
+    if (e != hipSuccess || !sums || (np == 1 && a.rows > 0 && a.C <= kNormRegisterC)) return e;
     ln_sum_kernel<<<(unsigned)((a.C + 31) / 32), 256, 0, stream>>>(a.part, a.dweight, a.dbias, (int)np, (int)a.C);
     return hipGetLastError();
 }

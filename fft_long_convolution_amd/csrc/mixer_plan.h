@@ -95,9 +95,11 @@ constexpr int64_t kNormRegisterC = 8192;
 // fill the chip (three of 256 threads or two of 512 to each of 256 compute units), no more than turns of
 // rows, since every one costs 8 C bytes written and read.  Measured (bf16, us, at 256, 512, 768 and 1024): 32768 rows of
 // 768: 75, 48, 42, 41; 16384 of 2048: 64, 47, 46, 47; 16384 of 4096: 111, 82, 97, 88; 8192 of 8192: 102, 90, 103, 105.
+// Three turns or fewer go to one workgroup, which leaves the sums itself and saves their launch.
 inline int64_t layernorm_parts(int64_t rows, int64_t C) {
     const int64_t per = C <= 128 ? 16 : C <= 1024 ? 4 : C <= 2048 ? 2 : 1;   // rows a workgroup has in hand
     const int64_t turns = (rows + per - 1) / per, most = C <= 2048 ? 768 : 512;
+    if (C <= kNormRegisterC && turns > 0 && turns <= 3) return 1;
     return turns < most ? turns : most;
 }
 

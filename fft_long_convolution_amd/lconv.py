@@ -1039,6 +1039,11 @@ def rotary(q, k, positions, inv_freq, interleaved=False, inverse=False, magnitud
     return yq, yk
 
 
+def _dense_like(x):
+    torch = _torch()
+    return torch.empty_like(x) if x.is_contiguous() else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+
+
 def _rows(name, t, shape, dtype):
     """(rows, C, row stride) of a tensor normalised over its last dimension: dense, or 2-D with a row
     stride."""
@@ -1074,10 +1079,10 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, need_stats=True, out=None, s
     dev = _same_gpu("x weight bias out", (x, weight, bias, out))
     ctx, st = _at(dev, stream)
     with ctx:
-        y = torch.empty(x.shape, dtype=x.dtype, device=dev) if out is None else out
+        y = _dense_like(x) if out is None else out
         ys = C if out is None else _rows("out", y, x.shape, x.dtype)[2]
         mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev) if need_stats else None
-        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev) if need_stats else None
+        rstd = torch.empty_like(mean) if need_stats else None
         _check(lconv_layernorm_fwd(_ptr(x), xs, _ptr(weight), _ptr(bias), _ptr(y), ys, _ptr(mean), _ptr(rstd), rows, C,
                                    float(eps), dt, st), "lconv_layernorm_fwd")
     return y, mean, rstd
@@ -1099,10 +1104,10 @@ def layer_norm_bwd(dy, x, weight, mean, rstd, need_dweight=True, need_dbias=True
     dev = _same_gpu("dy x weight mean rstd out", (dy, x, weight, mean, rstd, out))
     ctx, st = _at(dev, stream)
     with ctx:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=dev) if out is None else out
+        dx = _dense_like(x) if out is None else out
         dxs = C if out is None else _rows("out", dx, x.shape, x.dtype)[2]
         dw = torch.empty((C,), dtype=torch.float32, device=dev) if need_dweight and weight is not None else None
-        db = torch.empty((C,), dtype=torch.float32, device=dev) if need_dbias else None
+        db = None if not need_dbias else torch.empty_like(dw) if dw is not None else torch.empty((C,), dtype=torch.float32, device=dev)
         wsb = lconv_layernorm_bwd_workspace_bytes(rows, C) if dw is not None or db is not None else 0
         ws = torch.empty(wsb, dtype=torch.uint8, device=dev) if wsb else None
         _check(lconv_layernorm_bwd(_ptr(dy), dys, _ptr(x), xs, _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dx), dxs,

@@ -45,6 +45,11 @@ static void plans() {
     for (int64_t rows : {(int64_t)1, (int64_t)333, ((int64_t)1 << 31) - 1})
         for (int64_t C : {1, 7, 128, 129, 1001, 4096, 8192, 8193, 65536})
             if (lcv::layernorm_parts(rows, C) < 1 || lcv::layernorm_parts(rows, C) > rows) ++failures;
+    for (int64_t C : {1, 128, 1001, 8192, 8193})
+        if (lcv::layernorm_parts(0, C) != 0) {      // no rows leave no partial sum to be read
+            std::fprintf(stderr, "layernorm_parts(0, %lld) = %lld\n", (long long)C, (long long)lcv::layernorm_parts(0, C));
+            ++failures;
+        }
 }
 
 int main() {

@@ -34,7 +34,8 @@ bool overlap(const Range& a, const Range& b) {
 }
 
 // Strides of an operand [B][H][N][D]: resolves NULL to dense and checks them; `r` gets its range.
-// B, H, N > 0 here.
+// B, H, N > 0 here.  A dimension of length one may come with any stride; it leaves with 0, since the kernels also form
+// addresses a chunk away from a row's ends (the gradients' 31 tokens before a single one, which no lane then reads).
 lconv_status_t operand(const void* p, const lconv_strides_t* given, int64_t B, int64_t H, int64_t N, int64_t D,
                        lconv_dtype_t dt, bool written, lconv_strides_t* s, Range* r) {
     const int64_t es = (int64_t)dtype_size(dt);
@@ -45,6 +46,9 @@ lconv_status_t operand(const void* p, const lconv_strides_t* given, int64_t B, i
         s->n = D;
         if (!mul_ok(N, D, &s->h) || !mul_ok(H, s->h, &s->b) || !mul_ok(B, s->b, &t)) return LCONV_ERR_INVALID_SHAPE;
     }
+    if (B == 1) s->b = 0;
+    if (H == 1) s->h = 0;
+    if (N == 1) s->n = 0;
     struct Dim { int64_t n, st; } dim[3] = {{B, s->b}, {H, s->h}, {N, s->n}};
     int64_t last = D, t;                 // elements from the start to the end of the last row
     for (const Dim& d : dim) {

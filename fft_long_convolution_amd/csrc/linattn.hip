@@ -163,9 +163,8 @@ hipError_t launch_linattn_step(int dtype, const LinStepArgs& a, hipStream_t stre
     // few rows: 32 columns to a workgroup, four times the workgroups to share the latency.  Measured (D = 128, us, at 32
     // and 128 columns): 16 rows 4.7, 5.9; 64 rows 5.2, 6.3; 256 rows 8.2, 7.6; 1024 rows 28, 21; 4096 rows 91, 82
     const int64_t rows = a.B * a.H;
-    const bool narrow = rows * ((a.DV + 127) / 128) < 128;
-    const int cb = narrow ? 32 : 128;
-    const unsigned grid = (unsigned)(rows * ((a.DV + cb - 1) / cb));
+    const bool narrow = linattn_step_columns(rows, a.DV) == 32;
+    const unsigned grid = (unsigned)linattn_step_workgroups(rows, a.DV);
     return by_dtype(dtype, [&](auto io) {
         if (narrow) linattn_step_kernel<io.value, 32><<<grid, 256, 0, stream>>>(a);
         else linattn_step_kernel<io.value, 128><<<grid, 256, 0, stream>>>(a);

@@ -552,15 +552,15 @@ __global__ void __launch_bounds__(256, linattn_alone(KT, NW, IO == CT_F32) ? 1 :
 template <int IO, int KT, int NW, bool WIDE, bool EXACT>
 hipError_t launch_chunk_as(const LinJob& a, hipStream_t stream) {
     const int64_t rows = a.B * a.H;
-    const auto grid = [&](int64_t groups) { return (unsigned)((groups + 7) / 8 * 8 * a.nroles * a.ncb); };
+    const auto grid = [&](int nseg) { return (unsigned)linattn_workgroups(LinPlan{a.kt, a.nw, a.ncb, nseg, a.seg_len}, rows, a.nroles); };
     if (a.nseg > 1) {
-        linattn_chunk_kernel<IO, KT, NW, true, false, EXACT><<<grid(rows * (a.nseg - 1)), 256, 0, stream>>>(a);
+        linattn_chunk_kernel<IO, KT, NW, true, false, EXACT><<<grid(a.nseg - 1), 256, 0, stream>>>(a);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
         e = launch_linattn_join(a, IO == CT_F32, stream);
         if (e != hipSuccess) return e;
     }
-    linattn_chunk_kernel<IO, KT, NW, false, WIDE, EXACT><<<grid(rows * a.nseg), 256, 0, stream>>>(a);
+    linattn_chunk_kernel<IO, KT, NW, false, WIDE, EXACT><<<grid(a.nseg), 256, 0, stream>>>(a);
     return hipGetLastError();
 }
 

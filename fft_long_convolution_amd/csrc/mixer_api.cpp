@@ -99,7 +99,13 @@ bool linattn_dims_ok(int64_t B, int64_t H, int64_t G, int64_t N, int64_t Dk, int
     if (G < 1 || H % G || N >= ((int64_t)1 << 31)) return false;
     if (Dk < 8 || Dk > LCONV_LINATTN_MAX_D || Dk % 8 || Dv < 8 || Dv > LCONV_LINATTN_MAX_D || Dv % 8) return false;
     int64_t rows;
-    return mul_ok(B, H, &rows) && rows < ((int64_t)1 << 26);  // workgroups of a launch: a few per (b, h)
+    return mul_ok(B, H, &rows) && rows <= kMaxWorkgroups;     // a launch has a workgroup to a (b, h) at least
+}
+
+// whether the forward's launches fit a grid: at most three roles of four column blocks to a row, and few rows in segments
+constexpr int64_t kRowsThatFit = (int64_t)1 << 20;
+bool linattn_fwd_fits(int64_t B, int64_t H, int64_t N, int64_t Dk, int64_t Dv, lconv_dtype_t dtype) {
+    return B * H <= kRowsThatFit || linattn_workgroups(linattn_plan(B * H, 1, N, Dk, Dv, dtype), B * H, 1) <= kMaxWorkgroups;
 }
 
 // The chunk kernel reaches a chunk's 32 tokens by 32-bit byte offsets from its first: 31 strides have to fit.
@@ -143,6 +149,15 @@ BwdPlan bwd_plan(int64_t B, int64_t H, int64_t N, int64_t Dk, int64_t Dv, lconv_
     return p;
 }
 
+// whether the gradients' launches fit a grid, the decay's (which is on or not) among them
+bool linattn_bwd_fits(int64_t B, int64_t H, int64_t N, int64_t Dk, int64_t Dv, lconv_dtype_t dtype) {
+    if (B * H <= kRowsThatFit) return true;
+    const BwdPlan p = bwd_plan(B, H, N, Dk, Dv, dtype);
+    for (int i = 0; i < p.launches; ++i)
+        if (linattn_workgroups(p.plan[i], B * H, p.roles[i]) > kMaxWorkgroups) return false;
+    return linattn_tan_workgroups(B * H, N, Dv) <= kMaxWorkgroups;
+}
+
 // the decay's gradient: partial sums, and the segments' states
 size_t tan_part_bytes(int64_t rows, int64_t N, int64_t Dv) {
     return round256((size_t)(rows * linattn_tan_plan(rows, N, Dv).nseg) * (size_t)linattn_tan_blocks(Dv) * 4);
@@ -158,7 +173,9 @@ extern "C" {
 
 size_t lconv_linattn_workspace_bytes(int64_t B, int64_t H, int64_t G, int64_t N, int64_t Dk, int64_t Dv,
                                      lconv_dtype_t dtype) {
-    if (!dtype_ok(dtype) || B <= 0 || H <= 0 || N <= 0 || !linattn_dims_ok(B, H, G, N, Dk, Dv)) return 0;
+    if (!dtype_ok(dtype) || B <= 0 || H <= 0 || N <= 0 || !linattn_dims_ok(B, H, G, N, Dk, Dv) ||
+        !linattn_fwd_fits(B, H, N, Dk, Dv, dtype))
+        return 0;
     return linattn_states_bytes(linattn_plan(B * H, 1, N, Dk, Dv, dtype), B * H);
 }
 
@@ -171,7 +188,7 @@ lconv_status_t lconv_linattn_fwd(const void* q, const lconv_strides_t* q_strides
     if (!dtype_ok(dtype)) return LCONV_ERR_UNSUPPORTED;
     if (B < 0 || H < 0 || G < 0 || N < 0 || Dk < 0 || Dv < 0) return LCONV_ERR_INVALID_SHAPE;
     if (B == 0 || H == 0) return LCONV_SUCCESS;
-    if (!linattn_dims_ok(B, H, G, N, Dk, Dv)) return LCONV_ERR_UNSUPPORTED;
+    if (!linattn_dims_ok(B, H, G, N, Dk, Dv) || (N > 0 && !linattn_fwd_fits(B, H, N, Dk, Dv, dtype))) return LCONV_ERR_UNSUPPORTED;
     if (!aligned16(state_in) || !aligned16(state_out)) return LCONV_ERR_MISALIGNED;
     const int64_t states = B * H * Dk * Dv;
     const Range rsi = buffer(state_in, states, 4), rso = buffer(state_out, states, 4);
@@ -213,7 +230,9 @@ lconv_status_t lconv_linattn_fwd(const void* q, const lconv_strides_t* q_strides
 
 size_t lconv_linattn_bwd_workspace_bytes(int64_t B, int64_t H, int64_t G, int64_t N, int64_t Dk, int64_t Dv,
                                          lconv_dtype_t dtype) {
-    if (!dtype_ok(dtype) || B <= 0 || H <= 0 || N <= 0 || !linattn_dims_ok(B, H, G, N, Dk, Dv)) return 0;
+    if (!dtype_ok(dtype) || B <= 0 || H <= 0 || N <= 0 || !linattn_dims_ok(B, H, G, N, Dk, Dv) ||
+        !linattn_bwd_fits(B, H, N, Dk, Dv, dtype))
+        return 0;
     return head_grads_bytes(B, H, G, N, Dk) + head_grads_bytes(B, H, G, N, Dv) + tan_bytes(B * H, N, Dk, Dv) +
            bwd_plan(B, H, N, Dk, Dv, dtype).total;
 }
@@ -229,7 +248,8 @@ lconv_status_t lconv_linattn_bwd(const void* dy, const lconv_strides_t* dy_strid
     if (!dtype_ok(dtype)) return LCONV_ERR_UNSUPPORTED;
     if (B < 0 || H < 0 || G < 0 || N < 0 || Dk < 0 || Dv < 0) return LCONV_ERR_INVALID_SHAPE;
     if (H == 0) return LCONV_SUCCESS;
-    if (!linattn_dims_ok(B, H, G, N, Dk, Dv)) return LCONV_ERR_UNSUPPORTED;
+    if (!linattn_dims_ok(B, H, G, N, Dk, Dv) || (B > 0 && N > 0 && !linattn_bwd_fits(B, H, N, Dk, Dv, dtype)))
+        return LCONV_ERR_UNSUPPORTED;
     if (!aligned16(state_in) || !aligned16(dstate_out) || !aligned16(dstate_in) || !aligned16(dlog_decay))
         return LCONV_ERR_MISALIGNED;
     const int64_t states = B * H * Dk * Dv;
@@ -341,7 +361,7 @@ lconv_status_t lconv_linattn_step(const void* q, const lconv_strides_t* q_stride
     if (!dtype_ok(dtype)) return LCONV_ERR_UNSUPPORTED;
     if (B < 0 || H < 0 || G < 0 || Dk < 0 || Dv < 0 || nslots < 0) return LCONV_ERR_INVALID_SHAPE;
     if (B == 0 || H == 0) return LCONV_SUCCESS;
-    if (!linattn_dims_ok(B, H, G, 1, Dk, Dv)) return LCONV_ERR_UNSUPPORTED;
+    if (!linattn_dims_ok(B, H, G, 1, Dk, Dv) || linattn_step_workgroups(B * H, Dv) > kMaxWorkgroups) return LCONV_ERR_UNSUPPORTED;
     int64_t states;
     if (!slots && nslots < B) return LCONV_ERR_INVALID_SHAPE;
     if (!mul_ok(nslots, H * Dk * Dv, &states) || !mul_ok(states, 4, &states)) return LCONV_ERR_INVALID_SHAPE;
@@ -375,14 +395,15 @@ lconv_status_t lconv_rotary(const void* q, const lconv_strides_t* q_strides, con
     if (B == 0 || N == 0 || (H == 0 && (G == 0 || (!k && !yk)))) return LCONV_SUCCESS;
     if (D < 8 || D > 1024 || D % 8 || rot < 2 || rot > D || rot % 2 || (flags & ~3)) return LCONV_ERR_UNSUPPORTED;
     int64_t rows, t;
-    if (!mul_ok(B, N, &rows) || !mul_ok(rows, D, &t) || t >= ((int64_t)1 << 39) || H >= (1 << 20) || G >= (1 << 20))
+    const bool on[2] = {H > 0, G > 0 && (k || yk)};
+    if (!mul_ok(B, N, &rows) || !mul_ok(rows, D, &t) || t >= ((int64_t)1 << 39) || H >= (1 << 20) || G >= (1 << 20) ||
+        rotary_plan(rows, D, rot, (int)((on[0] ? H : 0) + (on[1] ? G : 0))).threads > 256 * kMaxWorkgroups)
         return LCONV_ERR_UNSUPPORTED;  // threads of one launch
     if (!inv_freq) return LCONV_ERR_NULL_POINTER;
     if (!mul_ok(B - 1, pos_stride, &t) || t > INT64_MAX / 8 - N) return LCONV_ERR_INVALID_SHAPE;
     const Range rp = buffer(positions, t + N, 4), rf = buffer(inv_freq, rot / 2, 4);
     RotaryArgs a{};
     Range rx[2]{}, ry[2]{};
-    const bool on[2] = {H > 0, G > 0 && (k || yk)};
     lconv_status_t st;
     if (on[0]) {
         if ((st = operand(q, q_strides, B, H, N, D, dtype, false, &a.q.s, &rx[0])) != LCONV_SUCCESS) return st;

@@ -72,6 +72,12 @@ inline size_t linattn_states_bytes(const LinPlan& p, int64_t rows) {
     return p.nseg > 1 ? (size_t)rows * (size_t)p.nseg * (size_t)(p.kt * 16 * p.ncb * 64 * p.nw) * 4 : 0;
 }
 
+// Threads along a launch's grid have to stay below 2^32: so many workgroups of 256.
+constexpr int64_t kMaxWorkgroups = ((int64_t)1 << 24) - 1;
+
+// Workgroups of the chunk kernel's main pass (the state pass has fewer): groups rounded up to the XCDs.
+inline int64_t linattn_workgroups(const LinPlan& p, int64_t rows, int nroles) { return (rows * p.nseg + 7) / 8 * 8 * nroles * p.ncb; }
+
 // The decay's gradient: column blocks, and segments of at least four chunks until two workgroups to a compute unit.
 // Measured (bf16, us beside the other gradients): 32 rows of 4096 tokens, D = 128, one segment 286, 4: 110, 8: 86, 16: 104;
 // 16 rows of 65536: 8: 892, 16: 663, 32: 677; 8 rows of 1000, D = 64, 1: 55, 4: 30, 8: 25, 16: 26; 128 rows of 2048: 1: 156, 4: 175.
@@ -86,6 +92,33 @@ inline LinTanPlan linattn_tan_plan(int64_t rows, int64_t N, int64_t DV) {
     while (nseg * 8 <= chunks && wgs * nseg * 2 <= 512) nseg *= 2;
     const int64_t len = (chunks + nseg - 1) / nseg * 32;
     return LinTanPlan{(int)((N + len - 1) / len), len};
+}
+
+inline int64_t linattn_tan_workgroups(int64_t rows, int64_t N, int64_t DV) { return rows * linattn_tan_plan(rows, N, DV).nseg * linattn_tan_blocks(DV); }
+
+// Single tokens: columns to a workgroup (see launch_linattn_step).
+inline int linattn_step_columns(int64_t rows, int64_t DV) { return rows * ((DV + 127) / 128) < 128 ? 32 : 128; }
+inline int64_t linattn_step_workgroups(int64_t rows, int64_t DV) {
+    const int cb = linattn_step_columns(rows, DV);
+    return rows * ((DV + cb - 1) / cb);
+}
+
+// Rotary: units of a token (8 pairs, or 16 copied elements), four heads to a thread where that leaves eight waves to a
+// compute unit.
+struct RotaryPlan {
+    int turns, units, per, hgroups;
+    int64_t threads;
+};
+inline RotaryPlan rotary_plan(int64_t tokens, int64_t D, int64_t rot, int heads) {
+    RotaryPlan p{};
+    p.turns = (int)((rot / 2 + 7) / 8);
+    p.units = p.turns + (int)((D - rot + 15) / 16);
+    const int64_t each = tokens * p.units;
+    p.per = 4;
+    while (p.per > 1 && each * ((heads + p.per - 1) / p.per) < 256 * 512) p.per /= 2;
+    p.hgroups = (heads + p.per - 1) / p.per;
+    p.threads = each * p.hgroups;
+    return p;
 }
 
 // Layer norm: rows up to this width are held in registers.

@@ -11,6 +11,7 @@
 // at most pi / 4, are Taylor polynomials in fp32 (next terms: x^11 / 11! < 2e-9, x^12 / 12! < 2e-10).
 #include "mixer_kernels.h"
 #include "mixer_io.h"
+#include "mixer_plan.h"
 
 namespace lcv {
 namespace {
@@ -118,14 +119,8 @@ __global__ void __launch_bounds__(256) rotary_kernel(RotaryArgs a, int units, in
 
 template <int IO>
 void go(const RotaryArgs& a, hipStream_t stream) {
-    const int turns = (a.rot / 2 + 7) / 8, units = turns + (a.D - a.rot + 15) / 16, heads = a.H + a.G;
-    const int64_t each = a.B * a.N * units;
-    // four heads to a thread where that leaves eight waves to a compute unit
-    int per = 4;
-    while (per > 1 && each * ((heads + per - 1) / per) < 256 * 512) per /= 2;
-    const int hgroups = (heads + per - 1) / per;
-    const int64_t total = each * hgroups;
-    rotary_kernel<IO><<<(unsigned)((total + 255) / 256), 256, 0, stream>>>(a, units, turns, per, hgroups, total);
+    const RotaryPlan p = rotary_plan(a.B * a.N, a.D, a.rot, a.H + a.G);
+    rotary_kernel<IO><<<(unsigned)((p.threads + 255) / 256), 256, 0, stream>>>(a, p.units, p.turns, p.per, p.hgroups, p.threads);
 }
 
 }  // namespace

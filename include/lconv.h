@@ -499,7 +499,7 @@ typedef struct {
  * Tokens are taken 32 at a time: a value that is not finite in k or v reaches the outputs from its token on,
  * one in v those of the up to 31 tokens before it as well; one in q its own row's.
  * Supported: Dk, Dv multiples of 8 in [8, 256]; H a multiple of G; N < 2^31; tokens at most 2^27 bytes apart
- * (strides' n, N > 1); every dtype.
+ * (strides' n, N > 1); launches of fewer than 2^32 threads (B H up to 2^20 always, single tokens 2^22); every dtype.
  * B, H or N = 0 is a no-op apart from state_out, which is set as for rows of length 0 (N = 0).
  */
 size_t lconv_linattn_workspace_bytes(int64_t B, int64_t H, int64_t G, int64_t N, int64_t Dk, int64_t Dv,
@@ -560,7 +560,8 @@ lconv_status_t lconv_linattn_step(const void* q, const lconv_strides_t* q_stride
  *   positions  int32, device, row b at positions + b * pos_stride (0: one row for all); NULL: 0 .. N-1
  *   inv_freq   [rot/2] fp32, device
  * yq may be q itself (same pointer and strides), likewise yk and k; otherwise no overlap.
- * Supported: D a multiple of 8 in [8, 1024]; rot even in [2, D]; every dtype.
+ * Supported: D a multiple of 8 in [8, 1024]; rot even in [2, D]; fewer than 2^32 threads, each with 8 pairs or 16 copied
+ * elements of a token in up to four heads; every dtype.
  */
 #define LCONV_ROTARY_HALF        0
 #define LCONV_ROTARY_INTERLEAVED 1

@@ -47,6 +47,11 @@ template <int LANES> __device__ __forceinline__ void row_sums(float& a, float& b
     }
 }
 
+// A variance below zero is rounding; a row with a NaN or an infinity has none, and its rstd is a NaN (fmaxf would make
+// it 1 / sqrt(eps)).  Its mean is what the values add up to: an infinity leaves only NaNs to the centred sum.
+__device__ __forceinline__ float rstd_of(float var, float eps) { return 1.f / sqrtf((var < 0.f ? 0.f : var) + eps); }
+__device__ __forceinline__ float mean_of(float first, float rest) { return rest == rest ? first + rest : first; }
+
 // raw 8-element groups of a row: group k of lane l is elements 8 (l + LANES k) ..
 template <int IO> struct Group { uint4 r[IO == CT_F32 ? 2 : 1]; };
 template <int IO> __device__ __forceinline__ Group<IO> load_group(const void* p, int64_t row, int c, int C) {
@@ -106,8 +111,7 @@ __global__ void __launch_bounds__(LANES < 256 ? 256 : LANES) ln_fwd_kernel(NormA
             }
         }
         row_sums<LANES>(s1, s2, red, 1);
-        const float rest = s1 * inv, var = fmaxf(s2 * inv - rest * rest, 0.f);
-        const float rstd = 1.f / sqrtf(var + a.eps);
+        const float rest = s1 * inv, rstd = rstd_of(s2 * inv - rest * rest, a.eps);
         if (!on) continue;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
@@ -129,7 +133,7 @@ __global__ void __launch_bounds__(LANES < 256 ? 256 : LANES) ln_fwd_kernel(NormA
             store8_part<IO>(a.y, row * a.ys + c, left(c, C), y);
         }
         if (lane == 0) {
-            if (a.mean) a.mean[row] = first + rest;
+            if (a.mean) a.mean[row] = mean_of(first, rest);
             if (a.rstd) a.rstd[row] = rstd;
         }
     }
@@ -163,8 +167,7 @@ __global__ void __launch_bounds__(256) ln_fwd_long_kernel(NormArgs a) {
             }
         }
         row_sums<256>(s1, s2, red, 1);
-        const float rest = s1 * inv, var = fmaxf(s2 * inv - rest * rest, 0.f);
-        const float rstd = 1.f / sqrtf(var + a.eps);
+        const float rest = s1 * inv, rstd = rstd_of(s2 * inv - rest * rest, a.eps);
         for (int c = 8 * threadIdx.x; c < C; c += 2048) {
             const int n = left(c, C);
             load8_part<IO>(a.x, xo + c, n, x);
@@ -183,7 +186,7 @@ __global__ void __launch_bounds__(256) ln_fwd_long_kernel(NormArgs a) {
             store8_part<IO>(a.y, row * a.ys + c, n, x);
         }
         if (threadIdx.x == 0) {
-            if (a.mean) a.mean[row] = first + rest;
+            if (a.mean) a.mean[row] = mean_of(first, rest);
             if (a.rstd) a.rstd[row] = rstd;
         }
     }

@@ -31,12 +31,11 @@ __global__ void __launch_bounds__(256, KT <= (IO == CT_BF16 ? 8 : 4) ? 2 : 1) li
     __shared__ __attribute__((aligned(16))) char Lq[STATE ? 16 : C * RK * 16], Lk[C * RK * 16], Lv[C * RV * 16], Ly[STATE ? 16 : C * RV * 16];
     __shared__ float red[4];
 
-    const int ncb = linattn_tan_blocks(a.DV), nseg = STATE ? a.nseg - 1 : a.nseg;
-    const int cb = (int)(blockIdx.x % ncb);
-    const int64_t group = blockIdx.x / ncb, bh = group / nseg;
-    const int seg = (int)(group - bh * nseg);
-    const int64_t b = bh / a.H;
-    const int h = (int)(bh - b * a.H);
+    // 32-bit divisions, which stay in scalar registers like the addresses that come from them
+    const uint32_t ncb = linattn_tan_blocks(a.DV), nseg = STATE ? a.nseg - 1 : a.nseg;
+    const uint32_t group = blockIdx.x / ncb, row = group / nseg, brow = row / (uint32_t)a.H;
+    const int cb = (int)(blockIdx.x - group * ncb), seg = (int)(group - row * nseg), h = (int)(row - brow * (uint32_t)a.H);
+    const int64_t b = brow, bh = row;
     const int64_t len = row_len(a.lengths, b, a.N), beg = seg * a.seg_len;
     const int64_t end = beg + a.seg_len < len ? beg + a.seg_len : len;
     if (STATE && beg + a.seg_len >= len) return;   // no segment follows
@@ -49,21 +48,28 @@ __global__ void __launch_bounds__(256, KT <= (IO == CT_BF16 ? 8 : 4) ? 2 : 1) li
     const int col = cb * 64 + wave * 16 + x;       // the lane's column of S and T
     const float lg = log_gamma(a.log_decay, h);
     const int64_t size = (int64_t)a.DK * a.DV;
+    // byte offset of the lane's row i of tile k in a state
+    const auto at = [&](int k, int i) LCV_INLINE {
+        const int d = M::state_row(k, g);
+        return only_if(d < a.DK & col < a.DV, (uint32_t)((d + i) * a.DV + col) * 4);
+    };
 
     f32x4 S[KT], T[KT];
     {
         const float* s = STATE ? nullptr : a.nseg > 1 ? a.states + (bh * a.nseg + seg) * 2 * size : a.s_in ? a.s_in + bh * size : nullptr;
         const float* t = !STATE && a.nseg > 1 ? s + size : nullptr;
 #pragma unroll
-        for (int k = 0; k < KT; ++k) {
-            const int d = M::state_row(k, g);
-            const bool in = d < a.DK && col < a.DV;
+        for (int k = 0; k < KT; ++k) S[k] = T[k] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (s)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                S[k][i] = s && in ? s[(int64_t)(d + i) * a.DV + col] : 0.f;
-                T[k][i] = t && in ? t[(int64_t)(d + i) * a.DV + col] : 0.f;
-            }
-        }
+            for (int k = 0; k < KT; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) S[k][i] = load_f32(s, at(k, i));
+        if (t)
+#pragma unroll
+            for (int k = 0; k < KT; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) T[k][i] = load_f32(t, at(k, i));
     }
     // weights: (i - j) gamma^(i-j) of a pair, the token's place and gamma^place against the state that enters
     float wD[CT][4], nI[CT], wI[CT], wU[CJ][ES], nU[CJ][ES], em1 = 0.f, cgc = 0.f;
@@ -90,15 +96,19 @@ __global__ void __launch_bounds__(256, KT <= (IO == CT_BF16 ? 8 : 4) ? 2 : 1) li
             }
     };
 
-    // a chunk on its way in registers, as stored (fp16: 8 bytes to a group of 4)
+    // A chunk on its way in registers, as stored (fp16: 8 bytes to a group of 4).  A lane without a row or a column loads
+    // from past the buffer's end, which gives zeros: no lane leaves the wave, here as for the states.  (With branches
+    // round these loads the widest heads' kernel, its registers all taken, had a value that every lane needs later moved
+    // to another register inside a branch, for the branch's lanes alone.)
     typedef typename std::conditional<IO == CT_F16, uint2, uint4>::type Raw;
     struct Chunk { Raw q[STATE ? 1 : NK], k[NK], v[NV], y[STATE ? 1 : NV]; };
     const auto get = [&](const LinOperand& o, int slot, int R, int rows, int c0, int D, int64_t t0) LCV_INLINE {
-        Raw r{};
+        constexpr uint32_t es = IO == CT_F32 ? 4 : 2;
         const int row = slot / R, c = c0 + slot % R * VEC;
-        if (row < rows && c < D)
-            __builtin_memcpy(&r, (const typename Elem<IO>::T*)o.p + row_base(o, b, h) + (t0 + row) * o.s.n + c, sizeof(r));
-        return r;
+        const char* const base = (const char*)o.p + (row_base(o, b, h) + t0 * o.s.n) * es;
+        const uint32_t off = only_if(row < rows & c < D, (uint32_t)row * (uint32_t)(o.s.n * es) + (uint32_t)c * es);
+        if constexpr (IO == CT_F16) return __builtin_bit_cast(Raw, __builtin_amdgcn_raw_buffer_load_b64(buffer_at(base), off, 0, 0));
+        else return __builtin_bit_cast(Raw, __builtin_amdgcn_raw_buffer_load_b128(buffer_at(base), off, 0, 0));
     };
     const auto load = [&](Chunk& f, int64_t t0) LCV_INLINE {
         const int rows = (int)(end - t0 < C ? end - t0 : C);
@@ -115,7 +125,7 @@ __global__ void __launch_bounds__(256, KT <= (IO == CT_BF16 ? 8 : 4) ? 2 : 1) li
     };
     const auto put = [&](char* tile, int slot, int R, const Raw& r) LCV_INLINE {
         const int row = slot / R;
-        if (row >= C) return;
+        if (C * R % 256 != 0 && row >= C) return;      // a narrow tile takes fewer lanes
         char* const p = tile + row * R * 16 + ((slot % R) ^ swizzle(row, R)) * 16;
         if constexpr (IO == CT_F16)
             *(f32x4*)p = f32x4{unpack_lo<CT_F16>(r.x), unpack_hi<CT_F16>(r.x), unpack_lo<CT_F16>(r.y), unpack_hi<CT_F16>(r.y)};
@@ -204,7 +214,7 @@ __global__ void __launch_bounds__(256, KT <= (IO == CT_BF16 ? 8 : 4) ? 2 : 1) li
                         const f32x4 r = M::mma(vf[jt], yf[it], f32x4{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            if (jt < it || x > 4 * g + i) tan += p[it][jt][i] * r[i] * wD[it - jt][i];
+                            tan += jt < it || x > 4 * g + i ? p[it][jt][i] * r[i] * wD[it - jt][i] : 0.f;
                     }
             }
             // dy of token x of the tile, columns 4 g .. 4 g + 3 of the wave's 16
@@ -271,25 +281,19 @@ __global__ void __launch_bounds__(256, KT <= (IO == CT_BF16 ? 8 : 4) ? 2 : 1) li
     if constexpr (STATE) {
         float* const s = a.states + (bh * a.nseg + seg + 1) * 2 * size;
 #pragma unroll
-        for (int t = 0; t < KT; ++t) {
-            const int d = M::state_row(t, g);
-            if (d >= a.DK || col >= a.DV) continue;
+        for (int t = 0; t < KT; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                s[(int64_t)(d + i) * a.DV + col] = S[t][i];
-                s[size + (int64_t)(d + i) * a.DV + col] = T[t][i];
+                store_f32(s, at(t, i), S[t][i]);
+                store_f32(s + size, at(t, i), T[t][i]);
             }
-        }
     } else {
         tan *= a.scale;
         if (a.ds_out && end == len) {
 #pragma unroll
-            for (int t = 0; t < KT; ++t) {
-                const int d = M::state_row(t, g);
-                if (d >= a.DK || col >= a.DV) continue;
+            for (int t = 0; t < KT; ++t)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) tan += T[t][i] * a.ds_out[bh * size + (int64_t)(d + i) * a.DV + col];
-            }
+                for (int i = 0; i < 4; ++i) tan += T[t][i] * load_f32(a.ds_out + bh * size, at(t, i));
         }
         for (int w = 32; w; w >>= 1) tan += __shfl_xor(tan, w);
         if (lane == 0) red[wave] = tan;

@@ -130,6 +130,17 @@ constexpr uint32_t kBufferBytes = 0xfc000000u, kNowhere = 0xfffffff0u;
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const char* base) {
     return __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, (int)kBufferBytes, 0x00020000);
 }
+// An offset, or past the buffer's end; as a maximum, which the compiler does not turn into a branch.
+__device__ __forceinline__ uint32_t only_if(bool in, uint32_t off) {
+    const uint32_t least = in ? 0u : kNowhere;
+    return off > least ? off : least;
+}
+__device__ __forceinline__ float load_f32(const float* base, uint32_t off) {
+    return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(buffer_at((const char*)base), off, 0, 0));
+}
+__device__ __forceinline__ void store_f32(float* base, uint32_t off, float v) {
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), buffer_at((const char*)base), off, 0, 0);
+}
 // 64 lanes' 16 bytes each to 1 KB of LDS in lane order, without registers for the data
 __device__ __forceinline__ void to_lds(const char* base, uint32_t off, char* dst) {
     typedef __attribute__((address_space(3))) void* L;

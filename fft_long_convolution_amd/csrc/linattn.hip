@@ -31,7 +31,7 @@ __global__ void __launch_bounds__(256) linattn_join_kernel(LinJob a, int f32) {
     *(f32x4*)st = S;
     const uint32_t b = bh / (uint32_t)a.H;
     const int64_t len = row_len(a.lengths, b, a.N);
-    const float em1 = expm1f(log_gamma(a.log_decay, (int)(bh - b * (uint32_t)a.H)) * (float)a.seg_len);
+    const DecayPair gamma = decay_pair(log_gamma(a.log_decay, (int)(bh - b * (uint32_t)a.H)), (float)a.seg_len);
     // a row's segments are in a chain of their own, but their sums are not: eight loads in flight
     int last = a.nseg;
     while (last > 1 && (last - 1) * a.seg_len >= len) --last;
@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(256) linattn_join_kernel(LinJob a, int f32) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             if (s + j < last) {
-                S += S * em1 + v[j];
+                S = decayed(S, gamma, v[j]);
                 *(f32x4*)(st + (s + j) * size) = S;
             }
     }

@@ -35,8 +35,8 @@
 // operands, like the result itself.  What S adds up is not: gamma^.. V is split into three bf16 parts
 // (two where no state leaves the call: 2^-17) or two fp16 parts, so that the state keeps fp32's accuracy over any length.
 // fp16 operands that may pass its range (P, S, gamma^.. V) are scaled to it by a power of two, per query,
-// per 16 columns and per column.  gamma^c S is S + (gamma^c - 1) S, so that a decay near one does not lose by rounding
-// its power.
+// per 16 columns and per column.  The state's factor gamma^c carries its rounding from chunk to chunk (next_decay), so that
+// neither a decay near one nor a fast one loses by its power.
 #pragma once
 #include "linattn_tiles.h"
 #include "mixer_plan.h"
@@ -213,11 +213,11 @@ __global__ void __launch_bounds__(256, linattn_alone(KT, NW, IO == CT_F32) ? 1 :
     float wP[CT][4], wI[CT], wU[CJ][ES];
 #pragma unroll
     for (int t = 0; t < CT; ++t) {
-        wI[t] = r.s_q * expf(lg * (float)(16 * t + x + 1 - off));
+        wI[t] = r.s_q * decay_power(lg, (float)(16 * t + x + 1 - off));
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int e = 16 * t + x - 4 * g - i;
-            wP[t][i] = r.s_q * r.s_kv * expf(lg * (float)(e > 0 ? e : 0));
+            wP[t][i] = r.s_q * r.s_kv * decay_power(lg, (float)(e > 0 ? e : 0));
         }
     }
 
@@ -263,16 +263,17 @@ __global__ void __launch_bounds__(256, linattn_alone(KT, NW, IO == CT_F32) ? 1 :
     for (int n = 0; n < (FOURS ? 1 : NW); ++n)
         oo[n] = mine + 16 * n < r.DV ? (uint32_t)(r.reverse ? 15 - x : x) * (uint32_t)(r.o.n * osz) + (uint32_t)(mine * osz) : kNowhere;
 
-    float em1 = 0.f;
+    float g_hi = 0.f, g_lo = 0.f, g_owed = 0.f;
     const auto weigh = [&](int c) LCV_INLINE {
-        em1 = expm1f(lg * (float)c);
+        g_hi = decay_power(lg, (float)c);
+        g_lo = g_owed = 0.f;
 #pragma unroll
         for (int j = 0; j < CJ; ++j)
 #pragma unroll
             for (int s = 0; s < ES; ++s) {
                 const int tok = 16 * TK * j + 16 * (s >> 2) + 4 * g + (s & 3);
                 const int e = c - 1 - tok + off;     // past the row's end V is zero; the power is kept finite
-                wU[j][s] = r.s_kv * expf(lg * (float)(e > 0 ? e : 0));
+                wU[j][s] = r.s_kv * decay_power(lg, (float)(e > 0 ? e : 0));
             }
     };
 
@@ -437,11 +438,12 @@ __global__ void __launch_bounds__(256, linattn_alone(KT, NW, IO == CT_F32) ? 1 :
         for (int n = 0; n < NW; ++n) split(n);
 
         // ---- the state moves on
+        const float gc = next_decay(g_hi, g_lo, g_owed);
         static_for<0, KT>([&](auto ti) LCV_INLINE {
             constexpr int t = ti.value;
             f32x4 d[NW];
 #pragma unroll
-            for (int n = 0; n < NW; ++n) d[n] = IO == CT_F16 ? f32x4{0.f, 0.f, 0.f, 0.f} : S[t][n] + S[t][n] * em1;
+            for (int n = 0; n < NW; ++n) d[n] = IO == CT_F16 ? f32x4{0.f, 0.f, 0.f, 0.f} : S[t][n] * gc;
 #pragma unroll
             for (int j = 0; j < CJ; ++j) {
                 const Frag kt = M::load_kt(Lk + j * TK * 16 * RK * 16, lk, t, RK);
@@ -452,7 +454,7 @@ __global__ void __launch_bounds__(256, linattn_alone(KT, NW, IO == CT_F32) ? 1 :
             }
 #pragma unroll
             for (int n = 0; n < NW; ++n) {
-                if constexpr (IO == CT_F16) S[t][n] += S[t][n] * em1 + d[n] * back[n];
+                if constexpr (IO == CT_F16) S[t][n] = S[t][n] * gc + d[n] * back[n];
                 else S[t][n] = d[n];
             }
             if constexpr (FULL && STATE) {
@@ -469,6 +471,11 @@ __global__ void __launch_bounds__(256, linattn_alone(KT, NW, IO == CT_F32) ? 1 :
 
     // ---- the chunks.  A chunk's loads have to be in when it begins.
     if (left > 0) weigh(left < C ? (int)left : C);
+    if (left >= C) {      // a last, shorter chunk has a factor of its own
+        const DecayPair gc = decay_pair(lg, (float)C);
+        g_hi = uniform(gc.hi);
+        g_lo = uniform(gc.lo);
+    }
     // STAGES chunks a turn, each stage by its own name: then the compiler knows which loads a read waits for.
     // Operations are counted in their order.  With three stages a chunk's loads are older than the stores of the two
     // chunks before it and the next chunk's loads, which may all be outstanding; with two stages older than the last

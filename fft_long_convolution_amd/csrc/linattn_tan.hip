@@ -72,27 +72,29 @@ __global__ void __launch_bounds__(256, KT <= (IO == CT_BF16 ? 8 : 4) ? 2 : 1) li
                 for (int i = 0; i < 4; ++i) T[k][i] = load_f32(t, at(k, i));
     }
     // weights: (i - j) gamma^(i-j) of a pair, the token's place and gamma^place against the state that enters
-    float wD[CT][4], nI[CT], wI[CT], wU[CJ][ES], nU[CJ][ES], em1 = 0.f, cgc = 0.f;
+    float wD[CT][4], nI[CT], wI[CT], wU[CJ][ES], nU[CJ][ES], cgc = 0.f;
+    float g_hi = 0.f, g_lo = 0.f, g_owed = 0.f;
 #pragma unroll
     for (int t = 0; t < CT; ++t) {
         nI[t] = (float)(16 * t + x + 1);
-        wI[t] = expf(lg * nI[t]);
+        wI[t] = decay_power(lg, nI[t]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int e = 16 * t + x - 4 * g - i;
-            wD[t][i] = e > 0 ? (float)e * expf(lg * (float)e) : 0.f;
+            wD[t][i] = e > 0 ? (float)e * decay_power(lg, (float)e) : 0.f;
         }
     }
     const auto weigh = [&](int c) LCV_INLINE {
-        em1 = expm1f(lg * (float)c);
-        cgc = (float)c * expf(lg * (float)c);
+        g_hi = decay_power(lg, (float)c);
+        g_lo = g_owed = 0.f;
+        cgc = (float)c * decay_power(lg, (float)c);
 #pragma unroll
         for (int j = 0; j < CJ; ++j)
 #pragma unroll
             for (int s = 0; s < ES; ++s) {
                 const int e = c - 1 - (16 * TK * j + 16 * (s >> 2) + 4 * g + (s & 3));    // past the row's end V is zero
                 nU[j][s] = (float)(e > 0 ? e : 0);
-                wU[j][s] = expf(lg * nU[j][s]);
+                wU[j][s] = decay_power(lg, nU[j][s]);
             }
     };
 
@@ -150,6 +152,11 @@ __global__ void __launch_bounds__(256, KT <= (IO == CT_BF16 ? 8 : 4) ? 2 : 1) li
     Chunk f;
     load(f, beg);
     weigh(end - beg < C ? (int)(end - beg) : C);
+    if (end - beg >= C) {      // a last, shorter chunk has a factor of its own
+        const DecayPair gc = decay_pair(lg, (float)C);
+        g_hi = uniform(gc.hi);
+        g_lo = uniform(gc.lo);
+    }
     for (int64_t t0 = beg; t0 < end; t0 += C) {
         const int c = (int)(end - t0 < C ? end - t0 : C);
         if (c < C) weigh(c);
@@ -262,10 +269,11 @@ __global__ void __launch_bounds__(256, KT <= (IO == CT_BF16 ? 8 : 4) ? 2 : 1) li
                 }
             }
         }
+        const float gc = next_decay(g_hi, g_lo, g_owed);
 #pragma unroll
         for (int t = 0; t < KT; ++t) {
-            T[t] += T[t] * em1 + S[t] * cgc;
-            S[t] += S[t] * em1;
+            T[t] = T[t] * gc + S[t] * cgc;
+            S[t] = S[t] * gc;
 #pragma unroll
             for (int j = 0; j < CJ; ++j) {
                 const Frag kt = M::load_kt(Lk + j * TK * 16 * RK * 16, lk, t, RK);
@@ -312,11 +320,12 @@ __global__ void __launch_bounds__(256) linattn_tan_join_kernel(LinTanArgs a) {
     float* const st = a.states + bh * a.nseg * 2 * size + e;
     *(f32x4*)st = S;
     *(f32x4*)(st + size) = T;
-    const float l = log_gamma(a.log_decay, (int)(bh % a.H)) * (float)a.seg_len, em1 = expm1f(l), cgc = (float)a.seg_len * expf(l);
+    const float lg = log_gamma(a.log_decay, (int)(bh % a.H)), n = (float)a.seg_len, cgc = n * decay_power(lg, n);
+    const DecayPair gamma = decay_pair(lg, n);
     for (int s = 1; s < a.nseg && s * a.seg_len < len; ++s) {
         float* const p = st + s * 2 * size;
-        T += T * em1 + S * cgc + *(const f32x4*)(p + size);
-        S += S * em1 + *(const f32x4*)p;
+        T = decayed(T, gamma, S * cgc + *(const f32x4*)(p + size));
+        S = decayed(S, gamma, *(const f32x4*)p);
         *(f32x4*)p = S;
         *(f32x4*)(p + size) = T;
     }

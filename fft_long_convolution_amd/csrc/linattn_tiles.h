@@ -160,6 +160,16 @@ template <int vm> __device__ __forceinline__ void wait_for_all_but() {
     __builtin_amdgcn_s_waitcnt((vm & 15) | ((vm >> 4) << 14) | (7 << 4));
 }
 
+// The state's factor from chunk to chunk, in one multiplication: gamma^c rounded, with what each rounding left out
+// carried into the next chunk's, so that the product of any number of them is gamma^(c n) to one rounding.  (A pair of
+// floats costs a second operation for every element of the state; one rounded factor drifts.)
+__device__ __forceinline__ float uniform(float v) { return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(v))); }
+__device__ __forceinline__ float next_decay(float hi, float lo, float& owed) {
+    const float t = lo + owed, g = hi + t;
+    owed = t - (g - hi);
+    return g;
+}
+
 // 2^(14 - e) and its inverse for a magnitude of binade e: brings the magnitude below 2^15
 __device__ __forceinline__ float to_f16_range(float m, float* back) {
     int e = (int)((__float_as_uint(m) >> 23) & 255u) - 127;

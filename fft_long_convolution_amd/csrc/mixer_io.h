@@ -62,11 +62,31 @@ __device__ __forceinline__ int64_t row_len(const int32_t* lengths, int64_t b, in
     return n < 0 ? 0 : n < N ? n : N;
 }
 
-// log(gamma), kept finite so that gamma^0 is 1 also where gamma is 0 (a NaN stays one).
+// log(gamma), kept finite, also times any number of tokens, so that gamma^0 is 1 where gamma is 0 (a NaN stays one).
 __device__ __forceinline__ float log_gamma(const float* log_decay, int h) {
     const float l = log_decay[h];
-    return l < -1e30f ? -1e30f : l;
+    return l < -1e20f ? -1e20f : l;
 }
+
+// gamma^n, relative to its own size: what the product's rounding leaves out (88 half-units for the smallest powers) is
+// put back.
+__device__ __forceinline__ float decay_power(float lg, float n) {
+    const float x = lg * n, g = expf(x);
+    return fmaf(g, fmaf(lg, n, -x), g);
+}
+
+// gamma^n as the sum of two floats.  A state that is multiplied over and over takes the product of all its factors, so
+// that the rounding of one factor would add up over its memory (gamma^n = 1 - 1e-4: ten thousand times half a unit).
+// S hi + S lo rounds once.  (S + S expm1 would do near one, but not for fast decays: 1 + expm1(-16) is 6 % off.)
+struct DecayPair {
+    float hi, lo;
+};
+__device__ __forceinline__ DecayPair decay_pair(float lg, float n) {
+    const double g = exp((double)lg * (double)n);
+    const float hi = (float)g;
+    return DecayPair{hi, (float)(g - (double)hi)};
+}
+template <typename V> __device__ __forceinline__ V decayed(V S, DecayPair g, V add) { return S * g.hi + (S * g.lo + add); }
 
 }  // namespace
 }  // namespace lcv

@@ -49,7 +49,8 @@ __global__ void __launch_bounds__(256) linattn_join_kernel(LinJob a, int f32) {
     }
 }
 
-// One token: S = gamma S + k v^T in place, y = scale S^T q.  The state's 8 Dk Dv bytes are read and
+// One token: S = gamma S + k v^T in place, y = scale S^T q, gamma as two floats so that thousands of tokens drift no more than
+// a prompt's chunks.  The state's 8 Dk Dv bytes are read and
 // written once, all else is small: bound by HBM, or by latency for few rows.  A workgroup takes CB columns
 // of one (b, h): 16-byte loads along a row, up to 16 of them in flight per thread, q and k as floats
 // through LDS while the state is on its way, y's sum over the rows through LDS.  Measured, D = 128: 256 sequences of 16
@@ -85,7 +86,7 @@ __global__ void __launch_bounds__(256) linattn_step_kernel(LinStepArgs a) {
     f32x4 v = {0.f, 0.f, 0.f, 0.f}, y = {0.f, 0.f, 0.f, 0.f};
     if (on)
         for (int i = 0; i < 4; ++i) v[i] = load1<IO>(a.v.p, row_base(a.v, b, h) + n + i);
-    const float gamma = expf(log_gamma(a.log_decay, h));
+    const DecayPair gamma = decay_pair(log_gamma(a.log_decay, h), 1.f);
     __syncthreads();
     for (int base = 0; base < a.DK; base += BATCH * RPP) {
 #pragma unroll
@@ -93,7 +94,7 @@ __global__ void __launch_bounds__(256) linattn_step_kernel(LinStepArgs a) {
             const int d = base + d0 + i * RPP;
             if (!on || d >= a.DK) continue;
             if (base) s[i] = *(const f32x4*)(S + (int64_t)d * a.DV);
-            s[i] = s[i] * gamma + v * qk[1][d];
+            s[i] = decayed(s[i], gamma, v * qk[1][d]);
             y += s[i] * qk[0][d];
             *(f32x4*)(S + (int64_t)d * a.DV) = s[i];
         }

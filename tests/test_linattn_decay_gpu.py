@@ -73,3 +73,21 @@ def check(lc, d, N):
         off = np.abs(wide(g.dlog_decay) - terms.sum(1)) / np.sqrt((terms ** 2).sum(1))
         say(f"   dlog_decay {off.max():.2e}")
         assert off.max() <= TOL_F32
+
+
+def test_thousands_of_single_tokens_keep_slow_decays(lc):
+    """The token form's factor is used once a token: rounded to fp32 it would drift by half a unit each, over a memory of
+    ten thousand tokens far beyond fp32's accuracy."""
+    import torch
+    say("[linattn token drift]")
+    rng = np.random.default_rng(620)
+    H, N, Dk, Dv = 12, 3000, 32, 32
+    q, k, v = (host(rng, (1, H, N, D), "f32").cuda() for D in (Dk, Dk, Dv))
+    ld = torch.tensor(np.float32(-np.logspace(-5, -1.5, H)), device="cuda")
+    S = host(rng, (1, H, Dk, Dv), "f32", 50.0).cuda()          # the size that the sums grow to
+    _, ref = mixer.linattn(wide(q), wide(k), wide(v), wide(ld), 1.0, wide(S))
+    for t in range(N):
+        lc.linear_attention_step(q[:, :, t], k[:, :, t], v[:, :, t], ld, S, scale=1.0)
+    e = [rel_rows(S[:, h:h + 1], ref[:, h:h + 1]) for h in range(H)]
+    say("   " + " ".join(f"{x:.1e}" for x in e))
+    assert max(e) <= TOL_F32

@@ -437,6 +437,10 @@ __global__ void __launch_bounds__(256, linattn_alone(KT, NW, IO == CT_F32) ? 1 :
 #pragma unroll
         for (int n = 0; n < NW; ++n) split(n);
 
+        // The waits count on it that this chunk's loads, all issued by now, stay ahead of its stores, which follow: vector
+        // memory operations do not cross here, anything else may.  (The built loops are checked for it by a test: without
+        // this the compiler had put two stores ahead of four loads in the fp32 kernel of 192 x 128.)
+        if constexpr (FULL && !STATE) __builtin_amdgcn_sched_barrier(0x78f);
         // ---- the state moves on
         const float gc = next_decay(g_hi, g_lo, g_owed);
         static_for<0, KT>([&](auto ti) LCV_INLINE {

@@ -125,34 +125,10 @@ void set_plan(LinJob* a, const LinPlan& p) {
     a->kt = p.kt; a->nw = p.nw; a->ncb = p.ncb; a->nseg = p.nseg; a->seg_len = p.seg_len;
 }
 
-// The gradients' roles by launch: dq and dk contract over Dv and have Dk columns, dv the other way round.
-// Roles of the same tiles go together: all three, or dq and dk.
-struct BwdPlan {
-    int launches, first[2], roles[2];   // roles first .. first + roles - 1 of (dq, dk, dv)
-    LinPlan plan[2];
-    size_t states[2];                   // bytes of one role's segment states
-    size_t total;
-};
-BwdPlan bwd_plan(int64_t B, int64_t H, int64_t N, int64_t Dk, int64_t Dv, lconv_dtype_t dtype) {
-    BwdPlan p{};
-    const int64_t rows = B * H;
-    const bool alike = linattn_kt(Dk) == linattn_kt(Dv);
-    const int64_t wide = Dk > Dv ? Dk : Dv;
-    p.launches = alike ? 1 : 2;
-    for (int i = 0; i < p.launches; ++i) {
-        p.first[i] = 2 * i;
-        p.roles[i] = alike ? 3 : 2 - i;
-        p.plan[i] = linattn_plan(rows, p.roles[i], N, alike ? wide : i ? Dk : Dv, alike ? wide : i ? Dv : Dk, dtype);
-        p.states[i] = linattn_states_bytes(p.plan[i], rows);
-        p.total += (size_t)p.roles[i] * p.states[i];
-    }
-    return p;
-}
-
 // whether the gradients' launches fit a grid, the decay's (which is on or not) among them
 bool linattn_bwd_fits(int64_t B, int64_t H, int64_t N, int64_t Dk, int64_t Dv, lconv_dtype_t dtype) {
     if (B * H <= kRowsThatFit) return true;
-    const BwdPlan p = bwd_plan(B, H, N, Dk, Dv, dtype);
+    const LinBwdPlan p = linattn_bwd_plan(B * H, N, Dk, Dv, dtype);
     for (int i = 0; i < p.launches; ++i)
         if (linattn_workgroups(p.plan[i], B * H, p.roles[i]) > kMaxWorkgroups) return false;
     return linattn_tan_workgroups(B * H, N, Dv) <= kMaxWorkgroups;
@@ -234,7 +210,7 @@ size_t lconv_linattn_bwd_workspace_bytes(int64_t B, int64_t H, int64_t G, int64_
         !linattn_bwd_fits(B, H, N, Dk, Dv, dtype))
         return 0;
     return head_grads_bytes(B, H, G, N, Dk) + head_grads_bytes(B, H, G, N, Dv) + tan_bytes(B * H, N, Dk, Dv) +
-           bwd_plan(B, H, N, Dk, Dv, dtype).total;
+           linattn_bwd_plan(B * H, N, Dk, Dv, dtype).total;
 }
 
 lconv_status_t lconv_linattn_bwd(const void* dy, const lconv_strides_t* dy_strides, const void* q,
@@ -289,7 +265,7 @@ lconv_status_t lconv_linattn_bwd(const void* dy, const lconv_strides_t* dy_strid
     float* gv = share > 1 ? (float*)ws : nullptr;
     ws += head_grads_bytes(B, H, G, N, Dv);
 
-    const BwdPlan plan = bwd_plan(B, H, N, Dk, Dv, dtype);
+    const LinBwdPlan plan = linattn_bwd_plan(B * H, N, Dk, Dv, dtype);
     float* const tan = (float*)ws;
     float* const tan_states = (float*)(ws + tan_part_bytes(B * H, N, Dv));
     ws += tan_bytes(B * H, N, Dk, Dv);

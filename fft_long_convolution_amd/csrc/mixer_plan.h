@@ -72,6 +72,29 @@ inline size_t linattn_states_bytes(const LinPlan& p, int64_t rows) {
     return p.nseg > 1 ? (size_t)rows * (size_t)p.nseg * (size_t)(p.kt * 16 * p.ncb * 64 * p.nw) * 4 : 0;
 }
 
+// The gradients' roles by launch: dq and dk contract over Dv and have Dk columns, dv the other way round.
+// Roles of the same tiles go together: all three, or dq and dk.
+struct LinBwdPlan {
+    int launches, first[2], roles[2];   // roles first .. first + roles - 1 of (dq, dk, dv)
+    LinPlan plan[2];
+    size_t states[2];                   // bytes of one role's segment states
+    size_t total;
+};
+inline LinBwdPlan linattn_bwd_plan(int64_t rows, int64_t N, int64_t Dk, int64_t Dv, lconv_dtype_t dtype) {
+    LinBwdPlan p{};
+    const bool alike = linattn_kt(Dk) == linattn_kt(Dv);
+    const int64_t wide = Dk > Dv ? Dk : Dv;
+    p.launches = alike ? 1 : 2;
+    for (int i = 0; i < p.launches; ++i) {
+        p.first[i] = 2 * i;
+        p.roles[i] = alike ? 3 : 2 - i;
+        p.plan[i] = linattn_plan(rows, p.roles[i], N, alike ? wide : i ? Dk : Dv, alike ? wide : i ? Dv : Dk, dtype);
+        p.states[i] = linattn_states_bytes(p.plan[i], rows);
+        p.total += (size_t)p.roles[i] * p.states[i];
+    }
+    return p;
+}
+
 // Threads along a launch's grid have to stay below 2^32: so many workgroups of 256.
 constexpr int64_t kMaxWorkgroups = ((int64_t)1 << 24) - 1;
 

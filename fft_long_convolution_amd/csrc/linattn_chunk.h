@@ -248,6 +248,10 @@ __global__ void __launch_bounds__(256, linattn_alone(KT, NW, IO == CT_F32) ? 1 :
                         for (int i = 0; i < 4; ++i) v[i] = s[(int64_t)(d + i) * srow + c];
                     }
                 }
+                if constexpr (IO == CT_F16) {      // an infinity would scale its 15 neighbours' columns to nothing; a NaN does not
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[i] = fabsf(v[i]) == __builtin_inff() ? __uint_as_float(0x7fc00000u) : v[i];
+                }
                 S[t][n] = v;
             }
     }
@@ -320,7 +324,9 @@ __global__ void __launch_bounds__(256, linattn_alone(KT, NW, IO == CT_F32) ? 1 :
         // gamma^.. V in parts that add up to its fp32 value
         constexpr int PARTS = IO == CT_F32 ? 1 : IO == CT_F16 || !EXACT ? 2 : 3;
         Frag u[PARTS][CJ][NW];
-        float back[NW];
+        float back[NW], none[NW];      // none: 0, or the NaN of a column whose V is not finite
+#pragma unroll
+        for (int n = 0; n < NW; ++n) none[n] = 0.f;
         const auto split = [&](int n) LCV_INLINE {
             float v[CJ][ES], m = 0.f;
 #pragma unroll
@@ -328,7 +334,7 @@ __global__ void __launch_bounds__(256, linattn_alone(KT, NW, IO == CT_F32) ? 1 :
                 M::unpack(vf[j][n], v[j]);
 #pragma unroll
                 for (int s = 0; s < ES; ++s) {
-                    v[j][s] *= wU[j][s];
+                    v[j][s] = fmaf(v[j][s], wU[j][s], none[n]);
                     if constexpr (IO == CT_F16) m = fmaxf(m, fabsf(v[j][s]));
                 }
             }
@@ -399,6 +405,53 @@ __global__ void __launch_bounds__(256, linattn_alone(KT, NW, IO == CT_F32) ? 1 :
                     for (int n = 0; n < NW; ++n) acc[it][n] = M::mma(sf[n], qf[it], acc[it][n]);
                 }
             });
+            // A V that is not finite must not reach the queries before it, whose 0 in P times V is a NaN: it leaves the product, and
+            // the later queries' column and the state's become NaN here.  In all other chunks it costs four vector
+            // instructions for 16 bytes of V and a branch: prompt of 32 rows of 4096 66 -> 68 us, gradients of 128 rows of 2048 153 -> 155.
+            float sum[NW];
+#pragma unroll
+            for (int n = 0; n < NW; ++n) {
+                sum[n] = 0.f;
+#pragma unroll
+                for (int j = 0; j < CJ; ++j) sum[n] = M::nan_of(vf[j][n], sum[n]);
+            }
+            if (__builtin_expect(__builtin_amdgcn_ballot_w64(__builtin_isunordered(sum[0], sum[NW - 1])) != 0, 0)) {
+                const float nan = __uint_as_float(0x7fc00000u);
+                int ahead = 4 * g - x;               // of the lane's first token in a tile to its query
+                asm volatile("" : "+v"(ahead));      // nothing of this is to be kept in registers through the other chunks
+#pragma unroll
+                for (int n = 0; n < NW; ++n) {
+                    Frag bad[CJ];
+                    float any = 0.f;
+#pragma unroll
+                    for (int j = 0; j < CJ; ++j) {
+                        float v[ES], one[ES];
+                        M::unpack(vf[j][n], v);
+#pragma unroll
+                        for (int e = 0; e < ES; ++e) {
+                            one[e] = fabsf(v[e]) < __builtin_inff() ? 0.f : 1.f;
+                            v[e] = one[e] != 0.f ? 0.f : v[e];
+                            any = fmaxf(any, one[e]);
+                        }
+                        vf[j][n] = M::pack(v);
+                        bad[j] = M::pack(one);
+                    }
+                    none[n] = max_over_g(any) != 0.f ? nan : 0.f;
+                    // how many such tokens a query has behind it
+#pragma unroll
+                    for (int it = 0; it < CT; ++it) {
+                        f32x4 behind = {0.f, 0.f, 0.f, 0.f}, w[CT];
+#pragma unroll
+                        for (int jt = 0; jt < CT; ++jt)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) w[jt][i] = jt < it || (jt == it && ahead + i <= 0) ? 1.f : 0.f;
+#pragma unroll
+                        for (int j = 0; j < CJ; ++j) behind = M::mma(bad[j], M::pack(w + TK * j), behind);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[it][n][i] = behind[i] != 0.f ? nan : acc[it][n][i];
+                    }
+                }
+            }
 #pragma unroll
             for (int it = 0; it < CT; ++it) {
 #pragma unroll

@@ -24,6 +24,8 @@ constexpr int lin_row_groups(int groups) {
     return r;
 }
 
+typedef short s16x2 __attribute__((__vector_size__(4)));
+
 template <int IO> struct Mx {  // bf16, fp16
     using E = uint16_t;
     static constexpr int C = 32;        // tokens of a chunk
@@ -83,6 +85,15 @@ template <int IO> struct Mx {  // bf16, fp16
     static __device__ __forceinline__ Frag pack(const float* v) {
         return Frag{{pack2<IO>(v[0], v[1]), pack2<IO>(v[2], v[3]), pack2<IO>(v[4], v[5]), pack2<IO>(v[6], v[7])}};
     }
+    // m, or a NaN if one of the elements is not finite
+    static __device__ __forceinline__ float nan_of(const Frag& f, float m) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (IO == CT_BF16) m = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(s16x2, f.w[i]), s16x2{0, 0}, m, false);
+            else m = __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, f.w[i]), f16x2{0, 0}, m, false);
+        }
+        return m;
+    }
 };
 
 template <> struct Mx<CT_F32> {
@@ -121,6 +132,11 @@ template <> struct Mx<CT_F32> {
         for (int i = 0; i < 4; ++i) v[i] = f.v[i];
     }
     static __device__ __forceinline__ Frag pack(const float* v) { return Frag{{v[0], v[1], v[2], v[3]}}; }
+    static __device__ __forceinline__ float nan_of(const Frag& f, float m) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m = fmaf(f.v[i], 0.f, m);
+        return m;
+    }
 };
 
 // Global memory from a scalar address on, by 32-bit offsets of the lanes: raw buffer accesses, whose address

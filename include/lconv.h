@@ -496,8 +496,9 @@ typedef struct {
  *   workspace  lconv_linattn_workspace_bytes(...) bytes (may be NULL if that is 0)
  * States and all sums are fp32; with 16-bit data the scores and the state are rounded once to the
  * dtype as matrix-core operands, while what the state adds up is kept to fp32's accuracy.
- * Tokens are taken 32 at a time: a value that is not finite in k or v reaches the outputs from its token on,
- * one in v those of the up to 31 tokens before it as well; one in q its own row's.
+ * A value that is not finite reaches what the recurrence lets it reach, as a value that is not finite (not always the same
+ * one): in k every column of its own and later tokens, in v its own column of them, in q its own token, in the state that
+ * enters its own column.  The gradients likewise, in their direction.
  * Supported: Dk, Dv multiples of 8 in [8, 256]; H a multiple of G; N < 2^31; tokens at most 2^27 bytes apart
  * (strides' n, N > 1); launches of fewer than 2^32 threads (B H up to 2^20 always, single tokens 2^22); every dtype.
  * B, H or N = 0 is a no-op apart from state_out, which is set as for rows of length 0 (N = 0).

@@ -28,38 +28,73 @@ def parse(text):
     return out
 
 
-def loops(code):
-    """Bodies of the innermost loops with at least two barriers and loads to LDS."""
+def graph(code):
+    """(successors, predecessors) of the instructions by place."""
     place = {c[0]: i for i, c in enumerate(code)}
-    found = []
-    for i, (pc, op, _, target) in enumerate(code):
-        if target is not None and target <= pc and target in place:
-            body = code[place[target]:i + 1]
-            if sum(c[1] == "s_barrier" for c in body) >= 2 and any(c[1].startswith("buffer_load") and "lds" in c[2] for c in body):
-                found.append((place[target], i, body))
-    return [b for s, e, b in found if not any(s <= s2 and e2 <= e and (s, e) != (s2, e2) for s2, e2, _ in found)]
+    succ = [[] for _ in code]
+    for i, (_, op, _, target) in enumerate(code):
+        if op not in ("s_branch", "s_endpgm") and i + 1 < len(code):
+            succ[i].append(i + 1)
+        if target in place:
+            succ[i].append(place[target])
+    pred = [[] for _ in code]
+    for i, t in enumerate(succ):
+        for j in t:
+            pred[j].append(i)
+    return succ, pred
 
 
-def loads_not_waited_for(body):
+def reach(start, edges):
+    seen, todo = {start}, [start]
+    while todo:
+        for j in edges[todo.pop()]:
+            if j not in seen:
+                seen.add(j)
+                todo.append(j)
+    return seen
+
+
+def loops(code):
+    """The loops with at least two barriers and loads to LDS, as (code, places): every instruction from which a barrier is
+    reached that reaches it again (blocks that the compiler moved out of line among them)."""
+    succ, pred = graph(code)
+    found, seen = [], set()
+    for i, c in enumerate(code):
+        if c[1] == "s_barrier" and i not in seen:
+            body = reach(i, succ) & reach(i, pred)
+            seen |= body
+            barriers = sum(code[j][1] == "s_barrier" for j in body)
+            if barriers >= 2 and any(code[j][1].startswith("buffer_load") and "lds" in code[j][2] for j in body):
+                found.append((code, body))
+    return found
+
+
+def loads_not_waited_for(loop):
     """Loads to LDS that may still be on their way when their stage is read: the loop has a barrier for each stage, and the
     last of those that follow a load opens the turn that reads it.  On the way there, by the path with the fewest vector
     memory operations, there has to be a wait that allows no more of them than have been issued since."""
-    at = {c[0]: i for i, c in enumerate(body)}
-    stages = sum(c[1] == "s_barrier" for c in body)
+    code, places = loop
+    succ, _ = graph(code)
+    at = {c[0]: i for i, c in enumerate(code)}
+    stages = sum(code[i][1] == "s_barrier" for i in places)
 
     def follow(i, left_out):
         """(next place, whether a store has just been left out).  A store of fp32 and one of the dtype stand as the two arms of
         a branch, each behind a jump of its own: of two stores in a row not both are left out."""
-        pc, op, _, target = body[i]
-        nxt = [] if op == "s_branch" else [((i + 1) % len(body), left_out and not op.startswith("buffer_store"))]
-        if target in at:
-            over = target > pc and any(c[1].startswith("buffer_store") for c in body[i:at[target]])
+        pc, op, _, target = code[i]
+        nxt = []
+        for j in succ[i]:
+            if j not in places:
+                continue
+            over = target in at and j == at[target] and target > pc and any(
+                k in places and code[k][1].startswith("buffer_store") for k in range(i, j))
             if not (over and left_out):
-                nxt.append((at[target], left_out or over))
+                nxt.append((j, over or (left_out and not op.startswith("buffer_store"))))
         return nxt
 
     bad = []
-    for start, (pc, op, args, _) in enumerate(body):
+    for start in sorted(places):
+        pc, op, args, _ = code[start]
         if not (op.startswith("buffer_load") and "lds" in args):
             continue
         fewest, todo = {}, [(j, s, 0, 0) for j, s in follow(start, False)]   # place, .., barriers passed, operations since
@@ -68,7 +103,7 @@ def loads_not_waited_for(body):
             if fewest.get((i, left_out, barriers), behind + 1) <= behind:
                 continue
             fewest[i, left_out, barriers] = behind
-            _, op, args, _ = body[i]
+            _, op, args, _ = code[i]
             if op == "s_waitcnt" and "vmcnt" in args and int(re.search(r"vmcnt\((\d+)\)", args).group(1)) <= behind:
                 continue                                        # done by here
             if op == "s_barrier":

@@ -1045,8 +1045,8 @@ def _dense_like(x):
 
 
 def _rows(name, t, shape, dtype):
-    """(rows, C, row stride) of a tensor normalised over its last dimension: dense, or 2-D with a row
-    stride."""
+    """(rows, C, row stride) of a tensor normalised over its last dimension: dense, or with contiguous rows that are evenly
+    spaced (a slice of the last dimension, one token of every sequence)."""
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor, got {type(t).__name__}")
@@ -1060,14 +1060,24 @@ def _rows(name, t, shape, dtype):
         rows *= n
     if t.is_contiguous():
         return rows, C, C
-    if t.dim() != 2 or t.stride(1) != 1 or t.stride(0) < C:
-        raise ValueError(f"{name} must be contiguous, or 2-D with contiguous rows")
-    return rows, C, t.stride(0)
+    step = whole = None                      # the spacing of rows, and what the dimensions so far span
+    for n, st in zip(reversed(shape[:-1]), reversed(t.stride()[:-1])):
+        if n == 1:
+            continue
+        if step is None:
+            step = st
+        elif st != whole:
+            step = -1
+            break
+        whole = st * n
+    if (t.stride(-1) != 1 and C > 1) or (step is not None and step < C):
+        raise ValueError(f"{name} must be contiguous, or have contiguous rows that are evenly spaced and do not overlap")
+    return rows, C, C if step is None else step
 
 
 def layer_norm(x, weight=None, bias=None, eps=1e-5, need_stats=True, out=None, stream=None):
-    """Layer norm over the last dimension of x [..., C]: (x - mean) rstd weight + bias; weight and bias
-    [C] in x's dtype, or None.  Returns (y, mean, rstd), the statistics in float32 and x's leading shape
+    """Layer norm over the last dimension of x [..., C], dense or with evenly spaced rows: (x - mean) rstd weight + bias;
+    weight and bias [C] in x's dtype, or None.  Returns (y, mean, rstd), the statistics in float32 and x's leading shape
     (None without need_stats).  out may be x."""
     torch = _torch()
     if not isinstance(x, torch.Tensor) or x.dim() < 1:

@@ -13,6 +13,13 @@ import torch
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 from fft_long_convolution_amd import lconv  # noqa: E402
 
+once = torch.autograd.function.once_differentiable     # the gradients have no gradient of their own: asking for one is an error
+
+
+def rows(t):
+    """A gradient as the calls take it: strided, but with contiguous rows (a sum's gradient is one element, repeated)."""
+    return t if t.stride(-1) == 1 or t.shape[-1] == 1 else t.contiguous()
+
 
 class LayerNorm(torch.autograd.Function):
     @staticmethod
@@ -22,6 +29,7 @@ class LayerNorm(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once
     def backward(ctx, dy):
         x, weight, mean, rstd = ctx.saved_tensors
         dx, dw, db = lconv.layer_norm_bwd(dy.contiguous(), x, weight, mean, rstd)
@@ -37,27 +45,30 @@ class Rotary(torch.autograd.Function):
         return lconv.rotary(q, k, positions, inv_freq)
 
     @staticmethod
+    @once
     def backward(ctx, dq, dk):
-        dq, dk = lconv.rotary(dq, dk, *ctx.saved_tensors, inverse=True)
+        dq, dk = lconv.rotary(rows(dq), rows(dk), *ctx.saved_tensors, inverse=True)
         return dq, dk, None, None
 
 
 class LinearAttention(torch.autograd.Function):
-    """The state after the last token is returned for serving and takes no part in the gradient."""
+    """y and the state after the last token, from a state or none; either result may be used, and each state has its gradient."""
 
     @staticmethod
-    def forward(ctx, q, k, v, log_decay, lengths):
-        y, state = lconv.linear_attention(q, k, v, log_decay, lengths=lengths)
-        ctx.save_for_backward(q, k, v, log_decay)
-        ctx.lengths = lengths
-        ctx.mark_non_differentiable(state)
-        return y, state
+    def forward(ctx, q, k, v, log_decay, lengths, state):
+        y, last = lconv.linear_attention(q, k, v, log_decay, state=state, lengths=lengths)
+        ctx.save_for_backward(q, k, v, log_decay, lengths, state)
+        ctx.set_materialize_grads(False)
+        return y, last
 
     @staticmethod
-    def backward(ctx, dy, _):
-        q, k, v, log_decay = ctx.saved_tensors
-        g = lconv.linear_attention_bwd(dy, q, k, v, log_decay, lengths=ctx.lengths, need_dlog_decay=True)
-        return g.dq, g.dk, g.dv, g.dlog_decay, None
+    @once
+    def backward(ctx, dy, dlast):
+        q, k, v, log_decay, lengths, state = ctx.saved_tensors
+        dy = torch.zeros(q.shape[:-1] + v.shape[-1:], dtype=q.dtype, device=q.device) if dy is None else rows(dy)
+        g = lconv.linear_attention_bwd(dy, q, k, v, log_decay, state=state, dstate=None if dlast is None else dlast.contiguous(),
+                                       lengths=lengths, need_dlog_decay=ctx.needs_input_grad[3])
+        return g.dq, g.dk, g.dv, g.dlog_decay, None, g.dstate
 
 
 class LongConv(torch.autograd.Function):
@@ -70,6 +81,7 @@ class LongConv(torch.autograd.Function):
         return lconv.fftconv(u, k_f, D, q=q, v=v)
 
     @staticmethod
+    @once
     def backward(ctx, dy):
         u, k_f, D, q, v = ctx.saved_tensors
         du, dq, dv, dk, dD = lconv.fftconv_bwd(dy.contiguous(), u, k_f, D, q=q, v=v)
@@ -98,10 +110,10 @@ class AttentionBlock(torch.nn.Module):
         h = (LayerNorm.apply(x, self.norm_w, self.norm_b) @ self.inp.t()).view(B, N, self.heads + 2 * self.shared, self.D)
         return (t.transpose(1, 2) for t in h.split((self.heads, self.shared, self.shared), dim=2))
 
-    def forward(self, x, positions, lengths=None):
+    def forward(self, x, positions, lengths=None, state=None):
         q, k, v = self.project(x)
         q, k = Rotary.apply(q, k, positions, self.inv_freq)
-        y, state = LinearAttention.apply(q, k, v, self.log_decay(), lengths)
+        y, state = LinearAttention.apply(q, k, v, self.log_decay(), lengths, state)
         return x + y.transpose(1, 2).reshape(x.shape) @ self.out.t(), state
 
     def step(self, x, positions, state, slots=None):

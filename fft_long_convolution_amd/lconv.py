@@ -966,9 +966,10 @@ def rotary_frequencies(rot, base=10000.0, scaling=None, factor=1.0, original=409
       "linear"    every frequency divided by factor (positions interpolated);
       "base"      the base raised to base * factor^(rot / (rot - 2)): the fastest pair keeps its
                   frequency, the slowest is divided by factor;
-      "by_parts"  pairs that turn more than `fast` times within `original` positions keep their
-                  frequency, those that turn less than `slow` times are divided by factor, a ramp in
-                  the pair's index between; magnitude 1 + 0.1 ln(factor)."""
+      "by_parts"  the interpolation by parts of YaRN (Peng, Quesnelle, Fan, Shippole 2023): pairs that turn
+                  at least `fast` times within `original` positions keep their frequency, those that turn at
+                  most `slow` times are divided by factor, a ramp in the pair's index between (from the last
+                  whole index of the one kind to the first of the other); magnitude 1 + 0.1 ln(factor)."""
     torch = _torch()
     if rot < 2 or rot % 2:
         raise ValueError(f"rot must be even and at least 2, got {rot}")
@@ -976,6 +977,8 @@ def rotary_frequencies(rot, base=10000.0, scaling=None, factor=1.0, original=409
         raise ValueError(f"unknown scaling {scaling!r}")
     if factor < 1.0:
         raise ValueError(f"factor must be at least 1, got {factor}")
+    if scaling == "by_parts" and not (base > 1.0 and original > 0 and fast > slow > 0):
+        raise ValueError(f"by_parts needs base > 1, original > 0 and fast > slow > 0, got {base}, {original}, {fast}, {slow}")
     magnitude = 1.0
     if scaling == "base" and rot > 2:
         base = base * factor ** (rot / (rot - 2))
@@ -984,10 +987,11 @@ def rotary_frequencies(rot, base=10000.0, scaling=None, factor=1.0, original=409
     if scaling == "linear":
         f = f / factor
     elif scaling == "by_parts":
-        # the pair whose wavelength fits `turns` times into the original context
+        # the index, whole or not, whose wavelength 2 pi base^(2p / rot) fits `turns` times into the original context; it falls
+        # with the turns, so the ramp's ends are at least one apart.  They may lie outside the pairs that there are.
         pair = lambda turns: rot * math.log(original / (turns * 2.0 * math.pi)) / (2.0 * math.log(base))  # noqa: E731
-        lo, hi = max(math.floor(pair(fast)), 0), min(math.ceil(pair(slow)), rot - 1)
-        ramp = ((p - lo) / max(hi - lo, 1e-3)).clamp(0.0, 1.0)
+        lo, hi = math.floor(pair(fast)), math.ceil(pair(slow))
+        ramp = ((p - lo) / (hi - lo)).clamp(0.0, 1.0)
         f = f * (1.0 - ramp) + f / factor * ramp
         magnitude = 1.0 + 0.1 * math.log(factor)
     return f.to(torch.float32).to(device), magnitude

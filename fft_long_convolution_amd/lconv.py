@@ -113,7 +113,10 @@ def load(path: str = LIB_PATH):
         "lconv_release": (i, []),
     }
     for name, (res, args) in sig.items():
-        f = getattr(lib, name)
+        f = getattr(lib, name, None)
+        if f is None:      # the version does not count entry points that were only added
+            raise RuntimeError(f"{path} has no {name}: it was built from older sources, build it again "
+                               "(python -m fft_long_convolution_amd.build)")
         f.restype = res
         f.argtypes = args
     _lib = lib

@@ -47,13 +47,13 @@
 extern "C" {
 #endif
 
-/* Bumped when entry points are added or a size query's result changes (3: the training pair
+/* Bumped when an entry point or a size query's result changes; entry points that are only added need not bump it, and a
+ * caller that may meet an older library looks for them by their names (3: the training pair
  * lconv_fftconv_fwd_save / lconv_fftconv_bwd_saved; the state-space workspace holds the scan's
  * part states.  4: lconv_prepare and lconv_fftconv_fwd_noalloc, two status codes.  5: 2D calls
  * take Hs x Ws images and a workspace; lconv_fftconv2d_workspace_bytes.  6: gradients and the
- * training pair for every supported N, with workspace arguments.  The mixer operators further
- * down -- linear attention, rotary positions, layer norm -- came beside version 8: they change
- * nothing that was there, and a caller finds them by their names). */
+ * training pair for every supported N, with workspace arguments.  Added within version 8: the mixer
+ * operators further down -- linear attention, rotary positions, layer norm). */
 #define LCONV_ABI_VERSION 8
 
 /* The last enumerator only widens the type's range to every int, so that any value a C caller

@@ -762,6 +762,8 @@ def _at(dev, stream):
     belong to the stream that the call runs on, so they are not handed out again before it is done."""
     torch = _torch()
     if stream is not None:
+        if stream.device.index != dev:
+            raise ValueError(f"the stream is on {stream.device}, the operands on cuda:{dev}")
         return torch.cuda.stream(stream), stream.cuda_stream     # also makes its device the current one
     raw = _raw_stream()(dev)
     return (_HERE if dev == torch.cuda.current_device() else torch.cuda.device(dev)), raw

@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(256) linattn_join_kernel(LinJob a, int f32) {
 // written once, all else is small: bound by HBM, or by latency for few rows.  A workgroup takes CB columns
 // of one (b, h): 16-byte loads along a row, up to 16 of them in flight per thread, q and k as floats
 // through LDS while the state is on its way, y's sum over the rows through LDS.  Measured, D = 128: 256 sequences of 16
-// heads (537 MB) 112 us, 4.8 TB/s (one load at a time 179 us); one sequence of 16 heads 5.3 us.
+// heads (537 MB) 108 us, 5.0 TB/s (one load at a time 179 us); one sequence of 16 heads 5.3 us.
 template <int IO, int CB>
 __global__ void __launch_bounds__(256) linattn_step_kernel(LinStepArgs a) {
     constexpr int LPR = CB / 4, RPP = 256 / LPR, BATCH = 16;   // lanes to a row, rows to a pass

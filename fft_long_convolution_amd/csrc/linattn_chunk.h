@@ -18,17 +18,17 @@
 //   O^T += S^T Q^T    S's accumulators (rows d = 4g + r, column n = x) are the left operand as they are
 //   S   += K^T V      both operands stand transposed to their rows in LDS: ds_read_b64_tr_b16 for 16-bit
 //                 types, four strided reads for fp32
-// Every wave forms all of P (12 of its 64 matrix products for a bf16 chunk at D = 128 and NW = 2) rather than share it
-// through LDS and a barrier.
+// Every wave forms all of P (12 of its 64 matrix products for a bf16 chunk at D = 128 and NW = 2; for fp32 96 of 236 at
+// NW = 1 and 96 of 376 at NW = 2) rather than share it through LDS and a barrier.
 //
-// What bounds it (bf16, D = 128).  Enough rows (gradients, 256 rows of 2048 tokens, 282 us): HBM, 4.8 TB/s of what is
-// read after the XCD's L2 has served the roles that walk together (7 tensors of the 9 asked for, by counters) and
-// written.  65536 tokens of 16 rows (361 us): HBM, the state pass 520 MB in 126 us and the main pass 1.1 GB in 208 us
-// (5.3 TB/s).  A prompt of 32 rows of 4096 (64 us): 24 us of state pass, 7 of scan, 33 of main pass, which moves
-// 152 MB in it; what is left to HBM's rate is the start and the end of workgroups that all begin at once.  One
-// workgroup to a compute unit: a chunk's chain, 1.22 us at NW = 2 and 0.91 at NW = 1; a wave's 254 vector
-// instructions and 64 matrix products of a chunk take 2040 cycles back to back, 2270 are measured with loads, stores
-// and barriers left out.  Eight waves that share one 128-column tile take the same 1.22 us a chunk, since the SIMD's
+// What bounds it (bf16, D = 128; times of calls back to back, times of single passes from a trace, which runs them one at a
+// time).  Enough rows (gradients, 256 rows of 2048 tokens, 285 us): HBM, 4.7 TB/s of what is read after the XCD's L2 has
+// served the roles that walk together (7 tensors of the 9 asked for, by counters) and written.  65536 tokens of 16 rows
+// (356 us): HBM; on average of 20 traced calls the state pass takes 143 us for 553 MB and the main pass 253 for 1.1 GB, at
+// least 116 and 212 (5.2 TB/s).  A prompt of 32 rows of 4096 (66 us): 24 us of state pass, 8 of scan, 40 of main pass, which
+// moves 154 MB in it; what is left to HBM's rate is the start and the end of workgroups that all begin at once.  One
+// workgroup to a compute unit: a chunk's chain, about 1.25 us at NW = 2 and 0.9 at NW = 1, of some 275 vector instructions
+// and 64 matrix products of a wave.  Eight waves that share one 128-column tile took the same time a chunk, since the SIMD's
 // instructions add up, and 64 tokens to a chunk spilled registers.
 //
 // Precision.  S, P and every sum are fp32.  For 16-bit types P and S are rounded to the type once as
@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(256, linattn_alone(KT, NW, IO == CT_F32) ? 1 :
         const int per = 16 / osz;
         const int groups = ((r.DV - cb * DVB < DVB ? r.DV - cb * DVB : DVB)) / per;
         int64_t t0 = beg > len ? beg : len, t1 = beg + a.seg_len < a.N ? beg + a.seg_len : a.N;
-        if (r.O && t1 > t0)
+        if (t1 > t0)
             for (int64_t i = tid; i < (t1 - t0) * groups; i += 256) {
                 const int64_t t = t0 + i / groups;
                 const int c = cb * DVB + (int)(i % groups) * per;

@@ -24,7 +24,7 @@ struct LinOperand {
 // precedes).  Q, K are DK wide, V and O DV wide, S is DK x DV.
 struct LinRole {
     LinOperand Q, K, V;
-    void* O;                  // NULL: only the state is wanted
+    void* O;
     lconv_strides_t o;
     int DK, DV;
     const float* s_in;        // [B][H] states, element (d, n) at d * s_row + n * s_col; NULL: zeros

@@ -102,8 +102,8 @@ constexpr int64_t kMaxWorkgroups = ((int64_t)1 << 24) - 1;
 inline int64_t linattn_workgroups(const LinPlan& p, int64_t rows, int nroles) { return (rows * p.nseg + 7) / 8 * 8 * nroles * p.ncb; }
 
 // The decay's gradient: column blocks, and segments of at least four chunks until two workgroups to a compute unit.
-// Measured (bf16, us beside the other gradients): 32 rows of 4096 tokens, D = 128, one segment 286, 4: 110, 8: 86, 16: 104;
-// 16 rows of 65536: 8: 892, 16: 663, 32: 677; 8 rows of 1000, D = 64, 1: 55, 4: 30, 8: 25, 16: 26; 128 rows of 2048: 1: 156, 4: 175.
+// Measured (bf16, us beside the other gradients): 32 rows of 4096 tokens, D = 128, one segment 240, 4: 97, 8: 81, 16: 104;
+// 16 rows of 65536: 8: 722, 16: 599, 32: 615; 8 rows of 1000, D = 64, 1: 32, 4: 17, 8: 15, 16: 12; 128 rows of 2048: 1: 110, 4: 152.
 #ifdef __HIPCC__
 __host__ __device__
 #endif

@@ -6,8 +6,8 @@
 // bytes, at any element's alignment (half layouts whose halves do not start on a 16-byte group).  Measured, 16384
 // tokens of 32 heads of 128, bf16 (268 MB): one head to a thread 70 us, two 54, four 52 (5.1 TB/s, what a copy
 // reaches), eight 52; with two or four heads' loads at a time 49 to 59 by layout.
-// The angle is formed and reduced to a quarter turn in fp64: position * inv_freq is exact there for any int32
-// position, while fp32 would be off by a fifth of a radian at a position of a million.  The sines of what is left,
+// The angle is formed and reduced to a quarter turn in fp64: position * inv_freq is off by at most 2^-53 of itself there,
+// 2.4e-7 of a radian at the largest int32 position, while fp32 would be off by a thirtieth of one at a position of a million.  The sines of what is left,
 // at most pi / 4, are Taylor polynomials in fp32 (next terms: x^11 / 11! < 2e-9, x^12 / 12! < 2e-10).
 #include "mixer_kernels.h"
 #include "mixer_io.h"

@@ -520,7 +520,8 @@ lconv_status_t lconv_linattn_fwd(const void* q, const lconv_strides_t* q_strides
  *   dlog_decay[h] = sum_{b,t} <G_t, gamma S_{t-1}>;  dk and dv summed over the heads that share them.
  *   dq [B][H][N][Dk], dk [B][G][N][Dk], dv [B][G][N][Dv] dtype, written (zeros past a row's length)
  *   dstate_in  [B][H][Dk][Dv] fp32, written, or NULL;  dlog_decay [H] fp32, written, or NULL
- *   workspace  lconv_linattn_bwd_workspace_bytes(...) bytes (may be NULL if that is 0)
+ *   workspace  lconv_linattn_bwd_workspace_bytes(...) bytes (may be NULL if that is 0); the decay's gradient's part of it is
+ *              asked for whether dlog_decay is wanted or not
  * Limits and the other arguments as for lconv_linattn_fwd.  No atomics: results repeat bit for bit.
  */
 size_t lconv_linattn_bwd_workspace_bytes(int64_t B, int64_t H, int64_t G, int64_t N, int64_t Dk, int64_t Dv,

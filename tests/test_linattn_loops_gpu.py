@@ -1,5 +1,4 @@
-"""Linear attention over enough rows and tokens for every pipelined chunk loop: each (type, contraction tiles, column tiles,
-whole rows or segments) that a plan can choose has a case here, checked on the first and last batch row against the float64
+"""Linear attention at 192 columns, whole rows in the pipelined chunk loop: the first and last batch row against the float64
 recurrence and, whole, against a second run bit for bit (a stage read before its loads are in would differ from run to run)."""
 import pytest
 

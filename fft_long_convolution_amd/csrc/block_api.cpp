@@ -1,0 +1,217 @@
+// block_api.cpp -- the C ABI of the gated linear recurrence: argument checks (host only, before any HIP call), workspaces and
+// dispatch.  See include/lconv.h for the contract.
+#include "lconv.h"
+
+#include "block_kernels.h"
+#include "mixer_checks.h"
+
+using namespace lcv;
+
+namespace {
+
+constexpr int64_t kMaxGrid = ((int64_t)1 << 24) - 1;      // workgroups of 256 threads: threads along a grid stay below 2^32
+
+// An operand [B][N][C] with contiguous channels; NULL strides: dense.  B, N, C > 0 here.
+lconv_status_t tokens(const void* p, const lconv_strides_t* given, int64_t B, int64_t N, int64_t C, lconv_dtype_t dt,
+                      bool written, TokOperand* o, Range* r) {
+    int64_t b, n, tb, tn;
+    if (given) {
+        b = given->b;
+        n = given->n;
+    } else {
+        n = C;
+        if (!mul_ok(N, C, &b)) return LCONV_ERR_INVALID_SHAPE;
+    }
+    if (B == 1) b = 0;
+    if (N == 1) n = 0;
+    if (b < 0 || n < 0 || !mul_ok(B - 1, b, &tb) || !mul_ok(N - 1, n, &tn)) return LCONV_ERR_INVALID_SHAPE;
+    if (tb > INT64_MAX / 32 || tn > INT64_MAX / 32 || C > INT64_MAX / 32) return LCONV_ERR_INVALID_SHAPE;
+    if (written) {      // rows apart: the smaller stride clears a row, the larger one all rows along the other
+        const bool nin = B == 1 || (N > 1 && n <= b);
+        const int64_t inner = nin ? n : b, span = (nin ? tn : tb) + C, count = nin ? N : B;
+        if (count > 1 && inner < C) return LCONV_ERR_INVALID_SHAPE;
+        if (B > 1 && N > 1 && (nin ? b : n) < span) return LCONV_ERR_INVALID_SHAPE;
+    }
+    if (!p) return LCONV_ERR_NULL_POINTER;
+    const size_t es = dtype_size(dt);
+    if ((uintptr_t)p % es) return LCONV_ERR_MISALIGNED;      // channels of any width: a token may begin at any element
+    *o = TokOperand{p, b, n};
+    *r = Range{p, (size_t)(tb + tn + C) * es, 0, 0};
+    const int64_t step = N > 1 ? n : b;          // slices of one token-major buffer
+    if ((N > 1 || B > 1) && step >= C && (N == 1 || B == 1 || b % step == 0)) {
+        r->foot = (size_t)C * es;
+        r->step = (size_t)step * es;
+    }
+    return LCONV_SUCCESS;
+}
+
+bool scan_flags_ok(int flags) {
+    const int gate = flags & 3, mix = flags & ~3;
+    return gate <= LCONV_GATE_RATE && (mix == LCONV_MIX_PLAIN || mix == LCONV_MIX_CONVEX || mix == LCONV_MIX_NORM);
+}
+
+// sizes that the kernels' indices hold: channels and segments in 32 bits, marks and states in 64
+bool scan_dims_ok(int64_t B, int64_t N, int64_t C) {
+    int64_t t;
+    if (N >= ((int64_t)1 << 31) || C > ((int64_t)1 << 24) || B > ((int64_t)1 << 24) || !mul_ok(B, C, &t)) return false;
+    if (!mul_ok(t, (N + kScanTile - 1) / kScanTile, &t) || t > INT64_MAX / 16) return false;
+    const ScanPlan p = scan_plan(B, N > 0 ? N : 1, C);
+    return B * p.cblocks * p.nseg <= kMaxGrid / 2 && B * ((C + 511) / 256) <= kMaxGrid;     // 512 threads; single tokens
+}
+
+size_t seg_bytes(const ScanPlan& p, int64_t B, int64_t C) {
+    return p.nseg > 1 ? round256((size_t)(B * p.nseg) * (size_t)C * 12) : 0;
+}
+
+void set_plan(ScanArgs* a, const ScanPlan& p) {
+    a->vec = p.vec; a->cblocks = p.cblocks; a->nseg = p.nseg; a->seg_len = p.seg_len; a->waves = p.waves;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t lconv_gated_scan_marks_bytes(int64_t B, int64_t N, int64_t C) {
+    if (B <= 0 || N <= 0 || C <= 0 || !scan_dims_ok(B, N, C)) return 0;
+    return (size_t)(B * ((N + kScanTile - 1) / kScanTile)) * (size_t)C * 4;
+}
+
+size_t lconv_gated_scan_workspace_bytes(int64_t B, int64_t N, int64_t C) {
+    if (B <= 0 || N <= 0 || C <= 0 || !scan_dims_ok(B, N, C)) return 0;
+    return seg_bytes(scan_plan(B, N, C), B, C);
+}
+
+size_t lconv_gated_scan_bwd_workspace_bytes(int64_t B, int64_t N, int64_t C, int flags) {
+    if (B <= 0 || N <= 0 || C <= 0 || !scan_flags_ok(flags) || !scan_dims_ok(B, N, C)) return 0;
+    const ScanPlan p = scan_plan(B, N, C);
+    return seg_bytes(p, B, C) + ((flags & 3) == LCONV_GATE_RATE ? round256((size_t)(B * p.nseg) * (size_t)C * 4) : 0);
+}
+
+lconv_status_t lconv_gated_scan_fwd(const void* x, const lconv_strides_t* x_strides, const void* z,
+                                    const lconv_strides_t* z_strides, const void* input_gate,
+                                    const lconv_strides_t* input_gate_strides, const float* rate, const float* state_in,
+                                    const int32_t* lengths, void* y, const lconv_strides_t* y_strides, float* state_out,
+                                    float* marks, int64_t B, int64_t N, int64_t C, int flags, lconv_dtype_t dtype,
+                                    void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    if (!dtype_ok(dtype) || !scan_flags_ok(flags)) return LCONV_ERR_UNSUPPORTED;
+    if (B < 0 || N < 0 || C < 0) return LCONV_ERR_INVALID_SHAPE;
+    if (B == 0 || C == 0) return LCONV_SUCCESS;
+    if (!scan_dims_ok(B, N, C)) return LCONV_ERR_UNSUPPORTED;
+    if (!aligned16(state_in) || !aligned16(state_out) || !aligned16(marks) || !aligned16(rate)) return LCONV_ERR_MISALIGNED;
+    const Range rsi = buffer(state_in, B * C, 4), rso = buffer(state_out, B * C, 4);
+    if (state_in != state_out && overlap(rsi, rso)) return LCONV_ERR_ALIASING;
+    if (N == 0) return state_out && state_in != state_out ? hip_status(launch_row_state(state_in, state_out, B * C, stream)) : LCONV_SUCCESS;
+    ScanArgs a{};
+    TokOperand yo{};
+    Range rx, rz, ri{}, ry;
+    lconv_status_t st;
+    if ((st = tokens(x, x_strides, B, N, C, dtype, false, &a.x, &rx)) != LCONV_SUCCESS) return st;
+    if ((st = tokens(z, z_strides, B, N, C, dtype, false, &a.z, &rz)) != LCONV_SUCCESS) return st;
+    if (input_gate && (st = tokens(input_gate, input_gate_strides, B, N, C, dtype, false, &a.i, &ri)) != LCONV_SUCCESS) return st;
+    if ((st = tokens(y, y_strides, B, N, C, dtype, true, &yo, &ry)) != LCONV_SUCCESS) return st;
+    const bool rated = (flags & 3) == LCONV_GATE_RATE;
+    if (rated && !rate) return LCONV_ERR_NULL_POINTER;
+    const Range rr = buffer(rated ? rate : nullptr, C, 4), rl = buffer(lengths, B, 4);
+    const Range rm = buffer(marks, (int64_t)lconv_gated_scan_marks_bytes(B, N, C), 1);
+    if (clash({ry, rso, rm}, {rx, rz, ri, rr, rl}) || overlap(ry, rsi) || overlap(rm, rsi)) return LCONV_ERR_ALIASING;
+    const ScanPlan p = scan_plan(B, N, C);
+    const size_t need = seg_bytes(p, B, C);
+    if (need > 0) {
+        if (!workspace || workspace_bytes < need) return LCONV_ERR_WORKSPACE;
+        if (!aligned16(workspace)) return LCONV_ERR_MISALIGNED;
+        if (clash({buffer(workspace, (int64_t)need, 1)}, {rx, rz, ri, ry, rsi, rso, rr, rl, rm})) return LCONV_ERR_ALIASING;
+    }
+    a.rate = rated ? rate : nullptr; a.state_in = state_in; a.lengths = lengths;
+    a.y = y; a.yb = yo.b; a.yn = yo.n; a.state_out = state_out; a.marks = marks; a.seg = (float*)workspace;
+    a.B = B; a.N = N; a.C = C; a.gate = flags & 3; a.mix = flags & ~3;
+    set_plan(&a, p);
+    return hip_status(launch_scan_fwd(dtype, a, stream));
+}
+
+lconv_status_t lconv_gated_scan_bwd(const void* dy, const lconv_strides_t* dy_strides, const void* x,
+                                    const lconv_strides_t* x_strides, const void* z, const lconv_strides_t* z_strides,
+                                    const void* input_gate, const lconv_strides_t* input_gate_strides, const float* rate,
+                                    const float* marks, const float* dstate_out, const int32_t* lengths, void* dx,
+                                    const lconv_strides_t* dx_strides, void* dz, const lconv_strides_t* dz_strides,
+                                    void* dinput_gate, const lconv_strides_t* dinput_gate_strides, float* drate,
+                                    float* dstate_in, int64_t B, int64_t N, int64_t C, int flags, lconv_dtype_t dtype,
+                                    void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    if (!dtype_ok(dtype) || !scan_flags_ok(flags)) return LCONV_ERR_UNSUPPORTED;
+    if (B < 0 || N < 0 || C < 0) return LCONV_ERR_INVALID_SHAPE;
+    if (C == 0) return LCONV_SUCCESS;
+    if (!scan_dims_ok(B, N, C)) return LCONV_ERR_UNSUPPORTED;
+    const bool rated = (flags & 3) == LCONV_GATE_RATE;
+    if (!rated) drate = nullptr;
+    if (!aligned16(marks) || !aligned16(rate) || !aligned16(drate) || !aligned16(dstate_in) || !aligned16(dstate_out))
+        return LCONV_ERR_MISALIGNED;
+    const Range rso = buffer(dstate_out, B * C, 4), rsi = buffer(dstate_in, B * C, 4), rdr = buffer(drate, C, 4);
+    if ((dstate_in != dstate_out && overlap(rsi, rso)) || overlap(rdr, rsi) || overlap(rdr, rso)) return LCONV_ERR_ALIASING;
+    if (B == 0 || N == 0) {     // no tokens: the state's gradient passes through, the rate has none
+        if (B > 0 && dstate_in && dstate_in != dstate_out && launch_row_state(dstate_out, dstate_in, B * C, stream) != hipSuccess)
+            return LCONV_ERR_HIP;
+        return drate ? hip_status(launch_row_state(nullptr, drate, C, stream)) : LCONV_SUCCESS;
+    }
+    ScanArgs a{};
+    TokOperand ox{}, oz{}, oi{};
+    Range rdy, rx, rz, ri{}, rdx, rdz, rdi{};
+    lconv_status_t st;
+    if ((st = tokens(dy, dy_strides, B, N, C, dtype, false, &a.dy, &rdy)) != LCONV_SUCCESS) return st;
+    if ((st = tokens(x, x_strides, B, N, C, dtype, false, &a.x, &rx)) != LCONV_SUCCESS) return st;
+    if ((st = tokens(z, z_strides, B, N, C, dtype, false, &a.z, &rz)) != LCONV_SUCCESS) return st;
+    if ((st = tokens(dx, dx_strides, B, N, C, dtype, true, &ox, &rdx)) != LCONV_SUCCESS) return st;
+    if ((st = tokens(dz, dz_strides, B, N, C, dtype, true, &oz, &rdz)) != LCONV_SUCCESS) return st;
+    if (input_gate) {
+        if ((st = tokens(input_gate, input_gate_strides, B, N, C, dtype, false, &a.i, &ri)) != LCONV_SUCCESS) return st;
+        if ((st = tokens(dinput_gate, dinput_gate_strides, B, N, C, dtype, true, &oi, &rdi)) != LCONV_SUCCESS) return st;
+    }
+    if (!marks || (rated && !rate)) return LCONV_ERR_NULL_POINTER;
+    const Range rr = buffer(rated ? rate : nullptr, C, 4), rl = buffer(lengths, B, 4);
+    const Range rm = buffer(marks, (int64_t)lconv_gated_scan_marks_bytes(B, N, C), 1);
+    if (clash({rdx, rdz, rdi, rsi, rdr}, {rdy, rx, rz, ri, rr, rl, rm}) || overlap(rdx, rso) || overlap(rdz, rso) || overlap(rdi, rso))
+        return LCONV_ERR_ALIASING;
+    const ScanPlan p = scan_plan(B, N, C);
+    const size_t need = lconv_gated_scan_bwd_workspace_bytes(B, N, C, flags);
+    if (need > 0) {
+        if (!workspace || workspace_bytes < need) return LCONV_ERR_WORKSPACE;
+        if (!aligned16(workspace)) return LCONV_ERR_MISALIGNED;
+        if (clash({buffer(workspace, (int64_t)need, 1)}, {rdy, rx, rz, ri, rdx, rdz, rdi, rso, rsi, rdr, rr, rl, rm})) return LCONV_ERR_ALIASING;
+    }
+    a.rate = rated ? rate : nullptr; a.state_in = dstate_out; a.lengths = lengths;
+    a.dx = dx; a.dxb = ox.b; a.dxn = ox.n; a.dz = dz; a.dzb = oz.b; a.dzn = oz.n; a.di = dinput_gate; a.dib = oi.b; a.din = oi.n;
+    a.state_out = dstate_in; a.marks = const_cast<float*>(marks); a.seg = (float*)workspace;
+    a.part = drate ? (float*)((char*)workspace + seg_bytes(p, B, C)) : nullptr; a.drate = drate;
+    a.B = B; a.N = N; a.C = C; a.gate = flags & 3; a.mix = flags & ~3;
+    set_plan(&a, p);
+    return hip_status(launch_scan_bwd(dtype, a, stream));
+}
+
+lconv_status_t lconv_gated_scan_step(const void* x, int64_t x_stride, const void* z, int64_t z_stride, const void* input_gate,
+                                     int64_t input_gate_stride, const float* rate, float* state, const int32_t* slots,
+                                     void* y, int64_t y_stride, int64_t B, int64_t C, int64_t nslots, int flags,
+                                     lconv_dtype_t dtype, hipStream_t stream) {
+    if (!dtype_ok(dtype) || !scan_flags_ok(flags)) return LCONV_ERR_UNSUPPORTED;
+    if (B < 0 || C < 0 || nslots < 0) return LCONV_ERR_INVALID_SHAPE;
+    if (B == 0 || C == 0) return LCONV_SUCCESS;
+    if (!scan_dims_ok(B, 1, C)) return LCONV_ERR_UNSUPPORTED;
+    int64_t states;
+    if ((!slots && nslots < B) || !mul_ok(nslots, 4 * C, &states)) return LCONV_ERR_INVALID_SHAPE;
+    ScanStepArgs a{};
+    TokOperand yo{};
+    Range rx, rz, ri{}, ry;
+    const lconv_strides_t sx{x_stride, 0, 0}, sz{z_stride, 0, 0}, si{input_gate_stride, 0, 0}, sy{y_stride, 0, 0};
+    lconv_status_t st;
+    if ((st = tokens(x, &sx, B, 1, C, dtype, false, &a.x, &rx)) != LCONV_SUCCESS) return st;
+    if ((st = tokens(z, &sz, B, 1, C, dtype, false, &a.z, &rz)) != LCONV_SUCCESS) return st;
+    if (input_gate && (st = tokens(input_gate, &si, B, 1, C, dtype, false, &a.i, &ri)) != LCONV_SUCCESS) return st;
+    if ((st = tokens(y, &sy, B, 1, C, dtype, true, &yo, &ry)) != LCONV_SUCCESS) return st;
+    const bool rated = (flags & 3) == LCONV_GATE_RATE;
+    if ((rated && !rate) || (!state && nslots > 0)) return LCONV_ERR_NULL_POINTER;
+    if (!aligned16(state) || !aligned16(rate)) return LCONV_ERR_MISALIGNED;
+    if (clash({ry, buffer(state, states, 1)}, {rx, rz, ri, buffer(rated ? rate : nullptr, C, 4), buffer(slots, B, 4)}))
+        return LCONV_ERR_ALIASING;
+    a.rate = rate; a.state = state; a.slots = slots; a.y = y; a.yb = yo.b;
+    a.B = B; a.C = C; a.nslots = nslots; a.gate = flags & 3; a.mix = flags & ~3;
+    return hip_status(launch_scan_step(dtype, a, stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,79 @@
+// block_kernels.h -- launchers of the gated recurrence, the q/k norms with rotary positions and the short convolution
+// (host-callable, defined in scan*.hip, qknorm.hip and shortconv.hip), and how their calls are cut into workgroups.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "lconv.h"
+
+namespace lcv {
+
+// An operand [B][N][C] whose channels are contiguous: element strides of its rows (the strides' h unused).
+struct TokOperand {
+    const void* p;
+    int64_t b, n;
+};
+
+// ---- gated linear recurrence ------------------------------------------------------------------------
+
+// Tokens of a wave's turn, waves of a workgroup, tokens of a tile: a tile's first state is a mark.
+constexpr int kScanTokens = 8, kScanWaves = 8, kScanTile = kScanTokens * kScanWaves;
+
+struct ScanArgs {
+    TokOperand x, z, i, dy;       // i.p NULL: no input gate; dy: gradients only
+    const float* rate;            // [C], LCONV_SCAN_RATE only
+    const float* state_in;        // [B][C] or NULL; gradients: dL/dstate_out
+    const int32_t* lengths;       // [B] or NULL
+    void* y;
+    int64_t yb, yn;
+    void *dx, *dz, *di;           // gradients
+    int64_t dxb, dxn, dzb, dzn, dib, din;
+    float* state_out;             // [B][C] or NULL; gradients: dL/dstate_in
+    float* marks;                 // [B][tiles][C]: forward written or NULL, gradients read
+    float* seg;                   // [B][nseg][3][C]: decays, their residues and sums of the segments (nseg > 1)
+    float* part;                  // [B nseg][C]: the rate's gradient, partial sums
+    float* drate;
+    int64_t B, N, C, seg_len;
+    int nseg, cblocks, waves, vec, gate, mix;
+};
+
+// How a call is cut: channels to a lane, blocks of 64 vec channels, segments of seg_len tokens (a multiple of a tile),
+// waves to a workgroup.
+struct ScanPlan {
+    int vec, cblocks, nseg, waves;
+    int64_t seg_len;
+};
+inline ScanPlan scan_plan(int64_t B, int64_t N, int64_t C) {
+    ScanPlan p{};
+    const int64_t tiles = (N + kScanTile - 1) / kScanTile;
+    p.vec = C % 2 == 0 && B * ((C + 127) / 128) >= 256 ? 2 : 1;
+    p.cblocks = (int)((C + 64 * p.vec - 1) / (64 * p.vec));
+    const int64_t rows = B * p.cblocks;
+    int64_t nseg = 1;
+    if (rows <= 128)
+        while (nseg * 2 * rows <= 1024 && nseg * 4 <= tiles) nseg *= 2;
+    const int64_t per = (tiles + nseg - 1) / nseg;
+    p.seg_len = per * kScanTile;
+    p.nseg = (int)((N + p.seg_len - 1) / p.seg_len);
+    p.waves = N >= kScanTile ? kScanWaves : (int)((N + kScanTokens - 1) / kScanTokens);
+    return p;
+}
+
+struct ScanStepArgs {
+    TokOperand x, z, i;           // rows b apart
+    const float* rate;
+    float* state;                 // [nslots][C]
+    const int32_t* slots;         // [B] or NULL
+    void* y;
+    int64_t yb;
+    int64_t B, C, nslots;
+    int gate, mix;
+};
+
+hipError_t launch_scan_fwd(int dtype, const ScanArgs& a, hipStream_t stream);
+hipError_t launch_scan_bwd(int dtype, const ScanArgs& a, hipStream_t stream);
+hipError_t launch_scan_step(int dtype, const ScanStepArgs& a, hipStream_t stream);
+// out = in (or zeros) for calls without tokens
+hipError_t launch_row_state(const float* in, float* out, int64_t n, hipStream_t stream);
+
+}  // namespace lcv

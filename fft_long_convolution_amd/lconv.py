@@ -8,8 +8,9 @@ Raw entry points keep the C names (``lconv_filter_fft``, ``lconv_fftconv_fwd``, 
 integer device pointers.  ``filter_fft``, ``fftconv``, ``fftconv_partial``, ``fftconv_sparse``,
 ``fftconv_bwd``, ``fftconv_save``, ``filter_fft2d`` and ``fftconv2d`` are convenience wrappers over torch
 tensors, and so are the mixer operators ``linear_attention``, ``linear_attention_bwd``,
-``linear_attention_step``, ``rotary`` (with ``rotary_frequencies``), ``layer_norm`` and
-``layer_norm_bwd``, which also take strided views whose last dimension is contiguous.
+``linear_attention_step``, ``rotary`` (with ``rotary_frequencies``), ``layer_norm``,
+``layer_norm_bwd``, ``gated_scan``, ``gated_scan_bwd`` and ``gated_scan_step``, which also take strided views whose last
+dimension is contiguous.
 """
 from __future__ import annotations
 
@@ -108,6 +109,13 @@ def load(path: str = LIB_PATH):
         "lconv_layernorm_fwd": (i, [vp, i64, vp, vp, vp, i64, vp, vp, i64, i64, f32, i, vp]),
         "lconv_layernorm_bwd_workspace_bytes": (sz, [i64, i64]),
         "lconv_layernorm_bwd": (i, [vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, vp, i64, i64, i, vp, sz, vp]),
+        "lconv_gated_scan_marks_bytes": (sz, [i64] * 3),
+        "lconv_gated_scan_workspace_bytes": (sz, [i64] * 3),
+        "lconv_gated_scan_fwd": (i, [vp, sp, vp, sp, vp, sp, vp, vp, vp, vp, sp, vp, vp] + [i64] * 3 + [i, i, vp, sz, vp]),
+        "lconv_gated_scan_bwd_workspace_bytes": (sz, [i64] * 3 + [i]),
+        "lconv_gated_scan_bwd": (i, [vp, sp, vp, sp, vp, sp, vp, sp, vp, vp, vp, vp, vp, sp, vp, sp, vp, sp, vp, vp]
+                                 + [i64] * 3 + [i, i, vp, sz, vp]),
+        "lconv_gated_scan_step": (i, [vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, i64] + [i64] * 3 + [i, i, vp]),
         "lconv_status_string": (ctypes.c_char_p, [i]),
         "lconv_abi_version": (i, []),
         "lconv_release": (i, []),
@@ -331,6 +339,36 @@ def lconv_layernorm_bwd(dy, dy_stride, x, x_stride, weight, mean, rstd, dx, dx_s
                         workspace, workspace_bytes, stream):
     return load().lconv_layernorm_bwd(dy, dy_stride, x, x_stride, weight, mean, rstd, dx, dx_stride, dweight, dbias,
                                       rows, C, dtype, workspace, workspace_bytes, stream)
+
+
+def lconv_gated_scan_marks_bytes(B, N, C):
+    return load().lconv_gated_scan_marks_bytes(B, N, C)
+
+
+def lconv_gated_scan_workspace_bytes(B, N, C):
+    return load().lconv_gated_scan_workspace_bytes(B, N, C)
+
+
+def lconv_gated_scan_fwd(x, xs, z, zs, input_gate, igs, rate, state_in, lengths, y, ys, state_out, marks, B, N, C, flags,
+                         dtype, workspace, workspace_bytes, stream):
+    return load().lconv_gated_scan_fwd(x, xs, z, zs, input_gate, igs, rate, state_in, lengths, y, ys, state_out, marks, B,
+                                       N, C, flags, dtype, workspace, workspace_bytes, stream)
+
+
+def lconv_gated_scan_bwd_workspace_bytes(B, N, C, flags):
+    return load().lconv_gated_scan_bwd_workspace_bytes(B, N, C, flags)
+
+
+def lconv_gated_scan_bwd(dy, dys, x, xs, z, zs, input_gate, igs, rate, marks, dstate_out, lengths, dx, dxs, dz, dzs,
+                         dinput_gate, digs, drate, dstate_in, B, N, C, flags, dtype, workspace, workspace_bytes, stream):
+    return load().lconv_gated_scan_bwd(dy, dys, x, xs, z, zs, input_gate, igs, rate, marks, dstate_out, lengths, dx, dxs,
+                                       dz, dzs, dinput_gate, digs, drate, dstate_in, B, N, C, flags, dtype, workspace,
+                                       workspace_bytes, stream)
+
+
+def lconv_gated_scan_step(x, xs, z, zs, input_gate, igs, rate, state, slots, y, ys, B, C, nslots, flags, dtype, stream):
+    return load().lconv_gated_scan_step(x, xs, z, zs, input_gate, igs, rate, state, slots, y, ys, B, C, nslots, flags,
+                                        dtype, stream)
 
 
 def lconv_abi_version():
@@ -1133,3 +1171,150 @@ def layer_norm_bwd(dy, x, weight, mean, rstd, need_dweight=True, need_dbias=True
                                    _ptr(dw), _ptr(db), rows, C, dt, _ptr(ws), wsb, st),
                "lconv_layernorm_bwd")
     return dx, dw, db
+
+
+# ---- gated linear recurrence --------------------------------------------------------------------
+
+GATES = {"log": 0, "sigmoid": 1, "rate": 2}            # LCONV_GATE_*
+MIXES = {"plain": 0, "convex": 4, "norm": 8}           # LCONV_MIX_*
+
+
+def _scan_operands(x, z, gate, mix, input_gate, rate, dims):
+    """(dtype code, flags, strides of x, z and input_gate) of a call's operands, checked where they fix the shape (dims 3:
+    with tokens, 2: single tokens, whose strides are those of their rows)."""
+    torch = _torch()
+    if not isinstance(x, torch.Tensor) or x.dim() != dims:
+        raise ValueError(f"x must be a {dims}-D torch tensor")
+    dt = _float_dtype("x", x)
+    if gate not in GATES or mix not in MIXES:
+        raise ValueError(f"unknown gate {gate!r} or mix {mix!r}; gates: {', '.join(GATES)}; mixes: {', '.join(MIXES)}")
+    if (rate is not None) != (gate == "rate"):
+        raise ValueError('rate goes with gate="rate", and only with it')
+    _need("rate", rate, (x.shape[-1],), torch.float32, optional=True)
+    shape, like = x.shape, x.dtype
+    s = (_tokens("x", x, shape, like), _tokens("z", z, shape, like),
+         None if input_gate is None else _tokens("input_gate", input_gate, shape, like))
+    return dt, GATES[gate] | MIXES[mix], s
+
+
+def _tokens(name, t, shape, dtype):
+    """An operand [B, N, C] (or [B, C]) of any strides whose last dimension is contiguous: its lconv_strides_t, None for a
+    dense one ([B, C]: the stride of its rows)."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor, got {type(t).__name__}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.is_contiguous():
+        return None if len(shape) == 3 else shape[-1]
+    if t.stride(-1) != 1 and shape[-1] > 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    s = t.stride()
+    return _strides_of(s[0], 0, s[1]) if len(shape) == 3 else s[0]
+
+
+def _token_output(name, t, like):
+    """An output given by the caller, or a new dense one shaped like x: (tensor, strides)."""
+    if t is None:
+        torch = _torch()
+        t = torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    return t, _tokens(name, t, like.shape, like.dtype)
+
+
+GatedScan = namedtuple("GatedScan", "y state marks")
+
+
+def gated_scan(x, z, gate="sigmoid", mix="plain", input_gate=None, rate=None, state=None, lengths=None, need_state=True,
+               need_marks=False, out=None, state_out=None, stream=None):
+    """Gated linear recurrence over x [B, N, C] with decays from z [B, N, C], from a state [B, C] in float32:
+
+        h_t = a_t h_{t-1} + m_t s_t x_t,    y_t = h_t
+
+    gate: "log" (log a = z, at most 0), "sigmoid" (a = sigmoid(z)) or "rate" (log a = -rate sigmoid(z), rate [C] in
+    float32, at least 0).  mix: "plain" (m = 1), "convex" (1 - a) or "norm" (sqrt(1 - a^2)).  s is sigmoid(input_gate), or 1
+    without one.  lengths: int32 [B], tokens past a row's length count for nothing and give y = 0.  Returns (y in x's dtype,
+    the state after each row's last token; None without need_state, marks for the gradient call; None without need_marks).
+    state_out may be `state` itself."""
+    torch = _torch()
+    dt, flags, (xs, zs, igs) = _scan_operands(x, z, gate, mix, input_gate, rate, 3)
+    B, N, C = x.shape
+    _need("state", state, (B, C), torch.float32, optional=True)
+    _need("state_out", state_out, (B, C), torch.float32, optional=True)
+    _lengths(lengths, B)
+    dev = _same_gpu("x z input_gate rate state lengths out state_out", (x, z, input_gate, rate, state, lengths, out, state_out))
+    ctx, st = _at(dev, stream)
+    with ctx:
+        y, ys = _token_output("out", out, x)
+        if state_out is None and need_state:
+            state_out = torch.empty((B, C), dtype=torch.float32, device=dev)
+        marks = torch.empty(lconv_gated_scan_marks_bytes(B, N, C) // 4, dtype=torch.float32, device=dev) if need_marks else None
+        wsb = lconv_gated_scan_workspace_bytes(B, N, C)
+        ws = torch.empty(wsb, dtype=torch.uint8, device=dev) if wsb else None
+        _check(lconv_gated_scan_fwd(_ptr(x), xs, _ptr(z), zs, _ptr(input_gate), igs, _ptr(rate), _ptr(state), _ptr(lengths),
+                                    _ptr(y), ys, _ptr(state_out), _ptr(marks), B, N, C, flags, dt, _ptr(ws), wsb, st),
+               "lconv_gated_scan_fwd")
+    return GatedScan(y, state_out, marks)
+
+
+GatedScanGrads = namedtuple("GatedScanGrads", "dx dz dinput_gate drate dstate")
+
+
+def gated_scan_bwd(dy, x, z, marks, gate="sigmoid", mix="plain", input_gate=None, rate=None, dstate=None, lengths=None,
+                   need_drate=True, need_dstate=True, stream=None):
+    """Gradients of gated_scan given dy [B, N, C], the marks that it returned for the same operands and, where the state it
+    returned was used, dstate [B, C] in float32.  Returns (dx, dz, dinput_gate in x's dtype, drate [C] and dstate [B, C], the
+    gradient of the state that entered, in float32); dinput_gate is None without one, drate without a rate or need_drate,
+    dstate without need_dstate."""
+    torch = _torch()
+    dt, flags, (xs, zs, igs) = _scan_operands(x, z, gate, mix, input_gate, rate, 3)
+    B, N, C = x.shape
+    dys = _tokens("dy", dy, x.shape, x.dtype)
+    _need("dstate", dstate, (B, C), torch.float32, optional=True)
+    _need("marks", marks, (lconv_gated_scan_marks_bytes(B, N, C) // 4,), torch.float32)
+    _lengths(lengths, B)
+    dev = _same_gpu("dy x z marks input_gate rate dstate lengths", (dy, x, z, marks, input_gate, rate, dstate, lengths))
+    ctx, st = _at(dev, stream)
+    with ctx:
+        dx, dxs = _token_output("dx", None, x)
+        dz, dzs = _token_output("dz", None, x)
+        dig, digs = (None, None) if input_gate is None else _token_output("dinput_gate", None, x)
+        dr = torch.empty((C,), dtype=torch.float32, device=dev) if rate is not None and need_drate else None
+        ds = torch.empty((B, C), dtype=torch.float32, device=dev) if need_dstate else None
+        wsb = lconv_gated_scan_bwd_workspace_bytes(B, N, C, flags)
+        ws = torch.empty(wsb, dtype=torch.uint8, device=dev) if wsb else None
+        _check(lconv_gated_scan_bwd(_ptr(dy), dys, _ptr(x), xs, _ptr(z), zs, _ptr(input_gate), igs, _ptr(rate), _ptr(marks),
+                                    _ptr(dstate), _ptr(lengths), _ptr(dx), dxs, _ptr(dz), dzs, _ptr(dig), digs, _ptr(dr),
+                                    _ptr(ds), B, N, C, flags, dt, _ptr(ws), wsb, st), "lconv_gated_scan_bwd")
+    return GatedScanGrads(dx, dz, dig, dr, ds)
+
+
+def gated_scan_step(x, z, state, gate="sigmoid", mix="plain", input_gate=None, rate=None, slots=None, out=None, stream=None):
+    """One token of every sequence: x, z and input_gate [B, C]; the states [slots, C] in float32 are moved on in place.
+    slots: int32 [B], the state that each row continues (outside the states: an idle row, y = 0); without it row b has state
+    b.  No two rows may have the same slot.  Returns y [B, C]."""
+    torch = _torch()
+    dt, flags, (xs, zs, igs) = _scan_operands(x, z, gate, mix, input_gate, rate, 2)
+    B, C = x.shape
+    nslots = _pool("state", state, 2, slots, B)
+    _need("state", state, (nslots, C), torch.float32)
+    dev = _same_gpu("x z input_gate rate state slots out", (x, z, input_gate, rate, state, slots, out))
+    ctx, st = _at(dev, stream)
+    with ctx:
+        y, ys = _token_output("out", out, x)
+        _check(lconv_gated_scan_step(_ptr(x), xs, _ptr(z), zs, _ptr(input_gate), igs or 0, _ptr(rate), _ptr(state), _ptr(slots),
+                                     _ptr(y), ys, B, C, nslots, flags, dt, st), "lconv_gated_scan_step")
+    return y
+
+
+def _pool(name, state, dims, slots, B):
+    """The number of states in a pool that single tokens find theirs in."""
+    torch = _torch()
+    if not isinstance(state, torch.Tensor) or state.dim() != dims:
+        raise ValueError(f"{name} must be a {dims}-D torch tensor")
+    if slots is not None:
+        _need("slots", slots, (B,), torch.int32)
+    elif state.shape[0] < B:
+        raise ValueError(f"{B} rows and {state.shape[0]} states: slots are needed")
+    return state.shape[0]

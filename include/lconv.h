@@ -53,7 +53,7 @@ extern "C" {
  * part states.  4: lconv_prepare and lconv_fftconv_fwd_noalloc, two status codes.  5: 2D calls
  * take Hs x Ws images and a workspace; lconv_fftconv2d_workspace_bytes.  6: gradients and the
  * training pair for every supported N, with workspace arguments.  Added within version 8: the mixer
- * operators further down -- linear attention, rotary positions, layer norm). */
+ * operators further down -- linear attention, rotary positions, layer norm; those of a recurrent block). */
 #define LCONV_ABI_VERSION 8
 
 /* The last enumerator only widens the type's range to every int, so that any value a C caller
@@ -601,6 +601,79 @@ lconv_status_t lconv_layernorm_bwd(const void* dy, int64_t dy_stride, const void
                                    const void* weight, const float* mean, const float* rstd, void* dx,
                                    int64_t dx_stride, float* dweight, float* dbias, int64_t rows, int64_t C,
                                    lconv_dtype_t dtype, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* ---- operators of a recurrent block: gated linear recurrence ------------------------------------ */
+
+/*
+ * Gated linear recurrence: for every channel of its own, with decays that follow the input,
+ *   h_t = a_t h_{t-1} + m_t s_t x_t,  h_{-1} = state_in,  y_t = h_t  for t < len[b];   y = 0 for t >= len[b];
+ *   state_out = h_{len-1} (state_in for a row of length 0).  Nothing past len[b] is read into a result.
+ * The flags give the decay and what keeps the input in scale:
+ *   LCONV_GATE_LOG      log a = z (at most 0; minus infinity: no memory)
+ *   LCONV_GATE_SIGMOID  a = sigmoid(z)
+ *   LCONV_GATE_RATE     log a = -rate[c] sigmoid(z), rate at least 0
+ *   LCONV_MIX_PLAIN     m = 1;   LCONV_MIX_CONVEX  m = 1 - a;   LCONV_MIX_NORM  m = sqrt(1 - a^2)
+ * and s = sigmoid(input_gate), 1 without one.
+ *   x, z, y      [B][N][C] dtype, channels contiguous;  input_gate the same or NULL
+ *   rate         [C] fp32, LCONV_GATE_RATE only (not read otherwise)
+ *   state_in     [B][C] fp32 or NULL (zeros);  state_out the same shape or NULL; the two may be one buffer
+ *   lengths      [B] int32, device, or NULL (every row N long); taken as min(max(len, 0), N)
+ *   marks        lconv_gated_scan_marks_bytes(B, N, C) bytes, written, or NULL: states along the way, which the gradient
+ *                call takes in place of y
+ *   workspace    lconv_gated_scan_workspace_bytes(B, N, C) bytes (may be NULL if that is 0)
+ * Strides are lconv_strides_t without h, in elements, of any size that keeps an output's rows apart; NULL: dense.  These
+ * operands may begin at any element, the others are 16-byte aligned.  Gates, states and sums are fp32, a's distance from 1 to its own size, so that memories of many thousand
+ * tokens neither end early nor drift.  A value that is not finite reaches what the recurrence lets it reach, as a value that
+ * is not finite: its own and later tokens of its channel (in the gradients its own and earlier ones).
+ * Supported: N < 2^31, B and C up to 2^24, every dtype, launches of fewer than 2^32 threads.  B, C or N = 0 is a no-op apart
+ * from state_out, which is set as for rows of length 0 (N = 0).
+ */
+#define LCONV_GATE_LOG     0
+#define LCONV_GATE_SIGMOID 1
+#define LCONV_GATE_RATE    2
+#define LCONV_MIX_PLAIN    0
+#define LCONV_MIX_CONVEX   4
+#define LCONV_MIX_NORM     8
+size_t lconv_gated_scan_marks_bytes(int64_t B, int64_t N, int64_t C);
+size_t lconv_gated_scan_workspace_bytes(int64_t B, int64_t N, int64_t C);
+lconv_status_t lconv_gated_scan_fwd(const void* x, const lconv_strides_t* x_strides, const void* z,
+                                    const lconv_strides_t* z_strides, const void* input_gate,
+                                    const lconv_strides_t* input_gate_strides, const float* rate, const float* state_in,
+                                    const int32_t* lengths, void* y, const lconv_strides_t* y_strides, float* state_out,
+                                    float* marks, int64_t B, int64_t N, int64_t C, int flags, lconv_dtype_t dtype,
+                                    void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Gradients of lconv_gated_scan_fwd, given dy = dL/dy and dstate_out = dL/dstate_out (NULL: zeros), from the marks of the
+ * forward call on the same operands, lengths and flags.  With G_t = dL/dh_t = dy_t + a_{t+1} G_{t+1} (for the last token
+ * dstate_out in place of a_{t+1} G_{t+1}) and l = log a:
+ *   dx = G m s;   dinput_gate = G m x s (1 - s);   dl = a G h_{t-1} + G s x dm/dl,  dm/dl = 0, -a, -a^2 / m (0 where m = 0);
+ *   dz = dl,  dl (1 - a),  dl l (1 - sigmoid(z));  drate[c] = -sum_{b,t} dl sigmoid(z);   dstate_in = a_0 G_0
+ *   dx, dz, dinput_gate  [B][N][C] dtype, written (zeros past a row's length); dinput_gate with input_gate only
+ *   drate      [C] fp32, written, or NULL;  dstate_in  [B][C] fp32, written, or NULL, may be dstate_out
+ *   workspace  lconv_gated_scan_bwd_workspace_bytes(B, N, C, flags) bytes (may be NULL if that is 0)
+ * No atomics: results repeat bit for bit.
+ */
+size_t lconv_gated_scan_bwd_workspace_bytes(int64_t B, int64_t N, int64_t C, int flags);
+lconv_status_t lconv_gated_scan_bwd(const void* dy, const lconv_strides_t* dy_strides, const void* x,
+                                    const lconv_strides_t* x_strides, const void* z, const lconv_strides_t* z_strides,
+                                    const void* input_gate, const lconv_strides_t* input_gate_strides, const float* rate,
+                                    const float* marks, const float* dstate_out, const int32_t* lengths, void* dx,
+                                    const lconv_strides_t* dx_strides, void* dz, const lconv_strides_t* dz_strides,
+                                    void* dinput_gate, const lconv_strides_t* dinput_gate_strides, float* drate,
+                                    float* dstate_in, int64_t B, int64_t N, int64_t C, int flags, lconv_dtype_t dtype,
+                                    void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * One token of every sequence of a serving batch: h = a h + m s x in place, y = h.
+ *   x, z, input_gate, y  [B][C] dtype, rows *_stride elements apart;  state  [nslots][C] fp32, read and written
+ *   slots  [B] int32, device, as for lconv_linattn_step: the state that row b continues (NULL: state b, nslots >= B); outside
+ *          [0, nslots) an idle row, y = 0.  No two rows may name the same slot.
+ */
+lconv_status_t lconv_gated_scan_step(const void* x, int64_t x_stride, const void* z, int64_t z_stride, const void* input_gate,
+                                     int64_t input_gate_stride, const float* rate, float* state, const int32_t* slots,
+                                     void* y, int64_t y_stride, int64_t B, int64_t C, int64_t nslots, int flags,
+                                     lconv_dtype_t dtype, hipStream_t stream);
 
 /* ---- misc ------------------------------------------------------------------------------- */
 

@@ -1,5 +1,5 @@
-// block_api.cpp -- the C ABI of the gated linear recurrence: argument checks (host only, before any HIP call), workspaces and
-// dispatch.  See include/lconv.h for the contract.
+// block_api.cpp -- the C ABI of the gated linear recurrence and of q/k norms with rotary positions: argument checks (host
+// only, before any HIP call), workspaces and dispatch.  See include/lconv.h for the contract.
 #include "lconv.h"
 
 #include "block_kernels.h"
@@ -212,6 +212,137 @@ lconv_status_t lconv_gated_scan_step(const void* x, int64_t x_stride, const void
     a.rate = rate; a.state = state; a.slots = slots; a.y = y; a.yb = yo.b;
     a.B = B; a.C = C; a.nslots = nslots; a.gate = flags & 3; a.mix = flags & ~3;
     return hip_status(launch_scan_step(dtype, a, stream));
+}
+
+}  // extern "C"
+
+namespace {
+
+constexpr int kQkFlags = LCONV_ROTARY_INTERLEAVED | LCONV_QKNORM_CENTRED;
+
+bool qk_dims_ok(int64_t B, int64_t H, int64_t G, int64_t N, int64_t D, int64_t rot, int flags) {
+    int64_t tokens, t;
+    if (D < 8 || D > LCONV_QKNORM_MAX_D || D % 8 || rot > D || rot % 2 || (flags & ~kQkFlags)) return false;
+    if (H >= (1 << 20) || G >= (1 << 20) || !mul_ok(B, N, &tokens) || !mul_ok(tokens, H + G, &t)) return false;
+    if (tokens == 0 || H + G == 0) return true;
+    if (tokens >= ((int64_t)1 << 31)) return false;
+    const QkPlan p = qk_plan(tokens, D, rot, (int)(H + G));
+    return p.items < ((int64_t)1 << 31) && (p.items * p.lanes + 255) / 256 <= kMaxGrid;
+}
+
+// positions, frequencies and weights: their ranges
+struct QkSides { Range pos, freq, w[2]; };
+lconv_status_t qk_sides(QkArgs* a, const int32_t* positions, int64_t pos_stride, const float* inv_freq, const void* q_weight,
+                        const void* k_weight, int64_t B, int64_t N, int64_t D, int64_t rot, lconv_dtype_t dtype, QkSides* r) {
+    int64_t t;
+    if (rot > 0 && !inv_freq) return LCONV_ERR_NULL_POINTER;
+    if (!mul_ok(B - 1, pos_stride, &t) || t > INT64_MAX / 8 - N) return LCONV_ERR_INVALID_SHAPE;
+    if (!aligned16(q_weight) || !aligned16(k_weight)) return LCONV_ERR_MISALIGNED;
+    r->pos = buffer(positions, t + N, 4);
+    r->freq = buffer(rot > 0 ? inv_freq : nullptr, rot / 2, 4);
+    r->w[0] = buffer(q_weight, D, dtype_size(dtype));
+    r->w[1] = buffer(k_weight, D, dtype_size(dtype));
+    a->w[0] = q_weight; a->w[1] = k_weight;
+    a->positions = positions; a->pos_stride = pos_stride; a->inv_freq = inv_freq;
+    return LCONV_SUCCESS;
+}
+
+bool same_place(const void* x, const lconv_strides_t& xs, const void* y, const lconv_strides_t& ys) {
+    return x == y && xs.b == ys.b && xs.h == ys.h && xs.n == ys.n;
+}
+
+}  // namespace
+
+extern "C" {
+
+lconv_status_t lconv_qknorm_rotary_fwd(const void* q, const lconv_strides_t* q_strides, const void* k,
+                                       const lconv_strides_t* k_strides, const void* q_weight, const void* k_weight,
+                                       const int32_t* positions, int64_t pos_stride, const float* inv_freq, float magnitude,
+                                       float eps, void* yq, const lconv_strides_t* yq_strides, void* yk,
+                                       const lconv_strides_t* yk_strides, int64_t B, int64_t H, int64_t G, int64_t N, int64_t D,
+                                       int64_t rot, int flags, lconv_dtype_t dtype, hipStream_t stream) {
+    if (!dtype_ok(dtype)) return LCONV_ERR_UNSUPPORTED;
+    if (B < 0 || H < 0 || G < 0 || N < 0 || D < 0 || rot < 0 || pos_stride < 0) return LCONV_ERR_INVALID_SHAPE;
+    if (!k && !yk) G = 0;
+    if (B == 0 || N == 0 || H + G == 0) return LCONV_SUCCESS;
+    if (!qk_dims_ok(B, H, G, N, D, rot, flags)) return LCONV_ERR_UNSUPPORTED;
+    QkArgs a{};
+    QkSides side{};
+    lconv_status_t st = qk_sides(&a, positions, pos_stride, inv_freq, q_weight, k_weight, B, N, D, rot, dtype, &side);
+    if (st != LCONV_SUCCESS) return st;
+    const int64_t heads[2] = {H, G};
+    const void* const in[2] = {q, k};
+    const lconv_strides_t *const is[2] = {q_strides, k_strides}, *const os[2] = {yq_strides, yk_strides};
+    void* const out[2] = {yq, yk};
+    Range rx[2]{}, ry[2]{};
+    bool inplace[2] = {false, false};
+    for (int i = 0; i < 2; ++i) {
+        if (heads[i] == 0) continue;
+        if ((st = operand(in[i], is[i], B, heads[i], N, D, dtype, false, &a.xs[i], &rx[i])) != LCONV_SUCCESS) return st;
+        if ((st = operand(out[i], os[i], B, heads[i], N, D, dtype, true, &a.ys[i], &ry[i])) != LCONV_SUCCESS) return st;
+        a.x[i] = in[i]; a.y[i] = out[i]; a.heads[i] = (int)heads[i];
+        inplace[i] = same_place(in[i], a.xs[i], out[i], a.ys[i]);
+    }
+    if (clash({ry[0], ry[1]}, {side.pos, side.freq, side.w[0], side.w[1]}) || overlap(ry[0], rx[1]) || overlap(ry[1], rx[0]) ||
+        (overlap(ry[0], rx[0]) && !inplace[0]) || (overlap(ry[1], rx[1]) && !inplace[1]))
+        return LCONV_ERR_ALIASING;
+    a.magnitude = magnitude; a.eps = eps; a.B = B; a.N = N; a.D = (int)D; a.rot = (int)rot; a.flags = flags;
+    return hip_status(launch_qknorm_fwd(dtype, a, stream));
+}
+
+size_t lconv_qknorm_rotary_bwd_workspace_bytes(int64_t B, int64_t H, int64_t G, int64_t N, int64_t D, int64_t rot) {
+    if (B <= 0 || H < 0 || G < 0 || H + G <= 0 || N <= 0 || rot < 0 || !qk_dims_ok(B, H, G, N, D, rot, 0)) return 0;
+    return (size_t)qk_parts(qk_plan(B * N, D, rot, (int)(H + G))) * 2 * (size_t)D * 4;
+}
+
+lconv_status_t lconv_qknorm_rotary_bwd(const void* dyq, const lconv_strides_t* dyq_strides, const void* dyk,
+                                       const lconv_strides_t* dyk_strides, const void* q, const lconv_strides_t* q_strides,
+                                       const void* k, const lconv_strides_t* k_strides, const void* q_weight,
+                                       const void* k_weight, const int32_t* positions, int64_t pos_stride,
+                                       const float* inv_freq, float magnitude, float eps, void* dq,
+                                       const lconv_strides_t* dq_strides, void* dk, const lconv_strides_t* dk_strides,
+                                       float* dq_weight, float* dk_weight, int64_t B, int64_t H, int64_t G, int64_t N, int64_t D,
+                                       int64_t rot, int flags, lconv_dtype_t dtype, void* workspace, size_t workspace_bytes,
+                                       hipStream_t stream) {
+    if (!dtype_ok(dtype)) return LCONV_ERR_UNSUPPORTED;
+    if (B < 0 || H < 0 || G < 0 || N < 0 || D < 0 || rot < 0 || pos_stride < 0) return LCONV_ERR_INVALID_SHAPE;
+    if (!k && !dyk && !dk) G = 0;
+    if (!qk_dims_ok(B, H, G, N, D, rot, flags)) return LCONV_ERR_UNSUPPORTED;
+    if (!aligned16(dq_weight) || !aligned16(dk_weight)) return LCONV_ERR_MISALIGNED;
+    const Range rdw[2] = {buffer(dq_weight, D, 4), buffer(dk_weight, D, 4)};
+    if (overlap(rdw[0], rdw[1])) return LCONV_ERR_ALIASING;
+    QkArgs a{};
+    a.dw[0] = dq_weight; a.dw[1] = dk_weight; a.D = (int)D;
+    const int64_t heads[2] = {H, G};
+    if (B == 0 || N == 0 || H + G == 0) return hip_status(launch_qknorm_bwd(dtype, a, stream));    // zeros to the weights' gradients
+    QkSides side{};
+    lconv_status_t st = qk_sides(&a, positions, pos_stride, inv_freq, q_weight, k_weight, B, N, D, rot, dtype, &side);
+    if (st != LCONV_SUCCESS) return st;
+    const void *const in[2] = {q, k}, *const grad[2] = {dyq, dyk};
+    const lconv_strides_t *const is[2] = {q_strides, k_strides}, *const gs[2] = {dyq_strides, dyk_strides},
+                          *const os[2] = {dq_strides, dk_strides};
+    void* const out[2] = {dq, dk};
+    Range rx[2]{}, rg[2]{}, ry[2]{};
+    for (int i = 0; i < 2; ++i) {
+        if (heads[i] == 0) continue;
+        if ((st = operand(grad[i], gs[i], B, heads[i], N, D, dtype, false, &a.dys[i], &rg[i])) != LCONV_SUCCESS) return st;
+        if ((st = operand(in[i], is[i], B, heads[i], N, D, dtype, false, &a.xs[i], &rx[i])) != LCONV_SUCCESS) return st;
+        if ((st = operand(out[i], os[i], B, heads[i], N, D, dtype, true, &a.ys[i], &ry[i])) != LCONV_SUCCESS) return st;
+        a.x[i] = in[i]; a.dy[i] = grad[i]; a.y[i] = out[i]; a.heads[i] = (int)heads[i];
+    }
+    if (clash({ry[0], ry[1], rdw[0], rdw[1]}, {rx[0], rx[1], rg[0], rg[1], side.pos, side.freq, side.w[0], side.w[1]}))
+        return LCONV_ERR_ALIASING;
+    if (dq_weight || dk_weight) {
+        const size_t need = lconv_qknorm_rotary_bwd_workspace_bytes(B, H, G, N, D, rot);
+        if (!workspace || workspace_bytes < need) return LCONV_ERR_WORKSPACE;
+        if (!aligned16(workspace)) return LCONV_ERR_MISALIGNED;
+        if (clash({buffer(workspace, (int64_t)need, 1)}, {rx[0], rx[1], rg[0], rg[1], ry[0], ry[1], rdw[0], rdw[1], side.pos,
+                                                          side.freq, side.w[0], side.w[1]}))
+            return LCONV_ERR_ALIASING;
+        a.part = (float*)workspace;
+    }
+    a.magnitude = magnitude; a.eps = eps; a.B = B; a.N = N; a.rot = (int)rot; a.flags = flags;
+    return hip_status(launch_qknorm_bwd(dtype, a, stream));
 }
 
 }  // extern "C"

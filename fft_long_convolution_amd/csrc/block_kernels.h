@@ -76,4 +76,46 @@ hipError_t launch_scan_step(int dtype, const ScanStepArgs& a, hipStream_t stream
 // out = in (or zeros) for calls without tokens
 hipError_t launch_row_state(const float* in, float* out, int64_t n, hipStream_t stream);
 
+// ---- norms of q and k with rotary positions -----------------------------------------------------------
+
+// Lanes to a head: a power of two that holds its units (8 pairs, or 16 elements that are only scaled).  An item is one token
+// of `per` heads, which share the token's sines.
+struct QkPlan {
+    int turns, units, lanes, per, hgroups;
+    int64_t items;
+};
+inline QkPlan qk_plan(int64_t tokens, int64_t D, int64_t rot, int heads) {
+    QkPlan p{};
+    p.turns = (int)((rot / 2 + 7) / 8);
+    p.units = p.turns + (int)((D - rot + 15) / 16);
+    p.lanes = 1;
+    while (p.lanes < p.units) p.lanes *= 2;
+    p.per = 4;
+    while (p.per > 1 && tokens * ((heads + p.per - 1) / p.per) * p.lanes < 256 * 512) p.per /= 2;
+    p.hgroups = (heads + p.per - 1) / p.per;
+    p.items = tokens * p.hgroups;
+    return p;
+}
+// Workgroups of the gradient call, each with a partial sum of both weights' gradients over its items.
+inline int64_t qk_parts(const QkPlan& p) {
+    const int64_t wgs = (p.items * p.lanes + 255) / 256;
+    return wgs < 1024 ? wgs : 1024;
+}
+
+struct QkArgs {
+    const void *x[2], *dy[2], *w[2];      // q and k; w NULL: ones
+    lconv_strides_t xs[2], dys[2], ys[2];
+    void* y[2];                           // forward: the results; gradients: dq, dk
+    float* dw[2];                         // [D] or NULL
+    float* part;                          // [parts][2][D]
+    const int32_t* positions;
+    int64_t pos_stride;
+    const float* inv_freq;
+    float magnitude, eps;
+    int64_t B, N;
+    int heads[2], D, rot, flags;
+};
+hipError_t launch_qknorm_fwd(int dtype, const QkArgs& a, hipStream_t stream);
+hipError_t launch_qknorm_bwd(int dtype, const QkArgs& a, hipStream_t stream);
+
 }  // namespace lcv

@@ -9,7 +9,7 @@ integer device pointers.  ``filter_fft``, ``fftconv``, ``fftconv_partial``, ``ff
 ``fftconv_bwd``, ``fftconv_save``, ``filter_fft2d`` and ``fftconv2d`` are convenience wrappers over torch
 tensors, and so are the mixer operators ``linear_attention``, ``linear_attention_bwd``,
 ``linear_attention_step``, ``rotary`` (with ``rotary_frequencies``), ``layer_norm``,
-``layer_norm_bwd``, ``gated_scan``, ``gated_scan_bwd`` and ``gated_scan_step``, which also take strided views whose last
+``layer_norm_bwd``, ``qk_norm_rotary``, ``qk_norm_rotary_bwd``, ``gated_scan``, ``gated_scan_bwd`` and ``gated_scan_step``, which also take strided views whose last
 dimension is contiguous.
 """
 from __future__ import annotations
@@ -116,6 +116,10 @@ def load(path: str = LIB_PATH):
         "lconv_gated_scan_bwd": (i, [vp, sp, vp, sp, vp, sp, vp, sp, vp, vp, vp, vp, vp, sp, vp, sp, vp, sp, vp, vp]
                                  + [i64] * 3 + [i, i, vp, sz, vp]),
         "lconv_gated_scan_step": (i, [vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, i64] + [i64] * 3 + [i, i, vp]),
+        "lconv_qknorm_rotary_fwd": (i, [vp, sp, vp, sp, vp, vp, vp, i64, vp, f32, f32, vp, sp, vp, sp] + [i64] * 6 + [i, i, vp]),
+        "lconv_qknorm_rotary_bwd_workspace_bytes": (sz, [i64] * 6),
+        "lconv_qknorm_rotary_bwd": (i, [vp, sp, vp, sp, vp, sp, vp, sp, vp, vp, vp, i64, vp, f32, f32, vp, sp, vp, sp, vp, vp]
+                                    + [i64] * 6 + [i, i, vp, sz, vp]),
         "lconv_status_string": (ctypes.c_char_p, [i]),
         "lconv_abi_version": (i, []),
         "lconv_release": (i, []),
@@ -369,6 +373,24 @@ def lconv_gated_scan_bwd(dy, dys, x, xs, z, zs, input_gate, igs, rate, marks, ds
 def lconv_gated_scan_step(x, xs, z, zs, input_gate, igs, rate, state, slots, y, ys, B, C, nslots, flags, dtype, stream):
     return load().lconv_gated_scan_step(x, xs, z, zs, input_gate, igs, rate, state, slots, y, ys, B, C, nslots, flags,
                                         dtype, stream)
+
+
+def lconv_qknorm_rotary_fwd(q, qs, k, ks, q_weight, k_weight, positions, pos_stride, inv_freq, magnitude, eps, yq, yqs, yk, yks,
+                            B, H, G, N, D, rot, flags, dtype, stream):
+    return load().lconv_qknorm_rotary_fwd(q, qs, k, ks, q_weight, k_weight, positions, pos_stride, inv_freq, magnitude, eps,
+                                          yq, yqs, yk, yks, B, H, G, N, D, rot, flags, dtype, stream)
+
+
+def lconv_qknorm_rotary_bwd_workspace_bytes(B, H, G, N, D, rot):
+    return load().lconv_qknorm_rotary_bwd_workspace_bytes(B, H, G, N, D, rot)
+
+
+def lconv_qknorm_rotary_bwd(dyq, dyqs, dyk, dyks, q, qs, k, ks, q_weight, k_weight, positions, pos_stride, inv_freq, magnitude,
+                            eps, dq, dqs, dk, dks, dq_weight, dk_weight, B, H, G, N, D, rot, flags, dtype, workspace,
+                            workspace_bytes, stream):
+    return load().lconv_qknorm_rotary_bwd(dyq, dyqs, dyk, dyks, q, qs, k, ks, q_weight, k_weight, positions, pos_stride,
+                                          inv_freq, magnitude, eps, dq, dqs, dk, dks, dq_weight, dk_weight, B, H, G, N, D, rot,
+                                          flags, dtype, workspace, workspace_bytes, stream)
 
 
 def lconv_abi_version():
@@ -1171,6 +1193,98 @@ def layer_norm_bwd(dy, x, weight, mean, rstd, need_dweight=True, need_dbias=True
                                    _ptr(dw), _ptr(db), rows, C, dt, _ptr(ws), wsb, st),
                "lconv_layernorm_bwd")
     return dx, dw, db
+
+
+# ---- norms of q and k with rotary positions ------------------------------------------------------
+
+QKNORM_CENTRED = 4
+
+
+def _qk_operands(q, k, q_weight, k_weight, positions, inv_freq):
+    """(dtype code, B, H, G, N, D, rot, position stride, strides of q and k), checked."""
+    torch = _torch()
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError("q must be a 4-D torch tensor")
+    dt = _float_dtype("q", q)
+    B, H, N, D = q.shape
+    qs = _view("q", q, (B, H, N, D), q.dtype)
+    G, ks = 0, None
+    if k is not None:
+        if not isinstance(k, torch.Tensor) or k.dim() != 4:
+            raise ValueError("k must be a 4-D torch tensor")
+        G = k.shape[1]
+        ks = _view("k", k, (B, G, N, D), q.dtype)
+    elif k_weight is not None:
+        raise ValueError("a weight for k without k")
+    _need("q_weight", q_weight, (D,), q.dtype, optional=True)
+    _need("k_weight", k_weight, (D,), q.dtype, optional=True)
+    rot, pos_stride = 0, 0
+    if inv_freq is not None:
+        if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
+            raise ValueError("inv_freq must be a 1-D torch tensor")
+        rot = 2 * inv_freq.shape[0]
+        _need("inv_freq", inv_freq, (rot // 2,), torch.float32)
+    if positions is not None:
+        if not isinstance(positions, torch.Tensor) or positions.dtype != torch.int32:
+            raise ValueError("positions must be an int32 torch tensor")
+        if tuple(positions.shape) not in ((B, N), (N,)):
+            raise ValueError(f"positions has shape {tuple(positions.shape)}, expected {(B, N)} or {(N,)}")
+        if N > 1 and positions.stride(-1) != 1:
+            raise ValueError("positions must be contiguous in its last dimension")
+        pos_stride = positions.stride(0) if positions.dim() == 2 and B > 1 else 0
+    return dt, B, H, G, N, D, rot, pos_stride, qs, ks
+
+
+def qk_norm_rotary(q, k, q_weight, k_weight, positions, inv_freq, eps=1e-6, centred=False, interleaved=False, magnitude=1.0,
+                   out=None, stream=None):
+    """Every head's row of q [B, H, N, D] and k [B, G, N, D] (or None) over its root mean square (centred: of the row less its
+    mean), times a weight [D] in q's dtype (None: ones), then ``rotary`` of its first 2 * len(inv_freq) dimensions (inv_freq
+    None: none), in one pass.  positions, interleaved, magnitude and out as for ``rotary``.  Returns (q', k')."""
+    dt, B, H, G, N, D, rot, pos_stride, qs, ks = _qk_operands(q, k, q_weight, k_weight, positions, inv_freq)
+    oq, ok = (None, None) if out is None else out
+    if k is None and ok is not None:
+        raise ValueError("an output for k without k")
+    dev = _same_gpu("q k q_weight k_weight positions inv_freq out_q out_k",
+                    (q, k, q_weight, k_weight, positions, inv_freq, oq, ok))
+    flags = (ROTARY_INTERLEAVED if interleaved else ROTARY_HALF) | (QKNORM_CENTRED if centred else 0)
+    ctx, st = _at(dev, stream)
+    with ctx:
+        yq, yqs = _outputs("out of q", oq, (B, H, N, D), q)
+        yk, yks = (None, None) if k is None else _outputs("out of k", ok, (B, G, N, D), k)
+        _check(lconv_qknorm_rotary_fwd(_ptr(q), qs, _ptr(k), ks, _ptr(q_weight), _ptr(k_weight), _ptr(positions), pos_stride,
+                                       _ptr(inv_freq), float(magnitude), float(eps), _ptr(yq), yqs, _ptr(yk), yks, B, H, G, N,
+                                       D, rot, flags, dt, st), "lconv_qknorm_rotary_fwd")
+    return yq, yk
+
+
+QkNormGrads = namedtuple("QkNormGrads", "dq dk dq_weight dk_weight")
+
+
+def qk_norm_rotary_bwd(dyq, dyk, q, k, q_weight, k_weight, positions, inv_freq, eps=1e-6, centred=False, interleaved=False,
+                       magnitude=1.0, need_dweight=True, stream=None):
+    """Gradients of qk_norm_rotary given those of its results, from its inputs.  Returns (dq, dk in q's dtype, dq_weight,
+    dk_weight [D] in float32; None for what is not there or, the weights', without need_dweight)."""
+    torch = _torch()
+    dt, B, H, G, N, D, rot, pos_stride, qs, ks = _qk_operands(q, k, q_weight, k_weight, positions, inv_freq)
+    dyqs = _view("dyq", dyq, (B, H, N, D), q.dtype)
+    if (k is None) != (dyk is None):
+        raise ValueError("dyk goes with k")
+    dyks = None if k is None else _view("dyk", dyk, (B, G, N, D), q.dtype)
+    dev = _same_gpu("dyq dyk q k q_weight k_weight positions inv_freq", (dyq, dyk, q, k, q_weight, k_weight, positions, inv_freq))
+    flags = (ROTARY_INTERLEAVED if interleaved else ROTARY_HALF) | (QKNORM_CENTRED if centred else 0)
+    ctx, st = _at(dev, stream)
+    with ctx:
+        dq, dqs = _outputs("dq", None, (B, H, N, D), q)
+        dk, dks = (None, None) if k is None else _outputs("dk", None, (B, G, N, D), k)
+        new = lambda w: torch.empty((D,), dtype=torch.float32, device=dev) if need_dweight and w is not None else None  # noqa: E731
+        dwq, dwk = new(q_weight), new(k_weight)
+        wsb = lconv_qknorm_rotary_bwd_workspace_bytes(B, H, G, N, D, rot) if dwq is not None or dwk is not None else 0
+        ws = torch.empty(wsb, dtype=torch.uint8, device=dev) if wsb else None
+        _check(lconv_qknorm_rotary_bwd(_ptr(dyq), dyqs, _ptr(dyk), dyks, _ptr(q), qs, _ptr(k), ks, _ptr(q_weight), _ptr(k_weight),
+                                       _ptr(positions), pos_stride, _ptr(inv_freq), float(magnitude), float(eps), _ptr(dq), dqs,
+                                       _ptr(dk), dks, _ptr(dwq), _ptr(dwk), B, H, G, N, D, rot, flags, dt, _ptr(ws), wsb, st),
+               "lconv_qknorm_rotary_bwd")
+    return QkNormGrads(dq, dk, dwq, dwk)
 
 
 # ---- gated linear recurrence --------------------------------------------------------------------

@@ -602,6 +602,47 @@ lconv_status_t lconv_layernorm_bwd(const void* dy, int64_t dy_stride, const void
                                    int64_t dx_stride, float* dweight, float* dbias, int64_t rows, int64_t C,
                                    lconv_dtype_t dtype, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
+/*
+ * Norms of queries and keys for each head, with their rotary positions in the same pass: for every head's row x [D]
+ *   u = x (LCONV_QKNORM_CENTRED: x - mean(x)),  r = 1 / sqrt(mean(u^2) + eps),  y = turn(r u weight)
+ * where turn is lconv_rotary's of the first `rot` dimensions (LCONV_ROTARY_INTERLEAVED or not; rot = 0: none), magnitude
+ * scaling the pairs that turn.
+ *   q, yq      [B][H][N][D] dtype;  k, yk  [B][G][N][D] dtype, or both NULL;  strides as for linear attention
+ *   q_weight, k_weight  [D] dtype or NULL (ones)
+ *   positions, pos_stride, inv_freq, magnitude  as for lconv_rotary (inv_freq may be NULL for rot = 0)
+ * Sums, statistics and angles as in lconv_layernorm_fwd and lconv_rotary; one rounding, of the result.  yq may be q itself
+ * (same pointer and strides), likewise yk and k; otherwise no overlap.  A value that is not finite stays within its row.
+ * Supported: D a multiple of 8 in [8, 512]; rot even in [0, D]; fewer than 2^31 tokens of four heads and 2^32 threads, 8 pairs
+ * or 16 elements of a token each; every dtype.
+ */
+#define LCONV_QKNORM_MAX_D   512
+#define LCONV_QKNORM_CENTRED 4
+lconv_status_t lconv_qknorm_rotary_fwd(const void* q, const lconv_strides_t* q_strides, const void* k,
+                                       const lconv_strides_t* k_strides, const void* q_weight, const void* k_weight,
+                                       const int32_t* positions, int64_t pos_stride, const float* inv_freq, float magnitude,
+                                       float eps, void* yq, const lconv_strides_t* yq_strides, void* yk,
+                                       const lconv_strides_t* yk_strides, int64_t B, int64_t H, int64_t G, int64_t N, int64_t D,
+                                       int64_t rot, int flags, lconv_dtype_t dtype, hipStream_t stream);
+
+/*
+ * Gradients of lconv_qknorm_rotary_fwd, given dyq and dyk, from its inputs (nothing is kept).  With n = turn^-1(dy), h = n weight:
+ *   dx = r (h - u r^2 mean(h u)), centred: less its mean;   dweight = sum over rows of n r u
+ *   dq [B][H][N][D], dk [B][G][N][D] dtype, written;  dq_weight, dk_weight [D] fp32, written, or NULL
+ *   workspace  lconv_qknorm_rotary_bwd_workspace_bytes(...) bytes (partial sums of the weights' gradients, added in a fixed
+ *              order: results repeat bit for bit); may be NULL when neither weight's gradient is wanted
+ * B = 0, N = 0 or no heads write zeros to dq_weight and dk_weight.  Outputs meet no input.
+ */
+size_t lconv_qknorm_rotary_bwd_workspace_bytes(int64_t B, int64_t H, int64_t G, int64_t N, int64_t D, int64_t rot);
+lconv_status_t lconv_qknorm_rotary_bwd(const void* dyq, const lconv_strides_t* dyq_strides, const void* dyk,
+                                       const lconv_strides_t* dyk_strides, const void* q, const lconv_strides_t* q_strides,
+                                       const void* k, const lconv_strides_t* k_strides, const void* q_weight,
+                                       const void* k_weight, const int32_t* positions, int64_t pos_stride,
+                                       const float* inv_freq, float magnitude, float eps, void* dq,
+                                       const lconv_strides_t* dq_strides, void* dk, const lconv_strides_t* dk_strides,
+                                       float* dq_weight, float* dk_weight, int64_t B, int64_t H, int64_t G, int64_t N, int64_t D,
+                                       int64_t rot, int flags, lconv_dtype_t dtype, void* workspace, size_t workspace_bytes,
+                                       hipStream_t stream);
+
 /* ---- operators of a recurrent block: gated linear recurrence ------------------------------------ */
 
 /*

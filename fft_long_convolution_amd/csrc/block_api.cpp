@@ -1,5 +1,5 @@
-// block_api.cpp -- the C ABI of the gated linear recurrence and of q/k norms with rotary positions: argument checks (host
-// only, before any HIP call), workspaces and dispatch.  See include/lconv.h for the contract.
+// block_api.cpp -- the C ABI of the gated linear recurrence, of q/k norms with rotary positions and of the short convolution:
+// argument checks (host only, before any HIP call), workspaces and dispatch.  See include/lconv.h for the contract.
 #include "lconv.h"
 
 #include "block_kernels.h"
@@ -343,6 +343,134 @@ lconv_status_t lconv_qknorm_rotary_bwd(const void* dyq, const lconv_strides_t* d
     }
     a.magnitude = magnitude; a.eps = eps; a.B = B; a.N = N; a.rot = (int)rot; a.flags = flags;
     return hip_status(launch_qknorm_bwd(dtype, a, stream));
+}
+
+}  // extern "C"
+
+namespace {
+
+bool conv_dims_ok(int64_t B, int64_t N, int64_t C, int64_t K) {
+    int64_t t;
+    if (K < 2 || K > LCONV_SHORTCONV_MAX_TAPS || N >= ((int64_t)1 << 31) || C > ((int64_t)1 << 24) || B > ((int64_t)1 << 24)) return false;
+    if (!mul_ok(B, C, &t) || t > INT64_MAX / 64) return false;
+    if (B == 0 || N == 0 || C == 0) return true;
+    const ConvPlan p = conv_plan(B, N, C, false);
+    return B * p.runs < ((int64_t)1 << 31) && (int64_t)p.cgroups * p.groups <= kMaxGrid && B * ((C + 511) / 256) <= kMaxGrid;
+}
+
+void set_plan(ConvArgs* a, const ConvPlan& p) {
+    a->vec = p.vec; a->cgroups = p.cgroups; a->runs = p.runs; a->groups = p.groups; a->run = p.run;
+}
+
+}  // namespace
+
+extern "C" {
+
+lconv_status_t lconv_shortconv_fwd(const void* x, const lconv_strides_t* x_strides, const void* weight, const void* bias,
+                                   const void* state_in, const int32_t* lengths, void* y, const lconv_strides_t* y_strides,
+                                   void* state_out, int64_t B, int64_t N, int64_t C, int64_t K, int flags, lconv_dtype_t dtype,
+                                   hipStream_t stream) {
+    if (!dtype_ok(dtype) || (flags & ~LCONV_SHORTCONV_SILU)) return LCONV_ERR_UNSUPPORTED;
+    if (B < 0 || N < 0 || C < 0 || K < 0) return LCONV_ERR_INVALID_SHAPE;
+    if (B == 0 || C == 0) return LCONV_SUCCESS;
+    if (!conv_dims_ok(B, N, C, K)) return LCONV_ERR_UNSUPPORTED;
+    if (!aligned16(weight) || !aligned16(bias) || !aligned16(state_in) || !aligned16(state_out)) return LCONV_ERR_MISALIGNED;
+    const size_t es = dtype_size(dtype);
+    const int64_t states = B * (K - 1) * C;
+    const Range rsi = buffer(state_in, states, es), rso = buffer(state_out, states, es);
+    if (state_in != state_out && overlap(rsi, rso)) return LCONV_ERR_ALIASING;
+    if (N == 0)
+        return state_out && state_in != state_out ? hip_status(launch_conv_state(dtype, state_in, state_out, states, stream)) : LCONV_SUCCESS;
+    ConvArgs a{};
+    TokOperand yo{};
+    Range rx, ry;
+    lconv_status_t st;
+    if ((st = tokens(x, x_strides, B, N, C, dtype, false, &a.x, &rx)) != LCONV_SUCCESS) return st;
+    if ((st = tokens(y, y_strides, B, N, C, dtype, true, &yo, &ry)) != LCONV_SUCCESS) return st;
+    if (!weight) return LCONV_ERR_NULL_POINTER;
+    if (clash({ry, rso}, {rx, buffer(weight, C * K, es), buffer(bias, C, es), buffer(lengths, B, 4)}) || overlap(ry, rsi))
+        return LCONV_ERR_ALIASING;
+    a.w = weight; a.bias = bias; a.state_in = state_in; a.lengths = lengths; a.y = y; a.yb = yo.b; a.yn = yo.n; a.state_out = state_out;
+    a.B = B; a.N = N; a.C = C; a.K = (int)K; a.silu = flags & LCONV_SHORTCONV_SILU;
+    set_plan(&a, conv_plan(B, N, C, false));
+    return hip_status(launch_conv_fwd(dtype, a, stream));
+}
+
+size_t lconv_shortconv_bwd_workspace_bytes(int64_t B, int64_t N, int64_t C, int64_t K) {
+    if (B <= 0 || N <= 0 || C <= 0 || !conv_dims_ok(B, N, C, K)) return 0;
+    return (size_t)conv_plan(B, N, C, true).groups * (size_t)(K + 1) * (size_t)C * 4;
+}
+
+lconv_status_t lconv_shortconv_bwd(const void* dy, const lconv_strides_t* dy_strides, const void* x,
+                                   const lconv_strides_t* x_strides, const void* weight, const void* bias, const void* state_in,
+                                   const void* dstate_out, const int32_t* lengths, void* dx, const lconv_strides_t* dx_strides,
+                                   float* dweight, float* dbias, void* dstate_in, int64_t B, int64_t N, int64_t C, int64_t K,
+                                   int flags, lconv_dtype_t dtype, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    if (!dtype_ok(dtype) || (flags & ~LCONV_SHORTCONV_SILU)) return LCONV_ERR_UNSUPPORTED;
+    if (B < 0 || N < 0 || C < 0 || K < 0) return LCONV_ERR_INVALID_SHAPE;
+    if (C == 0) return LCONV_SUCCESS;
+    if (!conv_dims_ok(B, N, C, K)) return LCONV_ERR_UNSUPPORTED;
+    if (!aligned16(weight) || !aligned16(bias) || !aligned16(state_in) || !aligned16(dstate_out) || !aligned16(dstate_in) ||
+        !aligned16(dweight) || !aligned16(dbias))
+        return LCONV_ERR_MISALIGNED;
+    const size_t es = dtype_size(dtype);
+    const int64_t states = B * (K - 1) * C;
+    const Range rsi = buffer(state_in, states, es), rdso = buffer(dstate_out, states, es), rdsi = buffer(dstate_in, states, es);
+    const Range rdw = buffer(dweight, C * K, 4), rdb = buffer(dbias, C, 4);
+    if (clash({rdsi, rdw, rdb}, {rsi, rdso})) return LCONV_ERR_ALIASING;
+    ConvArgs a{};
+    a.dw = dweight; a.db = dbias; a.K = (int)K; a.C = C; a.B = B; a.N = N; a.silu = flags & LCONV_SHORTCONV_SILU;
+    if (B == 0 || N == 0) {     // no tokens: the state's gradient passes through, the weights have none
+        if (B > 0 && dstate_in && launch_conv_state(dtype, dstate_out, dstate_in, states, stream) != hipSuccess) return LCONV_ERR_HIP;
+        return hip_status(launch_conv_bwd(dtype, a, stream));
+    }
+    TokOperand xo{};
+    Range rdy, rx, rdx;
+    lconv_status_t st;
+    if ((st = tokens(dy, dy_strides, B, N, C, dtype, false, &a.dy, &rdy)) != LCONV_SUCCESS) return st;
+    if ((st = tokens(x, x_strides, B, N, C, dtype, false, &a.x, &rx)) != LCONV_SUCCESS) return st;
+    if ((st = tokens(dx, dx_strides, B, N, C, dtype, true, &xo, &rdx)) != LCONV_SUCCESS) return st;
+    if (!weight) return LCONV_ERR_NULL_POINTER;
+    const Range rw = buffer(weight, C * K, es), rb = buffer(bias, C, es), rl = buffer(lengths, B, 4);
+    if (clash({rdx, rdsi, rdw, rdb}, {rdy, rx, rw, rb, rl, rsi, rdso})) return LCONV_ERR_ALIASING;
+    const ConvPlan p = conv_plan(B, N, C, true);
+    if (dweight || dbias) {
+        const size_t need = lconv_shortconv_bwd_workspace_bytes(B, N, C, K);
+        if (!workspace || workspace_bytes < need) return LCONV_ERR_WORKSPACE;
+        if (!aligned16(workspace)) return LCONV_ERR_MISALIGNED;
+        if (clash({buffer(workspace, (int64_t)need, 1)}, {rdy, rx, rdx, rw, rb, rl, rsi, rdso, rdsi, rdw, rdb})) return LCONV_ERR_ALIASING;
+        a.part = (float*)workspace;
+    }
+    a.w = weight; a.bias = bias; a.state_in = state_in; a.dstate_out = dstate_out; a.lengths = lengths;
+    a.y = dx; a.yb = xo.b; a.yn = xo.n; a.state_out = dstate_in;
+    set_plan(&a, p);
+    return hip_status(launch_conv_bwd(dtype, a, stream));
+}
+
+lconv_status_t lconv_shortconv_step(const void* x, int64_t x_stride, const void* weight, const void* bias, void* state,
+                                    const int32_t* slots, void* y, int64_t y_stride, int64_t B, int64_t C, int64_t K,
+                                    int64_t nslots, int flags, lconv_dtype_t dtype, hipStream_t stream) {
+    if (!dtype_ok(dtype) || (flags & ~LCONV_SHORTCONV_SILU)) return LCONV_ERR_UNSUPPORTED;
+    if (B < 0 || C < 0 || K < 0 || nslots < 0) return LCONV_ERR_INVALID_SHAPE;
+    if (B == 0 || C == 0) return LCONV_SUCCESS;
+    if (!conv_dims_ok(B, 1, C, K)) return LCONV_ERR_UNSUPPORTED;
+    const size_t es = dtype_size(dtype);
+    int64_t states;
+    if ((!slots && nslots < B) || !mul_ok(nslots, (K - 1) * C * (int64_t)es, &states)) return LCONV_ERR_INVALID_SHAPE;
+    ConvStepArgs a{};
+    TokOperand yo{};
+    Range rx, ry;
+    const lconv_strides_t sx{x_stride, 0, 0}, sy{y_stride, 0, 0};
+    lconv_status_t st;
+    if ((st = tokens(x, &sx, B, 1, C, dtype, false, &a.x, &rx)) != LCONV_SUCCESS) return st;
+    if ((st = tokens(y, &sy, B, 1, C, dtype, true, &yo, &ry)) != LCONV_SUCCESS) return st;
+    if (!weight || (!state && nslots > 0)) return LCONV_ERR_NULL_POINTER;
+    if (!aligned16(weight) || !aligned16(bias) || !aligned16(state)) return LCONV_ERR_MISALIGNED;
+    if (clash({ry, buffer(state, states, 1)}, {rx, buffer(weight, C * K, es), buffer(bias, C, es), buffer(slots, B, 4)}))
+        return LCONV_ERR_ALIASING;
+    a.w = weight; a.bias = bias; a.state = state; a.slots = slots; a.y = y; a.yb = yo.b;
+    a.B = B; a.C = C; a.nslots = nslots; a.K = (int)K; a.silu = flags & LCONV_SHORTCONV_SILU;
+    return hip_status(launch_conv_step(dtype, a, stream));
 }
 
 }  // extern "C"

@@ -118,4 +118,58 @@ struct QkArgs {
 hipError_t launch_qknorm_fwd(int dtype, const QkArgs& a, hipStream_t stream);
 hipError_t launch_qknorm_bwd(int dtype, const QkArgs& a, hipStream_t stream);
 
+// ---- short causal convolution ---------------------------------------------------------------------------
+
+constexpr int kConvMaxTaps = 8;
+
+struct ConvArgs {
+    TokOperand x, dy;             // dy: gradients only
+    const void *w, *bias;         // [C][K]; [C] or NULL
+    const void* state_in;         // [B][K-1][C] or NULL: the inputs before the first token, oldest first
+    const void* dstate_out;       // gradients: of the inputs that the call left, or NULL
+    const int32_t* lengths;
+    void* y;                      // gradients: dx
+    int64_t yb, yn;
+    void* state_out;              // [B][K-1][C] or NULL; gradients: dL/dstate_in
+    float *dw, *db;               // [C][K], [C] or NULL
+    float* part;                  // [groups][K + 1][C]: taps, then the bias
+    int64_t B, N, C, run;
+    int K, silu, vec, cgroups, runs, groups;
+};
+
+// How a call is cut: channels to a lane, groups of 64 vec channels, runs of tokens to a wave (never shorter than the K - 1
+// inputs before a run, so that only a row's first run meets its state), workgroups of four runs (gradients: each with a
+// partial sum over the runs that it takes in turn).
+struct ConvPlan {
+    int vec, cgroups, runs, groups;
+    int64_t run;
+};
+inline ConvPlan conv_plan(int64_t B, int64_t N, int64_t C, bool grad) {
+    ConvPlan p{};
+    p.vec = C % 4 == 0 ? 4 : 1;
+    p.cgroups = (int)((C + 64 * p.vec - 1) / (64 * p.vec));
+    p.run = 32;
+    while (p.run > kConvMaxTaps && B * ((N + p.run - 1) / p.run) * p.cgroups < 256 * 8) p.run /= 2;
+    const int64_t runs = (N + p.run - 1) / p.run, groups = (B * runs + 3) / 4, most = (1024 + p.cgroups - 1) / p.cgroups;
+    p.runs = (int)runs;
+    p.groups = (int)(grad && groups > most ? most : groups);
+    return p;
+}
+
+struct ConvStepArgs {
+    TokOperand x;
+    const void *w, *bias;
+    void* state;                  // [nslots][K-1][C]
+    const int32_t* slots;
+    void* y;
+    int64_t yb, B, C, nslots;
+    int K, silu;
+};
+
+hipError_t launch_conv_fwd(int dtype, const ConvArgs& a, hipStream_t stream);
+hipError_t launch_conv_bwd(int dtype, const ConvArgs& a, hipStream_t stream);
+hipError_t launch_conv_step(int dtype, const ConvStepArgs& a, hipStream_t stream);
+// out = in (or zeros), n elements, for calls without tokens
+hipError_t launch_conv_state(int dtype, const void* in, void* out, int64_t n, hipStream_t stream);
+
 }  // namespace lcv

@@ -1,14 +1,10 @@
 // scan_gates.h -- the gates of the linear recurrence h_t = a_t h_{t-1} + m_t sigmoid(i_t) x_t, in fp32.
 #pragma once
 #include "block_kernels.h"
-#include "mixer_io.h"
+#include "token_io.h"
 
 namespace lcv {
 namespace {
-
-__device__ __forceinline__ float fast_rcp(float x) { return __builtin_amdgcn_rcpf(x); }       // 1 ulp
-__device__ __forceinline__ float fast_sqrt(float x) { return __builtin_amdgcn_sqrtf(x); }     // 1 ulp
-__device__ __forceinline__ float sigmoid(float x) { return fast_rcp(1.f + __expf(-x)); }
 
 // A sigmoid s and 1 - s in one register, each to its own size: the smaller of the two, negative where that is 1 - s.
 __device__ __forceinline__ float folded_sigmoid(float x) {
@@ -53,38 +49,6 @@ __device__ __forceinline__ Decay rounded(Decay run) { return Decay{run.d <= 0.5f
 
 // sqrt(1 - a^2)
 __device__ __forceinline__ float norm_of(Decay g) { return fast_sqrt(g.d * (1.f + g.a)); }
-
-// V channels of one token as they are stored, and as fp32
-template <int IO, int V> struct RawV {
-    typename Elem<IO>::T e[V];
-};
-template <int IO, int V> __device__ __forceinline__ RawV<IO, V> load_raw_v(const void* base, int64_t token, uint32_t lane) {
-    RawV<IO, V> r;
-    __builtin_memcpy(&r, (const typename Elem<IO>::T*)base + token + lane, sizeof(r));
-    return r;
-}
-template <int IO, int V> __device__ __forceinline__ void widen(const RawV<IO, V>& r, float* x) {
-    if constexpr (IO == CT_F32) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) x[v] = r.e[v];
-    } else if constexpr (V == 2) {
-        uint32_t w;
-        __builtin_memcpy(&w, &r, 4);
-        x[0] = unpack_lo<IO>(w);
-        x[1] = unpack_hi<IO>(w);
-    } else {
-        x[0] = unpack_lo<IO>(r.e[0]);
-    }
-}
-template <int IO, int V> __device__ __forceinline__ void store_v(void* base, int64_t token, uint32_t lane, const float* x) {
-    typename Elem<IO>::T* p = (typename Elem<IO>::T*)base + token + lane;
-    if constexpr (IO == CT_F32) {
-        __builtin_memcpy(p, x, 4 * V);
-    } else {
-        const uint32_t w = pack2<IO>(x[0], V == 2 ? x[V - 1] : 0.f);
-        __builtin_memcpy(p, &w, 2 * V);
-    }
-}
 
 }  // namespace
 }  // namespace lcv

@@ -141,12 +141,18 @@ __global__ void __launch_bounds__(64 * kScanWaves) scan_fwd_kernel(ScanArgs a) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         rate[v] = a.rate ? a.rate[w.c + v] : 0.f;
-        h[v] = !STATES && a.state_in ? a.state_in[sc + v] : 0.f;
+        h[v] = (STATES ? w.seg == a.nseg - 1 : a.nseg == 1) && a.state_in ? a.state_in[sc + v] : 0.f;
         all[v] = Decay{1.f, 0.f};
     }
+    // Nothing follows the last segment: its place in the workspace keeps the state that enters the row, which the main pass
+    // takes from there, since its last segment may write another state over it before the first one begins.
     if constexpr (STATES) {
-        if (w.seg == a.nseg - 1) return;       // nothing follows it
-    } else {
+        if (w.seg == a.nseg - 1) {
+            if (w.wave == 0) leave_segment<V>(h, all, a, w);
+            return;
+        }
+    } else if (a.nseg > 1) {
+        join_segment<V>(h, a, w, a.nseg - 1);
         for (int k = 0; k < w.seg; ++k) join_segment<V>(h, a, w, k);
     }
     const int64_t mine = (int64_t)w.wave * kScanTokens;
@@ -245,13 +251,17 @@ __global__ void __launch_bounds__(64 * kScanWaves) scan_bwd_kernel(ScanArgs a) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         rate[v] = a.rate ? a.rate[w.c + v] : 0.f;
-        carry[v] = !REACH && a.state_in ? a.state_in[sc + v] : 0.f;
+        carry[v] = (REACH ? w.seg == 0 : a.nseg == 1) && a.state_in ? a.state_in[sc + v] : 0.f;
         all[v] = Decay{1.f, 0.f};
         drate[v] = 0.f;
     }
-    if constexpr (REACH) {
-        if (w.seg == 0) return;
-    } else {
+    if constexpr (REACH) {      // as in the forward pass, from the other end
+        if (w.seg == 0) {
+            if (w.wave == 0) leave_segment<V>(carry, all, a, w);
+            return;
+        }
+    } else if (a.nseg > 1) {
+        join_segment<V>(carry, a, w, 0);
         for (int k = a.nseg - 1; k > w.seg; --k) join_segment<V>(carry, a, w, k);
     }
     const int64_t mine = (int64_t)w.wave * kScanTokens;

@@ -9,7 +9,8 @@ integer device pointers.  ``filter_fft``, ``fftconv``, ``fftconv_partial``, ``ff
 ``fftconv_bwd``, ``fftconv_save``, ``filter_fft2d`` and ``fftconv2d`` are convenience wrappers over torch
 tensors, and so are the mixer operators ``linear_attention``, ``linear_attention_bwd``,
 ``linear_attention_step``, ``rotary`` (with ``rotary_frequencies``), ``layer_norm``,
-``layer_norm_bwd``, ``qk_norm_rotary``, ``qk_norm_rotary_bwd``, ``gated_scan``, ``gated_scan_bwd`` and ``gated_scan_step``, which also take strided views whose last
+``layer_norm_bwd``, ``qk_norm_rotary``, ``qk_norm_rotary_bwd``, ``gated_scan``, ``gated_scan_bwd``,
+``gated_scan_step``, ``short_conv``, ``short_conv_bwd`` and ``short_conv_step``, which also take strided views whose last
 dimension is contiguous.
 """
 from __future__ import annotations
@@ -120,6 +121,10 @@ def load(path: str = LIB_PATH):
         "lconv_qknorm_rotary_bwd_workspace_bytes": (sz, [i64] * 6),
         "lconv_qknorm_rotary_bwd": (i, [vp, sp, vp, sp, vp, sp, vp, sp, vp, vp, vp, i64, vp, f32, f32, vp, sp, vp, sp, vp, vp]
                                     + [i64] * 6 + [i, i, vp, sz, vp]),
+        "lconv_shortconv_fwd": (i, [vp, sp, vp, vp, vp, vp, vp, sp, vp] + [i64] * 4 + [i, i, vp]),
+        "lconv_shortconv_bwd_workspace_bytes": (sz, [i64] * 4),
+        "lconv_shortconv_bwd": (i, [vp, sp, vp, sp, vp, vp, vp, vp, vp, vp, sp, vp, vp, vp] + [i64] * 4 + [i, i, vp, sz, vp]),
+        "lconv_shortconv_step": (i, [vp, i64, vp, vp, vp, vp, vp, i64] + [i64] * 4 + [i, i, vp]),
         "lconv_status_string": (ctypes.c_char_p, [i]),
         "lconv_abi_version": (i, []),
         "lconv_release": (i, []),
@@ -391,6 +396,24 @@ def lconv_qknorm_rotary_bwd(dyq, dyqs, dyk, dyks, q, qs, k, ks, q_weight, k_weig
     return load().lconv_qknorm_rotary_bwd(dyq, dyqs, dyk, dyks, q, qs, k, ks, q_weight, k_weight, positions, pos_stride,
                                           inv_freq, magnitude, eps, dq, dqs, dk, dks, dq_weight, dk_weight, B, H, G, N, D, rot,
                                           flags, dtype, workspace, workspace_bytes, stream)
+
+
+def lconv_shortconv_fwd(x, xs, weight, bias, state_in, lengths, y, ys, state_out, B, N, C, K, flags, dtype, stream):
+    return load().lconv_shortconv_fwd(x, xs, weight, bias, state_in, lengths, y, ys, state_out, B, N, C, K, flags, dtype, stream)
+
+
+def lconv_shortconv_bwd_workspace_bytes(B, N, C, K):
+    return load().lconv_shortconv_bwd_workspace_bytes(B, N, C, K)
+
+
+def lconv_shortconv_bwd(dy, dys, x, xs, weight, bias, state_in, dstate_out, lengths, dx, dxs, dweight, dbias, dstate_in, B, N, C,
+                        K, flags, dtype, workspace, workspace_bytes, stream):
+    return load().lconv_shortconv_bwd(dy, dys, x, xs, weight, bias, state_in, dstate_out, lengths, dx, dxs, dweight, dbias,
+                                      dstate_in, B, N, C, K, flags, dtype, workspace, workspace_bytes, stream)
+
+
+def lconv_shortconv_step(x, xs, weight, bias, state, slots, y, ys, B, C, K, nslots, flags, dtype, stream):
+    return load().lconv_shortconv_step(x, xs, weight, bias, state, slots, y, ys, B, C, K, nslots, flags, dtype, stream)
 
 
 def lconv_abi_version():
@@ -1432,3 +1455,98 @@ def _pool(name, state, dims, slots, B):
     elif state.shape[0] < B:
         raise ValueError(f"{B} rows and {state.shape[0]} states: slots are needed")
     return state.shape[0]
+
+
+# ---- short convolution --------------------------------------------------------------------------
+
+SHORTCONV_SILU = 1
+
+
+def _conv_operands(x, weight, bias, activation, dims):
+    """(dtype code, flags, K, strides of x), checked."""
+    torch = _torch()
+    if not isinstance(x, torch.Tensor) or x.dim() != dims:
+        raise ValueError(f"x must be a {dims}-D torch tensor")
+    dt = _float_dtype("x", x)
+    if activation not in (None, "silu"):
+        raise ValueError(f"unknown activation {activation!r}; there are None and 'silu'")
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("weight must be a 2-D torch tensor")
+    K = weight.shape[1]
+    if not 2 <= K <= 8:
+        raise ValueError(f"weight has {K} taps; supported: 2 to 8")
+    C = x.shape[-1]
+    _need("weight", weight, (C, K), x.dtype)
+    _need("bias", bias, (C,), x.dtype, optional=True)
+    return dt, SHORTCONV_SILU if activation else 0, K, _tokens("x", x, x.shape, x.dtype)
+
+
+def short_conv(x, weight, bias=None, activation=None, state=None, lengths=None, need_state=True, out=None, state_out=None,
+               stream=None):
+    """Causal convolution along the tokens of x [B, N, C], one filter weight[c] of K taps (2 to 8, the last one on the token
+    itself) per channel, a bias [C] and, with activation "silu", p sigmoid(p), all in x's dtype.  state: [B, K - 1, C] in x's
+    dtype, the inputs before the first token, oldest first.  lengths: int32 [B], tokens past a row's length count for nothing
+    and give y = 0.  Returns (y, the last K - 1 inputs before each row's end; None without need_state).  state_out may be
+    `state` itself."""
+    torch = _torch()
+    dt, flags, K, xs = _conv_operands(x, weight, bias, activation, 3)
+    B, N, C = x.shape
+    _need("state", state, (B, K - 1, C), x.dtype, optional=True)
+    _need("state_out", state_out, (B, K - 1, C), x.dtype, optional=True)
+    _lengths(lengths, B)
+    dev = _same_gpu("x weight bias state lengths out state_out", (x, weight, bias, state, lengths, out, state_out))
+    ctx, st = _at(dev, stream)
+    with ctx:
+        y, ys = _token_output("out", out, x)
+        if state_out is None and need_state:
+            state_out = torch.empty((B, K - 1, C), dtype=x.dtype, device=dev)
+        _check(lconv_shortconv_fwd(_ptr(x), xs, _ptr(weight), _ptr(bias), _ptr(state), _ptr(lengths), _ptr(y), ys, _ptr(state_out),
+                                   B, N, C, K, flags, dt, st), "lconv_shortconv_fwd")
+    return y, state_out
+
+
+ShortConvGrads = namedtuple("ShortConvGrads", "dx dweight dbias dstate")
+
+
+def short_conv_bwd(dy, x, weight, bias=None, activation=None, state=None, dstate=None, lengths=None, need_dweight=True,
+                   stream=None):
+    """Gradients of short_conv given dy [B, N, C] and, where the state it returned was used, dstate [B, K - 1, C], from its
+    inputs.  Returns (dx in x's dtype, dweight [C, K] and dbias [C] in float32, dstate in x's dtype, the gradient of the state
+    that entered); dweight and dbias are None without need_dweight, dbias without a bias, dstate without a state."""
+    torch = _torch()
+    dt, flags, K, xs = _conv_operands(x, weight, bias, activation, 3)
+    B, N, C = x.shape
+    dys = _tokens("dy", dy, x.shape, x.dtype)
+    _need("state", state, (B, K - 1, C), x.dtype, optional=True)
+    _need("dstate", dstate, (B, K - 1, C), x.dtype, optional=True)
+    _lengths(lengths, B)
+    dev = _same_gpu("dy x weight bias state dstate lengths", (dy, x, weight, bias, state, dstate, lengths))
+    ctx, st = _at(dev, stream)
+    with ctx:
+        dx, dxs = _token_output("dx", None, x)
+        dw = torch.empty((C, K), dtype=torch.float32, device=dev) if need_dweight else None
+        db = torch.empty((C,), dtype=torch.float32, device=dev) if need_dweight and bias is not None else None
+        ds = None if state is None else torch.empty_like(state)
+        wsb = lconv_shortconv_bwd_workspace_bytes(B, N, C, K) if need_dweight else 0
+        ws = torch.empty(wsb, dtype=torch.uint8, device=dev) if wsb else None
+        _check(lconv_shortconv_bwd(_ptr(dy), dys, _ptr(x), xs, _ptr(weight), _ptr(bias), _ptr(state), _ptr(dstate), _ptr(lengths),
+                                   _ptr(dx), dxs, _ptr(dw), _ptr(db), _ptr(ds), B, N, C, K, flags, dt, _ptr(ws), wsb, st),
+               "lconv_shortconv_bwd")
+    return ShortConvGrads(dx, dw, db, ds)
+
+
+def short_conv_step(x, weight, state, bias=None, activation=None, slots=None, out=None, stream=None):
+    """One token of every sequence: x [B, C]; the inputs [slots, K - 1, C] in x's dtype move on by one in place.  slots: int32
+    [B], the state that each row continues (outside the states: an idle row, y = 0); without it row b has state b.  No two rows
+    may have the same slot.  Returns y [B, C]."""
+    dt, flags, K, xs = _conv_operands(x, weight, bias, activation, 2)
+    B, C = x.shape
+    nslots = _pool("state", state, 3, slots, B)
+    _need("state", state, (nslots, K - 1, C), x.dtype)
+    dev = _same_gpu("x weight bias state slots out", (x, weight, bias, state, slots, out))
+    ctx, st = _at(dev, stream)
+    with ctx:
+        y, ys = _token_output("out", out, x)
+        _check(lconv_shortconv_step(_ptr(x), xs, _ptr(weight), _ptr(bias), _ptr(state), _ptr(slots), _ptr(y), ys, B, C, K, nslots,
+                                    flags, dt, st), "lconv_shortconv_step")
+    return y

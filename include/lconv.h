@@ -643,7 +643,7 @@ lconv_status_t lconv_qknorm_rotary_bwd(const void* dyq, const lconv_strides_t* d
                                        int64_t rot, int flags, lconv_dtype_t dtype, void* workspace, size_t workspace_bytes,
                                        hipStream_t stream);
 
-/* ---- operators of a recurrent block: gated linear recurrence ------------------------------------ */
+/* ---- operators of a recurrent block: gated linear recurrence, short convolution ------------------ */
 
 /*
  * Gated linear recurrence: for every channel of its own, with decays that follow the input,
@@ -715,6 +715,51 @@ lconv_status_t lconv_gated_scan_step(const void* x, int64_t x_stride, const void
                                      int64_t input_gate_stride, const float* rate, float* state, const int32_t* slots,
                                      void* y, int64_t y_stride, int64_t B, int64_t C, int64_t nslots, int flags,
                                      lconv_dtype_t dtype, hipStream_t stream);
+
+/*
+ * Short causal convolution along the tokens, one filter of K taps per channel (what stands before a recurrence, or on the
+ * projections that a gated long convolution takes):
+ *   p_t = bias[c] + sum_{j<K} weight[c][j] x_{t-K+1+j},   y = p, or with LCONV_SHORTCONV_SILU p sigmoid(p);  y = 0 for t >= len[b]
+ *   x, y       [B][N][C] dtype, channels contiguous, strides as for lconv_gated_scan_fwd
+ *   weight     [C][K] dtype;  bias [C] dtype or NULL (zeros)
+ *   state_in   [B][K-1][C] dtype, the inputs before the first token, oldest first, or NULL (zeros);  state_out the same shape or
+ *              NULL: the last K - 1 inputs before len[b], those of state_in where the row is shorter; the two may be one buffer
+ *   lengths    [B] int32, device, or NULL (every row N long); taken as min(max(len, 0), N)
+ * Sums are fp32; nothing past len[b] is read into a result; a value that is not finite reaches its own channel's K tokens (0 times
+ * it is a NaN).  Supported: K in [2, 8]; N < 2^31, B and C up to 2^24, every dtype, launches of fewer than 2^32 threads.
+ */
+#define LCONV_SHORTCONV_MAX_TAPS 8
+#define LCONV_SHORTCONV_SILU     1
+lconv_status_t lconv_shortconv_fwd(const void* x, const lconv_strides_t* x_strides, const void* weight, const void* bias,
+                                   const void* state_in, const int32_t* lengths, void* y, const lconv_strides_t* y_strides,
+                                   void* state_out, int64_t B, int64_t N, int64_t C, int64_t K, int flags, lconv_dtype_t dtype,
+                                   hipStream_t stream);
+
+/*
+ * Gradients of lconv_shortconv_fwd, given dy and dstate_out = dL/dstate_out (NULL: zeros), from its inputs.  With dp = dy, or
+ * dy sigmoid(p) (1 + p (1 - sigmoid(p))):
+ *   dx_s = sum_j weight[c][j] dp_{s+K-1-j} (and dstate_out where token s is among the inputs that were left);
+ *   dweight[c][j] = sum_{b,t} dp_t x_{t-K+1+j};  dbias[c] = sum_{b,t} dp_t;  dstate_in: dx of the inputs before the first token
+ *   dx         [B][N][C] dtype, written (zeros past a row's length);  dstate_in [B][K-1][C] dtype, written, or NULL
+ *   dweight    [C][K] fp32, dbias [C] fp32, written, or NULL
+ *   workspace  lconv_shortconv_bwd_workspace_bytes(B, N, C, K) bytes (partial sums, added in a fixed order: results repeat bit
+ *              for bit); may be NULL when neither dweight nor dbias is wanted
+ * Outputs meet no input and each other.
+ */
+size_t lconv_shortconv_bwd_workspace_bytes(int64_t B, int64_t N, int64_t C, int64_t K);
+lconv_status_t lconv_shortconv_bwd(const void* dy, const lconv_strides_t* dy_strides, const void* x,
+                                   const lconv_strides_t* x_strides, const void* weight, const void* bias, const void* state_in,
+                                   const void* dstate_out, const int32_t* lengths, void* dx, const lconv_strides_t* dx_strides,
+                                   float* dweight, float* dbias, void* dstate_in, int64_t B, int64_t N, int64_t C, int64_t K,
+                                   int flags, lconv_dtype_t dtype, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * One token of every sequence of a serving batch: y from the pool's K - 1 inputs and x, which then move on by one in place.
+ *   x, y   [B][C] dtype, rows *_stride elements apart;  state [nslots][K-1][C] dtype;  slots as for lconv_linattn_step
+ */
+lconv_status_t lconv_shortconv_step(const void* x, int64_t x_stride, const void* weight, const void* bias, void* state,
+                                    const int32_t* slots, void* y, int64_t y_stride, int64_t B, int64_t C, int64_t K,
+                                    int64_t nslots, int flags, lconv_dtype_t dtype, hipStream_t stream);
 
 /* ---- misc ------------------------------------------------------------------------------- */
 

@@ -360,3 +360,29 @@ def test_against_differences(lc):
         got = float((grad.double() * d.double()).sum())
         say(f"   argument {k}: {got:.5f} against {want:.5f} of {terms:.1f}")
         assert abs(got - want) <= 2e-4 * terms
+
+
+@pytest.mark.parametrize("N", [60, 3000])
+def test_states_in_place(lc, N):
+    """One buffer for the state that enters and the one that leaves, in one piece and cut into segments, many rows: the same
+    bits as with two."""
+    import torch
+    say(f"[scan states in place] {N}")
+    rng = np.random.default_rng(709)
+    B, C = 2, 2000
+    x, z, _, _ = cuda(*inputs(rng, B, N, C, "bf16", "sigmoid", False))
+    assert (lc.lconv_gated_scan_workspace_bytes(B, N, C) > 0) == (N > 60)
+    s, dy = host(rng, (B, C), "f32").cuda(), host(rng, (B, N, C), "bf16").cuda()
+    want = lc.gated_scan(x, z, state=s, need_marks=True)
+    ds = lc.gated_scan_bwd(dy, x, z, want.marks, dstate=s)
+    st = torch.cuda.current_stream().cuda_stream
+    ws = torch.empty(lc.lconv_gated_scan_bwd_workspace_bytes(B, N, C, 1) or 16, dtype=torch.uint8, device="cuda")
+    for _ in range(5):
+        t = s.clone()
+        got = lc.gated_scan(x, z, state=t, state_out=t)
+        assert bool((got.y == want.y).all()) and bool((t == want.state).all())
+        t, dx, dz = s.clone(), torch.empty_like(x), torch.empty_like(x)
+        assert lc.lconv_gated_scan_bwd(dy.data_ptr(), None, x.data_ptr(), None, z.data_ptr(), None, None, None, None,
+                                       want.marks.data_ptr(), t.data_ptr(), None, dx.data_ptr(), None, dz.data_ptr(), None, None,
+                                       None, None, t.data_ptr(), B, N, C, 1, lc.BF16, ws.data_ptr(), ws.numel(), st) == 0
+        assert bool((t == ds.dstate).all()) and bool((dx == ds.dx).all()) and bool((dz == ds.dz).all())

@@ -24,7 +24,8 @@ HIP_SOURCES = ["fused1d_conv.hip", "fused1d_adj.hip", "fused1d_part.hip", "fused
                "fused1d.hip", "bwd1d.hip", "multipass.hip", "fftconv2d.hip", "fftconv3d.hip",
                "stage.hip", "ssm.hip", "noalloc.hip", "colmx.hip", "butterfly.hip", "fused1d_lbf.hip",
                "linattn.hip", "linattn_f32.hip", "linattn_f16.hip", "linattn_bf16.hip", "linattn_bf16_wide.hip", "linattn_tan.hip",
-               "rotary.hip", "layernorm.hip", "qknorm.hip", "scan.hip", "scan_f32.hip", "scan_f16.hip", "scan_bf16.hip", "shortconv.hip"]
+               "rotary.hip", "layernorm.hip", "qknorm.hip", "scan.hip", "scan_f32.hip", "scan_f16.hip", "scan_bf16.hip",
+               "scan_grad_f32.hip", "scan_grad_f16.hip", "scan_grad_bf16.hip", "shortconv.hip"]
 CPP_SOURCES = ["plan.cpp", "lconv_api.cpp", "mixer_api.cpp", "block_api.cpp"]
 COMMON = ["-O3", "-fPIC", "-std=c++17", "-I", INCLUDE, "-I", CSRC, "-Wall", "-Wno-unused-function"]
 DEVICE = ["--offload-arch=" + ARCH, "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",

@@ -51,12 +51,13 @@ bool scan_flags_ok(int flags) {
 }
 
 // sizes that the kernels' indices hold: channels and segments in 32 bits, marks and states in 64
-bool scan_dims_ok(int64_t B, int64_t N, int64_t C) {
+bool scan_dims_ok(int64_t B, int64_t N, int64_t C, lconv_dtype_t dtype) {
     int64_t t;
     if (N >= ((int64_t)1 << 31) || C > ((int64_t)1 << 24) || B > ((int64_t)1 << 24) || !mul_ok(B, C, &t)) return false;
-    if (!mul_ok(t, (N + kScanTile - 1) / kScanTile, &t) || t > INT64_MAX / 16) return false;
-    const ScanPlan p = scan_plan(B, N > 0 ? N : 1, C);
-    return B * p.cblocks * p.nseg <= kMaxGrid / 2 && B * ((C + 511) / 256) <= kMaxGrid;     // 512 threads; single tokens
+    if (!mul_ok(t, (N + kScanMark - 1) / kScanMark, &t) || t > INT64_MAX / 16) return false;
+    // workgroups of 1024 threads (gradients: 512), and single tokens
+    const ScanPlan p = scan_plan(B, N > 0 ? N : 1, C, dtype, false), g = scan_plan(B, N > 0 ? N : 1, C, dtype, true);
+    return B * p.cblocks * p.nseg <= kMaxGrid / 4 && B * g.cblocks * g.nseg <= kMaxGrid / 2 && B * ((C + 511) / 256) <= kMaxGrid;
 }
 
 size_t seg_bytes(const ScanPlan& p, int64_t B, int64_t C) {
@@ -72,18 +73,18 @@ void set_plan(ScanArgs* a, const ScanPlan& p) {
 extern "C" {
 
 size_t lconv_gated_scan_marks_bytes(int64_t B, int64_t N, int64_t C) {
-    if (B <= 0 || N <= 0 || C <= 0 || !scan_dims_ok(B, N, C)) return 0;
-    return (size_t)(B * ((N + kScanTile - 1) / kScanTile)) * (size_t)C * 4;
+    if (B <= 0 || N <= 0 || C <= 0 || !scan_dims_ok(B, N, C, LCONV_F32)) return 0;      // whose blocks are the most
+    return (size_t)(B * ((N + kScanMark - 1) / kScanMark)) * (size_t)C * 4;
 }
 
-size_t lconv_gated_scan_workspace_bytes(int64_t B, int64_t N, int64_t C) {
-    if (B <= 0 || N <= 0 || C <= 0 || !scan_dims_ok(B, N, C)) return 0;
-    return seg_bytes(scan_plan(B, N, C), B, C);
+size_t lconv_gated_scan_workspace_bytes(int64_t B, int64_t N, int64_t C, lconv_dtype_t dtype) {
+    if (!dtype_ok(dtype) || B <= 0 || N <= 0 || C <= 0 || !scan_dims_ok(B, N, C, dtype)) return 0;
+    return seg_bytes(scan_plan(B, N, C, dtype, false), B, C);
 }
 
-size_t lconv_gated_scan_bwd_workspace_bytes(int64_t B, int64_t N, int64_t C, int flags) {
-    if (B <= 0 || N <= 0 || C <= 0 || !scan_flags_ok(flags) || !scan_dims_ok(B, N, C)) return 0;
-    const ScanPlan p = scan_plan(B, N, C);
+size_t lconv_gated_scan_bwd_workspace_bytes(int64_t B, int64_t N, int64_t C, int flags, lconv_dtype_t dtype) {
+    if (!dtype_ok(dtype) || B <= 0 || N <= 0 || C <= 0 || !scan_flags_ok(flags) || !scan_dims_ok(B, N, C, dtype)) return 0;
+    const ScanPlan p = scan_plan(B, N, C, dtype, true);
     return seg_bytes(p, B, C) + ((flags & 3) == LCONV_GATE_RATE ? round256((size_t)(B * p.nseg) * (size_t)C * 4) : 0);
 }
 
@@ -96,7 +97,7 @@ lconv_status_t lconv_gated_scan_fwd(const void* x, const lconv_strides_t* x_stri
     if (!dtype_ok(dtype) || !scan_flags_ok(flags)) return LCONV_ERR_UNSUPPORTED;
     if (B < 0 || N < 0 || C < 0) return LCONV_ERR_INVALID_SHAPE;
     if (B == 0 || C == 0) return LCONV_SUCCESS;
-    if (!scan_dims_ok(B, N, C)) return LCONV_ERR_UNSUPPORTED;
+    if (!scan_dims_ok(B, N, C, dtype)) return LCONV_ERR_UNSUPPORTED;
     if (!aligned16(state_in) || !aligned16(state_out) || !aligned16(marks) || !aligned16(rate)) return LCONV_ERR_MISALIGNED;
     const Range rsi = buffer(state_in, B * C, 4), rso = buffer(state_out, B * C, 4);
     if (state_in != state_out && overlap(rsi, rso)) return LCONV_ERR_ALIASING;
@@ -114,7 +115,7 @@ lconv_status_t lconv_gated_scan_fwd(const void* x, const lconv_strides_t* x_stri
     const Range rr = buffer(rated ? rate : nullptr, C, 4), rl = buffer(lengths, B, 4);
     const Range rm = buffer(marks, (int64_t)lconv_gated_scan_marks_bytes(B, N, C), 1);
     if (clash({ry, rso, rm}, {rx, rz, ri, rr, rl}) || overlap(ry, rsi) || overlap(rm, rsi)) return LCONV_ERR_ALIASING;
-    const ScanPlan p = scan_plan(B, N, C);
+    const ScanPlan p = scan_plan(B, N, C, dtype, false);
     const size_t need = seg_bytes(p, B, C);
     if (need > 0) {
         if (!workspace || workspace_bytes < need) return LCONV_ERR_WORKSPACE;
@@ -139,7 +140,7 @@ lconv_status_t lconv_gated_scan_bwd(const void* dy, const lconv_strides_t* dy_st
     if (!dtype_ok(dtype) || !scan_flags_ok(flags)) return LCONV_ERR_UNSUPPORTED;
     if (B < 0 || N < 0 || C < 0) return LCONV_ERR_INVALID_SHAPE;
     if (C == 0) return LCONV_SUCCESS;
-    if (!scan_dims_ok(B, N, C)) return LCONV_ERR_UNSUPPORTED;
+    if (!scan_dims_ok(B, N, C, dtype)) return LCONV_ERR_UNSUPPORTED;
     const bool rated = (flags & 3) == LCONV_GATE_RATE;
     if (!rated) drate = nullptr;
     if (!aligned16(marks) || !aligned16(rate) || !aligned16(drate) || !aligned16(dstate_in) || !aligned16(dstate_out))
@@ -169,8 +170,8 @@ lconv_status_t lconv_gated_scan_bwd(const void* dy, const lconv_strides_t* dy_st
     const Range rm = buffer(marks, (int64_t)lconv_gated_scan_marks_bytes(B, N, C), 1);
     if (clash({rdx, rdz, rdi, rsi, rdr}, {rdy, rx, rz, ri, rr, rl, rm}) || overlap(rdx, rso) || overlap(rdz, rso) || overlap(rdi, rso))
         return LCONV_ERR_ALIASING;
-    const ScanPlan p = scan_plan(B, N, C);
-    const size_t need = lconv_gated_scan_bwd_workspace_bytes(B, N, C, flags);
+    const ScanPlan p = scan_plan(B, N, C, dtype, true);
+    const size_t need = lconv_gated_scan_bwd_workspace_bytes(B, N, C, flags, dtype);
     if (need > 0) {
         if (!workspace || workspace_bytes < need) return LCONV_ERR_WORKSPACE;
         if (!aligned16(workspace)) return LCONV_ERR_MISALIGNED;
@@ -192,7 +193,7 @@ lconv_status_t lconv_gated_scan_step(const void* x, int64_t x_stride, const void
     if (!dtype_ok(dtype) || !scan_flags_ok(flags)) return LCONV_ERR_UNSUPPORTED;
     if (B < 0 || C < 0 || nslots < 0) return LCONV_ERR_INVALID_SHAPE;
     if (B == 0 || C == 0) return LCONV_SUCCESS;
-    if (!scan_dims_ok(B, 1, C)) return LCONV_ERR_UNSUPPORTED;
+    if (!scan_dims_ok(B, 1, C, dtype)) return LCONV_ERR_UNSUPPORTED;
     int64_t states;
     if ((!slots && nslots < B) || !mul_ok(nslots, 4 * C, &states)) return LCONV_ERR_INVALID_SHAPE;
     ScanStepArgs a{};

@@ -16,8 +16,11 @@ struct TokOperand {
 
 // ---- gated linear recurrence ------------------------------------------------------------------------
 
-// Tokens of a wave's turn, waves of a workgroup, tokens of a tile: a tile's first state is a mark.
-constexpr int kScanTokens = 8, kScanWaves = 8, kScanTile = kScanTokens * kScanWaves;
+// Tokens of a wave's turn; the most waves of a workgroup (one or two channels to a lane; the gradient's registers leave room
+// for eight); tokens from one mark to the next, a tile of eight waves.
+constexpr int kScanTokens = 8, kScanMark = 64;
+constexpr int scan_waves(int vec) { return vec == 2 ? 8 : 16; }
+constexpr int kScanGradWaves = 8;
 
 struct ScanArgs {
     TokOperand x, z, i, dy;       // i.p NULL: no input gate; dy: gradients only
@@ -30,7 +33,7 @@ struct ScanArgs {
     int64_t dxb, dxn, dzb, dzn, dib, din;
     float* state_out;             // [B][C] or NULL; gradients: dL/dstate_in
     float* marks;                 // [B][tiles][C]: forward written or NULL, gradients read
-    float* seg;                   // [B][nseg][3][C]: decays, their residues and sums of the segments (nseg > 1)
+    float* seg;                   // [B][nseg][3][C]: decays (in two) and sums of the segments (nseg > 1)
     float* part;                  // [B nseg][C]: the rate's gradient, partial sums
     float* drate;
     int64_t B, N, C, seg_len;
@@ -43,19 +46,34 @@ struct ScanPlan {
     int vec, cblocks, nseg, waves;
     int64_t seg_len;
 };
-inline ScanPlan scan_plan(int64_t B, int64_t N, int64_t C) {
+// Two channels to a lane move 256 bytes of a 16-bit row at a time, which memory gives 10 % faster than 128, but leave half as many
+// workgroups; sixteen waves fill a compute unit that has one workgroup.  Calls of few rows go by segments, which read everything
+// twice but for y.  Measured (bf16, every input, us; channels to a lane, waves, segments):
+//   8 x 2048 x 4096    2, 8, 1: 114    1, 8, 1: 126    1, 16, 1: 123    2, 8, 16: 95 + 132
+//   16 x 2048 x 1024   1, 16, 1: 53    1, 8, 1: 63     2, 8, 4: 88
+//   4 x 2048 x 2048    1, 16, 1: 52    2, 8, 8: 52     2, 8, 1: 98
+//   2 x 2048 x 2048    2, 8, 8: 34     1, 16, 1: 51
+//   1 x 65536 x 4096   2, 8, 16: 638   1, 8, 16: 700   1, 16, 1: 1464
+//   1 x 777 x 333      1, 8, 8: 15     1, 16, 1: 24
+//   16 x 300 x 2048    1, 8, 1: 20     1, 16, 1: 26
+// Gradients: 4 x 2048 x 2048 in 1, 2, 4 segments 95, 77, 78; 3 x 1001 x 1000 in 1, 4, 8: 53, 28, 31; 1 x 65536 x 4096 in 1, 4,
+// 8, 16: 2870, 1140, 1043, 1050.
+inline ScanPlan scan_plan(int64_t B, int64_t N, int64_t C, lconv_dtype_t dtype, bool grad) {
     ScanPlan p{};
-    const int64_t tiles = (N + kScanTile - 1) / kScanTile;
-    p.vec = C % 2 == 0 && B * ((C + 127) / 128) >= 256 ? 2 : 1;
+    const int64_t ones = B * ((C + 63) / 64), twos = B * ((C + 127) / 128);      // rows of one and of two channels to a lane
+    const bool pairs = !grad && dtype != LCONV_F32 && C % 2 == 0, cut = ones <= (grad ? 128 : 96) && N > 256;
+    p.vec = pairs && (cut || twos >= 256) ? 2 : 1;
     p.cblocks = (int)((C + 64 * p.vec - 1) / (64 * p.vec));
     const int64_t rows = B * p.cblocks;
+    p.waves = p.vec == 2 || grad || cut || rows >= 512 ? 8 : 16;
+    const int64_t tile = p.waves * kScanTokens, tiles = (N + tile - 1) / tile;
     int64_t nseg = 1;
-    if (rows <= 128)
-        while (nseg * 2 * rows <= 1024 && nseg * 4 <= tiles) nseg *= 2;
+    if (cut)
+        while (nseg * 2 * rows <= (grad ? 256 : 512) && nseg * 2 <= tiles) nseg *= 2;
     const int64_t per = (tiles + nseg - 1) / nseg;
-    p.seg_len = per * kScanTile;
+    p.seg_len = per * tile;
     p.nseg = (int)((N + p.seg_len - 1) / p.seg_len);
-    p.waves = N >= kScanTile ? kScanWaves : (int)((N + kScanTokens - 1) / kScanTokens);
+    if (N < tile) p.waves = (int)((N + kScanTokens - 1) / kScanTokens);
     return p;
 }
 

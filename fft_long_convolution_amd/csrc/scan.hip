@@ -40,12 +40,12 @@ template <int IO, int V, bool GATED> __global__ void __launch_bounds__(256) scan
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const Decay k = a.gate == LCONV_GATE_SIGMOID ? decay_of_logit(z[v])
-                          : a.gate == LCONV_GATE_LOG     ? decay_of_log(z[v])
-                                                         : decay_of_log(-a.rate[c + v] * sigmoid(z[v]));
-            const float m = a.mix == LCONV_MIX_NORM ? norm_of(k) : a.mix == LCONV_MIX_CONVEX ? k.d : 1.f;
+                          : a.gate == LCONV_GATE_LOG     ? decay_of_log2(kLog2e * z[v])
+                                                         : decay_of_log2(-kLog2e * a.rate[c + v] * sigmoid(z[v]));
+            const float m = a.mix == LCONV_MIX_NORM ? norm_of(k) : a.mix == LCONV_MIX_CONVEX ? loss_of(k) : 1.f;
             float u = m * x[v];
             if constexpr (GATED) u *= sigmoid(g[v]);
-            y[v] = moved(k.a, residue(k), h[v], u);
+            y[v] = moved(k, h[v], u);
         }
         __builtin_memcpy(state, y, sizeof(y));
     }

@@ -1,8 +1,7 @@
-// scan_bf16.hip -- the gated linear recurrence and its gradients, bf16 data.
+// scan_bf16.hip -- the gated linear recurrence, bf16 data.
 #include "scan_kernels.h"
 #include "scan_launch.h"
 
 namespace lcv {
 hipError_t launch_scan_fwd_bf16(const ScanArgs& a, hipStream_t stream) { return scan_fwd<CT_BF16>(a, stream); }
-hipError_t launch_scan_bwd_bf16(const ScanArgs& a, hipStream_t stream) { return scan_bwd<CT_BF16>(a, stream); }
 }  // namespace lcv

@@ -1,8 +1,7 @@
-// scan_f32.hip -- the gated linear recurrence and its gradients, fp32 data.
+// scan_f32.hip -- the gated linear recurrence, fp32 data.
 #include "scan_kernels.h"
 #include "scan_launch.h"
 
 namespace lcv {
 hipError_t launch_scan_fwd_f32(const ScanArgs& a, hipStream_t stream) { return scan_fwd<CT_F32>(a, stream); }
-hipError_t launch_scan_bwd_f32(const ScanArgs& a, hipStream_t stream) { return scan_bwd<CT_F32>(a, stream); }
 }  // namespace lcv

@@ -6,49 +6,58 @@
 namespace lcv {
 namespace {
 
-// A sigmoid s and 1 - s in one register, each to its own size: the smaller of the two, negative where that is 1 - s.
-__device__ __forceinline__ float folded_sigmoid(float x) {
-    const float e = __expf(-fabsf(x)), small = fmaf(e, fast_rcp(1.f + e), 1e-37f);    // not zero: the sign is kept
-    return x >= 0.f ? -small : small;
-}
-__device__ __forceinline__ float unfolded(float w) { return w > 0.f ? w : 1.f + w; }              // s
-__device__ __forceinline__ float slope(float w) { return fabsf(w) * (1.f - fabsf(w)); }           // s (1 - s)
-
-// A decay a and d = 1 - a, each to its own size: memories of thousands of tokens are in d, which 1 - a has lost.
-// What a rounded to fp32 leaves out, (1 - a) - d (exact for a >= 1/2), goes along with it in the recurrence: a gate that
-// stays where it is would add the same rounding up over its memory.
-struct Decay {
-    float a, d;
+// A sigmoid and its slope s (1 - s) = e s^2 with e = exp(-x), each to its own size (for x below -69 the slope, less than
+// 1e-30 then, falls off faster than it should).
+struct Sigmoid {
+    float s, slope;
 };
-__device__ __forceinline__ Decay decay_of_log(float l) {       // a = exp(l), l <= 0
-    // -expm1(l) as a Taylor polynomial near zero (next term: 0.25^6 / 5040 of the sum, 5e-8)
-    const float p = -l * (1.f + l * (1.f / 2 + l * (1.f / 6 + l * (1.f / 24 + l * (1.f / 120 + l * (1.f / 720))))));
-    const float e = __expf(l);
-    const bool near = l > -0.25f;
-    return Decay{near ? 1.f - p : e, near ? p : 1.f - e};
+__device__ __forceinline__ Sigmoid sloped_sigmoid(float x) {
+    const float e = fast_exp2(-kLog2e * x), s = fast_rcp(1.f + e);
+    return Sigmoid{s, fminf(e, 1e30f) * s * s};
+}
+
+// A decay a as c + w: c = 1 and w = a - 1 near one, c = 0 and w = a elsewhere, so that both a and 1 - a keep their own size.
+// Memories of thousands of tokens are in 1 - a, which a rounded to fp32 has lost, and a gate that stays where it is would
+// add one rounding of a up over its memory.
+struct Decay {
+    float c, w;
+};
+__device__ __forceinline__ float value_of(Decay k) { return k.c + k.w; }
+__device__ __forceinline__ float loss_of(Decay k) { return (1.f - k.c) - k.w; }                   // 1 - a
+__device__ __forceinline__ Decay decay_of_log2(float l) {      // a = 2^l, l <= 0
+    // 2^l - 1 near zero by the quartic of least relative error for (2^l - 1) / l on [-0.25 log2(e), 0] (8e-9)
+    const float p = l * fmaf(l, fmaf(l, fmaf(l, fmaf(l, 0.00120165572f, 0.00957710668f), 0.055498831f), 0.240226269f), 0.693147182f);
+    const bool near = l > -0.36067376f;
+    return Decay{near ? 1.f : 0.f, near ? p : fast_exp2(l)};
 }
 __device__ __forceinline__ Decay decay_of_logit(float z) {     // a = sigmoid(z)
-    const float e = __expf(-fabsf(z)), big = fast_rcp(1.f + e), small = e * big;
-    const bool slow = z >= 0.f;
-    return Decay{slow ? 1.f - small : small, slow ? small : big};
+    const float e = fast_exp2(-kLog2e * fabsf(z)), small = e * fast_rcp(1.f + e);
+    const bool near = z >= 0.f;
+    return Decay{near ? 1.f : 0.f, near ? -small : small};
 }
-__device__ __forceinline__ float residue(Decay g) { return g.a >= 0.5f ? (1.f - g.a) - g.d : 0.f; }
+// 1 - a^2 as -w (2 + w) or 1 - w^2, and its root
+__device__ __forceinline__ float energy_of(Decay k) { return fmaf(-k.w, k.w, k.c > 0.f ? -2.f * k.w : 1.f); }
+__device__ __forceinline__ float norm_of(Decay k) { return fast_sqrt(energy_of(k)); }
 
-// A state h after one more token (or a run of tokens), the residue r of the decay a along
-__device__ __forceinline__ float moved(float a, float r, float h, float u) { return fmaf(a, h, fmaf(r, h, u)); }
-__device__ __forceinline__ float times(float x, float a, float r) { return fmaf(x, a, x * r); }
+// A state h after one more token or run of tokens, and x times a decay
+__device__ __forceinline__ float moved(Decay k, float h, float u) { return fmaf(k.c, h, fmaf(k.w, h, u)); }
+__device__ __forceinline__ float times(Decay k, float x) { return fmaf(k.c, x, k.w * x); }
 
-// The decay of a run of tokens.  Under gates that stay where they are every run has the same decay, and a rounding of it adds
-// up as a token's would: 1 - a is carried along, 1 - a b = (1 - a) + (1 - b) - (1 - a)(1 - b), and the product itself only
-// counts where little is left of it.
-__device__ __forceinline__ void lengthen(Decay& run, float a, float d) {
-    run.a *= a;
+// The decay of a run of tokens: its value and its loss, 1 - a b = (1 - a) + (1 - b) - (1 - a)(1 - b).  Under gates that stay
+// where they are every run has the same decay, and a rounding of it would add up as a token's; the value only counts where
+// little is left of it.
+struct RunDecay {
+    float a, d;
+};
+__device__ __forceinline__ void lengthen(RunDecay& run, Decay k) {
+    const float d = loss_of(k);
+    run.a = times(k, run.a);
     run.d += fmaf(-run.d, d, d);
 }
-__device__ __forceinline__ Decay rounded(Decay run) { return Decay{run.d <= 0.5f ? 1.f - run.d : run.a, run.d}; }
-
-// sqrt(1 - a^2)
-__device__ __forceinline__ float norm_of(Decay g) { return fast_sqrt(g.d * (1.f + g.a)); }
+__device__ __forceinline__ Decay whole(RunDecay run) {
+    const bool near = run.d <= 0.5f;
+    return Decay{near ? 1.f : 0.f, near ? -run.d : run.a};
+}
 
 }  // namespace
 }  // namespace lcv

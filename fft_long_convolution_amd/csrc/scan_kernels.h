@@ -2,59 +2,118 @@
 //
 //   h_t = a_t h_{t-1} + u_t,  u = m s x;   gradients: G_t = dy_t + g_{t+1},  g_t = a_t G_t
 // A wave takes 64 or 128 channels of 8 tokens, a lane one or two of the channels, so that the recurrence itself never
-// crosses lanes.  Of its tokens a wave first needs only the product of their decays and what they add up to from zero;
-// the 8 waves of a workgroup join these in order through LDS, one barrier to a tile of 64 tokens, and every wave then runs its
-// tokens from its own first state.  The workgroup walks along the sequence with the state in registers and the next tile's
-// loads on their way: one pass over the data.  Calls of few rows are cut into segments along the sequence: a first launch
-// finds the segments' products and sums, the second begins each segment with the join of those before it.
+// crosses lanes.  Of its tokens a wave first needs only their decay and what they add up from zero; the waves of a
+// workgroup leave these in LDS, one barrier to a tile, and every wave joins what stands before it and runs its
+// tokens from its own first state.  The last wave's last state enters the next tile.  The workgroup walks along the
+// sequence with the next tile's loads on their way: one pass over the data.  Calls of few rows are cut into segments along the
+// sequence: a first launch finds the segments' decays and sums, the second begins each segment with the join of those
+// before it.
 #pragma once
 #include "scan_gates.h"
 
 namespace lcv {
 namespace {
 
-// tokens of a wave's turn as loaded
+// A lane's channels, hidden from the optimiser where they are used: it would add them to the operands' pointers outside the
+// loop, and then a wave's part of an address to that by 64-bit vector additions, where an instruction adds a lane's 32 bits to a
+// wave's address by itself.
+__device__ __forceinline__ uint32_t in_place(uint32_t c) {
+    asm volatile("" : "+v"(c));
+    return c;
+}
+
+// tokens of a wave's turn as stored
 template <int IO, int V> struct Turn {
     RawV<IO, V> e[kScanTokens];
 };
-template <int IO, int V>
-__device__ __forceinline__ void load_turn(Turn<IO, V>& r, const TokOperand& o, int64_t row, int64_t t, int64_t len, uint32_t c) {
+// Tokens t .. of an operand's row.  CLAMP: those from `end` on replaced by the last one that there is (not used then).  No branch:
+// where ways meet, a load's register is copied, and the copy waits for the load.
+template <int IO, int V, bool CLAMP>
+__device__ __forceinline__ void load_turn(Turn<IO, V>& r, const TokOperand& o, int64_t row, int64_t t, int64_t end, uint32_t c) {
+    const typename Elem<IO>::T* p = (const typename Elem<IO>::T*)o.p + row + (!CLAMP || t < end ? t : end - 1) * o.n;
+    c = in_place(c);
 #pragma unroll
     for (int j = 0; j < kScanTokens; ++j) {
-        const int64_t at = t + j < len ? t + j : len - 1;      // past the end: a token that there is, not used
-        r.e[j] = load_raw_v<IO, V>(o.p, row + at * o.n, c);
+        r.e[j] = load_raw_v<IO, V>(p, 0, c);
+        p += !CLAMP || t + j + 1 < end ? o.n : 0;
     }
 }
-
-// a, 1 - a, m and the (folded) sigmoid behind a rate, of one token's channels
-template <int V> struct Gate {
-    float a[V], d[V], m[V], p[V];
-};
 template <int IO, int V>
-__device__ __forceinline__ void gates(Gate<V>* g, const Turn<IO, V>& z, const float* rate, int gate, int mix) {
-    float x[kScanTokens][V];
+__device__ __forceinline__ void store_turn(void* y, int64_t row, int64_t n, int64_t t, uint32_t c, const Turn<IO, V>& r, int tokens) {
+    typename Elem<IO>::T* p = (typename Elem<IO>::T*)y + row + t * n;
+    c = in_place(c);
 #pragma unroll
-    for (int j = 0; j < kScanTokens; ++j) widen<IO, V>(z.e[j], x[j]);
-    const auto each = [&](auto&& f) LCV_INLINE {
+    for (int j = 0; j < kScanTokens; ++j, p += n)
+        if (j < tokens) store_raw_v<IO, V>(p, 0, c, r.e[j]);
+}
+// A turn as fp32.  The registers that it was loaded into are free behind this, and the next turn's loads may follow at once.
+template <int V> struct Wide {
+    float e[kScanTokens][V];
+};
+template <int IO, int V> __device__ __forceinline__ void widen_turn(Wide<V>& w, const Turn<IO, V>& r) {
 #pragma unroll
-        for (int j = 0; j < kScanTokens; ++j)
+    for (int j = 0; j < kScanTokens; ++j) widen<IO, V>(r.e[j], w.e[j]);
+}
+// how many of a turn's tokens come before `end`
+__device__ __forceinline__ int tokens_before(int64_t t, int64_t end) {
+    return t >= end ? 0 : end - t < kScanTokens ? (int)(end - t) : kScanTokens;
+}
+
+// One token's decays and what its input is multiplied with; for the gradients also 1 / m of a norm and the sigmoid behind a rate
+template <int V> struct Gate {
+    Decay k[V];
+    float m[V], inv[V];
+    Sigmoid p[V];
+};
+// The gates of a turn's first n tokens (those behind forget nothing), and the decay of all of them: the logarithms' sum where
+// there are logarithms.  rate: -rate log2(e).
+template <int V, int GATE, int MIX, bool GRAD>
+__device__ __forceinline__ void gates(Gate<V>* g, Decay* run, const Wide<V>& z, const float* rate, int n) {
+    float sum[V] = {};
+    RunDecay all[V];
 #pragma unroll
-            for (int v = 0; v < V; ++v) f(g[j], x[j][v], v);
-    };
-    const auto set = [](Gate<V>& t, int v, Decay k) LCV_INLINE { t.a[v] = k.a; t.d[v] = k.d; };
-    if (gate == LCONV_GATE_SIGMOID) {
-        each([&](Gate<V>& t, float x, int v) LCV_INLINE { set(t, v, decay_of_logit(x)); });
-    } else if (gate == LCONV_GATE_LOG) {
-        each([&](Gate<V>& t, float x, int v) LCV_INLINE { set(t, v, decay_of_log(x)); });
-    } else {
-        each([&](Gate<V>& t, float x, int v) LCV_INLINE {
-            t.p[v] = folded_sigmoid(x);
-            set(t, v, decay_of_log(-rate[v] * unfolded(t.p[v])));
-        });
-    }
-    if (mix == LCONV_MIX_NORM) each([&](Gate<V>& t, float, int v) LCV_INLINE { t.m[v] = norm_of(Decay{t.a[v], t.d[v]}); });
-    else if (mix == LCONV_MIX_CONVEX) each([&](Gate<V>& t, float, int v) LCV_INLINE { t.m[v] = t.d[v]; });
-    else each([&](Gate<V>& t, float, int v) LCV_INLINE { t.m[v] = 1.f; });
+    for (int v = 0; v < V; ++v) all[v] = RunDecay{1.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < kScanTokens; ++j)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const float x = z.e[j][v];
+            Decay k;
+            if constexpr (GATE == LCONV_GATE_SIGMOID) {
+                k = decay_of_logit(x);
+                if (j >= n) k = Decay{1.f, 0.f};
+                lengthen(all[v], k);
+            } else {
+                float l = kLog2e * x;
+                if constexpr (GATE == LCONV_GATE_RATE) {
+                    if constexpr (GRAD) g[j].p[v] = sloped_sigmoid(x);
+                    l = rate[v] * (GRAD ? g[j].p[v].s : sigmoid(x));
+                }
+                l = j < n ? l : 0.f;
+                sum[v] += l;
+                k = decay_of_log2(l);
+            }
+            g[j].k[v] = k;
+            if constexpr (MIX == LCONV_MIX_NORM && GRAD) {
+                const float e = energy_of(k);
+                g[j].inv[v] = e > 0.f ? fast_rsqrt(e) : 0.f;
+                g[j].m[v] = e * g[j].inv[v];
+            } else {
+                g[j].m[v] = MIX == LCONV_MIX_NORM ? norm_of(k) : MIX == LCONV_MIX_CONVEX ? loss_of(k) : 1.f;
+            }
+        }
+#pragma unroll
+    for (int v = 0; v < V; ++v) run[v] = GATE == LCONV_GATE_SIGMOID ? whole(all[v]) : decay_of_log2(sum[v]);
+}
+template <int V, bool GATED> __device__ __forceinline__ void inputs(float (*u)[V], const Gate<V>* g, const Wide<V>& x, const Wide<V>& i, int n) {
+#pragma unroll
+    for (int j = 0; j < kScanTokens; ++j)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            u[j][v] = g[j].m[v] * x.e[j][v];
+            if constexpr (GATED) u[j][v] *= sigmoid(i.e[j][v]);
+            u[j][v] = j < n ? u[j][v] : 0.f;
+        }
 }
 
 // where a workgroup works: row b, channels c .. of a lane, tokens first .. end of a segment.  A lane past the last channels
@@ -87,356 +146,428 @@ template <int V> __device__ __forceinline__ LaneF<V> load_f(const float* p) {
 }
 template <int V> __device__ __forceinline__ void store_f(float* p, const float* x) { __builtin_memcpy(p, x, 4 * V); }
 
-// A segment for the state h that enters it from one side, [3][C]: its decay, the decay's residue, what it adds up from zero
+// A segment for the state h that enters it from one side, [3][C]: its decay (two), what it adds up from zero
 template <int V> __device__ __forceinline__ void join_segment(float* h, const ScanArgs& a, const Place<V>& w, int k) {
     const float* s = a.seg + (w.b * a.nseg + k) * 3 * a.C + w.c;
-    const LaneF<V> A = load_f<V>(s), r = load_f<V>(s + a.C), H = load_f<V>(s + 2 * a.C);
+    const LaneF<V> c = load_f<V>(s), r = load_f<V>(s + a.C), H = load_f<V>(s + 2 * a.C);
 #pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = moved(A.v[v], r.v[v], h[v], H.v[v]);
+    for (int v = 0; v < V; ++v) h[v] = moved(Decay{c.v[v], r.v[v]}, h[v], H.v[v]);
 }
 template <int V> __device__ __forceinline__ void leave_segment(const float* h, const Decay* all, const ScanArgs& a, const Place<V>& w) {
     float* s = a.seg + (w.b * a.nseg + w.seg) * 3 * a.C + w.c;
-    float A[V], r[V];
+    float c[V], r[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const Decay k = rounded(all[v]);
-        A[v] = k.a;
-        r[v] = residue(k);
-    }
-    store_f<V>(s, A);
+    for (int v = 0; v < V; ++v) c[v] = all[v].c, r[v] = all[v].w;
+    store_f<V>(s, c);
     store_f<V>(s + a.C, r);
     store_f<V>(s + 2 * a.C, h);
 }
 
-// What a wave leaves for the others, and what they do with it: decay, residue, and one or two sums
+// What a wave leaves for the others: its decay and a sum
 template <int V> __device__ __forceinline__ void leave(float* to, const Decay* run, const float* H) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        const Decay k = rounded(run[v]);
-        to[v] = k.a;
-        to[V + v] = residue(k);
+        to[v] = run[v].c;
+        to[V + v] = run[v].w;
         to[2 * V + v] = H[v];
     }
 }
-template <int V> __device__ __forceinline__ void lengthen_by(Decay* all, const float* from) {
+template <int V> __device__ __forceinline__ void join(float* h, const float* from, const float* sum) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const float d = (1.f - from[v]) - from[V + v];
-        all[v].a = times(all[v].a, from[v], from[V + v]);
-        all[v].d += fmaf(-all[v].d, d, d);
+    for (int v = 0; v < V; ++v) h[v] = moved(Decay{from[v], from[V + v]}, h[v], sum[v]);
+}
+// h past the waves before this one, or (BACK) from the last wave down to the one behind it: four at a time, so that four
+// reads from LDS wait together.
+template <int V, int W, bool BACK>
+__device__ __forceinline__ void join_waves(float* h, const float (*left)[64][W], int lane, int wave, int waves, int sum) {
+    const int count = BACK ? waves - 1 - wave : wave;
+    for (int e0 = 0; e0 < count; e0 += 4) {
+        float from[4][2 * V], add[4][V];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int k = e0 + e < count ? e0 + e : 0;
+            const float* const p = left[BACK ? waves - 1 - k : k][lane];
+            __builtin_memcpy(from[e], p, sizeof(from[e]));
+            __builtin_memcpy(add[e], p + sum, sizeof(add[e]));
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (e0 + e < count) join<V>(h, from[e], add[e]);
     }
 }
 
-// STATES: only the segments' decays and sums.
-template <int IO, int V, bool GATED, bool STATES>
-__global__ void __launch_bounds__(64 * kScanWaves) scan_fwd_kernel(ScanArgs a) {
-    __shared__ float join[2][kScanWaves][64][3 * V];
+template <int IO, int V, bool GATED, int GATE, int MIX> __global__ void __launch_bounds__(64 * scan_waves(V)) scan_fwd_kernel(ScanArgs a) {
+    __shared__ float left[2][scan_waves(V)][64][3 * V], edge[2][64][V];
     const Place<V> w = place<V>(a);
-    const int lane = threadIdx.x & 63, waves = a.waves;
+    const int lane = threadIdx.x & 63, last = a.waves - 1;
     const int64_t len = row_len(a.lengths, w.b, a.N), end = w.end < len ? w.end : len;
-    const int64_t xr = w.b * a.x.b, zr = w.b * a.z.b, ir = GATED ? w.b * a.i.b : 0;
+    const int64_t xr = w.b * a.x.b, zr = w.b * a.z.b, ir = GATED ? w.b * a.i.b : 0, yr = w.b * a.yb;
     const int64_t sc = w.b * a.C + w.c;
+    float* const marks = a.marks ? a.marks + w.b * ((a.N + kScanMark - 1) / kScanMark) * a.C + w.c : nullptr;
     float rate[V], h[V];
-    Decay all[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        rate[v] = a.rate ? a.rate[w.c + v] : 0.f;
-        h[v] = (STATES ? w.seg == a.nseg - 1 : a.nseg == 1) && a.state_in ? a.state_in[sc + v] : 0.f;
-        all[v] = Decay{1.f, 0.f};
+        rate[v] = GATE == LCONV_GATE_RATE ? -kLog2e * a.rate[w.c + v] : 0.f;
+        h[v] = a.nseg == 1 && a.state_in ? a.state_in[sc + v] : 0.f;
     }
-    // Nothing follows the last segment: its place in the workspace keeps the state that enters the row, which the main pass
-    // takes from there, since its last segment may write another state over it before the first one begins.
-    if constexpr (STATES) {
-        if (w.seg == a.nseg - 1) {
-            if (w.wave == 0) leave_segment<V>(h, all, a, w);
-            return;
-        }
-    } else if (a.nseg > 1) {
+    if (a.nseg > 1) {      // the state that enters the row stands in the last segment's place
         join_segment<V>(h, a, w, a.nseg - 1);
         for (int k = 0; k < w.seg; ++k) join_segment<V>(h, a, w, k);
     }
     const int64_t mine = (int64_t)w.wave * kScanTokens;
-    const int tile = waves * kScanTokens;
-    Turn<IO, V> x, z, i, nx, nz, ni;
-    const auto load = [&](int64_t t) LCV_INLINE {
-        load_turn<IO, V>(nx, a.x, xr, t, end, w.c);
-        load_turn<IO, V>(nz, a.z, zr, t, end, w.c);
-        if constexpr (GATED) load_turn<IO, V>(ni, a.i, ir, t, end, w.c);
+    const int tile = a.waves * kScanTokens;
+    Turn<IO, V> nx, nz, ni;
+    Wide<V> x, z, i;
+    const auto load = [&](int64_t t, auto clamp) LCV_INLINE {
+        load_turn<IO, V, clamp.value>(nx, a.x, xr, t, end, w.c);
+        load_turn<IO, V, clamp.value>(nz, a.z, zr, t, end, w.c);
+        if constexpr (GATED) load_turn<IO, V, clamp.value>(ni, a.i, ir, t, end, w.c);
     };
-    if (w.first < end) load(w.first + mine);
+    // A turn's results are stored at the beginning of the next one, in front of the wait for that one's loads: the number of
+    // memory operations behind the loads is the same on every way into the loop, so that the wait is for them alone and not
+    // for the stores.  The first turn stores zeros where its own results will stand.
+    Turn<IO, V> held{};
+    if (w.first < end) load(w.first + mine, std::true_type{});
+    if (w.wave == last) store_f<V>(edge[0][lane], h);
     int buf = 0;
-    const auto turn = [&](int64_t t0, auto full) LCV_INLINE {
+    const auto turn = [&](int64_t t0, auto full, auto clamp) LCV_INLINE {
         const int64_t t = t0 + mine;
-        x = nx; z = nz;
-        if constexpr (GATED) i = ni;
-        load(t + tile);
+        if constexpr (full) store_turn<IO, V>(a.y, yr, a.yn, t0 > w.first ? t - tile : t, w.c, held, kScanTokens);
+        widen_turn<IO, V>(z, nz);
+        widen_turn<IO, V>(x, nx);
+        if constexpr (GATED) widen_turn<IO, V>(i, ni);
+        __builtin_amdgcn_sched_barrier(0);
+        load(t + tile, clamp);
+        const int n = full ? kScanTokens : tokens_before(t, end);
         Gate<V> g[kScanTokens];
-        gates<IO, V>(g, z, rate, a.gate, a.mix);
-        float dk[kScanTokens][V], rs[kScanTokens][V], u[kScanTokens][V], H[V];
         Decay run[V];
+        gates<V, GATE, MIX, false>(g, run, z, rate, n);
+        float u[kScanTokens][V], H[V] = {};
+        inputs<V, GATED>(u, g, x, i, n);
 #pragma unroll
-        for (int v = 0; v < V; ++v) run[v] = Decay{1.f, 0.f}, H[v] = 0.f;
+        for (int j = 0; j < kScanTokens; ++j)
+#pragma unroll
+            for (int v = 0; v < V; ++v) H[v] = moved(g[j].k[v], H[v], u[j][v]);
+        leave<V>(left[buf][w.wave][lane], run, H);
+        __syncthreads();
+        LaneF<V> s = load_f<V>(edge[buf][lane]);
+        join_waves<V, 3 * V, false>(s.v, left[buf], lane, w.wave, a.waves, 2 * V);
+        if (marks && t % kScanMark == 0 && (full || t < end)) store_f<V>(marks + t / kScanMark * a.C, s.v);
 #pragma unroll
         for (int j = 0; j < kScanTokens; ++j) {
-            float xv[V], iv[V];
-            widen<IO, V>(x.e[j], xv);
-            if constexpr (GATED) widen<IO, V>(i.e[j], iv);
-            const bool on = full || t + j < end;
+            float y[V];
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const float in = g[j].m[v] * xv[v];
-                dk[j][v] = on ? g[j].a[v] : 1.f;
-                rs[j][v] = on ? residue(Decay{g[j].a[v], g[j].d[v]}) : 0.f;
-                u[j][v] = on ? (GATED ? in * sigmoid(iv[v]) : in) : 0.f;
-                H[v] = moved(dk[j][v], rs[j][v], H[v], u[j][v]);
-                lengthen(run[v], dk[j][v], on ? g[j].d[v] : 0.f);
+                s.v[v] = moved(g[j].k[v], s.v[v], u[j][v]);
+                y[v] = j < n ? s.v[v] : 0.f;
             }
+            held.e[j] = narrow<IO, V>(y);
         }
-        leave<V>(join[buf][w.wave][lane], run, H);
-        __syncthreads();
-        if (!STATES && a.marks && w.wave == 0)
-            store_f<V>(a.marks + (w.b * ((a.N + kScanTile - 1) / kScanTile) + t0 / kScanTile) * a.C + w.c, h);
-        float s[V] = {};
-        for (int k = 0; k < waves; ++k) {
-            const bool me = k == w.wave;
-            const float* from = join[buf][k][lane];
+        if (w.wave == last) {
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                s[v] = me ? h[v] : s[v];
-                h[v] = moved(from[v], from[V + v], h[v], from[2 * V + v]);
-            }
-            if constexpr (STATES) lengthen_by<V>(all, from);
+            for (int v = 0; v < V; ++v) h[v] = s.v[v];
+            store_f<V>(edge[buf ^ 1][lane], h);
         }
-        if constexpr (!STATES) {
-#pragma unroll
-            for (int j = 0; j < kScanTokens; ++j) {
-                float y[V];
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    s[v] = moved(dk[j][v], rs[j][v], s[v], u[j][v]);
-                    y[v] = full || t + j < end ? s[v] : 0.f;
-                }
-                if (full || t + j < w.end) store_v<IO, V>(a.y, w.b * a.yb + (t + j) * a.yn, w.c, y);
-            }
-        }
+        buf ^= 1;
     };
-    for (int64_t t0 = w.first; t0 < end; t0 += tile, buf ^= 1) {
-        if (t0 + tile <= end) turn(t0, std::true_type{});
-        else turn(t0, std::false_type{});
+    int64_t t0 = w.first;
+    for (; t0 + 2 * tile <= end; t0 += tile) turn(t0, std::true_type{}, std::false_type{});
+    if (t0 + tile <= end) {
+        turn(t0, std::true_type{}, std::true_type{});
+        t0 += tile;
     }
-    if constexpr (STATES) {
-        if (w.wave == 0) leave_segment<V>(h, all, a, w);
-    } else {
-        // tokens behind the tiles of the row's own, and marks that no token needs
-        const float zero[V] = {};
-        int64_t t0 = end > w.first ? w.first + (end - w.first + tile - 1) / tile * tile : w.first;
-        for (int64_t t = t0 + w.wave; t < w.end; t += waves) store_v<IO, V>(a.y, w.b * a.yb + t * a.yn, w.c, zero);
-        if (a.state_out && w.seg == a.nseg - 1 && w.wave == 0) store_f<V>(a.state_out + sc, h);
+    if (t0 > w.first) store_turn<IO, V>(a.y, yr, a.yn, t0 - tile + mine, w.c, held, kScanTokens);
+    if (t0 < end) {
+        turn(t0, std::false_type{}, std::true_type{});
+        store_turn<IO, V>(a.y, yr, a.yn, t0 + mine, w.c, held, tokens_before(t0 + mine, w.end));
+        t0 += tile;
     }
+    // tokens behind the row's own tiles
+    const float zero[V] = {};
+    for (int64_t t = t0 + w.wave; t < w.end; t += a.waves) store_v<IO, V>(a.y, yr + t * a.yn, w.c, zero);
+    if (a.state_out && w.seg == a.nseg - 1 && w.wave == last) store_f<V>(a.state_out + sc, h);
 }
 
-// The gradients, from the last tile to the first: a tile's states again from its mark, G from the carry.
-// REACH: only the segments' products and what they hand to the left.
-template <int IO, int V, bool GATED, bool REACH>
-__global__ void __launch_bounds__(64 * kScanWaves) scan_bwd_kernel(ScanArgs a) {
-    constexpr int W = REACH ? 3 * V : 4 * V;
-    __shared__ float join[2][kScanWaves][64][W];
+// The gradients, from the last tile to the first: a tile's states again from its mark, G from the first wave's last one.
+template <int IO, int V, bool GATED, int GATE, int MIX> __global__ void __launch_bounds__(64 * kScanGradWaves) scan_bwd_kernel(ScanArgs a) {
+    __shared__ float left[2][kScanGradWaves][64][4 * V], edge[2][64][V];
     const Place<V> w = place<V>(a);
     const int lane = threadIdx.x & 63, waves = a.waves;
     const int64_t len = row_len(a.lengths, w.b, a.N), end = w.end < len ? w.end : len;
     const int64_t xr = w.b * a.x.b, zr = w.b * a.z.b, ir = GATED ? w.b * a.i.b : 0, dr = w.b * a.dy.b;
-    const int64_t sc = w.b * a.C + w.c, marks = (a.N + kScanTile - 1) / kScanTile;
-    float rate[V], carry[V], drate[V];
-    Decay all[V];
+    const int64_t sc = w.b * a.C + w.c;
+    const float* const marks = a.marks + w.b * ((a.N + kScanMark - 1) / kScanMark) * a.C;
+    float rate[V], per_slope[V], carry[V], drate[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        rate[v] = a.rate ? a.rate[w.c + v] : 0.f;
-        carry[v] = (REACH ? w.seg == 0 : a.nseg == 1) && a.state_in ? a.state_in[sc + v] : 0.f;
-        all[v] = Decay{1.f, 0.f};
+        per_slope[v] = GATE == LCONV_GATE_RATE ? -a.rate[w.c + v] : 0.f;
+        rate[v] = kLog2e * per_slope[v];
+        carry[v] = a.nseg == 1 && a.state_in ? a.state_in[sc + v] : 0.f;
         drate[v] = 0.f;
     }
-    if constexpr (REACH) {      // as in the forward pass, from the other end
-        if (w.seg == 0) {
-            if (w.wave == 0) leave_segment<V>(carry, all, a, w);
-            return;
-        }
-    } else if (a.nseg > 1) {
+    if (a.nseg > 1) {      // what enters the row from behind stands in the first segment's place
         join_segment<V>(carry, a, w, 0);
         for (int k = a.nseg - 1; k > w.seg; --k) join_segment<V>(carry, a, w, k);
     }
     const int64_t mine = (int64_t)w.wave * kScanTokens;
     const int tile = waves * kScanTokens;
-    const float zero[V] = {};
-    Turn<IO, V> x, z, i, dy, nx, nz, ni, nd;
-    LaneF<V> mark{}, nmark{};
-    const auto load = [&](int64_t t0) LCV_INLINE {
+    Turn<IO, V> nx, nz, ni, nd;
+    Wide<V> x, z, i, d;
+    RawV<CT_F32, V> mark{}, nmark{};
+    const auto load = [&](int64_t t0, auto clamp) LCV_INLINE {
         const int64_t t = t0 + mine;
-        load_turn<IO, V>(nz, a.z, zr, t, end, w.c);
-        load_turn<IO, V>(nd, a.dy, dr, t, end, w.c);
-        if constexpr (!REACH) {
-            load_turn<IO, V>(nx, a.x, xr, t, end, w.c);
-            if constexpr (GATED) load_turn<IO, V>(ni, a.i, ir, t, end, w.c);
-            nmark = load_f<V>(a.marks + (w.b * marks + t0 / kScanTile) * a.C + w.c);
-        }
+        load_turn<IO, V, clamp.value>(nz, a.z, zr, t, end, w.c);
+        load_turn<IO, V, clamp.value>(nx, a.x, xr, t, end, w.c);
+        if constexpr (GATED) load_turn<IO, V, clamp.value>(ni, a.i, ir, t, end, w.c);
+        load_turn<IO, V, clamp.value>(nd, a.dy, dr, t, end, w.c);
+        nmark = load_raw_v<CT_F32, V>(marks, t0 / kScanMark * a.C, in_place(w.c));
     };
     const int64_t tiles = end > w.first ? (end - w.first + tile - 1) / tile : 0;
-    if constexpr (!REACH) {
+    {
+        const float zero[V] = {};
         for (int64_t t = w.first + tiles * tile + w.wave; t < w.end; t += waves) {
             store_v<IO, V>(a.dx, w.b * a.dxb + t * a.dxn, w.c, zero);
             store_v<IO, V>(a.dz, w.b * a.dzb + t * a.dzn, w.c, zero);
             if constexpr (GATED) store_v<IO, V>(a.di, w.b * a.dib + t * a.din, w.c, zero);
         }
     }
-    if (tiles) load(w.first + (tiles - 1) * tile);
+    if (tiles) load(w.first + (tiles - 1) * tile, std::true_type{});
+    if (w.wave == 0) store_f<V>(edge[0][lane], carry);
     int buf = 0;
-    const auto turn = [&](int64_t t0, auto full) LCV_INLINE {
+    Turn<IO, V> ox{}, oz{}, oi{};      // a turn's results, stored by the next one as in the forward pass
+    const auto store = [&](int64_t t, int there) LCV_INLINE {
+        store_turn<IO, V>(a.dx, w.b * a.dxb, a.dxn, t, w.c, ox, there);
+        store_turn<IO, V>(a.dz, w.b * a.dzb, a.dzn, t, w.c, oz, there);
+        if constexpr (GATED) store_turn<IO, V>(a.di, w.b * a.dib, a.din, t, w.c, oi, there);
+    };
+    const auto turn = [&](int64_t t0, int64_t before_t0, auto full) LCV_INLINE {
         const int64_t t = t0 + mine;
-        x = nx; z = nz; dy = nd; mark = nmark;
-        if constexpr (GATED) i = ni;
-        load(t0 > w.first ? t0 - tile : t0);
+        if constexpr (full) store(before_t0 + mine, kScanTokens);
+        widen_turn<IO, V>(z, nz);
+        widen_turn<IO, V>(x, nx);
+        if constexpr (GATED) widen_turn<IO, V>(i, ni);
+        widen_turn<IO, V>(d, nd);
+        mark = nmark;
+        __builtin_amdgcn_sched_barrier(0);
+        load(t0 > w.first ? t0 - tile : t0, std::integral_constant<bool, !full>{});
+        const int n = full ? kScanTokens : tokens_before(t, end);
         Gate<V> g[kScanTokens];
-        gates<IO, V>(g, z, rate, a.gate, REACH ? LCONV_MIX_PLAIN : a.mix);
-        float dk[kScanTokens][V], rs[kScanTokens][V], d[kScanTokens][V], H[V], R[V];
         Decay run[V];
+        gates<V, GATE, MIX, true>(g, run, z, rate, n);
+        float u[kScanTokens][V], H[V] = {}, R[V] = {}, before[kScanTokens][V];
+        Sigmoid in[kScanTokens][V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) run[v] = Decay{1.f, 0.f}, H[v] = R[v] = 0.f;
-        float xv[kScanTokens][V], sv[kScanTokens][V], before[kScanTokens][V];
-#pragma unroll
-        for (int j = 0; j < kScanTokens; ++j) {
-            const bool on = full || t + j < end;
-            widen<IO, V>(dy.e[j], d[j]);
-            if constexpr (!REACH) widen<IO, V>(x.e[j], xv[j]);
-            if constexpr (GATED && !REACH) {
-                widen<IO, V>(i.e[j], sv[j]);
-#pragma unroll
-                for (int v = 0; v < V; ++v) sv[j][v] = folded_sigmoid(sv[j][v]);
-            }
+        for (int j = 0; j < kScanTokens; ++j)
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                dk[j][v] = on ? g[j].a[v] : 1.f;
-                rs[j][v] = on ? residue(Decay{g[j].a[v], g[j].d[v]}) : 0.f;
-                d[j][v] = on ? d[j][v] : 0.f;
-                if constexpr (!REACH) {
-                    const float in = g[j].m[v] * xv[j][v];
-                    H[v] = moved(dk[j][v], rs[j][v], H[v], on ? (GATED ? in * unfolded(sv[j][v]) : in) : 0.f);
+                d.e[j][v] = j < n ? d.e[j][v] : 0.f;
+                u[j][v] = g[j].m[v] * x.e[j][v];
+                if constexpr (GATED) {
+                    in[j][v] = sloped_sigmoid(i.e[j][v]);
+                    u[j][v] *= in[j][v].s;
                 }
-                lengthen(run[v], dk[j][v], on ? g[j].d[v] : 0.f);
+                u[j][v] = j < n ? u[j][v] : 0.f;
+                H[v] = moved(g[j].k[v], H[v], u[j][v]);
             }
-        }
 #pragma unroll
         for (int j = kScanTokens - 1; j >= 0; --j)
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float G = d[j][v] + R[v];
-                R[v] = times(G, dk[j][v], rs[j][v]);
-            }
-        leave<V>(join[buf][w.wave][lane], run, R);
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-            if constexpr (!REACH) join[buf][w.wave][lane][3 * V + v] = H[v];
+            for (int v = 0; v < V; ++v) R[v] = times(g[j].k[v], d.e[j][v] + R[v]);
+        leave<V>(left[buf][w.wave][lane], run, R);
+        store_f<V>(left[buf][w.wave][lane] + 3 * V, H);
         __syncthreads();
-        float s[V] = {};
-        for (int q = waves - 1; q >= 0; --q) {
-            const bool me = q == w.wave;
-            const float* from = join[buf][q][lane];
+        LaneF<V> s = load_f<V>(edge[buf][lane]);
+        join_waves<V, 4 * V, true>(s.v, left[buf], lane, w.wave, waves, 2 * V);
+        join_waves<V, 4 * V, false>(mark.e, left[buf], lane, w.wave, waves, 3 * V);
+#pragma unroll
+        for (int j = 0; j < kScanTokens; ++j)
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                s[v] = me ? carry[v] : s[v];
-                carry[v] = moved(from[v], from[V + v], carry[v], from[2 * V + v]);
+                before[j][v] = mark.e[v];
+                mark.e[v] = moved(g[j].k[v], mark.e[v], u[j][v]);
             }
-            if constexpr (REACH) lengthen_by<V>(all, from);
+#pragma unroll
+        for (int j = kScanTokens - 1; j >= 0; --j) {
+            const bool on = j < n;
+            float gx[V], gz[V], gi[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const Decay k = g[j].k[v];
+                const float G = d.e[j][v] + s.v[v], av = value_of(k), Gm = G * g[j].m[v];
+                s.v[v] = times(k, G);
+                gx[v] = on ? (GATED ? Gm * in[j][v].s : Gm) : 0.f;
+                if constexpr (GATED) gi[v] = on ? Gm * x.e[j][v] * in[j][v].slope : 0.f;
+                // of log a: a (G h_{t-1} + G s x dm / da), dm / da = 0, -1, -a / m; a norm that is zero has the gradient zero
+                float dl = before[j][v];
+                if constexpr (MIX != LCONV_MIX_PLAIN) {
+                    const float sx = GATED ? in[j][v].s * x.e[j][v] : x.e[j][v];
+                    dl -= MIX == LCONV_MIX_CONVEX ? sx : sx * (av * g[j].inv[v]);
+                }
+                dl *= av * G;
+                if constexpr (GATE == LCONV_GATE_SIGMOID) dl *= loss_of(k);
+                if constexpr (GATE == LCONV_GATE_RATE) {
+                    drate[v] -= on ? dl * g[j].p[v].s : 0.f;
+                    dl *= per_slope[v] * g[j].p[v].slope;
+                }
+                gz[v] = on ? dl : 0.f;
+            }
+            ox.e[j] = narrow<IO, V>(gx);
+            oz.e[j] = narrow<IO, V>(gz);
+            if constexpr (GATED) oi.e[j] = narrow<IO, V>(gi);
         }
-        if constexpr (!REACH) {
-            for (int q = 0; q < w.wave; ++q) {
-                const float* from = join[buf][q][lane];
+        if (w.wave == 0) {
 #pragma unroll
-                for (int v = 0; v < V; ++v) mark.v[v] = moved(from[v], from[V + v], mark.v[v], from[3 * V + v]);
-            }
-#pragma unroll
-            for (int j = 0; j < kScanTokens; ++j)
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    const float in = g[j].m[v] * xv[j][v];
-                    before[j][v] = mark.v[v];
-                    mark.v[v] = moved(dk[j][v], rs[j][v], mark.v[v], GATED ? in * unfolded(sv[j][v]) : in);
-                }
-#pragma unroll
-            for (int j = kScanTokens - 1; j >= 0; --j) {
-                const bool on = full || t + j < end;
-                float ox[V], oz[V], oi[V];
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    const float G = d[j][v] + s[v], av = dk[j][v];
-                    s[v] = times(G, av, rs[j][v]);
-                    const float sg = GATED ? unfolded(sv[j][v]) : 1.f, sx = sg * xv[j][v], Gm = G * g[j].m[v];
-                    ox[v] = Gm * sg;
-                    if constexpr (GATED) oi[v] = Gm * xv[j][v] * slope(sv[j][v]);
-                    // of log a: a (G h_{t-1}) + (G s x) dm / dlog a; a norm that is zero has the gradient zero
-                    float dl = av * (G * before[j][v]);
-                    if (a.mix == LCONV_MIX_CONVEX) dl -= av * (G * sx);
-                    if (a.mix == LCONV_MIX_NORM) dl -= g[j].m[v] > 0.f ? G * sx * (av * av * fast_rcp(g[j].m[v])) : 0.f;
-                    if (a.gate == LCONV_GATE_SIGMOID) dl *= g[j].d[v];
-                    if (a.gate == LCONV_GATE_RATE) {
-                        drate[v] -= on ? dl * unfolded(g[j].p[v]) : 0.f;
-                        dl *= -rate[v] * slope(g[j].p[v]);
-                    }
-                    ox[v] = on ? ox[v] : 0.f;
-                    oz[v] = on ? dl : 0.f;
-                    if constexpr (GATED) oi[v] = on ? oi[v] : 0.f;
-                }
-                if (full || t + j < w.end) {
-                    store_v<IO, V>(a.dx, w.b * a.dxb + (t + j) * a.dxn, w.c, ox);
-                    store_v<IO, V>(a.dz, w.b * a.dzb + (t + j) * a.dzn, w.c, oz);
-                    if constexpr (GATED) store_v<IO, V>(a.di, w.b * a.dib + (t + j) * a.din, w.c, oi);
-                }
-            }
+            for (int v = 0; v < V; ++v) carry[v] = s.v[v];
+            store_f<V>(edge[buf ^ 1][lane], carry);
         }
+        buf ^= 1;
     };
-    for (int64_t k = tiles - 1; k >= 0; --k, buf ^= 1) {
-        const int64_t t0 = w.first + k * tile;
-        if (t0 + tile <= end) turn(t0, std::true_type{});
-        else turn(t0, std::false_type{});
+    int64_t t0 = w.first + (tiles - 1) * tile;
+    if (tiles && t0 + tile > end) {
+        turn(t0, t0, std::false_type{});
+        store(t0 + mine, tokens_before(t0 + mine, w.end));
+        t0 -= tile;
     }
-    if constexpr (REACH) {
-        if (w.wave == 0) leave_segment<V>(carry, all, a, w);
-    } else {
-        if (a.state_out && w.seg == 0 && w.wave == 0) store_f<V>(a.state_out + sc, carry);
-        if (a.part) {      // the waves' sums in order
-            __syncthreads();
+    if (t0 >= w.first) {
+        for (int64_t to = t0; t0 >= w.first; to = t0, t0 -= tile) turn(t0, to, std::true_type{});
+        store(w.first + mine, kScanTokens);
+    }
+    if (a.state_out && w.seg == 0 && w.wave == 0) store_f<V>(a.state_out + sc, carry);
+    if (GATE != LCONV_GATE_RATE || !a.part) return;
+    __syncthreads();       // the waves' sums in order
+    store_f<V>(left[0][w.wave][lane], drate);
+    __syncthreads();
+    if (w.wave) return;
+    float sum[V] = {};
+    for (int q = 0; q < waves; ++q)
 #pragma unroll
-            for (int v = 0; v < V; ++v) join[0][w.wave][lane][v] = drate[v];
-            __syncthreads();
-            if (w.wave == 0) {
-                float sum[V] = {};
-                for (int q = 0; q < waves; ++q)
+        for (int v = 0; v < V; ++v) sum[v] += left[0][q][lane][v];
+    store_f<V>(a.part + (w.b * a.nseg + w.seg) * a.C + w.c, sum);
+}
+
+// The segments' decays and what they add up from zero (BACK: what they hand to the left).  The waves take a piece of the
+// segment each, one after another along the sequence, and join at its end.
+// Nothing follows the last segment (BACK: comes before the first): its place in the workspace keeps the state that enters the row,
+// which the main pass takes from there, since it may write another one over it before its first segment begins.
+template <int IO, int V, bool GATED, int GATE, int MIX, bool BACK> __global__ void __launch_bounds__(512) scan_segments_kernel(ScanArgs a) {
+    __shared__ float left[8][64][3 * V];
+    const Place<V> w = place<V>(a);
+    const int lane = threadIdx.x & 63, waves = a.waves;
+    const int64_t len = row_len(a.lengths, w.b, a.N);
+    const TokOperand& from = BACK ? a.dy : a.x;
+    float rate[V], H[V];
+    Decay run[V];
+    RunDecay all[V];
 #pragma unroll
-                    for (int v = 0; v < V; ++v) sum[v] += join[0][q][lane][v];
-                store_f<V>(a.part + (w.b * a.nseg + w.seg) * a.C + w.c, sum);
-            }
+    for (int v = 0; v < V; ++v) {
+        rate[v] = GATE == LCONV_GATE_RATE ? -kLog2e * a.rate[w.c + v] : 0.f;
+        H[v] = 0.f;
+        run[v] = Decay{1.f, 0.f};
+        all[v] = RunDecay{1.f, 0.f};
+    }
+    if (w.seg == (BACK ? 0 : a.nseg - 1)) {
+        if (w.wave) return;
+        if (a.state_in) {
+            const LaneF<V> s = load_f<V>(a.state_in + w.b * a.C + w.c);
+#pragma unroll
+            for (int v = 0; v < V; ++v) H[v] = s.v[v];
         }
+        leave_segment<V>(H, run, a, w);
+        return;
     }
+    const int64_t piece = a.seg_len / waves, first = w.first + w.wave * piece;      // whole turns
+    const int64_t stop = first + piece < len ? first + piece : len, turns = stop > first ? (stop - first + kScanTokens - 1) / kScanTokens : 0;
+    Turn<IO, V> nx, nz, ni;
+    Wide<V> x, z, i;
+    const auto load = [&](int64_t k) LCV_INLINE {
+        const int64_t t = first + (BACK ? turns - 1 - k : k) * kScanTokens;
+        load_turn<IO, V, true>(nx, from, w.b * from.b, t, stop, w.c);
+        load_turn<IO, V, true>(nz, a.z, w.b * a.z.b, t, stop, w.c);
+        if constexpr (GATED) load_turn<IO, V, true>(ni, a.i, w.b * a.i.b, t, stop, w.c);
+    };
+    const auto turn = [&](int64_t k, auto full) LCV_INLINE {
+        const int64_t t = first + (BACK ? turns - 1 - k : k) * kScanTokens;
+        widen_turn<IO, V>(z, nz);
+        widen_turn<IO, V>(x, nx);
+        if constexpr (GATED) widen_turn<IO, V>(i, ni);
+        __builtin_amdgcn_sched_barrier(0);
+        load(k + 1 < turns ? k + 1 : k);
+        const int n = full ? kScanTokens : (int)(stop - t);
+        Gate<V> g[kScanTokens];
+        gates<V, GATE, MIX, false>(g, run, z, rate, n);
+        float u[kScanTokens][V];
+        inputs<V, GATED>(u, g, x, i, n);
+#pragma unroll
+        for (int e = 0; e < kScanTokens; ++e) {
+            const int j = BACK ? kScanTokens - 1 - e : e;
+#pragma unroll
+            for (int v = 0; v < V; ++v) H[v] = BACK ? times(g[j].k[v], u[j][v] + H[v]) : moved(g[j].k[v], H[v], u[j][v]);
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) lengthen(all[v], run[v]);
+    };
+    if (turns) load(0);
+    for (int64_t k = 0; k < turns; ++k) {
+        const int64_t t = first + (BACK ? turns - 1 - k : k) * kScanTokens;
+        if (t + kScanTokens <= stop) turn(k, std::true_type{});
+        else turn(k, std::false_type{});
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) run[v] = whole(all[v]);
+    leave<V>(left[w.wave][lane], run, H);
+    __syncthreads();
+    if (w.wave) return;
+#pragma unroll
+    for (int v = 0; v < V; ++v) all[v] = RunDecay{1.f, 0.f}, H[v] = 0.f;
+    for (int e = 0; e < waves; ++e) {
+        const float* const k = left[BACK ? waves - 1 - e : e][lane];
+        join<V>(H, k, k + 2 * V);
+#pragma unroll
+        for (int v = 0; v < V; ++v) lengthen(all[v], Decay{k[v], k[V + v]});
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) run[v] = whole(all[v]);
+    leave_segment<V>(H, run, a, w);
+}
+
+// f(gate, mix) for a call's flags
+template <typename F> void by_flags(int gate, int mix, F&& f) {
+    using std::integral_constant;
+    const auto go = [&](auto g) {
+        if (mix == LCONV_MIX_NORM) f(g, integral_constant<int, LCONV_MIX_NORM>{});
+        else if (mix == LCONV_MIX_CONVEX) f(g, integral_constant<int, LCONV_MIX_CONVEX>{});
+        else f(g, integral_constant<int, LCONV_MIX_PLAIN>{});
+    };
+    if (gate == LCONV_GATE_RATE) go(integral_constant<int, LCONV_GATE_RATE>{});
+    else if (gate == LCONV_GATE_SIGMOID) go(integral_constant<int, LCONV_GATE_SIGMOID>{});
+    else go(integral_constant<int, LCONV_GATE_LOG>{});
 }
 
 template <int IO, int V, bool GATED> hipError_t scan_fwd(const ScanArgs& a, hipStream_t stream) {
     const unsigned grid = (unsigned)(a.B * a.nseg * a.cblocks);
-    if (a.nseg > 1) scan_fwd_kernel<IO, V, GATED, true><<<grid, 64 * a.waves, 0, stream>>>(a);
-    scan_fwd_kernel<IO, V, GATED, false><<<grid, 64 * a.waves, 0, stream>>>(a);
+    by_flags(a.gate, a.mix, [&](auto gate, auto mix) {
+        if (a.nseg > 1) scan_segments_kernel<IO, V, GATED, gate.value, mix.value, false><<<grid, 64 * a.waves, 0, stream>>>(a);
+        scan_fwd_kernel<IO, V, GATED, gate.value, mix.value><<<grid, 64 * a.waves, 0, stream>>>(a);
+    });
     return hipGetLastError();
 }
 template <int IO> hipError_t scan_fwd(const ScanArgs& a, hipStream_t stream) {
-    if (a.vec == 1) return a.i.p ? scan_fwd<IO, 1, true>(a, stream) : scan_fwd<IO, 1, false>(a, stream);
-    return a.i.p ? scan_fwd<IO, 2, true>(a, stream) : scan_fwd<IO, 2, false>(a, stream);
+    if constexpr (IO != CT_F32) {
+        if (a.vec == 2) return a.i.p ? scan_fwd<IO, 2, true>(a, stream) : scan_fwd<IO, 2, false>(a, stream);
+    }
+    return a.i.p ? scan_fwd<IO, 1, true>(a, stream) : scan_fwd<IO, 1, false>(a, stream);
 }
 
-template <int IO, int V, bool GATED> hipError_t scan_bwd(const ScanArgs& a, hipStream_t stream) {
+template <int IO, bool GATED> hipError_t scan_bwd(const ScanArgs& a, hipStream_t stream) {
     const unsigned grid = (unsigned)(a.B * a.nseg * a.cblocks);
-    if (a.nseg > 1) scan_bwd_kernel<IO, V, false, true><<<grid, 64 * a.waves, 0, stream>>>(a);
-    scan_bwd_kernel<IO, V, GATED, false><<<grid, 64 * a.waves, 0, stream>>>(a);
+    by_flags(a.gate, a.mix, [&](auto gate, auto mix) {
+        if (a.nseg > 1) scan_segments_kernel<IO, 1, false, gate.value, LCONV_MIX_PLAIN, true><<<grid, 64 * a.waves, 0, stream>>>(a);
+        scan_bwd_kernel<IO, 1, GATED, gate.value, mix.value><<<grid, 64 * a.waves, 0, stream>>>(a);
+    });
     return hipGetLastError();
 }
 template <int IO> hipError_t scan_bwd(const ScanArgs& a, hipStream_t stream) {
-    if (a.vec == 1) return a.i.p ? scan_bwd<IO, 1, true>(a, stream) : scan_bwd<IO, 1, false>(a, stream);
-    return a.i.p ? scan_bwd<IO, 2, true>(a, stream) : scan_bwd<IO, 2, false>(a, stream);
+    return a.i.p ? scan_bwd<IO, true>(a, stream) : scan_bwd<IO, false>(a, stream);
 }
 
 }  // namespace

@@ -159,7 +159,7 @@ template <int IO, int V, int K> __global__ void __launch_bounds__(256) conv_bwd_
                         float p = taps.b[v];
 #pragma unroll
                         for (int j = 0; j < K; ++j) p = fmaf(taps.w[j][v], win[j].v[v], p);
-                        const float e = __expf(-fabsf(p)), big = fast_rcp(1.f + e), small = e * big;
+                        const float e = fast_exp2(-kLog2e * fabsf(p)), big = fast_rcp(1.f + e), small = e * big;
                         g *= (p >= 0.f ? big : small) * fmaf(p, p >= 0.f ? small : big, 1.f);
                     }
                     g = on ? g : 0.f;

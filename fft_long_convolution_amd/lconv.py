@@ -111,9 +111,9 @@ def load(path: str = LIB_PATH):
         "lconv_layernorm_bwd_workspace_bytes": (sz, [i64, i64]),
         "lconv_layernorm_bwd": (i, [vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, vp, i64, i64, i, vp, sz, vp]),
         "lconv_gated_scan_marks_bytes": (sz, [i64] * 3),
-        "lconv_gated_scan_workspace_bytes": (sz, [i64] * 3),
+        "lconv_gated_scan_workspace_bytes": (sz, [i64] * 3 + [i]),
         "lconv_gated_scan_fwd": (i, [vp, sp, vp, sp, vp, sp, vp, vp, vp, vp, sp, vp, vp] + [i64] * 3 + [i, i, vp, sz, vp]),
-        "lconv_gated_scan_bwd_workspace_bytes": (sz, [i64] * 3 + [i]),
+        "lconv_gated_scan_bwd_workspace_bytes": (sz, [i64] * 3 + [i, i]),
         "lconv_gated_scan_bwd": (i, [vp, sp, vp, sp, vp, sp, vp, sp, vp, vp, vp, vp, vp, sp, vp, sp, vp, sp, vp, vp]
                                  + [i64] * 3 + [i, i, vp, sz, vp]),
         "lconv_gated_scan_step": (i, [vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, i64] + [i64] * 3 + [i, i, vp]),
@@ -354,8 +354,8 @@ def lconv_gated_scan_marks_bytes(B, N, C):
     return load().lconv_gated_scan_marks_bytes(B, N, C)
 
 
-def lconv_gated_scan_workspace_bytes(B, N, C):
-    return load().lconv_gated_scan_workspace_bytes(B, N, C)
+def lconv_gated_scan_workspace_bytes(B, N, C, dtype):
+    return load().lconv_gated_scan_workspace_bytes(B, N, C, dtype)
 
 
 def lconv_gated_scan_fwd(x, xs, z, zs, input_gate, igs, rate, state_in, lengths, y, ys, state_out, marks, B, N, C, flags,
@@ -364,8 +364,8 @@ def lconv_gated_scan_fwd(x, xs, z, zs, input_gate, igs, rate, state_in, lengths,
                                        N, C, flags, dtype, workspace, workspace_bytes, stream)
 
 
-def lconv_gated_scan_bwd_workspace_bytes(B, N, C, flags):
-    return load().lconv_gated_scan_bwd_workspace_bytes(B, N, C, flags)
+def lconv_gated_scan_bwd_workspace_bytes(B, N, C, flags, dtype):
+    return load().lconv_gated_scan_bwd_workspace_bytes(B, N, C, flags, dtype)
 
 
 def lconv_gated_scan_bwd(dy, dys, x, xs, z, zs, input_gate, igs, rate, marks, dstate_out, lengths, dx, dxs, dz, dzs,
@@ -1387,7 +1387,7 @@ def gated_scan(x, z, gate="sigmoid", mix="plain", input_gate=None, rate=None, st
         if state_out is None and need_state:
             state_out = torch.empty((B, C), dtype=torch.float32, device=dev)
         marks = torch.empty(lconv_gated_scan_marks_bytes(B, N, C) // 4, dtype=torch.float32, device=dev) if need_marks else None
-        wsb = lconv_gated_scan_workspace_bytes(B, N, C)
+        wsb = lconv_gated_scan_workspace_bytes(B, N, C, dt)
         ws = torch.empty(wsb, dtype=torch.uint8, device=dev) if wsb else None
         _check(lconv_gated_scan_fwd(_ptr(x), xs, _ptr(z), zs, _ptr(input_gate), igs, _ptr(rate), _ptr(state), _ptr(lengths),
                                     _ptr(y), ys, _ptr(state_out), _ptr(marks), B, N, C, flags, dt, _ptr(ws), wsb, st),
@@ -1419,7 +1419,7 @@ def gated_scan_bwd(dy, x, z, marks, gate="sigmoid", mix="plain", input_gate=None
         dig, digs = (None, None) if input_gate is None else _token_output("dinput_gate", None, x)
         dr = torch.empty((C,), dtype=torch.float32, device=dev) if rate is not None and need_drate else None
         ds = torch.empty((B, C), dtype=torch.float32, device=dev) if need_dstate else None
-        wsb = lconv_gated_scan_bwd_workspace_bytes(B, N, C, flags)
+        wsb = lconv_gated_scan_bwd_workspace_bytes(B, N, C, flags, dt)
         ws = torch.empty(wsb, dtype=torch.uint8, device=dev) if wsb else None
         _check(lconv_gated_scan_bwd(_ptr(dy), dys, _ptr(x), xs, _ptr(z), zs, _ptr(input_gate), igs, _ptr(rate), _ptr(marks),
                                     _ptr(dstate), _ptr(lengths), _ptr(dx), dxs, _ptr(dz), dzs, _ptr(dig), digs, _ptr(dr),

@@ -661,7 +661,7 @@ lconv_status_t lconv_qknorm_rotary_bwd(const void* dyq, const lconv_strides_t* d
  *   lengths      [B] int32, device, or NULL (every row N long); taken as min(max(len, 0), N)
  *   marks        lconv_gated_scan_marks_bytes(B, N, C) bytes, written, or NULL: states along the way, which the gradient
  *                call takes in place of y
- *   workspace    lconv_gated_scan_workspace_bytes(B, N, C) bytes (may be NULL if that is 0)
+ *   workspace    lconv_gated_scan_workspace_bytes(B, N, C, dtype) bytes (may be NULL if that is 0)
  * Strides are lconv_strides_t without h, in elements, of any size that keeps an output's rows apart; NULL: dense.  These
  * operands may begin at any element, the others are 16-byte aligned.  Gates, states and sums are fp32, a's distance from 1 to its own size, so that memories of many thousand
  * tokens neither end early nor drift.  A value that is not finite reaches what the recurrence lets it reach, as a value that
@@ -676,7 +676,7 @@ lconv_status_t lconv_qknorm_rotary_bwd(const void* dyq, const lconv_strides_t* d
 #define LCONV_MIX_CONVEX   4
 #define LCONV_MIX_NORM     8
 size_t lconv_gated_scan_marks_bytes(int64_t B, int64_t N, int64_t C);
-size_t lconv_gated_scan_workspace_bytes(int64_t B, int64_t N, int64_t C);
+size_t lconv_gated_scan_workspace_bytes(int64_t B, int64_t N, int64_t C, lconv_dtype_t dtype);
 lconv_status_t lconv_gated_scan_fwd(const void* x, const lconv_strides_t* x_strides, const void* z,
                                     const lconv_strides_t* z_strides, const void* input_gate,
                                     const lconv_strides_t* input_gate_strides, const float* rate, const float* state_in,
@@ -692,10 +692,10 @@ lconv_status_t lconv_gated_scan_fwd(const void* x, const lconv_strides_t* x_stri
  *   dz = dl,  dl (1 - a),  dl l (1 - sigmoid(z));  drate[c] = -sum_{b,t} dl sigmoid(z);   dstate_in = a_0 G_0
  *   dx, dz, dinput_gate  [B][N][C] dtype, written (zeros past a row's length); dinput_gate with input_gate only
  *   drate      [C] fp32, written, or NULL;  dstate_in  [B][C] fp32, written, or NULL, may be dstate_out
- *   workspace  lconv_gated_scan_bwd_workspace_bytes(B, N, C, flags) bytes (may be NULL if that is 0)
+ *   workspace  lconv_gated_scan_bwd_workspace_bytes(B, N, C, flags, dtype) bytes (may be NULL if that is 0)
  * No atomics: results repeat bit for bit.
  */
-size_t lconv_gated_scan_bwd_workspace_bytes(int64_t B, int64_t N, int64_t C, int flags);
+size_t lconv_gated_scan_bwd_workspace_bytes(int64_t B, int64_t N, int64_t C, int flags, lconv_dtype_t dtype);
 lconv_status_t lconv_gated_scan_bwd(const void* dy, const lconv_strides_t* dy_strides, const void* x,
                                     const lconv_strides_t* x_strides, const void* z, const lconv_strides_t* z_strides,
                                     const void* input_gate, const lconv_strides_t* input_gate_strides, const float* rate,

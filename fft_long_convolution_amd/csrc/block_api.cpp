@@ -355,8 +355,11 @@ bool conv_dims_ok(int64_t B, int64_t N, int64_t C, int64_t K) {
     if (K < 2 || K > LCONV_SHORTCONV_MAX_TAPS || N >= ((int64_t)1 << 31) || C > ((int64_t)1 << 24) || B > ((int64_t)1 << 24)) return false;
     if (!mul_ok(B, C, &t) || t > INT64_MAX / 64) return false;
     if (B == 0 || N == 0 || C == 0) return true;
-    const ConvPlan p = conv_plan(B, N, C, false);
-    return B * p.runs < ((int64_t)1 << 31) && (int64_t)p.cgroups * p.groups <= kMaxGrid && B * ((C + 511) / 256) <= kMaxGrid;
+    for (bool inplace : {false, true}) {
+        const ConvPlan p = conv_plan(B, N, C, K, false, inplace);
+        if (B * p.runs >= ((int64_t)1 << 31) || (int64_t)p.cgroups * p.groups > kMaxGrid) return false;
+    }
+    return B * ((C + 511) / 256) <= kMaxGrid;      // single tokens
 }
 
 void set_plan(ConvArgs* a, const ConvPlan& p) {
@@ -393,13 +396,13 @@ lconv_status_t lconv_shortconv_fwd(const void* x, const lconv_strides_t* x_strid
         return LCONV_ERR_ALIASING;
     a.w = weight; a.bias = bias; a.state_in = state_in; a.lengths = lengths; a.y = y; a.yb = yo.b; a.yn = yo.n; a.state_out = state_out;
     a.B = B; a.N = N; a.C = C; a.K = (int)K; a.silu = flags & LCONV_SHORTCONV_SILU;
-    set_plan(&a, conv_plan(B, N, C, false));
+    set_plan(&a, conv_plan(B, N, C, K, false, state_in && state_in == state_out));
     return hip_status(launch_conv_fwd(dtype, a, stream));
 }
 
 size_t lconv_shortconv_bwd_workspace_bytes(int64_t B, int64_t N, int64_t C, int64_t K) {
     if (B <= 0 || N <= 0 || C <= 0 || !conv_dims_ok(B, N, C, K)) return 0;
-    return (size_t)conv_plan(B, N, C, true).groups * (size_t)(K + 1) * (size_t)C * 4;
+    return (size_t)conv_plan(B, N, C, K, true, false).groups * (size_t)(K + 1) * (size_t)C * 4;
 }
 
 lconv_status_t lconv_shortconv_bwd(const void* dy, const lconv_strides_t* dy_strides, const void* x,
@@ -434,7 +437,7 @@ lconv_status_t lconv_shortconv_bwd(const void* dy, const lconv_strides_t* dy_str
     if (!weight) return LCONV_ERR_NULL_POINTER;
     const Range rw = buffer(weight, C * K, es), rb = buffer(bias, C, es), rl = buffer(lengths, B, 4);
     if (clash({rdx, rdsi, rdw, rdb}, {rdy, rx, rw, rb, rl, rsi, rdso})) return LCONV_ERR_ALIASING;
-    const ConvPlan p = conv_plan(B, N, C, true);
+    const ConvPlan p = conv_plan(B, N, C, K, true, false);
     if (dweight || dbias) {
         const size_t need = lconv_shortconv_bwd_workspace_bytes(B, N, C, K);
         if (!workspace || workspace_bytes < need) return LCONV_ERR_WORKSPACE;

@@ -134,7 +134,7 @@ template <int V> __device__ __forceinline__ Place<V> place(const ScanArgs& a) {
     w.end = w.first + a.seg_len < a.N ? w.first + a.seg_len : a.N;
     w.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t c = (int64_t)w.cb * 64 * V + (threadIdx.x & 63) * V;
-    w.c = (uint32_t)(c < a.C ? c : a.C - V);
+    w.c = (uint32_t)(c < a.C - V ? c : a.C - V);
     return w;
 }
 

@@ -38,7 +38,7 @@ __device__ __forceinline__ Run run_of(const ConvArgs& a, uint32_t i) {
 template <int V> __device__ __forceinline__ uint32_t channel_of(const ConvArgs& a, uint32_t* group) {
     *group = blockIdx.x / (uint32_t)a.cgroups;
     const int64_t c = ((int64_t)(blockIdx.x - *group * (uint32_t)a.cgroups) * 64 + (threadIdx.x & 63)) * V;
-    return (uint32_t)(c < a.C ? c : a.C - V);
+    return (uint32_t)(c < a.C - V ? c : a.C - V);
 }
 
 // x of token t, which may lie before the row's first; zero at and behind its end

@@ -293,7 +293,8 @@ lconv_status_t lconv_qknorm_rotary_fwd(const void* q, const lconv_strides_t* q_s
 
 size_t lconv_qknorm_rotary_bwd_workspace_bytes(int64_t B, int64_t H, int64_t G, int64_t N, int64_t D, int64_t rot) {
     if (B <= 0 || H < 0 || G < 0 || H + G <= 0 || N <= 0 || rot < 0 || !qk_dims_ok(B, H, G, N, D, rot, 0)) return 0;
-    return (size_t)qk_parts(qk_plan(B * N, D, rot, (int)(H + G))) * 2 * (size_t)D * 4;
+    const QkGradPlan g = qk_grad_plan(B * N, D, rot, H, G);
+    return (size_t)(g.parts[0] + g.parts[1]) * (size_t)D * 4;
 }
 
 lconv_status_t lconv_qknorm_rotary_bwd(const void* dyq, const lconv_strides_t* dyq_strides, const void* dyk,

@@ -43,8 +43,13 @@ __device__ __forceinline__ Unit unit_of(const QkArgs& a, int u, int turns, int u
 }
 
 template <int IO> struct Head { Raw8<IO> lo, hi; };
-template <int IO> __device__ __forceinline__ Head<IO> load_head(const void* p, int64_t at, const Unit& t) {
-    return Head<IO>{raw8_part<IO>(p, at + t.lo, t.nlo), raw8_part<IO>(p, at + t.hi, t.nhi)};
+// FULL: every lane has two whole groups
+template <int IO, bool FULL> __device__ __forceinline__ Head<IO> load_head(const void* p, int64_t at, const Unit& t) {
+    return Head<IO>{raw8_part<IO>(p, at + t.lo, FULL ? 8 : t.nlo), raw8_part<IO>(p, at + t.hi, FULL ? 8 : t.nhi)};
+}
+template <int IO, bool FULL> __device__ __forceinline__ void store_head(void* p, int64_t at, const Unit& t, const float* x) {
+    store8_part<IO>(p, at + t.lo, FULL ? 8 : t.nlo, x);
+    store8_part<IO>(p, at + t.hi, FULL ? 8 : t.nhi, x + 8);
 }
 template <int IO> __device__ __forceinline__ void widen(const Head<IO>& h, float* x) {
     unpack_raw<IO>(h.lo.w, x);
@@ -70,10 +75,10 @@ __device__ __forceinline__ void turn_pairs(float* v, const float* c, const float
     }
 }
 
-__device__ __forceinline__ void token_sines(const QkArgs& a, const Unit& t, int64_t b, int64_t n, float* c, float* s) {
+template <bool FULL> __device__ __forceinline__ void token_sines(const QkArgs& a, const Unit& t, int64_t b, int64_t n, float* c, float* s) {
     const int64_t pos = a.positions ? (int64_t)a.positions[b * a.pos_stride + n] : n;
     float f[8];
-    load8_part<CT_F32>(a.inv_freq, t.p, t.n, f);
+    load8_part<CT_F32>(a.inv_freq, t.p, FULL ? 8 : t.n, f);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
         sines((double)pos * (double)f[k], &s[k], &c[k]);
@@ -83,11 +88,11 @@ __device__ __forceinline__ void token_sines(const QkArgs& a, const Unit& t, int6
 }
 
 // how many of a lane's 16 elements are the head's, by index
-__device__ __forceinline__ bool has(const Unit& t, int e) { return e < 8 ? e < t.nlo : e - 8 < t.nhi; }
+template <bool FULL> __device__ __forceinline__ bool has(const Unit& t, int e) { return FULL || (e < 8 ? e < t.nlo : e - 8 < t.nhi); }
 
 // u = x (centred: less its mean) in place; returns r.  The mean takes two sums: what the first one's rounding leaves shows in the
 // sum of the centred values.
-template <int LANES, bool CENTRED> __device__ __forceinline__ float normed(float* x, const Unit& t, int D, float eps) {
+template <int LANES, bool CENTRED, bool FULL> __device__ __forceinline__ float normed(float* x, const Unit& t, int D, float eps) {
     const float inv = 1.f / (float)D;
     float s = 0.f, q = 0.f;
     if constexpr (CENTRED) {
@@ -99,7 +104,7 @@ template <int LANES, bool CENTRED> __device__ __forceinline__ float normed(float
         s = 0.f;
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-            x[e] = has(t, e) ? x[e] - first : 0.f;
+            x[e] = has<FULL>(t, e) ? x[e] - first : 0.f;
             s += x[e];
         }
     }
@@ -112,16 +117,16 @@ template <int LANES, bool CENTRED> __device__ __forceinline__ float normed(float
         var -= rest * rest;
         var = var < 0.f ? 0.f : var;       // rounding; a NaN stays one
 #pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = has(t, e) ? x[e] - rest : 0.f;
+        for (int e = 0; e < 16; ++e) x[e] = has<FULL>(t, e) ? x[e] - rest : 0.f;
     }
     return 1.f / sqrtf(var + eps);
 }
 
-template <int IO> __device__ __forceinline__ void load_weights(const QkArgs& a, const Unit& t, float (*w)[16]) {
+template <int IO, bool FULL> __device__ __forceinline__ void load_weights(const QkArgs& a, const Unit& t, float (*w)[16]) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         if (a.w[i]) {
-            widen<IO>(load_head<IO>(a.w[i], 0, t), w[i]);
+            widen<IO>(load_head<IO, FULL>(a.w[i], 0, t), w[i]);
         } else {
 #pragma unroll
             for (int e = 0; e < 16; ++e) w[i][e] = 1.f;
@@ -129,7 +134,7 @@ template <int IO> __device__ __forceinline__ void load_weights(const QkArgs& a, 
     }
 }
 
-template <int IO, int LANES, bool CENTRED>
+template <int IO, int LANES, bool CENTRED, bool FULL>
 __global__ void __launch_bounds__(256) qknorm_fwd_kernel(QkArgs a, QkPlan p) {
     const int64_t g = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LANES;
     const bool any = g < p.items;                       // lanes of a group go together; a group past the last does as the first
@@ -140,73 +145,72 @@ __global__ void __launch_bounds__(256) qknorm_fwd_kernel(QkArgs a, QkPlan p) {
     const int h0 = (int)hg * p.per, all = a.heads[0] + a.heads[1], end = h0 + p.per < all ? h0 + p.per : all;
     const auto load = [&](int h) LCV_INLINE {
         const int i = h >= a.heads[0];
-        return load_head<IO>(a.x[i], b * a.xs[i].b + (int64_t)(i ? h - a.heads[0] : h) * a.xs[i].h + n * a.xs[i].n, t);
+        return load_head<IO, FULL>(a.x[i], b * a.xs[i].b + (int64_t)(i ? h - a.heads[0] : h) * a.xs[i].h + n * a.xs[i].n, t);
     };
     Head<IO> next = load(h0);
     float w[2][16], c[8], s[8];
-    load_weights<IO>(a, t, w);
-    if (t.turn) token_sines(a, t, b, n, c, s);
+    load_weights<IO, FULL>(a, t, w);
+    if (t.turn) token_sines<FULL>(a, t, b, n, c, s);
     for (int h = h0; h < end; ++h) {
         const Head<IO> now = next;
         if (h + 1 < end) next = load(h + 1);
         const int i = h >= a.heads[0];
         float x[16];
         widen<IO>(now, x);
-        const float r = normed<LANES, CENTRED>(x, t, a.D, a.eps);
+        const float r = normed<LANES, CENTRED, FULL>(x, t, a.D, a.eps);
 #pragma unroll
         for (int e = 0; e < 16; ++e) x[e] *= r * (i ? w[1][e] : w[0][e]);
         if (t.turn) turn_pairs(x, c, s, 1.f, inter);
         if (any) {
             const int64_t at = b * a.ys[i].b + (int64_t)(i ? h - a.heads[0] : h) * a.ys[i].h + n * a.ys[i].n;
-            store8_part<IO>(a.y[i], at + t.lo, t.nlo, x);
-            store8_part<IO>(a.y[i], at + t.hi, t.nhi, x + 8);
+            store_head<IO, FULL>(a.y[i], at, t, x);
         }
     }
 }
 
-template <int IO, int LANES, bool CENTRED>
-__global__ void __launch_bounds__(256) qknorm_bwd_kernel(QkArgs a, QkPlan p) {
+// Workgroups first .. of the grid are q's, the others k's.
+template <int IO, int LANES, bool CENTRED, bool FULL>
+__global__ void __launch_bounds__(256) qknorm_bwd_kernel(QkArgs a, QkGradPlan g) {
     constexpr int GROUPS = 256 / LANES;
+    const int i = (int)blockIdx.x >= g.parts[0], parts = g.parts[i], block = (int)blockIdx.x - (i ? g.parts[0] : 0), heads = a.heads[i];
+    const QkPlan& p = g.p[i];
     const bool inter = a.flags & LCONV_ROTARY_INTERLEAVED;
-    const int lane = threadIdx.x % LANES, all = a.heads[0] + a.heads[1];
+    const int lane = threadIdx.x % LANES;
     const Unit t = unit_of(a, lane, p.turns, p.units);
     const float inv = 1.f / (float)a.D;
-    float w[2][16], sum[2][16] = {};
-    load_weights<IO>(a, t, w);
-    for (int64_t g0 = (int64_t)blockIdx.x * GROUPS; g0 < p.items; g0 += (int64_t)gridDim.x * GROUPS) {
-        const int64_t g = g0 + threadIdx.x / LANES;
-        const bool any = g < p.items;
-        const uint32_t item = (uint32_t)(any ? g : 0), row = item / (uint32_t)p.hgroups, hg = item - row * (uint32_t)p.hgroups;
+    Head<IO> w{};
+    if (a.w[i]) w = load_head<IO, FULL>(a.w[i], 0, t);
+    float sum[16] = {};
+    for (int64_t g0 = (int64_t)block * GROUPS; g0 < p.items; g0 += (int64_t)parts * GROUPS) {
+        const int64_t at = g0 + threadIdx.x / LANES;
+        const bool any = at < p.items;
+        const uint32_t item = (uint32_t)(any ? at : 0), row = item / (uint32_t)p.hgroups, hg = item - row * (uint32_t)p.hgroups;
         const int64_t b = row / (uint64_t)a.N, n = row - b * a.N;
-        const int h0 = (int)hg * p.per, end = h0 + p.per < all ? h0 + p.per : all;
+        const int h0 = (int)hg * p.per, end = h0 + p.per < heads ? h0 + p.per : heads;
         Head<IO> nx, nd;
         const auto load = [&](int h) LCV_INLINE {
-            const int i = h >= a.heads[0];
-            const int64_t hh = i ? h - a.heads[0] : h;
-            nx = load_head<IO>(a.x[i], b * a.xs[i].b + hh * a.xs[i].h + n * a.xs[i].n, t);
-            nd = load_head<IO>(a.dy[i], b * a.dys[i].b + hh * a.dys[i].h + n * a.dys[i].n, t);
+            nx = load_head<IO, FULL>(a.x[i], b * a.xs[i].b + (int64_t)h * a.xs[i].h + n * a.xs[i].n, t);
+            nd = load_head<IO, FULL>(a.dy[i], b * a.dys[i].b + (int64_t)h * a.dys[i].h + n * a.dys[i].n, t);
         };
         load(h0);
         float c[8], s[8];
-        if (t.turn) token_sines(a, t, b, n, c, s);
+        if (t.turn) token_sines<FULL>(a, t, b, n, c, s);
         for (int h = h0; h < end; ++h) {
-            float u[16], d[16];
+            float u[16], d[16], wf[16];
             widen<IO>(nx, u);
             widen<IO>(nd, d);
             if (h + 1 < end) load(h + 1);
-            const int i = h >= a.heads[0];
-            const float r = normed<LANES, CENTRED>(u, t, a.D, a.eps);
+            const float r = normed<LANES, CENTRED, FULL>(u, t, a.D, a.eps);
             if (t.turn) turn_pairs(d, c, s, -1.f, inter);
+            widen<IO>(w, wf);
             float hu = 0.f, hs = 0.f;
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
                 u[e] *= r;
-                const float term = any ? d[e] * u[e] : 0.f;
-                sum[0][e] += i ? 0.f : term;
-                sum[1][e] += i ? term : 0.f;
-                d[e] *= i ? w[1][e] : w[0][e];
+                sum[e] += any ? d[e] * u[e] : 0.f;
+                if (a.w[i]) d[e] *= wf[e];
                 hu += d[e] * u[e];
-                if constexpr (CENTRED) hs += has(t, e) ? d[e] : 0.f;
+                if constexpr (CENTRED) hs += has<FULL>(t, e) ? d[e] : 0.f;
             }
             lane_sums<LANES>(hu, hs);
             hu *= inv;
@@ -214,44 +218,37 @@ __global__ void __launch_bounds__(256) qknorm_bwd_kernel(QkArgs a, QkPlan p) {
 #pragma unroll
             for (int e = 0; e < 16; ++e) d[e] = r * (d[e] - u[e] * hu - (CENTRED ? hs : 0.f));
             if (any) {
-                const int64_t at = b * a.ys[i].b + (int64_t)(i ? h - a.heads[0] : h) * a.ys[i].h + n * a.ys[i].n;
-                store8_part<IO>(a.y[i], at + t.lo, t.nlo, d);
-                store8_part<IO>(a.y[i], at + t.hi, t.nhi, d + 8);
+                const int64_t to = b * a.ys[i].b + (int64_t)h * a.ys[i].h + n * a.ys[i].n;
+                store_head<IO, FULL>(a.y[i], to, t, d);
             }
         }
     }
     if (!a.part) return;
     // the groups of a wave join by lanes, the waves through LDS, in a fixed order
-    __shared__ float join[4][2][16][LANES];
+    __shared__ float join[4][16][LANES];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int e = 0; e < 16; ++e) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-#pragma unroll
-            for (int k = LANES; k < 64; k *= 2) sum[i][e] += __shfl_xor(sum[i][e], k);
-            if ((threadIdx.x & 63) < LANES) join[threadIdx.x >> 6][i][e][lane] = sum[i][e];
-        }
+        for (int k = LANES; k < 64; k *= 2) sum[e] += __shfl_xor(sum[e], k);
+        if ((threadIdx.x & 63) < LANES) join[threadIdx.x >> 6][e][lane] = sum[e];
+    }
     __syncthreads();
     if (threadIdx.x >= LANES) return;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) sum[i][e] = (join[0][i][e][lane] + join[1][i][e][lane]) + (join[2][i][e][lane] + join[3][i][e][lane]);
-        const int64_t at = ((int64_t)blockIdx.x * 2 + i) * a.D;
-        store8_part<CT_F32>(a.part, at + t.lo, t.nlo, sum[i]);
-        store8_part<CT_F32>(a.part, at + t.hi, t.nhi, sum[i] + 8);
-    }
+    for (int e = 0; e < 16; ++e) sum[e] = (join[0][e][lane] + join[1][e][lane]) + (join[2][e][lane] + join[3][e][lane]);
+    const int64_t to = (int64_t)blockIdx.x * a.D;
+    store_head<CT_F32, FULL>(a.part, to, t, sum);
 }
 
-// The weights' gradients from the workgroups' sums: a workgroup takes 32 columns of q or k, its 8 groups of lanes every eighth
-// part, and joins the groups in order.
-__global__ void __launch_bounds__(256) qknorm_sum_kernel(const float* part, float* dq, float* dk, int parts, int D) {
-    __shared__ float join[8][32];
-    const int l = threadIdx.x & 31, q = threadIdx.x >> 5, c = blockIdx.x * 32 + l, i = blockIdx.y;
+// The weights' gradients from the workgroups' sums: a workgroup takes 32 columns of q or k, its 32 groups of lanes every
+// 32nd part, and joins the groups in order.
+__global__ void __launch_bounds__(1024) qknorm_sum_kernel(const float* part, float* dq, float* dk, int qparts, int kparts, int D) {
+    __shared__ float join[32][33];
+    const int l = threadIdx.x & 31, q = threadIdx.x >> 5, c = blockIdx.x * 32 + l, i = blockIdx.y, end = i ? qparts + kparts : qparts;
     float u = 0.f;
     if (c < D) {
 #pragma unroll 8
-        for (int k = q; k < parts; k += 8) u += part[((int64_t)k * 2 + i) * D + c];
+        for (int k = (i ? qparts : 0) + q; k < end; k += 32) u += part[(int64_t)k * D + c];
     }
     join[q][l] = u;
     __syncthreads();
@@ -259,7 +256,7 @@ __global__ void __launch_bounds__(256) qknorm_sum_kernel(const float* part, floa
     if (q || c >= D || !out) return;
     float s = 0.f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) s += join[k][l];
+    for (int k = 0; k < 32; ++k) s += join[k][l];
     out[c] = s;
 }
 
@@ -280,6 +277,18 @@ template <typename F> hipError_t by_dtype(int dtype, F&& f) {
     return hipGetLastError();
 }
 
+// f(centred, full) for a call
+template <typename F> void by_form(const QkArgs& a, const QkPlan& p, F&& f) {
+    using std::integral_constant;
+    const bool full = a.rot % 16 == 0 && (a.D - a.rot) % 16 == 0 && p.lanes == p.units;
+    const auto go = [&](auto centred) {
+        if (full) f(centred, integral_constant<bool, true>{});
+        else f(centred, integral_constant<bool, false>{});
+    };
+    if (a.flags & LCONV_QKNORM_CENTRED) go(integral_constant<bool, true>{});
+    else go(integral_constant<bool, false>{});
+}
+
 }  // namespace
 
 hipError_t launch_qknorm_fwd(int dtype, const QkArgs& a, hipStream_t stream) {
@@ -287,28 +296,31 @@ hipError_t launch_qknorm_fwd(int dtype, const QkArgs& a, hipStream_t stream) {
     const unsigned grid = (unsigned)((p.items * p.lanes + 255) / 256);
     return by_dtype(dtype, [&](auto io) {
         by_lanes(p.lanes, [&](auto lanes) {
-            if (a.flags & LCONV_QKNORM_CENTRED) qknorm_fwd_kernel<io.value, lanes.value, true><<<grid, 256, 0, stream>>>(a, p);
-            else qknorm_fwd_kernel<io.value, lanes.value, false><<<grid, 256, 0, stream>>>(a, p);
+            by_form(a, p, [&](auto centred, auto full) {
+                qknorm_fwd_kernel<io.value, lanes.value, centred.value, full.value><<<grid, 256, 0, stream>>>(a, p);
+            });
         });
     });
 }
 
 hipError_t launch_qknorm_bwd(int dtype, const QkArgs& a, hipStream_t stream) {
     const int64_t tokens = a.B * a.N;
-    int parts = 0;
+    QkGradPlan g{};
     hipError_t e = hipSuccess;
-    if (tokens > 0) {
-        const QkPlan p = qk_plan(tokens, a.D, a.rot, a.heads[0] + a.heads[1]);
-        parts = (int)qk_parts(p);
+    if (tokens > 0 && a.heads[0] + a.heads[1] > 0) {
+        g = qk_grad_plan(tokens, a.D, a.rot, a.heads[0], a.heads[1]);
+        const unsigned grid = (unsigned)(g.parts[0] + g.parts[1]);
+        const QkPlan& p = g.p[a.heads[0] ? 0 : 1];
         e = by_dtype(dtype, [&](auto io) {
             by_lanes(p.lanes, [&](auto lanes) {
-                if (a.flags & LCONV_QKNORM_CENTRED) qknorm_bwd_kernel<io.value, lanes.value, true><<<parts, 256, 0, stream>>>(a, p);
-                else qknorm_bwd_kernel<io.value, lanes.value, false><<<parts, 256, 0, stream>>>(a, p);
+                by_form(a, p, [&](auto centred, auto full) {
+                    qknorm_bwd_kernel<io.value, lanes.value, centred.value, full.value><<<grid, 256, 0, stream>>>(a, g);
+                });
             });
         });
     }
     if (e != hipSuccess || (!a.dw[0] && !a.dw[1])) return e;
-    qknorm_sum_kernel<<<dim3((unsigned)((a.D + 31) / 32), 2), 256, 0, stream>>>(a.part, a.dw[0], a.dw[1], parts, a.D);
+    qknorm_sum_kernel<<<dim3((unsigned)((a.D + 31) / 32), 2), 1024, 0, stream>>>(a.part, a.dw[0], a.dw[1], g.parts[0], g.parts[1], a.D);
     return hipGetLastError();
 }
 

@@ -434,7 +434,10 @@ def status_string(status: int) -> str:
 
 # ---- torch wrappers ---------------------------------------------------------------------------
 
+@functools.lru_cache(maxsize=None)
 def _torch():
+    """torch, imported when a tensor first comes (and kept: an import statement takes a quarter of a microsecond each time, of
+    which a call for single tokens would meet a dozen)."""
     import torch
     return torch
 
@@ -472,7 +475,7 @@ def _need(name, t, shape, dtype, optional=False):
         raise TypeError(f"{name} must be a torch tensor, got {type(t).__name__}")
     if t.dtype != dtype:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous (a strided or transposed view would be read as dense rows)")
@@ -867,9 +870,11 @@ def _same_gpu(names, operands):
     dev = None
     for t in operands:
         if t is not None:
-            if not t.is_cuda or (dev is not None and t.get_device() != dev):
-                _on_gpu(**dict(zip(names.split(), operands)))    # says which
-            dev = t.get_device()
+            at = t.get_device()                                   # less than zero: not a GPU
+            if at != dev:
+                if at < 0 or dev is not None:
+                    _on_gpu(**dict(zip(names.split(), operands)))    # says which
+                dev = at
     return dev
 
 
@@ -898,8 +903,11 @@ def _view(name, t, shape, dtype):
 def _in_order_of(x, shape):
     """An empty [B, H, N, D] tensor with x's order of heads and tokens."""
     torch = _torch()
-    if x.dim() == 4 and x.shape[1] > 1 and x.shape[2] > 1 and x.stride(1) < x.stride(2):
-        return torch.empty((shape[0], shape[2], shape[1], shape[3]), dtype=x.dtype, device=x.device).transpose(1, 2)
+    if x.dim() == 4 and x.shape[1] > 1 and x.shape[2] > 1:
+        s = x.stride()
+        if s[1] < s[2]:
+            B, H, N, D = shape
+            return torch.empty_strided(shape, (N * H * D, D, H * D, 1), dtype=x.dtype, device=x.device)
     return torch.empty(shape, dtype=x.dtype, device=x.device)
 
 

@@ -177,17 +177,18 @@ struct ConvPlan {
 };
 // The last lane of a width that four does not divide shares channels with the one before it; inplace (one buffer for both
 // states) forbids that, since the two may be in different workgroups, one of which would read what the other has written.
-// Runs: every wave reads K - 1 tokens of its neighbours again, and few calls have waves to spare.  Measured (bf16, us, forward /
-// gradients): 8 x 2048 x 4096, K = 4: runs of 16 46 / 110, 32 47 / 96, 64 49 / 97; 1 x 65536 x 2048, K = 8: 32 117 / 269,
-// 64 113 / 235, 128 115 / 223; 2 x 2048 x 2048, K = 4: 8 10 / 22, 16 10 / 20, 32 11 / 25; 3 x 1001 x 1000, K = 3: 8 6.4 / 15,
-// 16 6.5 / 17, 32 8.9 / 23.
+// Runs: every wave reads K - 1 tokens of its neighbours again, and few calls have waves to spare.  The gradients' waves take
+// runs in turn, as many waves as the chip holds (three workgroups to a compute unit by their registers, of more than four taps
+// two).  Measured (bf16, us, forward / gradients): 8 x 2048 x 4096, K = 4: runs of 16 49 / 108, 32 48 / 94, 64 49 / 99, in 512,
+// 768, 1024 workgroups 103, 94, 107; 1 x 65536 x 2048, K = 8: 32 119 / 256, 64 114 / 232, 128 116 / 206, in 512, 768, 1024
+// workgroups 206, 215, 213; 2 x 2048 x 2048, K = 4: 16 10 / 20, 32 11 / 23; 3 x 1001 x 1000, K = 3: 16 6.5 / 16, 32 8.8 / 21.
 inline ConvPlan conv_plan(int64_t B, int64_t N, int64_t C, int64_t K, bool grad, bool inplace) {
     ConvPlan p{};
     p.vec = C % 4 == 0 || (C > 4 && !inplace) ? 4 : 1;
     p.cgroups = (int)((C + 64 * p.vec - 1) / (64 * p.vec));
     p.run = K <= 4 ? 32 : grad ? 128 : 64;
     while (p.run > kConvMaxTaps && B * ((N + p.run - 1) / p.run) * p.cgroups < 256 * 8) p.run /= 2;
-    const int64_t runs = (N + p.run - 1) / p.run, groups = (B * runs + 3) / 4, most = (1024 + p.cgroups - 1) / p.cgroups;
+    const int64_t runs = (N + p.run - 1) / p.run, groups = (B * runs + 3) / 4, most = ((K <= 4 ? 768 : 512) + p.cgroups - 1) / p.cgroups;
     p.runs = (int)runs;
     p.groups = (int)(grad && groups > most ? most : groups);
     return p;

@@ -121,7 +121,8 @@ template <int IO, int V, int K> __global__ void __launch_bounds__(256) conv_bwd_
     const uint32_t total = (uint32_t)(a.B * a.runs);
     for (uint32_t i = group * 4 + wave; i < total; i += (uint32_t)a.groups * 4) {
         const Run r = run_of(a, i);
-        const int64_t xr = r.b * a.x.b, dr = r.b * a.dy.b, last = r.len - 1;
+        const int64_t xr = r.b * a.x.b, dr = r.b * a.dy.b;
+        const int64_t mine = r.t1 < r.len ? r.t1 : r.len, last = (r.t1 + K - 1 < r.len ? r.t1 + K - 1 : r.len) - 1;
         Lane<V> win[K], acc[K];          // acc[j] = dx of token t-K+1+j, what the tokens up to t add
 #pragma unroll
         for (int j = 0; j < K - 1; ++j) win[j + 1] = input<IO, V, K>(a, r, r.t0 - (K - 1) + j, c);
@@ -136,15 +137,16 @@ template <int IO, int V, int K> __global__ void __launch_bounds__(256) conv_bwd_
                 nd[k] = load_raw_v<IO, V>(a.dy.p, dr + at * a.dy.n, c);
             }
         };
-        if (r.len > 0) load(r.t0);
-        for (int64_t t0 = r.t0; t0 < r.t1 + K - 1; t0 += kGradBatch) {
+        // INNER: tokens of this run and of the row
+        const auto batch = [&](int64_t t0, auto inner) LCV_INLINE {
+            constexpr bool INNER = decltype(inner)::value;
 #pragma unroll
             for (int k = 0; k < kGradBatch; ++k) x[k] = nx[k], d[k] = nd[k];
-            if (r.len > 0) load(t0 + kGradBatch);
+            if (INNER || r.len > 0) load(t0 + kGradBatch);
 #pragma unroll
             for (int k = 0; k < kGradBatch; ++k) {
                 const int64_t t = t0 + k, s = t - (K - 1);
-                const bool on = t <= last, own = t < r.t1;
+                const bool on = INNER || t < r.len, own = INNER || t < mine;
                 float xv[V], dv[V];
                 widen<IO, V>(x[k], xv);
                 widen<IO, V>(d[k], dv);
@@ -153,23 +155,23 @@ template <int IO, int V, int K> __global__ void __launch_bounds__(256) conv_bwd_
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     win[K - 1].v[v] = on ? xv[v] : 0.f;
-                    acc[K - 1].v[v] = 0.f;
                     float g = dv[v];
                     if (a.silu) {
                         float p = taps.b[v];
 #pragma unroll
                         for (int j = 0; j < K; ++j) p = fmaf(taps.w[j][v], win[j].v[v], p);
-                        const float e = fast_exp2(-kLog2e * fabsf(p)), big = fast_rcp(1.f + e), small = e * big;
-                        g *= (p >= 0.f ? big : small) * fmaf(p, p >= 0.f ? small : big, 1.f);
+                        // s (1 + p (1 - s)), 1 - s = e s to its own size (where e is cut off, s is less than 1e-30)
+                        const float e = fast_exp2(-kLog2e * p), sig = fast_rcp(1.f + e);
+                        g *= sig * fmaf(p, fminf(e, 1e30f) * sig, 1.f);
                     }
                     g = on ? g : 0.f;
-                    const float mine = own ? g : 0.f;
-                    db[v] += mine;
+                    const float part = own ? g : 0.f;
+                    db[v] += part;
+                    acc[K - 1].v[v] = taps.w[K - 1][v] * g;
 #pragma unroll
-                    for (int j = 0; j < K; ++j) {
-                        dw[j][v] = fmaf(mine, win[j].v[v], dw[j][v]);
-                        acc[j].v[v] = fmaf(taps.w[j][v], g, acc[j].v[v]);
-                    }
+                    for (int j = 0; j < K; ++j) dw[j][v] = fmaf(part, win[j].v[v], dw[j][v]);
+#pragma unroll
+                    for (int j = 0; j < K - 1; ++j) acc[j].v[v] = fmaf(taps.w[j][v], g, acc[j].v[v]);
                 }
                 // dx of token s is complete
                 if (s >= r.t0 ? s < r.t1 : (r.first && a.state_out && s >= -(K - 1))) {
@@ -183,7 +185,11 @@ template <int IO, int V, int K> __global__ void __launch_bounds__(256) conv_bwd_
                     else store_v<IO, V>(a.state_out, (r.b * (K - 1) + s + K - 1) * a.C, c, acc[0].v);
                 }
             }
-        }
+        };
+        if (r.len > 0) load(r.t0);
+        int64_t t0 = r.t0;
+        for (; t0 + kGradBatch <= mine; t0 += kGradBatch) batch(t0, std::true_type{});
+        for (; t0 < r.t1 + K - 1; t0 += kGradBatch) batch(t0, std::false_type{});
     }
     if (!a.part) return;
     // the waves join through LDS, in their order
@@ -268,10 +274,10 @@ template <typename F> hipError_t by_dtype(int dtype, F&& f) {
     else f(std::integral_constant<int, CT_BF16>{});
     return hipGetLastError();
 }
-template <typename F> void by_taps(int K, bool four, F&& f) {
+template <typename F> void by_taps(int K, int vec, F&& f) {
     using std::integral_constant;
     const auto go = [&](auto k) {
-        if (four) f(integral_constant<int, 4>{}, k);
+        if (vec == 4) f(integral_constant<int, 4>{}, k);
         else f(integral_constant<int, 1>{}, k);
     };
     switch (K) {
@@ -289,7 +295,7 @@ template <typename F> void by_taps(int K, bool four, F&& f) {
 
 hipError_t launch_conv_fwd(int dtype, const ConvArgs& a, hipStream_t stream) {
     return by_dtype(dtype, [&](auto io) {
-        by_taps(a.K, a.vec == 4, [&](auto v, auto k) {
+        by_taps(a.K, a.vec, [&](auto v, auto k) {
             conv_fwd_kernel<io.value, v.value, k.value><<<(unsigned)a.cgroups * (unsigned)a.groups, 256, 0, stream>>>(a);
         });
     });
@@ -299,7 +305,7 @@ hipError_t launch_conv_bwd(int dtype, const ConvArgs& a, hipStream_t stream) {
     hipError_t e = hipSuccess;
     if (a.groups > 0)
         e = by_dtype(dtype, [&](auto io) {
-            by_taps(a.K, a.vec == 4, [&](auto v, auto k) {
+            by_taps(a.K, a.vec, [&](auto v, auto k) {
                 conv_bwd_kernel<io.value, v.value, k.value><<<(unsigned)a.cgroups * (unsigned)a.groups, 256, 0, stream>>>(a);
             });
         });
@@ -310,7 +316,7 @@ hipError_t launch_conv_bwd(int dtype, const ConvArgs& a, hipStream_t stream) {
 
 hipError_t launch_conv_step(int dtype, const ConvStepArgs& a, hipStream_t stream) {
     return by_dtype(dtype, [&](auto io) {
-        by_taps(a.K, a.C % 4 == 0, [&](auto v, auto k) {
+        by_taps(a.K, a.C % 4 == 0 ? 4 : 1, [&](auto v, auto k) {
             const unsigned grid = (unsigned)((a.B * (a.C / v.value) + 255) / 256);
             conv_step_kernel<io.value, v.value, k.value><<<grid, 256, 0, stream>>>(a);
         });

@@ -23,7 +23,8 @@ __global__ void __launch_bounds__(256) scan_rate_kernel(const float* part, float
     drate[c] = s;
 }
 
-// One token: h = a h + u in place, y = h.  Each element is read and written once: latency for few rows, HBM for many.
+// One token: h = a h + u in place, y = h.  Each element is read and written once: latency for few rows (64 x 2048 in bf16, 2.1 MB:
+// 3.3 us, about what an empty launch takes), HBM for many.
 template <int IO, int V, bool GATED> __global__ void __launch_bounds__(256) scan_step_kernel(ScanStepArgs a) {
     const int64_t per = a.C / V, i = (int64_t)blockIdx.x * 256 + threadIdx.x, b = i / per;
     const uint32_t c = (uint32_t)(i - b * per) * V;

@@ -8,6 +8,12 @@
 // sequence with the next tile's loads on their way: one pass over the data.  Calls of few rows are cut into segments along the
 // sequence: a first launch finds the segments' decays and sums, the second begins each segment with the join of those
 // before it.
+// Bound by HBM where a call has rows enough: 8 x 2048 x 4096 in bf16 with every input takes 113 us, 537 MB at 4.8 TB/s (the same
+// reads and writes with no arithmetic 106), under 37 vector instructions to a token and channel, 63 us of issue.  In segments
+// 1 x 65536 x 2048, sigmoid and convex, takes 122 us for the segments' sums (537 MB, 4.4 TB/s; 21 instructions and two slow ones
+// are 90 us of issue) and 158 for the pass (805 MB, 5.1 TB/s).  Gradients of 8 x 2048 x 2048 with every input: 117 us for 470 MB,
+// 4.0 TB/s; there is one workgroup to a compute unit, and 73 instructions to a token and channel on two waves of a SIMD wait for
+// each other at the barrier (31 % of the waves' cycles).
 #pragma once
 #include "scan_gates.h"
 

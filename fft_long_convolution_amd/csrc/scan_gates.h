@@ -6,14 +6,14 @@
 namespace lcv {
 namespace {
 
-// A sigmoid and its slope s (1 - s) = e s^2 with e = exp(-x), each to its own size (for x below -69 the slope, less than
-// 1e-30 then, falls off faster than it should).
+// A sigmoid s and 1 - s = e s with e = exp(-x), each to its own size (for x below -69, where s is less than 1e-30, 1 - s falls off
+// instead of staying at one); the slope is their product.
 struct Sigmoid {
-    float s, slope;
+    float s, rest;
 };
 __device__ __forceinline__ Sigmoid sloped_sigmoid(float x) {
     const float e = fast_exp2(-kLog2e * x), s = fast_rcp(1.f + e);
-    return Sigmoid{s, fminf(e, 1e30f) * s * s};
+    return Sigmoid{s, fminf(e, 1e30f) * s};
 }
 
 // A decay a as c + w: c = 1 and w = a - 1 near one, c = 0 and w = a elsewhere, so that both a and 1 - a keep their own size.

@@ -371,37 +371,45 @@ template <int IO, int V, bool GATED, int GATE, int MIX> __global__ void __launch
         Gate<V> g[kScanTokens];
         Decay run[V];
         gates<V, GATE, MIX, true>(g, run, z, rate, n);
-        float u[kScanTokens][V], H[V] = {}, R[V] = {}, before[kScanTokens][V];
+        // Within a turn a decay is one number: its rounding meets eight tokens.  From turn to turn runs go by `run`, and so does
+        // what the next tile begins with.
+        float u[kScanTokens][V], H[V] = {}, R[V] = {}, before[kScanTokens][V], av[kScanTokens][V];
         Sigmoid in[kScanTokens][V];
 #pragma unroll
         for (int j = 0; j < kScanTokens; ++j)
 #pragma unroll
             for (int v = 0; v < V; ++v) {
+                av[j][v] = value_of(g[j].k[v]);
                 d.e[j][v] = j < n ? d.e[j][v] : 0.f;
-                u[j][v] = g[j].m[v] * x.e[j][v];
                 if constexpr (GATED) {
                     in[j][v] = sloped_sigmoid(i.e[j][v]);
-                    u[j][v] *= in[j][v].s;
+                    x.e[j][v] *= in[j][v].s;
                 }
+                u[j][v] = g[j].m[v] * x.e[j][v];
                 u[j][v] = j < n ? u[j][v] : 0.f;
-                H[v] = moved(g[j].k[v], H[v], u[j][v]);
+                H[v] = fmaf(av[j][v], H[v], u[j][v]);
             }
 #pragma unroll
         for (int j = kScanTokens - 1; j >= 0; --j)
 #pragma unroll
-            for (int v = 0; v < V; ++v) R[v] = times(g[j].k[v], d.e[j][v] + R[v]);
+            for (int v = 0; v < V; ++v) R[v] = av[j][v] * (d.e[j][v] + R[v]);
         leave<V>(left[buf][w.wave][lane], run, R);
         store_f<V>(left[buf][w.wave][lane] + 3 * V, H);
         __syncthreads();
         LaneF<V> s = load_f<V>(edge[buf][lane]);
         join_waves<V, 4 * V, true>(s.v, left[buf], lane, w.wave, waves, 2 * V);
         join_waves<V, 4 * V, false>(mark.e, left[buf], lane, w.wave, waves, 3 * V);
+        if (w.wave == 0) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) carry[v] = moved(run[v], s.v[v], R[v]);
+            store_f<V>(edge[buf ^ 1][lane], carry);
+        }
 #pragma unroll
         for (int j = 0; j < kScanTokens; ++j)
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 before[j][v] = mark.e[v];
-                mark.e[v] = moved(g[j].k[v], mark.e[v], u[j][v]);
+                mark.e[v] = fmaf(av[j][v], mark.e[v], u[j][v]);
             }
 #pragma unroll
         for (int j = kScanTokens - 1; j >= 0; --j) {
@@ -409,33 +417,25 @@ template <int IO, int V, bool GATED, int GATE, int MIX> __global__ void __launch
             float gx[V], gz[V], gi[V];
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const Decay k = g[j].k[v];
-                const float G = d.e[j][v] + s.v[v], av = value_of(k), Gm = G * g[j].m[v];
-                s.v[v] = times(k, G);
+                const float G = d.e[j][v] + s.v[v], Gm = G * g[j].m[v];
+                s.v[v] = av[j][v] * G;
                 gx[v] = on ? (GATED ? Gm * in[j][v].s : Gm) : 0.f;
-                if constexpr (GATED) gi[v] = on ? Gm * x.e[j][v] * in[j][v].slope : 0.f;
-                // of log a: a (G h_{t-1} + G s x dm / da), dm / da = 0, -1, -a / m; a norm that is zero has the gradient zero
+                if constexpr (GATED) gi[v] = on ? Gm * x.e[j][v] * in[j][v].rest : 0.f;
+                // of log a: a G (h_{t-1} + s x dm / da), dm / da = 0, -1, -a / m; a norm that is zero has the gradient zero
                 float dl = before[j][v];
-                if constexpr (MIX != LCONV_MIX_PLAIN) {
-                    const float sx = GATED ? in[j][v].s * x.e[j][v] : x.e[j][v];
-                    dl -= MIX == LCONV_MIX_CONVEX ? sx : sx * (av * g[j].inv[v]);
-                }
-                dl *= av * G;
-                if constexpr (GATE == LCONV_GATE_SIGMOID) dl *= loss_of(k);
+                if constexpr (MIX != LCONV_MIX_PLAIN) dl -= MIX == LCONV_MIX_CONVEX ? x.e[j][v] : x.e[j][v] * (av[j][v] * g[j].inv[v]);
+                dl *= s.v[v];
+                if constexpr (GATE == LCONV_GATE_SIGMOID) dl *= loss_of(g[j].k[v]);
                 if constexpr (GATE == LCONV_GATE_RATE) {
-                    drate[v] -= on ? dl * g[j].p[v].s : 0.f;
-                    dl *= per_slope[v] * g[j].p[v].slope;
+                    dl *= g[j].p[v].s;
+                    drate[v] -= on ? dl : 0.f;
+                    dl *= per_slope[v] * g[j].p[v].rest;
                 }
                 gz[v] = on ? dl : 0.f;
             }
             ox.e[j] = narrow<IO, V>(gx);
             oz.e[j] = narrow<IO, V>(gz);
             if constexpr (GATED) oi.e[j] = narrow<IO, V>(gi);
-        }
-        if (w.wave == 0) {
-#pragma unroll
-            for (int v = 0; v < V; ++v) carry[v] = s.v[v];
-            store_f<V>(edge[buf ^ 1][lane], carry);
         }
         buf ^= 1;
     };

@@ -56,13 +56,18 @@ struct ScanPlan {
 //   1 x 65536 x 4096   2, 8, 16: 638   1, 8, 16: 700   1, 16, 1: 1464
 //   1 x 777 x 333      1, 8, 8: 15     1, 16, 1: 24
 //   16 x 300 x 2048    1, 8, 1: 20     1, 16, 1: 26
-// Gradients: 4 x 2048 x 2048 in 1, 2, 4 segments 95, 77, 78; 3 x 1001 x 1000 in 1, 4, 8: 53, 28, 31; 1 x 65536 x 4096 in 1, 4,
-// 8, 16: 2870, 1140, 1043, 1050.
+//   600 x 512 x 64     1, 8, 1: 27     2, 8, 1: 40 (sigmoid, convex: half the lanes without channels)
+// The gradients' registers leave a compute unit one workgroup, mostly: they go by rounds of 256, and a round of two channels takes
+// 7/4 of one (every input, one / two channels): 8 x 2048 x 4096 237 / 211, 9 x 2048 x 2048 206 / 176, 64 x 512 x 1024 128 / 116, but
+// 300 x 512 x 128 89 / 94; in segments 1 x 65536 x 2048 601 / 519, 4 x 2048 x 2048 76 / 65, 3 x 1001 x 1000 30 / 27, but 2 x 700 x 64
+// 24 / 25.  Segments (one channel): 4 x 2048 x 2048 in 1, 2, 4 95, 77, 78; 3 x 1001 x 1000 in 1, 4, 8 53, 28, 31; 1 x 65536 x 4096 in
+// 1, 4, 8, 16 2870, 1140, 1043, 1050.
 inline ScanPlan scan_plan(int64_t B, int64_t N, int64_t C, lconv_dtype_t dtype, bool grad) {
     ScanPlan p{};
     const int64_t ones = B * ((C + 63) / 64), twos = B * ((C + 127) / 128);      // rows of one and of two channels to a lane
-    const bool pairs = !grad && dtype != LCONV_F32 && C % 2 == 0, cut = ones <= (grad ? 128 : 96) && N > 256;
-    p.vec = pairs && (cut || twos >= 256) ? 2 : 1;
+    const bool pairs = dtype != LCONV_F32 && C % 2 == 0 && C > 64, cut = ones <= (grad ? 128 : 96) && N > 256;
+    const auto rounds = [](int64_t rows) { return (rows + 255) / 256; };
+    p.vec = pairs && (cut || (grad ? 7 * rounds(twos) < 4 * rounds(ones) : twos >= 256)) ? 2 : 1;
     p.cblocks = (int)((C + 64 * p.vec - 1) / (64 * p.vec));
     const int64_t rows = B * p.cblocks;
     p.waves = p.vec == 2 || grad || cut || rows >= 512 ? 8 : 16;

@@ -11,9 +11,9 @@
 // Bound by HBM where a call has rows enough: 8 x 2048 x 4096 in bf16 with every input takes 113 us, 537 MB at 4.8 TB/s (the same
 // reads and writes with no arithmetic 106), under 37 vector instructions to a token and channel, 63 us of issue.  In segments
 // 1 x 65536 x 2048, sigmoid and convex, takes 122 us for the segments' sums (537 MB, 4.4 TB/s; 21 instructions and two slow ones
-// are 90 us of issue) and 158 for the pass (805 MB, 5.1 TB/s).  Gradients of 8 x 2048 x 2048 with every input: 117 us for 470 MB,
-// 4.0 TB/s; there is one workgroup to a compute unit, and 73 instructions to a token and channel on two waves of a SIMD wait for
-// each other at the barrier (31 % of the waves' cycles).
+// are 90 us of issue) and 158 for the pass (805 MB, 5.1 TB/s).  Gradients with every input:
+// 8 x 2048 x 4096, two channels to a lane, 211 us for 940 MB, 4.5 TB/s; 8 x 2048 x 2048, whose 256 workgroups take one channel to a
+// lane and so 128 bytes of a row at a time, 115 us for 470 MB, 4.1 TB/s (the forward pass's reads and writes alone reach 4.4 so).
 #pragma once
 #include "scan_gates.h"
 
@@ -575,16 +575,19 @@ template <int IO> hipError_t scan_fwd(const ScanArgs& a, hipStream_t stream) {
     return a.i.p ? scan_fwd<IO, 1, true>(a, stream) : scan_fwd<IO, 1, false>(a, stream);
 }
 
-template <int IO, bool GATED> hipError_t scan_bwd(const ScanArgs& a, hipStream_t stream) {
+template <int IO, int V, bool GATED> hipError_t scan_bwd(const ScanArgs& a, hipStream_t stream) {
     const unsigned grid = (unsigned)(a.B * a.nseg * a.cblocks);
     by_flags(a.gate, a.mix, [&](auto gate, auto mix) {
-        if (a.nseg > 1) scan_segments_kernel<IO, 1, false, gate.value, LCONV_MIX_PLAIN, true><<<grid, 64 * a.waves, 0, stream>>>(a);
-        scan_bwd_kernel<IO, 1, GATED, gate.value, mix.value><<<grid, 64 * a.waves, 0, stream>>>(a);
+        if (a.nseg > 1) scan_segments_kernel<IO, V, false, gate.value, LCONV_MIX_PLAIN, true><<<grid, 64 * a.waves, 0, stream>>>(a);
+        scan_bwd_kernel<IO, V, GATED, gate.value, mix.value><<<grid, 64 * a.waves, 0, stream>>>(a);
     });
     return hipGetLastError();
 }
 template <int IO> hipError_t scan_bwd(const ScanArgs& a, hipStream_t stream) {
-    return a.i.p ? scan_bwd<IO, true>(a, stream) : scan_bwd<IO, false>(a, stream);
+    if constexpr (IO != CT_F32) {
+        if (a.vec == 2) return a.i.p ? scan_bwd<IO, 2, true>(a, stream) : scan_bwd<IO, 2, false>(a, stream);
+    }
+    return a.i.p ? scan_bwd<IO, 1, true>(a, stream) : scan_bwd<IO, 1, false>(a, stream);
 }
 
 }  // namespace

@@ -25,7 +25,7 @@ namespace lcv {
 static void covers(const ScanArgs& a, bool grad) {
     const int64_t tile = (int64_t)a.waves * kScanTokens;
     need(a.waves >= 1 && a.waves <= (grad ? kScanGradWaves : scan_waves(a.vec)), "waves", a.waves, a.vec, grad);
-    need((int64_t)a.cblocks * 64 * a.vec >= a.C && (a.vec == 1 || a.C % 2 == 0) && (!grad || a.vec == 1), "blocks", a.C, a.cblocks, a.vec);
+    need((int64_t)a.cblocks * 64 * a.vec >= a.C && (a.vec == 1 || a.C % 2 == 0), "blocks", a.C, a.cblocks, a.vec);
     need(a.nseg >= 1 && a.nseg * a.seg_len >= a.N && (a.nseg - 1) * a.seg_len < a.N, "segments", a.N, a.nseg, a.seg_len);
     need(a.nseg == 1 || (a.waves == 8 && a.seg_len % tile == 0 && a.seg_len % kScanMark == 0), "segment", a.waves, a.seg_len, tile);
     need(tile % kScanMark == 0 || (a.nseg == 1 && a.N <= tile), "marks", a.N, tile, a.nseg);

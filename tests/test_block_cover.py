@@ -11,8 +11,8 @@ from tests import test_qk_norm_gpu as norm
 from tests import test_short_conv_gpu as conv
 from tests.test_sanitizers import CSRC, HERE, ROOT, _run, _tool, outdir  # noqa: F401
 
-# many rows of one channel to a lane; many short ones of two
-SCAN = [(520, 70, 3), (257, 30, 2)]
+# many rows of one channel to a lane; of two, short ones too and a width that ends inside a wave; two channels in segments
+SCAN = [(520, 70, 3), (257, 70, 66), (256, 30, 130), (130, 70, 66), (130, 30, 128), (3, 600, 70), (1, 1537, 130)]
 # more runs, and more rows, than the gradients' waves
 CONV = [(2100, 40, 3), (4200, 9, 4)]
 # lanes that a head's units fill or not, items of four heads

@@ -50,6 +50,8 @@ struct ScanPlan {
 // workgroups; sixteen waves fill a compute unit that has one workgroup.  Calls of few rows go by segments, which read everything
 // twice but for y.  Measured (bf16, every input, us; channels to a lane, waves, segments):
 //   8 x 2048 x 4096    2, 8, 1: 114    1, 8, 1: 126    1, 16, 1: 123    2, 8, 16: 95 + 132
+//   10 x 2048 x 2048   2, 8, 1: 95     1, 16, 1: 107 (a second round of 256 workgroups)
+//   8 x 2048 x 2048    1, 16, 1: 64    2, 8, 1: 94
 //   16 x 2048 x 1024   1, 16, 1: 53    1, 8, 1: 63     2, 8, 4: 88
 //   4 x 2048 x 2048    1, 16, 1: 52    2, 8, 8: 52     2, 8, 1: 98
 //   2 x 2048 x 2048    2, 8, 8: 34     1, 16, 1: 51
@@ -67,7 +69,7 @@ inline ScanPlan scan_plan(int64_t B, int64_t N, int64_t C, lconv_dtype_t dtype, 
     const int64_t ones = B * ((C + 63) / 64), twos = B * ((C + 127) / 128);      // rows of one and of two channels to a lane
     const bool pairs = dtype != LCONV_F32 && C % 2 == 0 && C > 64, cut = ones <= (grad ? 128 : 96) && N > 256;
     const auto rounds = [](int64_t rows) { return (rows + 255) / 256; };
-    p.vec = pairs && (cut || (grad ? 7 * rounds(twos) < 4 * rounds(ones) : twos >= 256)) ? 2 : 1;
+    p.vec = pairs && (cut || (grad ? 7 * rounds(twos) < 4 * rounds(ones) : ones > 256)) ? 2 : 1;
     p.cblocks = (int)((C + 64 * p.vec - 1) / (64 * p.vec));
     const int64_t rows = B * p.cblocks;
     p.waves = p.vec == 2 || grad || cut || rows >= 512 ? 8 : 16;

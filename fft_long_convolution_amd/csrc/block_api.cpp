@@ -51,10 +51,15 @@ bool scan_flags_ok(int flags) {
 }
 
 // sizes that the kernels' indices hold: channels and segments in 32 bits, marks and states in 64
-bool scan_dims_ok(int64_t B, int64_t N, int64_t C, lconv_dtype_t dtype) {
+bool scan_sizes_ok(int64_t B, int64_t N, int64_t C) {
     int64_t t;
     if (N >= ((int64_t)1 << 31) || C > ((int64_t)1 << 24) || B > ((int64_t)1 << 24) || !mul_ok(B, C, &t)) return false;
-    if (!mul_ok(t, (N + kScanMark - 1) / kScanMark, &t) || t > INT64_MAX / 16) return false;
+    return mul_ok(t, (N + kScanMark - 1) / kScanMark, &t) && t <= INT64_MAX / 16;
+}
+
+// and those that a launch has threads for, which differ by type, as 16-bit calls may have two channels to a lane
+bool scan_dims_ok(int64_t B, int64_t N, int64_t C, lconv_dtype_t dtype) {
+    if (!scan_sizes_ok(B, N, C)) return false;
     // workgroups of 1024 threads (gradients: 512), and single tokens
     const ScanPlan p = scan_plan(B, N > 0 ? N : 1, C, dtype, false), g = scan_plan(B, N > 0 ? N : 1, C, dtype, true);
     return B * p.cblocks * p.nseg <= kMaxGrid / 4 && B * g.cblocks * g.nseg <= kMaxGrid / 2 && B * ((C + 511) / 256) <= kMaxGrid;
@@ -73,7 +78,7 @@ void set_plan(ScanArgs* a, const ScanPlan& p) {
 extern "C" {
 
 size_t lconv_gated_scan_marks_bytes(int64_t B, int64_t N, int64_t C) {
-    if (B <= 0 || N <= 0 || C <= 0 || !scan_dims_ok(B, N, C, LCONV_F32)) return 0;      // whose blocks are the most
+    if (B <= 0 || N <= 0 || C <= 0 || !scan_sizes_ok(B, N, C)) return 0;      // whatever a launch of some type takes
     return (size_t)(B * ((N + kScanMark - 1) / kScanMark)) * (size_t)C * 4;
 }
 

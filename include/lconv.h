@@ -660,7 +660,7 @@ lconv_status_t lconv_qknorm_rotary_bwd(const void* dyq, const lconv_strides_t* d
  *   state_in     [B][C] fp32 or NULL (zeros);  state_out the same shape or NULL; the two may be one buffer
  *   lengths      [B] int32, device, or NULL (every row N long); taken as min(max(len, 0), N)
  *   marks        lconv_gated_scan_marks_bytes(B, N, C) bytes, written, or NULL: states along the way, which the gradient
- *                call takes in place of y
+ *                call takes in place of y (the size goes by B, N and C alone and is there for every call that any dtype supports)
  *   workspace    lconv_gated_scan_workspace_bytes(B, N, C, dtype) bytes (may be NULL if that is 0)
  * Strides are lconv_strides_t without h, in elements, of any size that keeps an output's rows apart; NULL: dense.  These
  * operands may begin at any element, the others are 16-byte aligned.  Gates, states and sums are fp32, a's distance from 1 to its own size, so that memories of many thousand

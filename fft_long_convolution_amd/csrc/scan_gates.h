@@ -6,14 +6,14 @@
 namespace lcv {
 namespace {
 
-// A sigmoid s and 1 - s = e s with e = exp(-x), each to its own size (for x below -69, where s is less than 1e-30, 1 - s falls off
-// instead of staying at one); the slope is their product.
+// A sigmoid s and 1 - s = e s with e = exp(-x), each to its own size; the slope is their product.  Where e is past 2^126, s is too
+// small for the reciprocal and both are zero.
 struct Sigmoid {
     float s, rest;
 };
 __device__ __forceinline__ Sigmoid sloped_sigmoid(float x) {
     const float e = fast_exp2(-kLog2e * x), s = fast_rcp(1.f + e);
-    return Sigmoid{s, fminf(e, 1e30f) * s};
+    return Sigmoid{s, fminf(e, 0x1p126f) * s};
 }
 
 // A decay a as c + w: c = 1 and w = a - 1 near one, c = 0 and w = a elsewhere, so that both a and 1 - a keep their own size.

@@ -162,9 +162,9 @@ template <int IO, int V, int K> __global__ void __launch_bounds__(256) conv_bwd_
                         float p = taps.b[v];
 #pragma unroll
                         for (int j = 0; j < K; ++j) p = fmaf(taps.w[j][v], win[j].v[v], p);
-                        // s (1 + p (1 - s)), 1 - s = e s to its own size (where e is cut off, s is less than 1e-30)
+                        // s (1 + p (1 - s)), 1 - s = e s to its own size (where e is cut off, s is too small for the reciprocal and zero)
                         const float e = fast_exp2(-kLog2e * p), sig = fast_rcp(1.f + e);
-                        g *= sig * fmaf(p, fminf(e, 1e30f) * sig, 1.f);
+                        g *= sig * fmaf(p, fminf(e, 0x1p126f) * sig, 1.f);
                     }
                     g = on ? g : 0.f;
                     const float part = own ? g : 0.f;

@@ -166,14 +166,18 @@ template <int IO, int V, int K> __global__ void __launch_bounds__(256) conv_bwd_
                         const float e = fast_exp2(-kLog2e * p), sig = fast_rcp(1.f + e);
                         g *= sig * fmaf(p, fminf(e, 0x1p126f) * sig, 1.f);
                     }
-                    g = on ? g : 0.f;
-                    const float part = own ? g : 0.f;
-                    db[v] += part;
-                    acc[K - 1].v[v] = taps.w[K - 1][v] * g;
+                    // what the row does not have is left out, not multiplied by zero: an input or a weight may be no number
+                    acc[K - 1].v[v] = 0.f;
+                    if (on) {
+                        acc[K - 1].v[v] = taps.w[K - 1][v] * g;
 #pragma unroll
-                    for (int j = 0; j < K; ++j) dw[j][v] = fmaf(part, win[j].v[v], dw[j][v]);
+                        for (int j = 0; j < K - 1; ++j) acc[j].v[v] = fmaf(taps.w[j][v], g, acc[j].v[v]);
+                    }
+                    if (own) {
+                        db[v] += g;
 #pragma unroll
-                    for (int j = 0; j < K - 1; ++j) acc[j].v[v] = fmaf(taps.w[j][v], g, acc[j].v[v]);
+                        for (int j = 0; j < K; ++j) dw[j][v] = fmaf(g, win[j].v[v], dw[j][v]);
+                    }
                 }
                 // dx of token s is complete
                 if (s >= r.t0 ? s < r.t1 : (r.first && a.state_out && s >= -(K - 1))) {

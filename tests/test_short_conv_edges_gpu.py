@@ -1,4 +1,4 @@
-"""Gradients of the short convolution at the ends: SiLU's slope far out."""
+"""Gradients of the short convolution at the ends: SiLU's slope far out, values that are not finite."""
 import numpy as np
 import pytest
 
@@ -42,3 +42,51 @@ def test_slopes_far_out(lc, dtype):
     off = float(np.max(over / (size * (SLACK + 1.25 * 2.0 ** -24 * np.abs(P)))))
     say(f"   {off:.2f}")
     assert np.all(np.isfinite(got)) and off <= 1
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("C", [3, 24])
+@pytest.mark.parametrize("silu", [False, True])
+def test_values_that_are_not_finite(lc, dtype, C, silu):
+    """A weight that is not finite reaches its channel's tokens and none behind a row's length; an input reaches the gradients of the
+    taps that met it: the last one's alone, for a row's last token."""
+    import torch
+    rng = np.random.default_rng(1401)
+    act = "silu" if silu else None
+    for K in (2, 4, 8):
+        for B, N, ends in ((5, 45, [45, 0, 1, 17, 33]), (2, 300, [300, 299])):
+            say(f"[conv edges] not finite {dtype} K={K} silu={silu} {(B, N, C)}")
+            n = torch.tensor(ends, dtype=torch.int32)
+            x, dy, w = host(rng, (B, N, C), dtype), host(rng, (B, N, C), dtype), host(rng, (C, K), dtype)
+            s, ds = host(rng, (B, K - 1, C), dtype), host(rng, (B, K - 1, C), dtype)
+            gx, gdy, gw, gn, gs, gds = cuda(x, dy, w, n, s, ds)
+            clean = lc.short_conv_bwd(gdy, gx, gw, activation=act, state=gs, dstate=gds, lengths=gn)
+            for bad in (float("nan"), float("inf")):
+                for j in (0, K - 1):
+                    v = gw.clone()
+                    v[1, j] = bad
+                    g = lc.short_conv_bwd(gdy, gx, v, activation=act, state=gs, dstate=gds, lengths=gn)
+                    for b, end in enumerate(ends):
+                        assert not bool(g.dx[b, end:].any()), (K, end)
+                        if end == 0:
+                            assert bool((g.dstate[b] == gds[b]).all())
+                        if end > 1:
+                            # token t's own tap K - 1 - j meets dp of token s + K - 1 - j
+                            hit = g.dx[b, :max(end - (K - 1 - j), 0), 1]
+                            past = g.dx[b, max(end - (K - 1 - j), 0):end, 1]
+                            assert silu or (not bool(hit.isfinite().any()) and bool(past.isfinite().all()))
+                    rest = [c for c in range(C) if c != 1]
+                    assert bool((g.dx[..., rest] == clean.dx[..., rest]).all())
+                    assert bool((g.dweight[rest] == clean.dweight[rest]).all())
+            if silu:
+                continue
+            # a row's last input: tap K - 1 alone meets it
+            for b, end in enumerate(ends):
+                if end == 0:
+                    continue
+                y = gx.clone()
+                y[b, end - 1, 2] = float("inf")
+                g = lc.short_conv_bwd(gdy, y, gw, activation=act, state=gs, dstate=gds, lengths=gn)
+                assert not bool(g.dweight[2, K - 1].isfinite())
+                assert bool((g.dweight[2, :K - 1] == clean.dweight[2, :K - 1]).all()), (K, end)
+                assert bool((g.dx == clean.dx).all())

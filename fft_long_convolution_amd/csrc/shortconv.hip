@@ -157,26 +157,29 @@ template <int IO, int V, int K> __global__ void __launch_bounds__(256) conv_bwd_
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     win[K - 1].v[v] = on ? xv[v] : 0.f;
-                    float g = dv[v];
                     if (a.silu) {
                         float p = taps.b[v];
 #pragma unroll
                         for (int j = 0; j < K; ++j) p = fmaf(taps.w[j][v], win[j].v[v], p);
                         // s (1 + p (1 - s)), 1 - s = e s to its own size (where e is cut off, s is too small for the reciprocal and zero)
                         const float e = fast_exp2(-kLog2e * p), sig = fast_rcp(1.f + e);
-                        g *= sig * fmaf(p, fminf(e, 0x1p126f) * sig, 1.f);
+                        dv[v] *= sig * fmaf(p, fminf(e, 0x1p126f) * sig, 1.f);
                     }
-                    // what the row does not have is left out, not multiplied by zero: an input or a weight may be no number
-                    acc[K - 1].v[v] = 0.f;
-                    if (on) {
-                        acc[K - 1].v[v] = taps.w[K - 1][v] * g;
+                }
+                // what the row does not have is left out, not multiplied by zero: an input or a weight may be no number
+                acc[K - 1] = Lane<V>{};
+                if (on) {
 #pragma unroll
-                        for (int j = 0; j < K - 1; ++j) acc[j].v[v] = fmaf(taps.w[j][v], g, acc[j].v[v]);
-                    }
-                    if (own) {
-                        db[v] += g;
+                    for (int v = 0; v < V; ++v)
 #pragma unroll
-                        for (int j = 0; j < K; ++j) dw[j][v] = fmaf(g, win[j].v[v], dw[j][v]);
+                        for (int j = 0; j < K; ++j) acc[j].v[v] = fmaf(taps.w[j][v], dv[v], acc[j].v[v]);
+                }
+                if (own) {
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        db[v] += dv[v];
+#pragma unroll
+                        for (int j = 0; j < K; ++j) dw[j][v] = fmaf(dv[v], win[j].v[v], dw[j][v]);
                     }
                 }
                 // dx of token s is complete

@@ -35,9 +35,11 @@ __device__ __forceinline__ Decay decay_of_logit(float z) {     // a = sigmoid(z)
     const bool near = z >= 0.f;
     return Decay{near ? 1.f : 0.f, near ? -small : small};
 }
-// 1 - a^2 as -w (2 + w) or 1 - w^2, and its root
+// 1 - a^2 as -w (2 + w) or 1 - w^2, its root and one over that (0 for nothing).  A decay may lose less than 2^-126, which the
+// hardware's roots take for zero (an inverse one gives infinity): the least loss there is, 2^-149, is a normal number times 2^32.
 __device__ __forceinline__ float energy_of(Decay k) { return fmaf(-k.w, k.w, k.c > 0.f ? -2.f * k.w : 1.f); }
-__device__ __forceinline__ float norm_of(Decay k) { return fast_sqrt(energy_of(k)); }
+__device__ __forceinline__ float norm_of(Decay k) { return 0x1p-16f * fast_sqrt(0x1p32f * energy_of(k)); }
+__device__ __forceinline__ float inverse_norm(float energy) { return energy > 0.f ? 0x1p16f * fast_rsqrt(0x1p32f * energy) : 0.f; }
 
 // A state h after one more token or run of tokens, and x times a decay
 __device__ __forceinline__ float moved(Decay k, float h, float u) { return fmaf(k.c, h, fmaf(k.w, h, u)); }

@@ -102,7 +102,7 @@ __device__ __forceinline__ void gates(Gate<V>* g, Decay* run, const Wide<V>& z, 
             g[j].k[v] = k;
             if constexpr (MIX == LCONV_MIX_NORM && GRAD) {
                 const float e = energy_of(k);
-                g[j].inv[v] = e > 0.f ? fast_rsqrt(e) : 0.f;
+                g[j].inv[v] = inverse_norm(e);
                 g[j].m[v] = e * g[j].inv[v];
             } else {
                 g[j].m[v] = MIX == LCONV_MIX_NORM ? norm_of(k) : MIX == LCONV_MIX_CONVEX ? loss_of(k) : 1.f;

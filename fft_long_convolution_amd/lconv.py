@@ -1379,8 +1379,8 @@ def gated_scan(x, z, gate="sigmoid", mix="plain", input_gate=None, rate=None, st
 
         h_t = a_t h_{t-1} + m_t s_t x_t,    y_t = h_t
 
-    gate: "log" (log a = z, at most 0), "sigmoid" (a = sigmoid(z)) or "rate" (log a = -rate sigmoid(z), rate [C] in
-    float32, at least 0).  mix: "plain" (m = 1), "convex" (1 - a) or "norm" (sqrt(1 - a^2)).  s is sigmoid(input_gate), or 1
+    gate: "log" (log a = z, at most 0; a z above 0 is not refused, and leaves its channel's results without meaning), "sigmoid"
+    (a = sigmoid(z)) or "rate" (log a = -rate sigmoid(z), rate [C] in float32, at least 0).  mix: "plain" (m = 1), "convex" (1 - a) or "norm" (sqrt(1 - a^2)).  s is sigmoid(input_gate), or 1
     without one.  lengths: int32 [B], tokens past a row's length count for nothing and give y = 0.  Returns (y in x's dtype,
     the state after each row's last token; None without need_state, marks for the gradient call; None without need_marks).
     state_out may be `state` itself."""

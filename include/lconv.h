@@ -663,9 +663,11 @@ lconv_status_t lconv_qknorm_rotary_bwd(const void* dyq, const lconv_strides_t* d
  *                call takes in place of y (the size goes by B, N and C alone and is there for every call that any dtype supports)
  *   workspace    lconv_gated_scan_workspace_bytes(B, N, C, dtype) bytes (may be NULL if that is 0)
  * Strides are lconv_strides_t without h, in elements, of any size that keeps an output's rows apart; NULL: dense.  These
- * operands may begin at any element, the others are 16-byte aligned.  Gates, states and sums are fp32, a's distance from 1 to its own size, so that memories of many thousand
- * tokens neither end early nor drift.  A value that is not finite reaches what the recurrence lets it reach, as a value that
- * is not finite: its own and later tokens of its channel (in the gradients its own and earlier ones).
+ * operands may begin at any element, the others are 16-byte aligned.  Gates, states and sums are fp32, a's distance from 1 to its
+ * own size, so that memories of many thousand tokens neither end early nor drift; exponentials below 2^-126 are zero.  A log a
+ * above 0 is not checked for: the results of its channel from there on (gradients: of its whole row) are then of no meaning.
+ * A value that is not finite reaches what the recurrence lets it reach, as a value that is not finite: its own and later tokens of
+ * its row and channel.
  * Supported: N < 2^31, B and C up to 2^24, every dtype, launches of fewer than 2^32 threads.  B, C or N = 0 is a no-op apart
  * from state_out, which is set as for rows of length 0 (N = 0).
  */
@@ -693,7 +695,12 @@ lconv_status_t lconv_gated_scan_fwd(const void* x, const lconv_strides_t* x_stri
  *   dx, dz, dinput_gate  [B][N][C] dtype, written (zeros past a row's length); dinput_gate with input_gate only
  *   drate      [C] fp32, written, or NULL;  dstate_in  [B][C] fp32, written, or NULL, may be dstate_out
  *   workspace  lconv_gated_scan_bwd_workspace_bytes(B, N, C, flags, dtype) bytes (may be NULL if that is 0)
- * No atomics: results repeat bit for bit.
+ * No atomics: results repeat bit for bit.  A value that is not finite reaches, as one that is not, in its row and channel:
+ *   dy, dstate_out  dx, dz and dinput_gate of its own and earlier tokens; dstate_in
+ *   x               dz of later tokens; its own dinput_gate and (but for LCONV_MIX_PLAIN) dz
+ *   input_gate      what x does, and its own dx
+ *   z               dz of every token; dx and dinput_gate of earlier tokens and (but for LCONV_MIX_PLAIN) its own; dstate_in
+ * and any of them drate of its channel.
  */
 size_t lconv_gated_scan_bwd_workspace_bytes(int64_t B, int64_t N, int64_t C, int flags, lconv_dtype_t dtype);
 lconv_status_t lconv_gated_scan_bwd(const void* dy, const lconv_strides_t* dy_strides, const void* x,

@@ -59,8 +59,10 @@ struct ScanPlan {
 //   1 x 777 x 333      1, 8, 8: 15     1, 16, 1: 24
 //   16 x 300 x 2048    1, 8, 1: 20     1, 16, 1: 26
 //   600 x 512 x 64     1, 8, 1: 27     2, 8, 1: 40 (sigmoid, convex: half the lanes without channels)
-// The gradients' registers leave a compute unit one workgroup, mostly: they go by rounds of 256, and a round of two channels takes
-// 7/4 of one (every input, one / two channels): 8 x 2048 x 4096 237 / 211, 9 x 2048 x 2048 206 / 176, 64 x 512 x 1024 128 / 116, but
+// With two channels to a lane a compute unit holds one workgroup of the gradients (of log or sigmoid, plain, without an input gate:
+// two); with one channel one of those with an input gate and rate and norm, rate and convex, or sigmoid and norm (130 to 144
+// registers), two of the others.  They go by rounds of 256, and a round of two channels takes 7/4 of one, as measured where one
+// workgroup is all there is, for the others too (every input, one / two channels): 8 x 2048 x 4096 237 / 211, 9 x 2048 x 2048 206 / 176, 64 x 512 x 1024 128 / 116, but
 // 300 x 512 x 128 89 / 94; in segments 1 x 65536 x 2048 601 / 519, 4 x 2048 x 2048 76 / 65, 3 x 1001 x 1000 30 / 27, but 2 x 700 x 64
 // 24 / 25.  Segments (one channel): 4 x 2048 x 2048 in 1, 2, 4 95, 77, 78; 3 x 1001 x 1000 in 1, 4, 8 53, 28, 31; 1 x 65536 x 4096 in
 // 1, 4, 8, 16 2870, 1140, 1043, 1050.
@@ -122,8 +124,9 @@ inline QkPlan qk_plan(int64_t tokens, int64_t D, int64_t rot, int heads) {
     return p;
 }
 // The gradients' workgroups keep to q or to k, each with a partial sum of that weight's gradient over its items; at most as
-// many for both as the chip holds at once (three to a compute unit), shared out by heads.  Measured (bf16, D = 128, 16 + 16
-// heads of 4 x 4096 tokens, us, at most 512, 768, 1024): 90, 86, 97; workgroups that take q and k in turn, 1024: 114.
+// many for both as the chip holds at once in 16 bits (three to a compute unit; of fp32, with 176 registers, two, so that a third of
+// its workgroups begin when others have ended), shared out by heads.  Measured (bf16, D = 128, 16 + 16 heads of 4 x 4096 tokens, us,
+// at most 512, 768, 1024): 90, 86, 97; workgroups that take q and k in turn, 1024: 114.
 struct QkGradPlan {
     QkPlan p[2];
     int parts[2];
@@ -185,8 +188,9 @@ struct ConvPlan {
 // The last lane of a width that four does not divide shares channels with the one before it; inplace (one buffer for both
 // states) forbids that, since the two may be in different workgroups, one of which would read what the other has written.
 // Runs: every wave reads K - 1 tokens of its neighbours again, and few calls have waves to spare.  The gradients' waves take
-// runs in turn, as many waves as the chip holds (three workgroups to a compute unit by their registers, of more than four taps
-// two).  Measured (bf16, us, forward / gradients): 8 x 2048 x 4096, K = 4: runs of 16 49 / 108, 32 48 / 94, 64 49 / 99, in 512,
+// runs in turn: 768 workgroups, or 512 of more than four taps, as measured at 4 and 8 taps in bf16.  By their registers a compute
+// unit holds three workgroups of 3 or 4 taps and two of 6 to 8; of 2 taps it would hold four, of 5 in 16 bits three.  Measured
+// (bf16, us, forward / gradients): 8 x 2048 x 4096, K = 4: runs of 16 49 / 108, 32 48 / 94, 64 49 / 99, in 512,
 // 768, 1024 workgroups 103, 94, 107; 1 x 65536 x 2048, K = 8: 32 119 / 256, 64 114 / 232, 128 116 / 206, in 512, 768, 1024
 // workgroups 206, 215, 213; 2 x 2048 x 2048, K = 4: 16 10 / 20, 32 11 / 23; 3 x 1001 x 1000, K = 3: 16 6.5 / 16, 32 8.8 / 21.
 inline ConvPlan conv_plan(int64_t B, int64_t N, int64_t C, int64_t K, bool grad, bool inplace) {

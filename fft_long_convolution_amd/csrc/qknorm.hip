@@ -5,8 +5,9 @@
 // One read and one write of q and k (gradients: two reads, one write), bound by HBM.  A head's row lives in the registers of
 // up to 64 lanes, two groups of 8 elements each, laid out as the pairs that turn together, so that sums cross lanes and
 // turns do not.  A group of lanes takes one token of up to four heads: they share the sines, and the next head's loads are on
-// their way.  Measured (bf16, D = 128, 16 + 16 heads of 4 x 4096 tokens): 55 us forward (268 MB, 4.9 TB/s), 86 for the gradients and
-// their sums (403 MB, 4.7 TB/s); one token of 64 x (16 + 4) heads 4.2 us, a launch and the sines' arithmetic in 64 bits.
+// their way.  Measured (bf16, D = 128, 16 + 16 heads of 4 x 4096 tokens, other inputs each call): 55 us forward (268 MB, 4.9 TB/s;
+// 47 where the call before has left its inputs in the cache), 83 for the gradients and their sums (403 MB, 4.9 TB/s); one token
+// of 64 x (16 + 4) heads 4.2 us, a launch and the sines' arithmetic in 64 bits.
 #include "block_kernels.h"
 #include "mixer_io.h"
 #include "rotary_turn.h"

@@ -8,12 +8,14 @@
 // sequence with the next tile's loads on their way: one pass over the data.  Calls of few rows are cut into segments along the
 // sequence: a first launch finds the segments' decays and sums, the second begins each segment with the join of those
 // before it.
-// Bound by HBM where a call has rows enough: 8 x 2048 x 4096 in bf16 with every input takes 113 us, 537 MB at 4.8 TB/s (the same
-// reads and writes with no arithmetic 106), under 37 vector instructions to a token and channel, 63 us of issue.  In segments
-// 1 x 65536 x 2048, sigmoid and convex, takes 122 us for the segments' sums (537 MB, 4.4 TB/s; 21 instructions and two slow ones
-// are 90 us of issue) and 158 for the pass (805 MB, 5.1 TB/s).  Gradients with every input:
-// 8 x 2048 x 4096, two channels to a lane, 211 us for 940 MB, 4.5 TB/s; 8 x 2048 x 2048, whose 256 workgroups take one channel to a
-// lane and so 128 bytes of a row at a time, 115 us for 470 MB, 4.1 TB/s (the forward pass's reads and writes alone reach 4.4 so).
+// Bound by HBM where a call has rows enough (times of calls in a row, every call on other inputs than the last):
+// 8 x 2048 x 4096 in bf16 with every input takes 113 us, 537 MB at 4.8 TB/s (the same reads and writes with no arithmetic 106),
+// under 39 vector instructions to a token and channel, 66 us of issue; sigmoid and convex in fp32 164, 805 MB at 4.9 TB/s.  In
+// segments 1 x 65536 x 2048, sigmoid and convex, takes 287 us: by a trace, averages, 128 for the segments' sums (537 MB, 4.2 TB/s;
+// 21 instructions and two slow ones are 90 us of issue) and 166 for the pass (805 MB, 4.8 TB/s).  Gradients, the rate's sum with
+// them: 8 x 2048 x 4096 with every input, two channels to a lane, 209 us for 940 MB, 4.5 TB/s; 8 x 2048 x 2048, whose 256 workgroups
+// take one channel to a lane and so 128 bytes of a row at a time, 118 us for 470 MB, 4.0 TB/s (the forward pass's reads and writes
+// alone reach 4.4 so); sigmoid and convex in fp32 279 us for 1.34 GB, 4.8 TB/s.
 #pragma once
 #include "scan_gates.h"
 
@@ -155,6 +157,8 @@ template <int V> __device__ __forceinline__ void store_f(float* p, const float* 
 // The segments before this one (BACK: behind it) for the state h: each [3][C], its decay (two) and what it adds up from zero.  The
 // first to join is what enters the row, which stands in the place of the last segment (BACK: of the first).  Eight at a time, so
 // that their reads wait together, behind the first tile's (5 x 777 x 333 in fp32, 7 segments: 7.3 us for 8.4 one after another).
+// Bound by that chain in long and narrow rows, which have up to 512 segments: 1 x 65536 x 128, sigmoid and convex, 136 us, of which
+// the data's share is below 20.
 template <int V, bool BACK> __device__ __forceinline__ void join_segments(float* h, const ScanArgs& a, const Place<V>& w) {
     constexpr int BATCH = 8;
     const int count = BACK ? a.nseg - w.seg : w.seg + 1;

@@ -6,8 +6,8 @@
 // channels of a run of tokens, a lane one or four of them, with the last K inputs and the weights in its registers; the K - 1
 // inputs before a run are read again, through the caches.  A token is the same for a whole wave, so lengths and ends cost
 // scalar instructions only.  Measured at 8 x 2048 x 4096, K = 4, SiLU, bf16: 48 us forward (268 MB, 5.6 TB/s in a row of calls, part
-// of it from the caches; 52 beside its gradients) and 94 for the gradients and their sum (403 MB at 4.6 TB/s without the sum's 5
-// us; 33 vector instructions to a token and channel are 56 us of issue).
+// of it from the caches; 52 with other inputs each call) and 96 for the gradients and their sum (403 MB at 4.4 TB/s without the sum's
+// 5 us; 32 vector instructions to a token and channel are 55 us of issue); in fp32 116 (537 MB, 4.6 TB/s) and 175 (805 MB, 4.7).
 #include "block_kernels.h"
 #include "token_io.h"
 

@@ -7,7 +7,8 @@ namespace {
 
 constexpr float kLog2e = 1.44269504f;
 
-// Single instructions, off by one unit in the last place; exponentials below 2^-126 are zero.
+// Single instructions, off by one unit in the last place; exponentials below 2^-126 are zero, and a number below that is zero to
+// the roots and the reciprocal (whose inverse is infinite).
 __device__ __forceinline__ float fast_rcp(float x) { return __builtin_amdgcn_rcpf(x); }
 __device__ __forceinline__ float fast_sqrt(float x) { return __builtin_amdgcn_sqrtf(x); }
 __device__ __forceinline__ float fast_rsqrt(float x) { return __builtin_amdgcn_rsqf(x); }

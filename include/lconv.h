@@ -610,8 +610,10 @@ lconv_status_t lconv_layernorm_bwd(const void* dy, int64_t dy_stride, const void
  *   q, yq      [B][H][N][D] dtype;  k, yk  [B][G][N][D] dtype, or both NULL;  strides as for linear attention
  *   q_weight, k_weight  [D] dtype or NULL (ones)
  *   positions, pos_stride, inv_freq, magnitude  as for lconv_rotary (inv_freq may be NULL for rot = 0)
- * Sums, statistics and angles as in lconv_layernorm_fwd and lconv_rotary; one rounding, of the result.  yq may be q itself
- * (same pointer and strides), likewise yk and k; otherwise no overlap.  A value that is not finite stays within its row.
+ * Sums, statistics and angles as in lconv_layernorm_fwd and lconv_rotary; one rounding, of the result.  Squares are fp32: a row
+ * whose sum of them passes 2^128 (values from about 1e19 on) has r = 0, and values below 1e-19 count for less than their size
+ * beside an eps that is as small.  yq may be q itself (same pointer and strides), likewise yk and k; otherwise no overlap.  A value
+ * that is not finite stays within its row.
  * Supported: D a multiple of 8 in [8, 512]; rot even in [0, D]; fewer than 2^31 tokens of four heads and 2^32 threads, 8 pairs
  * or 16 elements of a token each; every dtype.
  */
